@@ -1,7 +1,8 @@
 /*
  * mtp_rs.h -- C ABI of the GB300 (sm_103a) library for multi-token-prediction
- * rejection-sampling verification, per-position row statistics and the fused
- * forward+backward of the end-to-end TV loss.
+ * rejection-sampling verification, per-position row statistics, the fused
+ * forward+backward of the end-to-end TV loss, and the operators of
+ * tree-shaped drafts (attention, beam selection, commit).
  *
  * Method references (page title, section):
  *   [BB] "Breaking Entropy Bounds: Accelerating RL Training via MTP with
@@ -318,6 +319,167 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
                      mtp_dtype dtype, float temperature, int N, int gamma, int K, int V, float grad_scale,
                      int loss_kind, float tau_max, float *loss, float *alpha, float *grad_draft_logits,
                      int32_t *row_flags, mtp_stream_t stream);
+
+/*
+ * Tree-shaped drafts.  A drafter that keeps several continuations per step
+ * hands over a tree of T nodes: node i is a drafted token, parents[b, i] < i
+ * the node it continues (-1: it continues the cached text itself; a NULL
+ * `parents` is a chain, parents[b, i] = i - 1).  n_nodes [B] (NULL: T) is the
+ * number of nodes that sequence b really has; it may be 0.  The keys and
+ * values of past tokens lie in a paged cache [num_pages, page_size, Hkv, D]:
+ * token t of sequence b is row t % page_size of page
+ * page_table[b, t / page_size], t < cache_len[b].  Those of the nodes are
+ * separate, [B, T, Hkv, D]; mtp_tree_commit writes the accepted ones behind
+ * the cached tokens.  Pages may have any size and order, and entries of the
+ * table beyond the tokens a call needs are not read.  A length or node count
+ * out of range, a page outside [0, num_pages) and a parent out of range flag
+ * the sequence MTP_ROW_BAD_ID.
+ *
+ * The calls below that need scratch memory take it from the caller
+ * (`workspace`, 16-byte aligned, its size from the function of the same name
+ * with _workspace); its contents before and after a call mean nothing.  Calls
+ * that may run at the same time need workspaces of their own.
+ */
+#define MTP_MAX_NODES 64    /* nodes of a tree */
+#define MTP_MAX_BEAMS 64    /* beams of a sequence in mtp_beam_select */
+#define MTP_MAX_SELECT 64   /* continuations mtp_beam_select returns */
+
+/*
+ * mtp_tree_attention -- attention of the nodes of a drafted tree over the
+ * paged cache and over the nodes on their own path [EM Related Work,
+ * "Speculative Decoding": tree attention verifies all candidates in one
+ * pass]; with T = 1 the decoding step of a single token.
+ *
+ * For sequence b, node i < n_nodes[b], query head hq (key head h = hq /
+ * (Hq / Hkv)): over the keys k_j of the cache_len[b] cached tokens and of
+ * node i and its ancestors,
+ *   s_j = scale q[b,i,hq] . k_j,  out[b,i,hq] = sum_j softmax(s)_j v_j,
+ *   lse[b,i,hq] = ln sum_j exp s_j.
+ * Rows of nodes >= n_nodes[b] are left as they were.  A node that a row does
+ * not see never reaches its output, not even where its value is infinite or
+ * NaN; nor do rows of a page behind the sequence's last token.  A flagged
+ * sequence gets NaN rows.
+ *
+ *   q [B, T, Hq, D], k_new and v_new [B, T, Hkv, D], k_cache and v_cache
+ *   [num_pages, page_size, Hkv, D]: elements of `dtype`, D contiguous, the
+ *   other strides in elements below (so that q, k and v may be parts of one
+ *   projection and the cache may have its heads outside its tokens)
+ *   out [B, T, Hq, D] dtype, lse [B, T, Hq] float32 or NULL, contiguous
+ *   row_flags [B] or NULL.
+ * Requirements: 1 <= T <= MTP_MAX_NODES, Hq a multiple of Hkv, 1 <= D <= 256,
+ * 0 < scale, max_pages * page_size < 2^31 - 2^16 (else MTP_ERR_INVALID_ARG);
+ * pointers aligned to their elements (else MTP_ERR_MISALIGNED).  Scores, softmax statistics
+ * and outputs are accumulated in float32; with bfloat16 storage the softmax
+ * weights are rounded to bfloat16 for their product with the values (the
+ * weights' sum is not).
+ */
+typedef struct mtp_tree_attention_args {
+    const void *q, *k_new, *v_new, *k_cache, *v_cache;
+    const int32_t *page_table; /* [B, max_pages] */
+    const int32_t *cache_len;  /* [B] */
+    const int32_t *parents;    /* [B, T] or NULL */
+    const int32_t *n_nodes;    /* [B] or NULL */
+    void *out;
+    float *lse;
+    int32_t *row_flags;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_stride[3], k_new_stride[3], v_new_stride[3]; /* b, t, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];          /* page, token, head */
+    int dtype; /* mtp_dtype */
+    int B, T, Hq, Hkv, D;
+    int num_pages, page_size, max_pages;
+    float scale;
+} mtp_tree_attention_args;
+
+int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream);
+/* Bytes of workspace for a call with these sizes, strides and addresses of
+ * the inputs (the workspace fields are not read); -1 for arguments that the
+ * call would refuse. */
+int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
+
+/*
+ * mtp_beam_select -- the K best continuations of a sequence's W beams (one
+ * level of a draft tree, or one step of beam search): over w < W, v < V
+ *   score(w, v) = scores[b,w] + ln softmax(logits[b,w] / T_b)(v),
+ * the K largest, best first; equal scores go to the smaller beam, then the
+ * smaller token.  A continuation of probability 0 is never selected: where
+ * fewer than K are left the rest has token and parent -1 and score -inf.  A
+ * beam with score -inf is dead: its logits are not read.
+ *
+ *   logits [B, W, V] dtype, scores [B, W] float32, temperature [B] (> 0, else
+ *   MTP_ROW_BAD_TEMP)
+ *   tokens, parents [B, K] int32, out_scores [B, K] float32 (required),
+ *   row_flags [B] or NULL; a flagged sequence (a score or a read logit NaN or
+ *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and parents -1
+ *   and scores NaN.
+ * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24
+ * (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  Scores are
+ * formed and compared in float64.
+ */
+int mtp_beam_select(const void *logits, mtp_dtype dtype, const float *scores, const float *temperature, int B, int W, int V,
+                    int K, int32_t *tokens, int32_t *parents, float *out_scores, int32_t *row_flags, void *workspace,
+                    int64_t workspace_bytes, mtp_stream_t stream);
+int64_t mtp_beam_select_workspace(mtp_dtype dtype, int B, int W, int V, int K);
+
+/*
+ * mtp_beam_reorder -- states of the selected beams: out[n, b, k] =
+ * states[n, b, parents[b, k]] for n < N0 (layers, say), rows of row_bytes
+ * bytes.  states [N0, B, W, row], out [N0, B, K, row], contiguous, not
+ * overlapping (MTP_ERR_INVALID_ARG).  A parent outside [0, W) -- the empty
+ * places of mtp_beam_select -- gives a row of zeros and flags the sequence
+ * MTP_ROW_BAD_ID.  row_flags [B] or NULL.
+ */
+int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, int W, int K, int64_t row_bytes, void *out,
+                     int32_t *row_flags, mtp_stream_t stream);
+
+/*
+ * mtp_tree_commit -- verification of a drafted tree against the target's
+ * tokens, and the accepted path's keys and values written to the cache.
+ *
+ * Node 0 is the root: the last token of the text, whose key and value are new
+ * like the drafts' (parents[b,0] = -1).  target_tokens[b,i] is the target's
+ * own token after node i -- drawn from its distribution there
+ * (mtp_draft_sample over the target's logits [B T, V]) or its arg max.  From
+ * the root on, the path goes to the first child whose token is the target's
+ * token after the current node, until there is none; the tokens that the
+ * target drew are emitted, so whatever the tree holds the output follows the
+ * target's distribution.  Nodes that continue the cached text (parent -1)
+ * other than the root are never reached.
+ *   out_tokens [B, T]: the accepted drafts, then the target's token after the
+ *     last of them, then -1
+ *   path [B, T]: the nodes of the path, the root first, then -1
+ *   accept_len [B]: accepted drafts (the path without the root)
+ *   new_len [B]: cache_len + the path's nodes.
+ * For every layer, the keys and values of the path's nodes go to tokens
+ * cache_len, cache_len + 1, .. of the sequence; nothing else of the cache is
+ * written.  A sequence of no nodes, or a flagged one (also: no room in the
+ * page table for the path, a target token < 0 on it), has accept_len -1, tokens and path -1,
+ * new_len = cache_len, and its cache stays as it was.
+ *
+ *   k_new, v_new [layers, B, T, Hkv, D], k_cache, v_cache [layers, num_pages,
+ *   page_size, Hkv, D] dtype, D contiguous, strides in elements; layers = 0
+ *   writes no cache (all four may be NULL).  The pages that the path goes to
+ *   must belong to one sequence only, and the new keys and values must not
+ *   overlap the cache.  new_len must not be cache_len itself.
+ */
+typedef struct mtp_tree_commit_args {
+    const int32_t *tokens, *target_tokens; /* [B, T] */
+    const int32_t *parents;                /* [B, T] or NULL */
+    const int32_t *n_nodes;                /* [B] or NULL */
+    const int32_t *page_table;             /* [B, max_pages] */
+    const int32_t *cache_len;              /* [B] */
+    const void *k_new, *v_new;
+    void *k_cache, *v_cache;
+    int32_t *out_tokens, *accept_len, *path, *new_len, *row_flags;
+    int64_t k_new_stride[4], v_new_stride[4];     /* layer, b, t, head */
+    int64_t k_cache_stride[4], v_cache_stride[4]; /* layer, page, token, head */
+    int dtype;
+    int layers, B, T, Hkv, D;
+    int num_pages, page_size, max_pages;
+} mtp_tree_commit_args;
+
+int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t stream);
 
 /*
  * mtp_query_plan -- the launch plan a call would use on the current device

@@ -22,9 +22,11 @@ from . import build as _build
 __all__ = [
     "mtp_rs_verify", "mtp_to_verify", "mtp_gumbel_verify", "mtp_draft_sample", "mtp_row_stats",
     "mtp_rs_diagnostics", "mtp_tv_loss_fwd_bwd", "mtp_tv_loss_ex", "mtp_tv_loss_topk",
+    "mtp_tree_attention", "mtp_beam_select", "mtp_beam_reorder", "mtp_tree_commit",
     "mtp_query_plan", "mtp_status_string", "mtp_set_tuning", "mtp_get_tuning", "tuning", "check_row_flags",
     "MTPError", "load_library", "MTP_ERR_TIMEOUT", "KERNEL_AUTO", "KERNEL_STREAM", "KERNEL_RESIDENT", "KERNEL_TMEM",
-    "VerifyResult", "TOVerifyResult", "StatsResult", "DiagResult", "TVLossResult", "SampleResult", "ROW_NONFINITE",
+    "VerifyResult", "TOVerifyResult", "StatsResult", "DiagResult", "TVLossResult", "SampleResult",
+    "TreeAttentionResult", "BeamResult", "ReorderResult", "CommitResult", "MAX_NODES", "MAX_BEAMS", "MAX_SELECT", "ROW_NONFINITE",
     "ROW_BAD_ID", "ROW_BAD_TEMP", "ROW_ZERO_MASS", "ROW_BAD_UNIFORM", "ROW_TIMEOUT", "ERROR_BITS", "MAX_GAMMA", "EXPORTED_SYMBOLS",
 ]
 
@@ -34,6 +36,8 @@ MAX_GAMMA = 32
 DTYPE_F32, DTYPE_BF16 = 0, 1
 EXPORTED_SYMBOLS = ("mtp_rs_verify", "mtp_to_verify", "mtp_gumbel_verify", "mtp_draft_sample", "mtp_row_stats",
                     "mtp_rs_diagnostics", "mtp_tv_loss_fwd_bwd", "mtp_tv_loss_ex", "mtp_tv_loss_topk",
+                    "mtp_tree_attention", "mtp_tree_attention_workspace", "mtp_beam_select", "mtp_beam_select_workspace",
+                    "mtp_beam_reorder", "mtp_tree_commit",
                     "mtp_query_plan", "mtp_set_tuning", "mtp_get_tuning", "mtp_status_string")
 MTP_OK, MTP_ERR_INVALID_ARG, MTP_ERR_UNSUPPORTED_DTYPE, MTP_ERR_MISALIGNED, MTP_ERR_CUDA, MTP_ERR_TIMEOUT, \
     MTP_ERR_NO_DEVICE = range(7)
@@ -94,6 +98,20 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False):
     lib.mtp_rs_diagnostics.restype = I
     lib.mtp_tv_loss_fwd_bwd.argtypes = [P, P, I, F, I, I, I, F, P, P, P, P, P]
     lib.mtp_tv_loss_fwd_bwd.restype = I
+    # structs are passed packed (a bytes object)
+    S, L = ctypes.c_char_p, ctypes.c_int64
+    lib.mtp_tree_attention.argtypes = [S, P]
+    lib.mtp_tree_attention.restype = I
+    lib.mtp_tree_attention_workspace.argtypes = [S]
+    lib.mtp_tree_attention_workspace.restype = L
+    lib.mtp_beam_select.argtypes = [P, I, P, P, I, I, I, I, P, P, P, P, P, L, P]
+    lib.mtp_beam_select.restype = I
+    lib.mtp_beam_select_workspace.argtypes = [I, I, I, I, I]
+    lib.mtp_beam_select_workspace.restype = L
+    lib.mtp_beam_reorder.argtypes = [P, P, I, I, I, I, L, P, P, P]
+    lib.mtp_beam_reorder.restype = I
+    lib.mtp_tree_commit.argtypes = [S, P]
+    lib.mtp_tree_commit.restype = I
     lib.mtp_query_plan.argtypes = [I, I, I, I, I, P, P, P, P]
     lib.mtp_query_plan.restype = I
     lib.mtp_set_tuning.argtypes = [P]
@@ -547,3 +565,8 @@ def mtp_tv_loss_fwd_bwd(target_logits, draft_logits, temperature: float = 1.0, g
     if rc:
         raise MTPError(name, rc)
     return out
+
+
+from .tree import (  # noqa: E402
+    MAX_BEAMS, MAX_NODES, MAX_SELECT, BeamResult, CommitResult, ReorderResult, TreeAttentionResult, mtp_beam_reorder,
+    mtp_beam_select, mtp_tree_attention, mtp_tree_commit)

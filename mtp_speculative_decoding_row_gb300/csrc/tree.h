@@ -1,0 +1,106 @@
+// tree.h -- internal interface of the tree-decoding operators: tree attention
+// over a paged cache, beam selection, beam reordering and tree commit.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mtp {
+
+constexpr int MAX_NODES = 64;  // drafted nodes per tree: one 64-bit ancestor mask per node
+
+// ------------------------------------------------------- tree attention --
+
+struct TreeAttnArgs {
+    const void *q, *k_new, *v_new, *k_cache, *v_cache;
+    const int32_t *table;    // [B, max_pages]
+    const int32_t *len;      // [B]
+    const int32_t *parents;  // [B, T] or null (a chain)
+    const int32_t *nodes;    // [B] or null (T)
+    void *out;               // [B, T, Hq, D]
+    float *lse;              // [B, T, Hq] or null
+    int32_t *flags;          // [B] or null
+    float *part;             // partial results, two slots per CTA (attn_slot_floats each)
+    int32_t *desc;           // ATTN_DESC ints per group: the unit to join (see tree_attention.cuh)
+    int64_t qs[3], ks[3], vs[3], kcs[3], vcs[3];  // element strides: (b, t, h) and (page, token, head)
+    int B, T, Hq, Hkv, D, G;
+    int num_pages, page_size, max_pages;
+    int rows;                // T * G: query rows of one (sequence, key head)
+    int mtiles;              // row tiles of BM rows
+    int groups;              // CTAs / mtiles: each group of CTAs walks one range of key tiles
+    int bm;                  // query rows of one tile
+    int ktile;               // keys of one tile
+    int per_page;            // tiles of one page (pages of at least a tile), else 0
+    float scale_log2;        // scale * log2(e)
+    int vec;                 // SIMT kernel: 16-byte loads are aligned
+};
+
+constexpr int ATTN_DESC = 4;
+
+// Floats of one partial slot: running maximum and sum of each row, then the
+// unnormalised output rows.
+__host__ __device__ inline size_t attn_slot_floats(int bm, int d) { return static_cast<size_t>(bm) * (d + 2); }
+
+// SIMT kernel (csrc/tree_attention_simt.cu).
+constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256;
+const void *attn_simt_func(int dtype, int D);
+uint32_t attn_simt_smem(int D);
+const void *attn_join_func(int dtype);
+constexpr int JOIN_ROWS = 16, JOIN_THREADS = 128;
+
+// ------------------------------------------------------- beam selection --
+
+constexpr int BEAM_MAX_K = 64;     // continuations selected per sequence
+constexpr int BEAM_MAX_W = 64;     // beams of a sequence
+
+struct BeamArgs {
+    const void *logits;   // [B, W, V]
+    const float *scores;  // [B, W]
+    const float *temp;    // [B]
+    int B, W, V, K;
+    int KL;               // candidates kept of each part: min(K, V)
+    int parts;            // parts each row is cut into
+    int part_elems;       // elements of one part (a multiple of the 16-byte vector)
+    float *part_max;      // [B * W, parts] maximum of z
+    double *part_sum;     // [B * W, parts] sum of 2^((z - max) k)
+    int *part_flag;       // [B * W, parts]
+    float *cand_z;        // [B * W, parts, KL] candidates, best first
+    int *cand_v;          // their vocabulary indices (-1: none)
+    int32_t *tokens, *parents;  // [B, K]
+    float *best;                // [B, K]
+    int32_t *flags;             // [B] or null
+};
+
+constexpr int BEAM_THREADS = 256;
+const void *beam_part_func(int dtype);
+const void *beam_join_func();
+
+// ------------------------------------------------- reorder and commit ----
+
+struct ReorderArgs {
+    const unsigned char *src;  // [N0, B, W, bytes]
+    unsigned char *dst;        // [N0, B, K, bytes]
+    const int32_t *parents;    // [B, K]
+    int32_t *flags;            // [B] or null
+    int N0, B, W, K;
+    long long bytes;           // of one row
+};
+const void *reorder_func(int width);  // word size: 16, 4, 2 or 1 bytes
+constexpr int REORDER_THREADS = 256, REORDER_UNROLL = 4, REORDER_BLOCK = REORDER_THREADS * REORDER_UNROLL;  // words of a block
+
+struct CommitArgs {
+    const int32_t *tokens, *target, *parents, *nodes;  // [B, T]; nodes [B] or null
+    const int32_t *table, *len;
+    const unsigned char *k_new, *v_new;
+    unsigned char *k_cache, *v_cache;
+    // byte strides: new (layer, b, t, h), cache (layer, page, token, head)
+    long long ks[4], vs[4], kcs[4], vcs[4];
+    int N0, B, T, Hkv;
+    int row_bytes;  // bytes of one head's key or value
+    int num_pages, page_size, max_pages;
+    int32_t *out, *accept, *path, *new_len, *flags;
+};
+const void *commit_func(int width);  // word size: 16, 4 or 2 bytes
+constexpr int COMMIT_THREADS = 128;
+
+}  // namespace mtp

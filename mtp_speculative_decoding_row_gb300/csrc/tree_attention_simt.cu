@@ -1,0 +1,346 @@
+// tree_attention_simt.cu -- tree attention on the FP32 pipes, and the join of
+// units whose keys several CTAs share (tree_attention.cuh has the split).
+//
+// This kernel takes what the tensor-core kernel does not: float32 storage
+// (whose products a bf16 or tf32 tensor product would round), head sizes
+// other than 64, 128 and 256, and caches whose pages or strides a tiled copy
+// cannot address.  One CTA holds 32 query rows and walks tiles of 64 keys:
+// keys and values in shared memory as float32, scores and outputs in
+// registers, the running maximum m and sum l of the softmax per row
+//   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
+//   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j       (s in units of log2 e),
+// all in float32.
+#include "tree_attention.cuh"
+
+namespace mtp {
+namespace {
+
+constexpr int BM = SIMT_BM, BN = SIMT_BN, NT = SIMT_THREADS;
+
+template <typename T>
+__device__ __forceinline__ float ld1(const void *p, int64_t i);
+template <>
+__device__ __forceinline__ float ld1<float>(const void *p, int64_t i) {
+    return __ldg(static_cast<const float *>(p) + i);
+}
+template <>
+__device__ __forceinline__ float ld1<bf16_t>(const void *p, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(p) + i)) << 16);
+}
+
+// One row of D elements at p + off into shared memory, zero beyond D: each of
+// `nl` threads of a row (index l) copies every nl-th vector.
+template <typename T, int DP>
+__device__ __forceinline__ void row_to_smem(float *dst, const void *p, int64_t off, int D, int l, int nl, bool vec) {
+    constexpr int VEC = Store<T>::VEC;
+    if (vec) {  // D is a multiple of VEC and every row starts on 16 bytes
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p) + off * Store<T>::ES);
+        for (int c = l; c < DP / VEC; c += nl) {
+            float z[VEC];
+            Store<T>::unpack(c * VEC < D ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u), z);
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4)
+                *reinterpret_cast<float4 *>(dst + c * VEC + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+        }
+    } else {
+        for (int c = l; c < DP; c += nl) dst[c] = c < D ? ld1<T>(p, off + c) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(bf16_t *p, float x) {
+    // round to nearest even; a NaN keeps its sign and becomes quiet
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(p->bits) : "f"(x));
+}
+
+template <typename T, int DC>
+__global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ TreeAttnArgs A) {
+    constexpr int DP = DC * 64, KS = DP + 4;  // key row stride: rows of a float4 column in different banks
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *sq = reinterpret_cast<float *>(smem);  // [BM][KS]
+    float *sk = sq + BM * KS;                     // [BN][KS]
+    float *sv = sk + BN * KS;                     // [BN][DP]
+    float *sp = sv + BN * DP;                     // [BM][BN + 4]
+    float *sm = sp + BM * (BN + 4);               // [BM] maximum
+    float *sl = sm + BM;                          // [BM] sum
+    float *sf = sl + BM;                          // [BM] factor of the old rows
+    uint64_t *smask = reinterpret_cast<uint64_t *>(sf + BM);  // [MAX_NODES]
+    long long *scan = reinterpret_cast<long long *>(smask + MAX_NODES);  // [NT / 32]
+    __shared__ int s_flag;
+
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
+    const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
+    const bool vec = A.vec != 0;
+
+    AttnWalk walk;
+    walk.start<NT>(A, group, scan);
+    AttnPiece pc, last = {};
+    bool any = false;
+    while (walk.next(A, pc)) {
+        any = true;
+        last = pc;
+        const int b = pc.b, h = pc.h;
+        bool bad_len, bad_nodes;
+        attn_len(A, b, bad_len);
+        const int n = attn_nodes(A, b, bad_nodes);
+        const int rows_n = bad_nodes ? A.rows : n * A.G;  // rows that are written
+        if (tid == 0) s_flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
+        __syncthreads();
+        int bad = attn_check_pages(A, b, pc.len, tid, NT);
+        if (tid < n) {
+            bool bad_up = false;
+            smask[tid] = attn_mask(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, tid, bad_up);
+            if (bad_up) bad |= F_BAD_ID;
+        }
+        if (bad) atomicOr(&s_flag, bad);
+        {
+            const int r = tid >> 3;  // 8 threads a row
+            const int t = (row0 + r) / A.G, g = row0 + r - t * A.G;
+            if (r < rows)
+                row_to_smem<T, DP>(sq + r * KS, A.q, b * A.qs[0] + t * A.qs[1] + (static_cast<int64_t>(h) * A.G + g) * A.qs[2],
+                                   A.D, tid & 7, 8, vec);
+            else
+                for (int c = tid & 7; c < DP; c += 8) sq[r * KS + c] = 0.f;
+        }
+        if (tid < BM) {
+            sm[tid] = -INFINITY;
+            sl[tid] = 0.f;
+        }
+        float acc[2][DC * 4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < DC * 4; ++c) acc[i][c] = 0.f;
+
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const bool tree = t == pc.prefix;
+            const int valid = tree ? n : min(BN, pc.len - t * BN);
+            {
+                const int j = tid >> 2, l = tid & 3;  // 4 threads a key
+                if (j < valid) {
+                    int64_t ko, vo;
+                    if (tree) {
+                        ko = b * A.ks[0] + j * A.ks[1] + h * A.ks[2];
+                        vo = b * A.vs[0] + j * A.vs[1] + h * A.vs[2];
+                    } else {
+                        const int pos = t * BN + j, page = pos / A.page_size, off = pos - page * A.page_size;
+                        const int64_t pid = attn_page(A, b, page);
+                        ko = pid * A.kcs[0] + off * A.kcs[1] + h * A.kcs[2];
+                        vo = pid * A.vcs[0] + off * A.vcs[1] + h * A.vcs[2];
+                    }
+                    row_to_smem<T, DP>(sk + j * KS, tree ? A.k_new : A.k_cache, ko, A.D, l, 4, vec);
+                    row_to_smem<T, DP>(sv + j * DP, tree ? A.v_new : A.v_cache, vo, A.D, l, 4, vec);
+                }
+            }
+            __syncthreads();
+            // scores of rows 2 ty, 2 ty + 1 against keys tx + 16 i
+            float s[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+            const float *q0 = sq + 2 * ty * KS;
+#pragma unroll 4
+            for (int d = 0; d < DP; d += 4) {
+                const float4 a0 = *reinterpret_cast<const float4 *>(q0 + d);
+                const float4 a1 = *reinterpret_cast<const float4 *>(q0 + KS + d);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 k = *reinterpret_cast<const float4 *>(sk + (tx + 16 * c) * KS + d);
+                    s[0][c] = fmaf(a0.x, k.x, fmaf(a0.y, k.y, fmaf(a0.z, k.z, fmaf(a0.w, k.w, s[0][c]))));
+                    s[1][c] = fmaf(a1.x, k.x, fmaf(a1.y, k.y, fmaf(a1.z, k.z, fmaf(a1.w, k.w, s[1][c]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * ty + i;
+                const uint64_t see = tree && r < rows && (row0 + r) / A.G < n ? smask[(row0 + r) / A.G] : 0ull;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = tx + 16 * c;
+                    const bool on = tree ? ((see >> j) & 1ull) != 0 : j < valid;
+                    sp[r * (BN + 4) + j] = on ? s[i][c] : -INFINITY;
+                }
+            }
+            __syncthreads();
+            {  // softmax: 8 threads a row
+                const int r = tid >> 3, l = tid & 7;
+                float *p = sp + r * (BN + 4);
+                float x[8], top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = p[l + 8 * i];
+                    top = max_nan(top, x[i]);
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, d));
+                const float m0 = sm[r], m1 = max_nan(m0, top);
+                const float ref = m1 == -INFINITY ? 0.f : m1 * A.scale_log2;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = exp2f(fmaf(x[i], A.scale_log2, -ref));
+                    p[l + 8 * i] = x[i];
+                    sum += x[i];
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL, sum, d);
+                __syncwarp();
+                if (l == 0) {
+                    const float f = m0 == -INFINITY ? 0.f : exp2f(fmaf(m0, A.scale_log2, -ref));
+                    sf[r] = f;
+                    sl[r] = sl[r] * f + sum;
+                    sm[r] = m1;
+                }
+            }
+            __syncthreads();
+            {  // outputs of rows 2 ty, 2 ty + 1, columns 64 c + 4 tx ..
+                const float f0 = sf[2 * ty], f1 = sf[2 * ty + 1];
+                uint64_t see0 = ~0ull, see1 = ~0ull;
+                if (tree) {  // a node that a row does not see never reaches it, not even as 0 times infinity
+                    const int r = row0 + 2 * ty, t0 = r / A.G, t1 = (r + 1) / A.G;
+                    see0 = 2 * ty < rows && t0 < n ? smask[t0] : 0ull;
+                    see1 = 2 * ty + 1 < rows && t1 < n ? smask[t1] : 0ull;
+                }
+#pragma unroll
+                for (int c = 0; c < DC * 4; ++c) {
+                    acc[0][c] *= f0;
+                    acc[1][c] *= f1;
+                }
+                const float *p0 = sp + 2 * ty * (BN + 4), *p1 = p0 + BN + 4;
+                for (int j = 0; j < valid; ++j) {
+                    const float w0 = p0[j], w1 = p1[j];
+                    const bool on0 = (see0 >> j) & 1ull, on1 = (see1 >> j) & 1ull;
+#pragma unroll
+                    for (int c = 0; c < DC; ++c) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sv + j * DP + 64 * c + 4 * tx);
+                        if (on0) {
+                            acc[0][4 * c] = fmaf(w0, v.x, acc[0][4 * c]);
+                            acc[0][4 * c + 1] = fmaf(w0, v.y, acc[0][4 * c + 1]);
+                            acc[0][4 * c + 2] = fmaf(w0, v.z, acc[0][4 * c + 2]);
+                            acc[0][4 * c + 3] = fmaf(w0, v.w, acc[0][4 * c + 3]);
+                        }
+                        if (on1) {
+                            acc[1][4 * c] = fmaf(w1, v.x, acc[1][4 * c]);
+                            acc[1][4 * c + 1] = fmaf(w1, v.y, acc[1][4 * c + 1]);
+                            acc[1][4 * c + 2] = fmaf(w1, v.z, acc[1][4 * c + 2]);
+                            acc[1][4 * c + 3] = fmaf(w1, v.w, acc[1][4 * c + 3]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        const int flag = s_flag;
+        if (A.flags && tid == 0 && h == 0 && mtile == 0) A.flags[b] = flag;
+        const bool whole = pc.whole();
+        float *slot = whole ? nullptr : A.part + attn_slot(A, group, mtile, pc.first) * attn_slot_floats(BM, A.D);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * ty + i;
+            if (row0 + r >= rows_n || r >= rows) continue;
+            const float l = flag ? NAN : sl[r];
+            if (whole) {
+                const int t = (row0 + r) / A.G, hq = h * A.G + row0 + r - t * A.G;
+                const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
+                const float inv = 1.f / l;
+                T *o = static_cast<T *>(A.out) + at * A.D;
+#pragma unroll
+                for (int c = 0; c < DC * 4; ++c) {
+                    const int d = 64 * (c >> 2) + 4 * tx + (c & 3);
+                    if (d < A.D) put(o + d, acc[i][c] * inv);
+                }
+                if (A.lse && tx == 0) A.lse[at] = (sm[r] * A.scale_log2 + log2f(l)) * LN2;
+            } else {
+                float *o = slot + 2 * BM + static_cast<size_t>(r) * A.D;
+#pragma unroll
+                for (int c = 0; c < DC * 4; ++c) {
+                    const int d = 64 * (c >> 2) + 4 * tx + (c & 3);
+                    if (d < A.D) o[d] = acc[i][c];
+                }
+                if (tx == 0) {
+                    slot[r] = sm[r] * A.scale_log2;
+                    slot[BM + r] = l;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (mtile == 0 && tid == 0) attn_write_desc(A, group, walk, any, last);
+}
+
+// Join one unit that begins in group blockIdx.x / mtiles and goes on in the
+// next groups: with m the largest of the parts' maxima, o = sum_i 2^(m_i - m)
+// o_i / sum_i 2^(m_i - m) l_i, the parts in the order of their keys.  Block
+// (x, y) takes 16 rows, four columns to a thread.
+template <typename T>
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
+    const int *d = A.desc + static_cast<size_t>(group) * ATTN_DESC;
+    const int parts = d[2];
+    if (parts == 0) return;
+    const int b = d[0], h = d[1];
+    bool bad;
+    const int n = attn_nodes(A, b, bad);
+    const int rows = min(A.bm, (bad ? A.rows : n * A.G) - mtile * A.bm);
+    const size_t slot_floats = attn_slot_floats(A.bm, A.D);
+    const float *first = A.part + attn_slot(A, group, mtile, d[3] == 0) * slot_floats;
+    const float *next = A.part + attn_slot(A, group + 1, mtile, true) * slot_floats;
+    const size_t step = 2 * slot_floats * A.mtiles;
+    const int quads = (A.D + 3) / 4;
+    for (int i = threadIdx.x; i < JOIN_ROWS * quads; i += JOIN_THREADS) {
+        const int r = blockIdx.y * JOIN_ROWS + i / quads, c = 4 * (i % quads);
+        if (r >= rows) continue;
+        float top = first[r];
+        for (int k = 1; k < parts; ++k) top = max_nan(top, next[(k - 1) * step + r]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float *s = k == 0 ? first : next + (k - 1) * step;
+            const float w = exp2f(s[r] - ref);
+            l = fmaf(w, s[A.bm + r], l);
+            const float *x = s + 2 * A.bm + static_cast<size_t>(r) * A.D + c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < A.D) o[e] = fmaf(w, x[e], o[e]);
+        }
+        const int row = mtile * A.bm + r, t = row / A.G, hq = h * A.G + row - t * A.G;
+        const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
+        const float inv = 1.f / l;
+        T *out = static_cast<T *>(A.out) + at * A.D + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < A.D) put(out + e, o[e] * inv);
+        if (A.lse && c == 0) A.lse[at] = (ref + log2f(l)) * LN2;
+    }
+}
+
+}  // namespace
+
+uint32_t attn_simt_smem(int D) {
+    const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    const size_t f = static_cast<size_t>(BM) * (dp + 4) + BN * (dp + 4) + BN * dp + BM * (BN + 4) + 3 * BM;
+    return static_cast<uint32_t>(f * 4 + MAX_NODES * 8 + (NT / 32) * 8);
+}
+
+const void *attn_simt_func(int dtype, int D) {
+    const int dc = D <= 64 ? 1 : D <= 128 ? 2 : 4;
+    if (dtype == 0)
+        return dc == 1   ? reinterpret_cast<const void *>(attn_simt_impl<float, 1>)
+               : dc == 2 ? reinterpret_cast<const void *>(attn_simt_impl<float, 2>)
+                         : reinterpret_cast<const void *>(attn_simt_impl<float, 4>);
+    return dc == 1   ? reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 1>)
+           : dc == 2 ? reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 2>)
+                     : reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 4>);
+}
+
+const void *attn_join_func(int dtype) {
+    return dtype == 0 ? reinterpret_cast<const void *>(attn_join_impl<float>)
+                      : reinterpret_cast<const void *>(attn_join_impl<bf16_t>);
+}
+
+}  // namespace mtp
