@@ -393,9 +393,9 @@ typedef struct mtp_tree_attention_args {
 } mtp_tree_attention_args;
 
 int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream);
-/* Bytes of workspace for a call with these sizes, strides and addresses of
- * the inputs (the workspace fields are not read); -1 for arguments that the
- * call would refuse. */
+/* Bytes of workspace for calls with these sizes and types, whatever their
+ * pointers and strides (those are not read); -1 for sizes that the call would
+ * refuse. */
 int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
 
 /*

@@ -45,6 +45,11 @@ __host__ __device__ inline size_t attn_slot_floats(int bm, int d) { return stati
 constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256;
 const void *attn_simt_func(int dtype, int D);
 uint32_t attn_simt_smem(int D);
+// Tensor-core kernel (csrc/tree_attention_umma.cu): bfloat16, D 64, 128, 256.
+constexpr int UMMA_BM = 128, UMMA_THREADS = 256;
+const void *attn_umma_func(int D);
+uint32_t attn_umma_smem(int D);
+int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype);
 constexpr int JOIN_ROWS = 16, JOIN_THREADS = 128;
 

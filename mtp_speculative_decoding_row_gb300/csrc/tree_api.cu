@@ -1,5 +1,6 @@
 // tree_api.cu -- the C ABI of the tree-decoding operators (include/mtp_rs.h):
 // argument validation, launch plans and launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -66,7 +67,8 @@ int resident(int dev, const void *func, uint32_t smem, int threads) {
 
 // `after`: a kernel that waits for the launch before it itself
 // (griddepcontrol.wait), so that its CTAs may be set up while that one ends.
-int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream, bool after = false) {
+int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream, bool after = false,
+           const void *map1 = nullptr, const void *map2 = nullptr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -77,7 +79,7 @@ int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 1 : 0;
-    void *kargs[] = {const_cast<void *>(args)};
+    void *kargs[] = {const_cast<void *>(args), const_cast<void *>(map1), const_cast<void *>(map2)};
     return cudaLaunchKernelExC(&cfg, func, kargs) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 
@@ -105,19 +107,36 @@ int attn_sizes(const mtp_tree_attention_args &a) {
     return MTP_OK;
 }
 
-int attn_plan(const mtp_tree_attention_args &a, AttnPlan &p) {
+// Whether the tensor-core kernel takes these sizes: bfloat16, its head sizes,
+// and pages whose rows are whole groups of the swizzle (8) or at least a tile.
+bool umma_sizes(const mtp_tree_attention_args &a) {
+    return a.dtype == MTP_DTYPE_BF16 && (a.D == 64 || a.D == 128 || a.D == 256) &&
+           (a.page_size % 8 == 0 || a.page_size >= attn_umma_bn(a.D));
+}
+
+int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     int dev, sms;
     if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
-    p.func = attn_simt_func(a.dtype, a.D);
-    p.smem = attn_simt_smem(a.D);
-    p.threads = SIMT_THREADS;
-    p.bm = SIMT_BM;
-    p.ktile = SIMT_BN;
+    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
+    if (umma) {
+        p.func = attn_umma_func(a.D);
+        p.smem = attn_umma_smem(a.D);
+        p.threads = UMMA_THREADS;
+        p.bm = UMMA_BM;
+        const int bn = attn_umma_bn(a.D);
+        p.per_page = a.page_size >= bn ? (a.page_size + bn - 1) / bn : 0;
+        p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
+    } else {
+        p.func = attn_simt_func(a.dtype, a.D);
+        p.smem = attn_simt_smem(a.D);
+        p.threads = SIMT_THREADS;
+        p.bm = SIMT_BM;
+        p.ktile = SIMT_BN;
+    }
     const int per_sm = resident(dev, p.func, p.smem, p.threads);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
     p.rows = a.T * (a.Hq / a.Hkv);
     p.mtiles = (p.rows + p.bm - 1) / p.bm;
-    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
     p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
     const long long all = p.max_tiles * a.Hkv * (a.B > 0 ? a.B : 1);
@@ -127,6 +146,44 @@ int attn_plan(const mtp_tree_attention_args &a, AttnPlan &p) {
     p.part_bytes = (p.part_bytes + 15) / 16 * 16;
     p.desc_bytes = static_cast<size_t>(p.groups) * ATTN_DESC * sizeof(int32_t);
     return MTP_OK;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// A paged cache as a 4-dimensional tensor (D, token, head, page), copied in
+// boxes of 64 elements x `rows` tokens.  False where the addresses or strides
+// cannot be described: the other kernel takes the call.
+bool cache_map(CUtensorMap *map, const mtp_tree_attention_args &a, const void *base, const int64_t *s, int rows) {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.page_size),
+                                static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.num_pages)};
+    const int64_t by[3] = {s[1], s[2], s[0]};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        const int64_t bytes = dims[i + 1] > 1 ? by[i] * 2 : static_cast<int64_t>(a.D) * 2;
+        if (bytes <= 0 || bytes % 16 != 0 || bytes >= (1ll << 40)) return false;
+        strides[i] = static_cast<cuuint64_t>(bytes);
+    }
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, ones[4] = {1, 1, 1, 1};
+    const EncodeTiled f = encode_tiled();
+    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool vec_ok(const void *p, const int64_t *s, int es) {
@@ -139,8 +196,14 @@ bool vec_ok(const void *p, const int64_t *s, int es) {
 extern "C" int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args) {
     if (!args || attn_sizes(*args) != MTP_OK) return -1;
     AttnPlan p;
-    if (attn_plan(*args, p) != MTP_OK) return -1;
-    return static_cast<int64_t>(p.bytes());
+    if (attn_plan(*args, false, p) != MTP_OK) return -1;
+    size_t bytes = p.bytes();
+    if (umma_sizes(*args)) {
+        AttnPlan u;
+        if (attn_plan(*args, true, u) != MTP_OK) return -1;
+        if (u.bytes() > bytes) bytes = u.bytes();
+    }
+    return static_cast<int64_t>(bytes);
 }
 
 extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream) {
@@ -156,10 +219,6 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
                           reinterpret_cast<uintptr_t>(a.v_new) | reinterpret_cast<uintptr_t>(a.k_cache) |
                           reinterpret_cast<uintptr_t>(a.v_cache) | reinterpret_cast<uintptr_t>(a.out);
     if (low % es != 0 || reinterpret_cast<uintptr_t>(a.workspace) % 16 != 0) return MTP_ERR_MISALIGNED;
-    AttnPlan p;
-    const int pc = attn_plan(a, p);
-    if (pc != MTP_OK) return pc;
-    if (a.workspace_bytes < static_cast<int64_t>(p.bytes())) return MTP_ERR_INVALID_ARG;
     TreeAttnArgs A = {};
     A.q = a.q;
     A.k_new = a.k_new;
@@ -173,8 +232,6 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.out = a.out;
     A.lse = a.lse;
     A.flags = a.row_flags;
-    A.desc = static_cast<int32_t *>(a.workspace);
-    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
     // the stride of a dimension of one says nothing
     const int nq[3] = {a.B, a.T, a.Hq}, nk[3] = {a.B, a.T, a.Hkv}, nc[3] = {a.num_pages, a.page_size, a.Hkv};
     for (int i = 0; i < 3; ++i) {
@@ -193,16 +250,29 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.num_pages = a.num_pages;
     A.page_size = a.page_size;
     A.max_pages = a.max_pages;
+    A.scale_log2 = a.scale * kLog2e;
+    A.vec = a.D % (16 / es) == 0 && vec_ok(a.q, A.qs, es) && vec_ok(a.k_new, A.ks, es) && vec_ok(a.v_new, A.vs, es) &&
+            vec_ok(a.k_cache, A.kcs, es) && vec_ok(a.v_cache, A.vcs, es);
+    // the tensor cores wherever sizes and alignment allow: at one query row
+    // of 128 they still keep up with the memory (a tile's products take 0.7
+    // us, its bytes 1.5 us)
+    CUtensorMap kmap, vmap;
+    const int bn = attn_umma_bn(a.D), boxrows = a.page_size < bn ? a.page_size : bn;
+    const bool umma = umma_sizes(a) && A.vec && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+                      cache_map(&kmap, a, a.k_cache, A.kcs, boxrows) && cache_map(&vmap, a, a.v_cache, A.vcs, boxrows);
+    AttnPlan p;
+    const int pc = attn_plan(a, umma, p);
+    if (pc != MTP_OK) return pc;
+    if (a.workspace_bytes < static_cast<int64_t>(p.bytes())) return MTP_ERR_INVALID_ARG;
+    A.desc = static_cast<int32_t *>(a.workspace);
+    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
     A.rows = p.rows;
     A.mtiles = p.mtiles;
     A.groups = p.groups;
     A.bm = p.bm;
     A.ktile = p.ktile;
     A.per_page = p.per_page;
-    A.scale_log2 = a.scale * kLog2e;
-    A.vec = a.D % (16 / es) == 0 && vec_ok(a.q, A.qs, es) && vec_ok(a.k_new, A.ks, es) && vec_ok(a.v_new, A.vs, es) &&
-            vec_ok(a.k_cache, A.kcs, es) && vec_ok(a.v_cache, A.vcs, es);
-    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream);
+    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, false, &kmap, &vmap);
     if (e != MTP_OK || !p.joins()) return e;
     return launch(attn_join_func(a.dtype), dim3(p.groups * p.mtiles, (p.bm + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A,
                   stream, true);
