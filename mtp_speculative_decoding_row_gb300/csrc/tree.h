@@ -31,6 +31,7 @@ struct TreeAttnArgs {
     int bm;                  // query rows of one tile
     int ktile;               // keys of one tile
     int per_page;            // tiles of one page (pages of at least a tile), else 0
+    int qrows, slots;        // tensor-core kernel: query rows in shared memory (a multiple of 8), slots of its ring
     float scale_log2;        // scale * log2(e)
     int vec;                 // SIMT kernel: 16-byte loads are aligned
 };
@@ -46,9 +47,13 @@ constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256;
 const void *attn_simt_func(int dtype, int D);
 uint32_t attn_simt_smem(int D);
 // Tensor-core kernel (csrc/tree_attention_umma.cu): bfloat16, D 64, 128, 256.
-constexpr int UMMA_BM = 128, UMMA_THREADS = 256;
-const void *attn_umma_func(int D);
-uint32_t attn_umma_smem(int D);
+constexpr uint32_t UMMA_SMEM = 232448;  // 227 KB per CTA
+struct UmmaPlan {
+    const void *func;
+    int threads, bm, qrows, slots;
+    uint32_t smem;
+};
+UmmaPlan attn_umma_plan(int D, int rows);
 int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype);
 constexpr int JOIN_ROWS = 16, JOIN_THREADS = 128;

@@ -55,8 +55,12 @@ int resident(int dev, const void *func, uint32_t smem, int threads) {
     for (auto &f : g_funcs)
         if (f.device == dev && f.func == func && f.smem == smem) return f.per_sm;
     int n = 0;
-    if (smem > kMaxSmem ||
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+    // the limit is the kernel's largest, not this call's size: calls of one
+    // kernel differ in it
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, func) != cudaSuccess ||
+        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kMaxSmem - at.sharedSizeBytes)) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         n = 0;
@@ -90,7 +94,7 @@ bool good_dtype(int d) { return d == MTP_DTYPE_F32 || d == MTP_DTYPE_BF16; }
 struct AttnPlan {
     const void *func = nullptr;
     uint32_t smem = 0;
-    int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0;
+    int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0;
     bool joins() const { return max_tiles > 1 && groups > 1; }
@@ -118,11 +122,15 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     int dev, sms;
     if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
     const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
+    p.rows = a.T * (a.Hq / a.Hkv);
     if (umma) {
-        p.func = attn_umma_func(a.D);
-        p.smem = attn_umma_smem(a.D);
-        p.threads = UMMA_THREADS;
-        p.bm = UMMA_BM;
+        const UmmaPlan u = attn_umma_plan(a.D, p.rows);
+        p.func = u.func;
+        p.smem = u.smem;
+        p.threads = u.threads;
+        p.bm = u.bm;
+        p.qrows = u.qrows;
+        p.slots = u.slots;
         const int bn = attn_umma_bn(a.D);
         p.per_page = a.page_size >= bn ? (a.page_size + bn - 1) / bn : 0;
         p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
@@ -135,7 +143,6 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     }
     const int per_sm = resident(dev, p.func, p.smem, p.threads);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
-    p.rows = a.T * (a.Hq / a.Hkv);
     p.mtiles = (p.rows + p.bm - 1) / p.bm;
     p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
@@ -271,6 +278,8 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.groups = p.groups;
     A.bm = p.bm;
     A.ktile = p.ktile;
+    A.qrows = p.qrows;
+    A.slots = p.slots;
     A.per_page = p.per_page;
     const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, false, &kmap, &vmap);
     if (e != MTP_OK || !p.joins()) return e;

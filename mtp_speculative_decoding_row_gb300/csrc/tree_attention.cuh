@@ -77,10 +77,10 @@ __device__ __forceinline__ long long attn_lo(long long W, int g, int groups) { r
 // of the block call it; `scan` is shared memory of NT / 32 long longs, two at least), next()
 // steps on.
 struct AttnWalk {
-    long long W, lo, hi, at;  // all tiles, this group's range, the next tile
-    int groups;               // groups that have tiles: no range of theirs is empty
-    int b, h, tile;           // where `at` is
-    int len, prefix;
+    long long W = 0, lo = 0, hi = 0, at = 0;  // all tiles, this group's range, the next tile
+    int groups = 0;                           // groups that have tiles: no range of theirs is empty
+    int b = 0, h = 0, tile = 0;               // where `at` is
+    int len = 0, prefix = 0;
 
     template <int NT>
     __device__ __forceinline__ void start(const TreeAttnArgs &A, int g, long long *scan) {

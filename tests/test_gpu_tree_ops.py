@@ -265,6 +265,25 @@ def test_tree_attention_is_repeatable(dtype, T, D):
         assert torch.equal(a, mtp.mtp_tree_attention(**x).out)
 
 
+@pytest.mark.parametrize("D, T, Hq, Hkv, ps", [(64, 8, 8, 2, 32), (128, 8, 16, 2, 16), (128, 40, 16, 2, 16), (64, 3, 2, 1, 128),
+                                               (256, 5, 8, 2, 32), (64, 64, 12, 2, 24)])
+def test_tree_attention_back_to_back(D, T, Hq, Hkv, ps):
+    """Many launches behind one another, each with many short and long pieces
+    per CTA: the hand-over of shared memory between copies, loads and products
+    must not depend on how they are timed."""
+    rng = random.Random(D + T)
+    lens = [rng.choice([0, 1, ps, 200, 900]) + rng.randint(0, 50) for _ in range(60)]
+    x = attn_case(13, "bf16", 60, T, Hq, Hkv, D, ps, lens, nodes=[rng.randint(1, T) for _ in range(60)])
+    a = run_attention(x).out
+    g = on_gpu(x)
+    out = mtp.TreeAttentionResult(torch.full_like(a, 7.0), None, torch.zeros(60, dtype=i32, device="cuda"))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        mtp.mtp_tree_attention(**g, out=out)
+        wrong += (out.out != a).sum() + out.row_flags.count_nonzero()
+    assert wrong.item() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_graphs_and_streams(dtype):
     """Two captured graphs with lengths that change between replays, replayed
