@@ -30,7 +30,7 @@ struct TreeAttnArgs {
     int groups;              // CTAs / mtiles: each group of CTAs walks one range of key tiles
     int bm;                  // query rows of one tile
     int ktile;               // keys of one tile
-    int per_page;            // tiles of one page (pages of at least a tile), else 0
+    int per_page;            // tiles of one page where pages are larger than a tile and no multiple of it, else 0
     int qrows, slots;        // tensor-core kernel: query rows in shared memory (a multiple of 8), slots of its ring
     float scale_log2;        // scale * log2(e)
     int vec;                 // SIMT kernel: 16-byte loads are aligned

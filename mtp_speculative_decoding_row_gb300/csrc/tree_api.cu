@@ -132,7 +132,7 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
         p.qrows = u.qrows;
         p.slots = u.slots;
         const int bn = attn_umma_bn(a.D);
-        p.per_page = a.page_size >= bn ? (a.page_size + bn - 1) / bn : 0;
+        p.per_page = a.page_size > bn && a.page_size % bn != 0 ? (a.page_size + bn - 1) / bn : 0;
         p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
     } else {
         p.func = attn_simt_func(a.dtype, a.D);

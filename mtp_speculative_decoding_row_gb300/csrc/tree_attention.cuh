@@ -42,9 +42,10 @@ __device__ __forceinline__ int attn_nodes(const TreeAttnArgs &A, int b, bool &ba
     return bad ? 0 : n;
 }
 
-// Tiles of cached keys of a sequence of `len` tokens.  Pages of at least a
-// tile are cut into per_page tiles each; smaller pages are taken several to
-// a tile of ktile keys.
+// Tiles of cached keys of a sequence of `len` tokens.  Tiles follow one another
+// every ktile keys -- whole pages, or equal parts of one -- except where pages
+// are larger than a tile and no multiple of it (per_page > 0): there every
+// page is cut into per_page tiles of its own, the last of them short.
 __device__ __forceinline__ int attn_prefix_tiles(const TreeAttnArgs &A, int len) {
     if (A.per_page == 0) return (len + A.ktile - 1) / A.ktile;
     const int full = len / A.page_size, rest = len - full * A.page_size;

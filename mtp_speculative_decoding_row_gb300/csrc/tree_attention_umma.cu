@@ -7,13 +7,16 @@
 // group) stay in shared memory for the piece.
 //   warp 0      copies key and value tiles page by page into a ring of slots
 //               (cp.async.bulk.tensor, 128-byte swizzle)
-//   warp 1      one lane issues S = Q K^T into a score buffer of TMEM and,
-//               when the weights are back, O += P V with P read from TMEM
-//   warps 2, 3  load the queries, the new keys and values and the ancestor
-//               masks of a piece, and check its page table
+//   warps 1, 2  issue S = Q K^T into a score buffer of TMEM and, when the
+//               weights are back, O += P V with P read from TMEM; a warp for
+//               each group of softmax warps, so that neither waits for the
+//               other's weights
+//   warp 3      loads the new keys and values and the ancestor masks of a
+//               piece, and checks its page table
 //   warps 4 ..  softmax: a thread has one row of a score tile, so the running
 //               maximum and sum need no exchange.  Weights go back to TMEM as
-//               bfloat16 over the scores they came from.
+//               bfloat16 over the scores they came from.  The same warps load
+//               the next piece's queries while the last products run.
 // The softmax of a tile takes longer than its copy or its products, so two
 // score tiles are worked on at a time by two groups of four warps, each with
 // its own accumulator in TMEM:
@@ -39,7 +42,7 @@
 namespace mtp {
 namespace {
 
-constexpr int LOADERS = 64;
+constexpr int LOADERS = 32;
 constexpr float RESCALE = 8.f;  // rescale when the maximum rose by this many powers of two
 constexpr int MAX_SLOTS = 14;
 enum Mode { ONE = 0, KEYS = 1, ROWS = 2 };
@@ -49,22 +52,21 @@ struct Cfg {
     static constexpr int NT = MODE == ONE ? 256 : 384;
     static constexpr int BN = D == 256 ? 64 : 128;
     static constexpr int CH = D / 64;                      // 64-element blocks of a row
+    static constexpr int GROUPS = MODE == ONE ? 1 : 2;     // of softmax warps
     static constexpr uint32_t SLOT = BN * D * 2;           // a key or value tile
     static constexpr uint32_t S_COL = 128;                 // score buffers at columns 0 and 128
     static constexpr uint32_t O_COL = 256;                 // accumulators at 256 and 256 + D
 };
 
-// What the loaders say about a piece lies in a ring of four: the products are
-// at most two tiles, and so two pieces, ahead of the softmax, and the loaders
-// one piece ahead of the products.
+// What the loader says about a piece lies in a ring of four.
 struct Control {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], s_full[2], p_full[2], o_done[2], q_full, q_empty, tree;
-    uint64_t grant[8];            // two slots of the ring are the loaders' to fill (at most slots / 2 at a time)
-    uint64_t masks[4], ready[4];  // a piece's masks are there; all that the loaders found out is
+    uint64_t full[2 * MAX_SLOTS], empty[MAX_SLOTS], s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2];
+    uint64_t grant[8];            // two slots of the ring are the loader's to fill (at most slots / 2 at a time)
+    uint64_t masks[4], ready[4], done[4];  // a piece's masks are there; all that the loader found out is; it has been read
     uint64_t stats, joined;       // KEYS: both groups' statistics are there; both have read the accumulators
     uint64_t mask[4][MAX_NODES];
-    uint64_t poison[4][2];
-    int flag[4][2];
+    uint64_t poison[4];
+    int flag[4];
     long long scan[12];
     AttnWalk begin;
     float m[2][128], l[2][128];   // KEYS: the groups' statistics
@@ -72,18 +74,24 @@ struct Control {
     int dead;
 };
 
-// A ring position: slot index and the parity of its current use.
+// A ring position: the slot and how often the ring has gone round.  A slot has
+// two barriers for "full", for even and odd laps: in KEYS mode a reader passes
+// over the other group's slots without waiting for them, and could take the
+// lap before last for its own if there were one barrier with a parity bit.
+// (When it looks at a slot in lap k it has read a slot that was filled after
+// this one in lap k - 1, and that fill had waited for lap k - 2 to be read.)
 struct Ring {
     int slots;
-    int slot = 0;
-    uint32_t phase = 0;
+    int slot = 0, lap = 0;
     __device__ __forceinline__ explicit Ring(int n) : slots(n) {}
     __device__ __forceinline__ void step() {
         if (++slot == slots) {
             slot = 0;
-            phase ^= 1u;
+            ++lap;
         }
     }
+    __device__ __forceinline__ int full() const { return 2 * slot + (lap & 1); }  // index of the barrier
+    __device__ __forceinline__ uint32_t phase() const { return (lap >> 1) & 1; }  // its parity
 };
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
@@ -110,28 +118,60 @@ __device__ __forceinline__ void mask_block(uint32_t (&s)[32], int c, int valid, 
     }
 }
 
+// Weights of one block of scores, stored as bfloat16 in 16 columns at p_addr;
+// their sum goes to acc.
+__device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2, uint64_t N2, uint64_t (&acc)[2], uint32_t p_addr) {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float a, b;
+        f2unpack(f2fma(f2pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), K2, N2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        acc[(i >> 1) & 1] = f2add(acc[(i >> 1) & 1], f2pack(a, b));
+        p[i / 2] = bf16x2(a, b);
+    }
+    tmem_st16(p_addr, p);
+}
+
+__device__ __forceinline__ void max_block(const uint32_t (&s)[32], float (&t)[4]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        t[(i >> 1) & 3] = max3(t[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+}
+
 // Softmax of one score tile: CH blocks of 32 columns, of which a row sees the
-// first `valid` or, of a tree tile, those in `see`.  The scores are read from
-// TMEM twice, once for the maximum and once for the weights, the next block
-// while one is worked on: a row's 128 scores never lie in registers at once.
+// first `valid` or, of a tree tile, those in `see`.  Two blocks are in
+// registers at a time; of four, the last two are read a second time for their
+// weights, while those of the first two are worked on (168 registers a thread
+// do not hold a row of 128 scores and what else is needed).  Block c's weights
+// go to columns 16 c .. of the tile, over scores that have been read.
 template <int CH, bool TREE>
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int valid, uint64_t see,
                                              bool first, float &m, float &l, uint32_t o_bar, uint32_t o_phase, bool &ok) {
     uint32_t s[2][32];
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     __syncwarp();  // TMEM accesses are warp-wide, and the lanes may have left a wait one by one
-    tmem_ld32(s_addr, s[0]);
-    tmem_wait_ld32(s[0]);
+    if (CH == 4) {
+        tmem_ld32(s_addr + 64, s[0]);
+        tmem_ld32(s_addr + 96, s[1]);
+        tmem_wait_ld32(s);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if (c + 1 < CH) tmem_ld32(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
-        uint32_t(&x)[32] = s[c & 1];
-        mask_block<TREE>(x, c, valid, see);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) t[(i >> 1) & 3] = max3(t[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-        if (c + 1 < CH) tmem_wait_ld32(s[(c + 1) & 1]);
+        for (int c = 0; c < 2; ++c) {
+            mask_block<TREE>(s[c], c + 2, valid, see);
+            max_block(s[c], t);
+        }
     }
-    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+#pragma unroll
+    for (int c = 0; c < (CH == 1 ? 1 : 2); ++c) tmem_ld32(s_addr + 32 * c, s[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < (CH == 1 ? 1 : 2); ++c) {
+        tmem_use32(s[c]);
+        mask_block<TREE>(s[c], c, valid, see);
+        max_block(s[c], t);
+    }
+    const float top = max3(t[0], t[1], fmaxf(t[2], t[3])) * scale;
     if (first) {
         m = top;
         l = 0.f;
@@ -146,39 +186,30 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
             l *= f;
 #pragma unroll 1
             for (int c = 0; c < ocols; c += 32) {
+                uint32_t o[32];
                 __syncwarp();
-                tmem_ld32(o_addr + c, s[0]);
-                tmem_wait_ld32(s[0]);
+                tmem_ld32(o_addr + c, o);
+                tmem_wait_ld32(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[0][i] = __float_as_uint(__uint_as_float(s[0][i]) * f);
-                tmem_st32(o_addr + c, s[0]);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(o_addr + c, o);
                 tmem_wait_st();
             }
         }
     }
     const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
     uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-    __syncwarp();
-    tmem_ld32(s_addr, s[0]);
-    tmem_wait_ld32(s[0]);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if (c + 1 < CH) tmem_ld32(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
-        uint32_t(&x)[32] = s[c & 1];
-        mask_block<TREE>(x, c, valid, see);
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            float a, b;
-            f2unpack(f2fma(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), K2, N2), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            acc[(i >> 1) & 1] = f2add(acc[(i >> 1) & 1], f2pack(a, b));
-            p[i / 2] = bf16x2(a, b);
-        }
-        // block c's weights lie over scores of blocks <= c
-        tmem_st16(s_addr + 16 * c, p);
-        if (c + 1 < CH) tmem_wait_ld32(s[(c + 1) & 1]);
+    weigh_block(s[0], K2, N2, acc, s_addr);
+    if (CH == 4) tmem_ld32(s_addr + 64, s[0]);
+    if (CH >= 2) weigh_block(s[1], K2, N2, acc, s_addr + 16);
+    if (CH == 4) {
+        tmem_wait_ld32(s[0]);
+        tmem_ld32(s_addr + 96, s[1]);
+        mask_block<TREE>(s[0], 2, valid, see);
+        weigh_block(s[0], K2, N2, acc, s_addr + 32);
+        tmem_wait_ld32(s[1]);
+        mask_block<TREE>(s[1], 3, valid, see);
+        weigh_block(s[1], K2, N2, acc, s_addr + 48);
     }
     float a0, a1, b0, b1;
     f2unpack(acc[0], a0, a1);
@@ -211,22 +242,23 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     }
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < A.slots; ++i) {
-            mbar_init(smem_addr(&ctl.full[i]), 1);
-            mbar_init(smem_addr(&ctl.empty[i]), 1);
+            mbar_init(smem_addr(&ctl.full[2 * i]), 1);
+            mbar_init(smem_addr(&ctl.full[2 * i + 1]), 1);
+            mbar_init(smem_addr(&ctl.empty[i]), MODE == ROWS ? 2 : 1);  // products that read a slot
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_full[i]), 128);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
+            mbar_init(smem_addr(&ctl.q_full[i]), MODE == KEYS ? 256 : 128);  // ROWS: a group's own rows
+            mbar_init(smem_addr(&ctl.q_empty[i]), MODE == KEYS ? 2 : 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&ctl.grant[i]), 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&ctl.masks[i]), LOADERS);
             mbar_init(smem_addr(&ctl.ready[i]), LOADERS);
+            mbar_init(smem_addr(&ctl.done[i]), 128 * C::GROUPS);
         }
-        mbar_init(smem_addr(&ctl.q_full), LOADERS);
-        mbar_init(smem_addr(&ctl.q_empty), 1);
-        mbar_init(smem_addr(&ctl.tree), LOADERS);
         mbar_init(smem_addr(&ctl.stats), 256);
         mbar_init(smem_addr(&ctl.joined), 256);
         ctl.dead = 0;
@@ -256,15 +288,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         // ---------------------------------------------------- copies ----
         Ring r(A.slots);
         int grants = 0;
-        uint32_t lap = 0;  // the first use of every slot needs no wait
-        const int boxrows = A.per_page ? C::BN : A.page_size;
+        const int boxrows = min(C::BN, A.page_size);
         while (ok && walk.next(A, pc)) {
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
                 if (t == pc.prefix) {  // the loaders fill these two slots once they are free
                     for (int i = 0; i < 2; ++i) {
-                        if (lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), r.phase ^ 1u) && ok;
+                        if (r.lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                         r.step();
-                        if (r.slot == 0) lap = 1;
                     }
                     ok = __all_sync(FULL, ok);
                     if (lane == 0 && ok) mbar_arrive(smem_addr(&ctl.grant[grants & 7]));
@@ -274,13 +304,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 int pos, valid;
                 attn_tile(A, pc.len, t, pos, valid);
                 const int page0 = pos / A.page_size, off = pos - page0 * A.page_size;
-                const int pages = A.per_page ? 1 : (valid + A.page_size - 1) / A.page_size;
+                const int pages = A.page_size >= C::BN ? 1 : (valid + A.page_size - 1) / A.page_size;
                 const int mine = lane < pages ? attn_page(A, pc.b, page0 + lane) : 0;  // at most BN / 8 pages
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), r.phase ^ 1u) && ok;
+                    // (the first use of every slot needs no wait)
+                    if (r.lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                     ok = __all_sync(FULL, ok);
                     if (!ok) break;
-                    const uint32_t full = smem_addr(&ctl.full[r.slot]), dst = ring0 + r.slot * C::SLOT;
+                    const uint32_t full = smem_addr(&ctl.full[r.full()]), dst = ring0 + r.slot * C::SLOT;
                     const void *map = kv ? static_cast<const void *>(&vmap) : static_cast<const void *>(&kmap);
                     if (elect_one()) mbar_arrive_expect_tx(full, pages * C::CH * boxrows * 128);
                     __syncwarp();
@@ -294,199 +325,190 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                         __syncwarp();
                     }
                     r.step();
-                    if (r.slot == 0) lap = 1;
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (warp <= C::GROUPS) {
         // -------------------------------------------------- products ----
         Ring r(A.slots);
+        const int g = warp - 1;      // the group of softmax warps; ONE: both score buffers
+        const int qi = MODE == ROWS ? g : 0;
+        const uint64_t qdesc = umma_desc(sq + qi * C::CH * qblock);
         uint32_t q_phase = 0;
-        int count[2] = {0, 0};  // score tiles of each group of warps (ONE: of each buffer)
-        int n_tiles = 0;
-        // the weights' product that is still to be issued, for each of the two
-        bool have[2] = {false, false}, first[2] = {}, release[2] = {};
-        int steps[2] = {}, slot[2] = {};
-        uint32_t phase[2] = {};
-        auto pv = [&](int s) {
-            ok = mbar_wait_bounded(smem_addr(&ctl.p_full[s]), (count[s] - 1) & 1) && ok;
-            ok = mbar_wait_bounded(smem_addr(&ctl.full[slot[s]]), phase[s]) && ok;
+        int count0 = 0, count1 = 0;  // score tiles of buffer 0 and 1 (KEYS, ROWS: of the group, in count0)
+        // O += P V of a tile: its buffer, the use of it, its slot of the ring
+        auto pv = [&](int buf, int use, const Ring &at, int steps, bool first) {
+            ok = mbar_wait_bounded(smem_addr(&ctl.p_full[buf]), (use - 1) & 1) && ok;
+            ok = mbar_wait_bounded(smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
             ok = __all_sync(FULL, ok);
-            have[s] = false;
             if (!ok) return;
             tmem_fence_after_sync();
             if (elect_one()) {
-                const uint32_t v = ring0 + slot[s] * C::SLOT, o = tmem + C::O_COL + (MODE == ONE ? 0 : s * D);
-                for (int k = 0; k < steps[s]; ++k)
-                    umma_ts(o, tmem + s * C::S_COL + 8 * k, umma_desc(v + k * 2048, C::BN * 128), umma_idesc(D, true),
-                            !(first[s] && k == 0));
-                if (release[s]) umma_commit(smem_addr(&ctl.empty[slot[s]]));
-                umma_commit(smem_addr(&ctl.o_done[s]));
+                const uint64_t v = umma_desc(ring0 + at.slot * C::SLOT, C::BN * 128);
+                const uint32_t o = tmem + C::O_COL + (MODE == ONE ? 0 : g * D), p = tmem + buf * C::S_COL;
+                if (steps == C::BN / 16) {
+#pragma unroll
+                    for (int k = 0; k < C::BN / 16; ++k)
+                        umma_ts(o, p + 8 * k, v + k * (2048 >> 4), umma_idesc(D, true), !(first && k == 0));
+                } else {
+                    for (int k = 0; k < steps; ++k)
+                        umma_ts(o, p + 8 * k, v + k * (2048 >> 4), umma_idesc(D, true), !(first && k == 0));
+                }
+                umma_commit(smem_addr(&ctl.o_done[buf]));
+                umma_commit(smem_addr(&ctl.empty[at.slot]));
+            }
+            __syncwarp();
+        };
+        auto qk = [&](int buf, int slot, uint32_t idesc) {
+            tmem_fence_after_sync();
+            if (elect_one()) {
+                const uint64_t k = umma_desc(ring0 + slot * C::SLOT);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    umma_ss(tmem + buf * C::S_COL, qdesc + (((i >> 2) * qblock + (i & 3) * 32) >> 4),
+                            k + (((i >> 2) * (C::BN * 128) + (i & 3) * 32) >> 4), idesc, i > 0);
+                umma_commit(smem_addr(&ctl.s_full[buf]));
+                umma_commit(smem_addr(&ctl.empty[slot]));
             }
             __syncwarp();
         };
         while (ok && walk.next(A, pc)) {
             bool bad;
             const int n = attn_nodes(A, pc.b, bad);
-            ok = mbar_wait_bounded(smem_addr(&ctl.q_full), q_phase) && ok;
+            ok = mbar_wait_bounded(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
             q_phase ^= 1u;
+            // the tile whose weights' product is still to be issued
+            bool have = false, old_first = false;
+            int old_steps = 0, old_buf = 0;
+            Ring old(A.slots);
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+                const Ring kr = r;
+                r.step();
+                const Ring vr = r;
+                r.step();
+                if (MODE == KEYS && ((t - pc.t0) & 1) != g) continue;
                 int pos, valid;
                 if (t == pc.prefix)
                     valid = n > 0 ? n : 1;
                 else
                     attn_tile(A, pc.len, t, pos, valid);
-                const int k_slot = r.slot;
-                const uint32_t k_phase = r.phase;
-                r.step();
-#pragma unroll
-                for (int half = 0; half < (MODE == ROWS ? 2 : 1); ++half) {
-                    const int s = MODE == ROWS ? half : MODE == KEYS ? (t - pc.t0) & 1 : n_tiles & 1;
-                    // the group's last weights first: they lie where the scores go.
-                    // (ONE: the other buffer is free; its last product follows the
-                    // scores unless the keys are not there yet.)
-                    if (MODE != ONE && have[s]) pv(s);
-                    if (MODE == ONE && have[s ^ 1] &&
-                        !__all_sync(FULL, mbar_test_wait(smem_addr(&ctl.full[k_slot]), k_phase)))
-                        pv(s ^ 1);
-                    ok = mbar_wait_bounded(smem_addr(&ctl.full[k_slot]), k_phase) && ok;
-                    ok = __all_sync(FULL, ok);
-                    if (!ok) break;
-                    tmem_fence_after_sync();
-                    if (elect_one()) {
-                        const uint32_t k = ring0 + k_slot * C::SLOT, q = sq + (MODE == ROWS ? s * C::CH * qblock : 0);
-                        const uint32_t idesc = umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false);
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            umma_ss(tmem + s * C::S_COL, umma_desc(q + (i >> 2) * qblock + (i & 3) * 32),
-                                    umma_desc(k + (i >> 2) * (C::BN * 128) + (i & 3) * 32), idesc, i > 0);
-                        if (MODE != ROWS || s == 1) {
-                            umma_commit(smem_addr(&ctl.empty[k_slot]));
-                            if (t + 1 == pc.t1) umma_commit(smem_addr(&ctl.q_empty));
-                        }
-                        umma_commit(smem_addr(&ctl.s_full[s]));
-                    }
-                    __syncwarp();
-                    if (MODE == ONE && have[s ^ 1]) pv(s ^ 1);
-                    have[s] = true;
-                    first[s] = MODE == KEYS ? t - pc.t0 < 2 : t == pc.t0;
-                    release[s] = MODE != ROWS || s == 1;
-                    steps[s] = round16(valid) / 16;
-                    slot[s] = r.slot;
-                    phase[s] = r.phase;
-                    ++count[s];
+                const uint32_t idesc = umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false);
+                const int buf = MODE == ONE ? (t - pc.t0) & 1 : g;
+                // One buffer: its last weights have to be used before new scores
+                // go there.  Two: the scores first, unless their keys are not
+                // there yet.
+                if (have && (MODE != ONE || !__all_sync(FULL, mbar_test_wait(smem_addr(&ctl.full[kr.full()]), kr.phase())))) {
+                    pv(old_buf, MODE == ONE && old_buf ? count1 : count0, old, old_steps, old_first);
+                    have = false;
                 }
-                r.step();
-                ++n_tiles;
+                ok = mbar_wait_bounded(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
+                qk(buf, kr.slot, idesc);
+                if (MODE == ONE && have)
+                    pv(old_buf, old_buf ? count1 : count0, old, old_steps, old_first);
+                if (MODE == ONE && buf)
+                    ++count1;
+                else
+                    ++count0;
+                have = true;
+                old_first = MODE == KEYS ? t - pc.t0 < 2 : t == pc.t0;
+                old = vr;
+                old_steps = round16(valid) / 16;
+                old_buf = buf;
             }
-            // the piece's last weights, the older ones first
-            const int older = MODE == KEYS ? (pc.t1 - pc.t0) & 1 : 0;
-            if (ok && have[older]) pv(older);
-            if (ok && have[older ^ 1]) pv(older ^ 1);
+            // all scores of the piece are on their way: its queries may go
+            if (elect_one()) {
+                if (have)
+                    umma_commit(smem_addr(&ctl.q_empty[qi]));
+                else
+                    mbar_arrive(smem_addr(&ctl.q_empty[qi]));
+            }
+            __syncwarp();
+            if (ok && have) pv(old_buf, MODE == ONE && old_buf ? count1 : count0, old, old_steps, old_first);
         }
-    } else if (warp < 4) {
-        // ------------------------------------- queries and new tokens ----
-        const int lt = tid - 64;
+    } else if (warp == 3) {
+        // --------------------------------------- new keys and values ----
         Ring r(A.slots);
-        uint32_t q_phase = 0, tree_phase = 0;
         int grants = 0;
-        const bf16_t *gq = static_cast<const bf16_t *>(A.q);
-        const int vecs = rows * (D / 8);
         for (int np = 0; ok && walk.next(A, pc); ++np) {
             const int b = pc.b, h = pc.h;
             bool bad_len, bad_nodes;
             attn_len(A, b, bad_len);
             const int n = attn_nodes(A, b, bad_nodes);
-            auto q_vec = [&](int i) {
-                const int rr = row0 + i / (D / 8), u = i % (D / 8), t = rr / A.G, g = rr - t * A.G;
-                return __ldg(reinterpret_cast<const uint4 *>(gq + b * A.qs[0] + t * A.qs[1] +
-                                                             (static_cast<int64_t>(h) * A.G + g) * A.qs[2]) +
-                             u);
-            };
-            auto q_put = [&](int i, const uint4 &x) {
-                const int rr = i / (D / 8), u = i % (D / 8);
-                *reinterpret_cast<uint4 *>(smem + ((rr >> 7) * C::CH + (u >> 3)) * qblock + sw128(rr & 127, u & 7)) = x;
-            };
-            constexpr int AHEAD = 8;  // vectors of a thread that are under way while the last piece ends
-            uint4 x[AHEAD];
-#pragma unroll
-            for (int e = 0; e < AHEAD; ++e)
-                if (lt + e * LOADERS < vecs) x[e] = q_vec(lt + e * LOADERS);
-            if (np > 0) {
-                ok = mbar_wait_bounded(smem_addr(&ctl.q_empty), q_phase) && ok;
-                q_phase ^= 1u;
+            if (np >= 4) {
+                ok = mbar_wait_bounded(smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
-#pragma unroll
-            for (int e = 0; e < AHEAD; ++e)
-                if (lt + e * LOADERS < vecs) q_put(lt + e * LOADERS, x[e]);
-#pragma unroll 4
-            for (int i = lt + AHEAD * LOADERS; i < vecs; i += LOADERS) q_put(i, q_vec(i));
             int flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
-            if (lt < n) {
+            for (int i = lane; i < n; i += 32) {
                 bool bad_up = false;
-                ctl.mask[np & 3][lt] = attn_mask(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, lt, bad_up);
+                ctl.mask[np & 3][i] = attn_mask(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, i, bad_up);
                 if (bad_up) flag |= F_BAD_ID;
             }
-            fence_proxy_async();
-            mbar_arrive(smem_addr(&ctl.q_full));
             mbar_arrive(smem_addr(&ctl.masks[np & 3]));
+            for (int t = pc.t0; t < min(pc.t1, pc.prefix); ++t) {
+                r.step();
+                r.step();
+            }
             uint64_t poison = 0;
-            for (int t = pc.t0; t < pc.t1; ++t) {
+            if (pc.t1 > pc.prefix) {
+                ok = mbar_wait_bounded(smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
+                ++grants;
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (t == pc.prefix) {
-                        if (kv == 0) {
-                            ok = mbar_wait_bounded(smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
-                            ++grants;
-                        }
-                        unsigned char *dst = ring + r.slot * C::SLOT;
-                        const bf16_t *src = static_cast<const bf16_t *>(kv ? A.v_new : A.k_new);
-                        const int64_t *st = kv ? A.vs : A.ks;
-                        // of the keys no more than the sequence's nodes is
-                        // looked at; the values behind them are zero, and so
-                        // is one that is not finite (its rows get it later)
-                        const int fill = kv ? round16(n > 0 ? n : 1) : n;
-                        if (ok) {
-#pragma unroll 4
-                            for (int i = lt; i < fill * (D / 8); i += LOADERS) {
-                                const int j = i / (D / 8), u = i % (D / 8);
-                                uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                                if (j < n) y = __ldg(reinterpret_cast<const uint4 *>(src + b * st[0] + j * st[1] + h * st[2]) + u);
-                                if (kv) {
-                                    uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                    unsigned char *dst = ring + r.slot * C::SLOT;
+                    const bf16_t *src = static_cast<const bf16_t *>(kv ? A.v_new : A.k_new);
+                    const int64_t *st = kv ? A.vs : A.ks;
+                    src += b * st[0] + h * st[2];
+                    // Of the keys no more than the sequence's nodes is looked
+                    // at; the values behind them are zero, and so is one that
+                    // is not finite (its rows get it later).
+                    const int fill = (kv ? round16(n > 0 ? n : 1) : n) * (D / 8);
+                    if (ok) {
+                        for (int i0 = lane; i0 < fill; i0 += 32 * 8) {
+                            uint4 y[8];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const bool lo = (w[e] & 0x7f80u) == 0x7f80u, hi = (w[e] & 0x7f800000u) == 0x7f800000u;
+                            for (int e = 0; e < 8; ++e) {
+                                const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
+                                y[e] = j < n ? __ldg(reinterpret_cast<const uint4 *>(src + j * st[1]) + u) : make_uint4(0u, 0u, 0u, 0u);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
+                                if (i0 + 32 * e >= fill) break;
+                                if (kv) {
+                                    uint32_t w[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        const bool lo = (w[q] & 0x7f80u) == 0x7f80u, hi = (w[q] & 0x7f800000u) == 0x7f800000u;
                                         if (lo || hi) poison |= 1ull << j;
-                                        w[e] = (lo ? 0u : w[e] & 0xffffu) | (hi ? 0u : w[e] & 0xffff0000u);
+                                        w[q] = (lo ? 0u : w[q] & 0xffffu) | (hi ? 0u : w[q] & 0xffff0000u);
                                     }
-                                    y = make_uint4(w[0], w[1], w[2], w[3]);
+                                    y[e] = make_uint4(w[0], w[1], w[2], w[3]);
                                 }
-                                *reinterpret_cast<uint4 *>(dst + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) = y;
+                                *reinterpret_cast<uint4 *>(dst + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) = y[e];
                             }
                         }
-                        fence_proxy_async();
-                        // everyone waits: a thread that went on would arrive
-                        // a second time in the same phase
-                        mbar_arrive(smem_addr(&ctl.tree));
-                        ok = mbar_wait_bounded(smem_addr(&ctl.tree), tree_phase) && ok;
-                        tree_phase ^= 1u;
-                        if (lt == 0) mbar_arrive(smem_addr(&ctl.full[r.slot]));
                     }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl.full[r.full()]));
                     r.step();
                 }
             }
-            flag |= attn_check_pages(A, b, pc.len, lt, LOADERS);
+            flag |= attn_check_pages(A, b, pc.len, lane, LOADERS);
             flag = __reduce_or_sync(FULL, flag);
-            if (lane == 0) ctl.flag[np & 3][warp - 2] = flag;
             const uint32_t plo = __reduce_or_sync(FULL, static_cast<uint32_t>(poison));
             const uint32_t phi = __reduce_or_sync(FULL, static_cast<uint32_t>(poison >> 32));
-            if (lane == 0) ctl.poison[np & 3][warp - 2] = (static_cast<uint64_t>(phi) << 32) | plo;
+            if (lane == 0) {
+                ctl.flag[np & 3] = flag;
+                ctl.poison[np & 3] = (static_cast<uint64_t>(phi) << 32) | plo;
+            }
             mbar_arrive(smem_addr(&ctl.ready[np & 3]));
             ok = __all_sync(FULL, ok);
         }
-    } else {
+    } else if (warp >= 4) {
         // --------------------------------------------------- softmax ----
         const int wg = (warp - 4) >> 2;                 // group of four warps
         const int wt = (tid - 128) & 127;               // this thread's row
@@ -497,10 +519,43 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const bool busy = lrow - lane < rows;           // the warp has rows
         const int rr = row0 + lrow, node = rr / A.G;
         const uint32_t o_addr = lanes + C::O_COL + (MODE == ONE ? 0 : wg * D);
+        const int qi = MODE == ROWS ? wg : 0;
         Ring r(A.slots);
-        int count = 0;                                  // score tiles of this group
+        int count0 = 0, count1 = 0;                     // uses of the group's score buffer (ONE: of both)
         uint32_t join_phase = 0;
-        for (int np = 0; ok && walk.next(A, pc); ++np) {
+        // The queries of piece `np` into shared memory, by the threads that
+        // arrive on q_full[qi], once the scores of the piece before are done.
+        auto load_q = [&](const AttnPiece &p, int np) {
+            constexpr int LOAD = MODE == KEYS ? 256 : 128, AHEAD = 8;
+            const int lt = MODE == KEYS ? tid - 128 : wt;
+            const int q0 = MODE == ROWS ? 128 * wg : 0, vecs = max(0, min(rows - q0, 128)) * (D / 8);
+            const bf16_t *src = static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2];
+            bool waited = np == 0;
+            for (int i0 = lt; i0 < vecs || !waited; i0 += LOAD * AHEAD) {
+                uint4 x[AHEAD];
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const int i = i0 + e * LOAD, row = row0 + q0 + i / (D / 8), t = row / A.G;
+                    if (i < vecs) x[e] = __ldg(reinterpret_cast<const uint4 *>(src + t * A.qs[1] + (row - t * A.G) * A.qs[2]) + i % (D / 8));
+                }
+                if (!waited) {
+                    ok = mbar_wait_bounded(smem_addr(&ctl.q_empty[qi]), (np - 1) & 1) && ok;
+                    waited = true;
+                }
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const int i = i0 + e * LOAD, row = i / (D / 8), u = i % (D / 8);
+                    if (i < vecs && ok)
+                        *reinterpret_cast<uint4 *>(smem + (qi * C::CH + (u >> 3)) * qblock + sw128(row, u & 7)) = x[e];
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(smem_addr(&ctl.q_full[qi]));
+            ok = __all_sync(FULL, ok);
+        };
+        bool more = walk.next(A, pc);
+        if (more) load_q(pc, 0);
+        for (int np = 0; ok && more; ++np) {
             const int b = pc.b, h = pc.h;
             bool bad;
             const int n = attn_nodes(A, b, bad);
@@ -508,18 +563,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             bool first = true;
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
                 r.step();  // the keys' slot
-                const int v_slot = r.slot;
-                const uint32_t v_phase = r.phase;
+                const Ring vr = r;
                 r.step();
                 if (MODE == KEYS && ((t - pc.t0) & 1) != wg) continue;
-                const int buf = MODE == ONE ? count & 1 : wg;
-                const uint32_t phase = MODE == ONE ? (count >> 1) & 1 : count & 1;
+                const int buf = MODE == ONE ? (t - pc.t0) & 1 : wg;
+                const int use = MODE == ONE && buf ? count1 : count0;
                 const uint32_t s_addr = lanes + buf * C::S_COL;
-                ok = mbar_wait_bounded(smem_addr(&ctl.s_full[buf]), phase) && ok;
+                ok = mbar_wait_bounded(smem_addr(&ctl.s_full[buf]), use & 1) && ok;
                 tmem_fence_after_sync();
                 // the product before this one into the accumulator
                 const uint32_t o_bar = smem_addr(&ctl.o_done[MODE == ONE ? buf ^ 1 : wg]);
-                const uint32_t o_phase = MODE == ONE ? ((count - 1) >> 1) & 1 : (count - 1) & 1;
+                const uint32_t o_phase = ((MODE == ONE ? buf ? count0 : count1 : count0) - 1) & 1;
                 if (t == pc.prefix) {
                     ok = mbar_wait_bounded(smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
                     const uint64_t see = live && node < n ? ctl.mask[np & 3][node] : 0ull;
@@ -537,13 +591,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                                                         ok);
                     const int end = round16(valid);
                     // What lies behind the last key meets a weight of 0: it has
-                    // to be a number.  (ROWS: the first group's product is the
-                    // first to read it, and the first group writes it.)
-                    if (valid < end && (MODE != ROWS || wg == 0)) {
-                        ok = mbar_wait_bounded(smem_addr(&ctl.full[v_slot]), v_phase) && ok;
+                    // to be a number.  (ROWS: each group sees to it for its own
+                    // product; both write the same.)
+                    if (valid < end) {
+                        ok = mbar_wait_bounded(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
                         for (int i = wt; i < (end - valid) * (D / 8); i += 128) {
                             const int j = valid + i / (D / 8), u = i % (D / 8);
-                            *reinterpret_cast<uint4 *>(ring + v_slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
+                            *reinterpret_cast<uint4 *>(ring + vr.slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async();
@@ -552,14 +606,22 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 first = false;
                 tmem_fence_before_sync();
                 mbar_arrive(smem_addr(&ctl.p_full[buf]));
-                ++count;
+                if (MODE == ONE && buf)
+                    ++count1;
+                else
+                    ++count0;
                 ok = __all_sync(FULL, ok);
             }
+            if (!ok) break;
+            AttnPiece next;
+            more = walk.next(A, next);
+            if (more) load_q(next, np + 1);
             // ------------------------------------------------ results ----
             ok = mbar_wait_bounded(smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
             if (!first) {
-                const int buf = MODE == ONE ? (count - 1) & 1 : wg;
-                ok = mbar_wait_bounded(smem_addr(&ctl.o_done[buf]), MODE == ONE ? ((count - 1) >> 1) & 1 : (count - 1) & 1) && ok;
+                const int buf = MODE == ONE ? (pc.t1 - 1 - pc.t0) & 1 : wg;
+                const int use = MODE == ONE && buf ? count1 : count0;
+                ok = mbar_wait_bounded(smem_addr(&ctl.o_done[buf]), (use - 1) & 1) && ok;
             }
             ok = __all_sync(FULL, ok);
             if (!ok) break;
@@ -586,10 +648,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 f1 = ex2(m1 - ref);
                 l = f0 * ctl.l[0][wt] + f1 * ctl.l[1][wt];
             }
-            const int flag = ctl.flag[np & 3][0] | ctl.flag[np & 3][1];
+            const int flag = ctl.flag[np & 3];
             if (A.flags && tid == 128 && h == 0 && mtile == 0) A.flags[b] = flag;
             const uint64_t seen = pc.t1 == pc.prefix + 1 && live && node < n
-                                      ? ctl.mask[np & 3][node] & (ctl.poison[np & 3][0] | ctl.poison[np & 3][1])
+                                      ? ctl.mask[np & 3][node] & ctl.poison[np & 3]
                                       : 0ull;
             if (flag) l = NAN;
             const bool whole = pc.whole();
@@ -654,14 +716,15 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
             }
             tmem_fence_before_sync();
+            mbar_arrive(smem_addr(&ctl.done[np & 3]));
             if (MODE == KEYS) {  // the next piece's products may write the accumulators
                 mbar_arrive(smem_addr(&ctl.joined));
                 ok = mbar_wait_bounded(smem_addr(&ctl.joined), join_phase) && ok;
                 join_phase ^= 1u;
                 ok = __all_sync(FULL, ok);
             }
+            pc = next;
         }
-        __syncwarp();
     }
     // ---------------------------------------------------------- the end ----
     __syncwarp();

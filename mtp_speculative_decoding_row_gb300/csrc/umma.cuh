@@ -132,6 +132,12 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
 }
 
+// Ties registers of an earlier load to the wait before this.
+__device__ __forceinline__ void tmem_use32(uint32_t (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+}
+
 // Two floats rounded to bfloat16, `lo` in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t r;
