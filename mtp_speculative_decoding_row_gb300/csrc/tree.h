@@ -55,8 +55,8 @@ struct UmmaPlan {
 };
 UmmaPlan attn_umma_plan(int D, int rows);
 int attn_umma_bn(int D);  // keys of a tile
-const void *attn_join_func(int dtype);
-constexpr int JOIN_ROWS = 16, JOIN_THREADS = 128;
+const void *attn_join_func(int dtype, int D);
+constexpr int JOIN_ROWS = 4, JOIN_THREADS = 128;  // rows of a block, a warp each
 
 // ------------------------------------------------------- beam selection --
 

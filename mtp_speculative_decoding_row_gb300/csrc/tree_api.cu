@@ -283,7 +283,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.per_page = p.per_page;
     const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, false, &kmap, &vmap);
     if (e != MTP_OK || !p.joins()) return e;
-    return launch(attn_join_func(a.dtype), dim3(p.groups * p.mtiles, (p.bm + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A,
+    return launch(attn_join_func(a.dtype, a.D), dim3(p.groups * p.mtiles, ((p.rows < p.bm ? p.rows : p.bm) + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A,
                   stream, true);
 }
 

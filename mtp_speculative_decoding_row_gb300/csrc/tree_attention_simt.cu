@@ -273,50 +273,87 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 
 // Join one unit that begins in group blockIdx.x / mtiles and goes on in the
 // next groups: with m the largest of the parts' maxima, o = sum_i 2^(m_i - m)
-// o_i / sum_i 2^(m_i - m) l_i, the parts in the order of their keys.  Block
-// (x, y) takes 16 rows, four columns to a thread.
-template <typename T>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
+// o_i / sum_i 2^(m_i - m) l_i, the parts in the order of their keys.  A warp
+// takes one row and lane i the columns 4 i ..; the maxima and sums of 32 parts
+// are loaded by the 32 lanes at once and handed round, and four parts' rows are
+// on their way at a time: what bounds this kernel is the time of a load, not
+// their number (a row of 20 parts read one after the other took 30 us), so it
+// also keeps its registers few and many warps on an SM.
+constexpr int JOIN_AHEAD = 4;
+
+template <typename T, int NQ>
+__global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
-    const int *d = A.desc + static_cast<size_t>(group) * ATTN_DESC;
-    const int parts = d[2];
+    const int4 d = *reinterpret_cast<const int4 *>(A.desc + static_cast<size_t>(group) * ATTN_DESC);
+    const int b = d.x, h = d.y, parts = d.z;
     if (parts == 0) return;
-    const int b = d[0], h = d[1];
     bool bad;
     const int n = attn_nodes(A, b, bad);
-    const int rows = min(A.bm, (bad ? A.rows : n * A.G) - mtile * A.bm);
+    const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= min(A.bm, (bad ? A.rows : n * A.G) - mtile * A.bm)) return;
     const size_t slot_floats = attn_slot_floats(A.bm, A.D);
-    const float *first = A.part + attn_slot(A, group, mtile, d[3] == 0) * slot_floats;
+    const float *first = A.part + attn_slot(A, group, mtile, d.w == 0) * slot_floats;
     const float *next = A.part + attn_slot(A, group + 1, mtile, true) * slot_floats;
     const size_t step = 2 * slot_floats * A.mtiles;
-    const int quads = (A.D + 3) / 4;
-    for (int i = threadIdx.x; i < JOIN_ROWS * quads; i += JOIN_THREADS) {
-        const int r = blockIdx.y * JOIN_ROWS + i / quads, c = 4 * (i % quads);
-        if (r >= rows) continue;
-        float top = first[r];
-        for (int k = 1; k < parts; ++k) top = max_nan(top, next[(k - 1) * step + r]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float *s = k == 0 ? first : next + (k - 1) * step;
-            const float w = exp2f(s[r] - ref);
+    auto part = [&](int k) { return k == 0 ? first : next + (k - 1) * step; };
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = max_nan(top, part(k)[r]);
+#pragma unroll
+    for (int e = 1; e < 32; e <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, e));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f, o[NQ][4] = {};
+    const bool quads = A.D % 4 == 0;  // (rows of part results start on 16 bytes then)
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float w = 0.f;
+        if (k0 + lane < parts) {
+            const float *s = part(k0 + lane);
+            w = exp2f(s[r] - ref);
             l = fmaf(w, s[A.bm + r], l);
-            const float *x = s + 2 * A.bm + static_cast<size_t>(r) * A.D + c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < A.D) o[e] = fmaf(w, x[e], o[e]);
         }
-        const int row = mtile * A.bm + r, t = row / A.G, hq = h * A.G + row - t * A.G;
-        const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
-        const float inv = 1.f / l;
-        T *out = static_cast<T *>(A.out) + at * A.D + c;
+        const int here = min(32, parts - k0);
+        for (int i0 = 0; i0 < here; i0 += JOIN_AHEAD) {
+            float4 x[JOIN_AHEAD][NQ];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < A.D) put(out + e, o[e] * inv);
-        if (A.lse && c == 0) A.lse[at] = (ref + log2f(l)) * LN2;
+            for (int i = 0; i < JOIN_AHEAD; ++i)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int c = 4 * lane + 128 * q;
+                    x[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i0 + i >= here || c >= A.D) continue;
+                    const float *s = part(k0 + i0 + i) + 2 * A.bm + static_cast<size_t>(r) * A.D + c;
+                    if (quads)
+                        x[i][q] = *reinterpret_cast<const float4 *>(s);
+                    else
+                        x[i][q] = make_float4(s[0], c + 1 < A.D ? s[1] : 0.f, c + 2 < A.D ? s[2] : 0.f, c + 3 < A.D ? s[3] : 0.f);
+                }
+#pragma unroll
+            for (int i = 0; i < JOIN_AHEAD; ++i) {
+                const float wi = __shfl_sync(FULL, w, (i0 + i) & 31);
+                if (i0 + i >= here) continue;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    o[q][0] = fmaf(wi, x[i][q].x, o[q][0]);
+                    o[q][1] = fmaf(wi, x[i][q].y, o[q][1]);
+                    o[q][2] = fmaf(wi, x[i][q].z, o[q][2]);
+                    o[q][3] = fmaf(wi, x[i][q].w, o[q][3]);
+                }
+            }
+        }
     }
+    l = warp_allsum(l);
+    const int row = mtile * A.bm + r, t = row / A.G, hq = h * A.G + row - t * A.G;
+    const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
+    const float inv = 1.f / l;
+    T *out = static_cast<T *>(A.out) + at * A.D;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = 4 * lane + 128 * q + e;
+            if (c < A.D) put(out + c, o[q][e] * inv);
+        }
+    if (A.lse && lane == 0) A.lse[at] = (ref + log2f(l)) * LN2;
 }
 
 }  // namespace
@@ -338,9 +375,12 @@ const void *attn_simt_func(int dtype, int D) {
                      : reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 4>);
 }
 
-const void *attn_join_func(int dtype) {
-    return dtype == 0 ? reinterpret_cast<const void *>(attn_join_impl<float>)
-                      : reinterpret_cast<const void *>(attn_join_impl<bf16_t>);
+const void *attn_join_func(int dtype, int D) {
+    if (D <= 128)
+        return dtype == 0 ? reinterpret_cast<const void *>(attn_join_impl<float, 1>)
+                          : reinterpret_cast<const void *>(attn_join_impl<bf16_t, 1>);
+    return dtype == 0 ? reinterpret_cast<const void *>(attn_join_impl<float, 2>)
+                      : reinterpret_cast<const void *>(attn_join_impl<bf16_t, 2>);
 }
 
 }  // namespace mtp
