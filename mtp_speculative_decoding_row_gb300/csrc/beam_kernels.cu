@@ -9,13 +9,15 @@
 // float64 -- candidates of two beams may lie closer than float32 tells apart
 // -- and merges the sorted lists.
 //
-// A part keeps its candidates in shared memory as 64-bit keys: the logit's
-// bits in an order-preserving form, then the complement of the index, so one
-// integer comparison orders by value and then by smaller index.  The K-th
-// largest of the threads' maxima over the first 4 vectors each bounds the
-// K-th best from below; what follows is compared with that bound vector by
-// vector (one comparison for 8 bf16 logits), and few pass.  When the list is
-// full it is cut to its K best and the bound rises.
+// Candidates are 64-bit keys: the logit's bits in an order-preserving form,
+// then the complement of the index, so one integer comparison orders by value
+// and then by smaller index.  The K-th largest of the threads' maxima over
+// their first 4 vectors bounds the K-th best from below; the rest is compared
+// with that bound 4 vectors at a time, and few pass.  Each warp keeps a list
+// of its own, so nothing waits for another warp while the row streams by; a
+// list that is full is cut to its K best, and the bound rises for all warps.
+// What bounds the kernel is the row's bytes: the exponentials take about half
+// of the time of the loads.
 //
 // Rows may start on any element.  A vector is always elements [8 j, 8 j + 8)
 // (4 j of float32) of the row, put together from two aligned loads where the
@@ -30,7 +32,9 @@ namespace {
 
 constexpr int NT = BEAM_THREADS;
 constexpr int UN = 4;        // vectors of a thread per round
-constexpr int CAP = 2048;    // candidates held by a part
+constexpr int NW = NT / 32;
+constexpr int CAP = 192;     // candidates held by a warp
+constexpr int SMEM_CAND = 4096;  // candidates that the join holds in shared memory
 
 // Order-preserving bits of a float (the two zeros are equal).
 __device__ __forceinline__ uint32_t order_bits(float z) {
@@ -69,21 +73,24 @@ __device__ __forceinline__ uint4 minus_inf_vec() {
     return make_uint4(w, w, w, w);
 }
 
-// Vector j of a row (elements j VEC ..), -inf beyond the row's V elements.
+// Vector j of a row (elements j VEC ..), all of it in the row.
 template <typename T>
-__device__ __forceinline__ uint4 row_vec(const unsigned char *row, uint32_t sh, int j, int V) {
+__device__ __forceinline__ uint4 row_vec(const unsigned char *row, uint32_t sh, int j) {
+    const uint4 *a = reinterpret_cast<const uint4 *>(row - sh) + j;
+    if (sh == 0) return __ldg(a);
+    return realign(__ldg(a), __ldg(a + 1), sh);  // the row's bytes reach into the second load
+}
+
+// The row's last vector, -inf beyond its V elements.
+template <typename T>
+__device__ __noinline__ uint4 row_tail(const unsigned char *row, int j, int V) {
     constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
-    if ((j + 1) * VEC <= V) {
-        const uint4 *a = reinterpret_cast<const uint4 *>(row - sh) + j;
-        if (sh == 0) return __ldg(a);
-        return realign(__ldg(a), __ldg(a + 1), sh);  // the row's bytes reach into the second load
-    }
     uint32_t w[4] = {minus_inf_vec<T>().x, minus_inf_vec<T>().x, minus_inf_vec<T>().x, minus_inf_vec<T>().x};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         if (j * VEC + e >= V) break;
         if (ES == 4)
-            w[e] = __ldg(reinterpret_cast<const uint32_t *>(row) + j * VEC + e);
+            w[e & 3] = __ldg(reinterpret_cast<const uint32_t *>(row) + j * VEC + e);
         else {
             const uint32_t x = __ldg(reinterpret_cast<const unsigned short *>(row) + j * VEC + e);
             w[e / 2] = (e & 1) ? (w[e / 2] & 0x0000ffffu) | (x << 16) : (w[e / 2] & 0xffff0000u) | x;
@@ -92,62 +99,67 @@ __device__ __forceinline__ uint4 row_vec(const unsigned char *row, uint32_t sh, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Keys of the vectors in `raw` that beat `bound` go into the list; `dup` > 0:
-// except those among its first `dup` entries (a round that is done again).
-template <typename T>
-__device__ __forceinline__ void offer(const uint4 (&raw)[UN], const int (&at)[UN], uint64_t bound, uint64_t *list, int *count,
-                                      int dup) {
-    constexpr int VEC = Store<T>::VEC;
-    const float zb = order_float(static_cast<uint32_t>(bound >> 32));
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-        if (!(Store<T>::vmax(raw[u]) >= zb)) continue;
-        float z[VEC];
-        Store<T>::unpack(raw[u], z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (!(z[e] >= zb) || z[e] == -INFINITY) continue;
-            const uint64_t key = make_key(z[e], at[u] * VEC + e);
-            if (key < bound) continue;
-            bool seen = false;
-            for (int i = 0; i < dup; ++i) seen |= list[i] == key;
-            if (seen) continue;
-            const int i = atomicAdd(count, 1);
-            if (i < CAP) list[i] = key;
-        }
-    }
-}
-
-// Cut list[0 .. n) to its `keep` largest, sorted: each key's rank is the
-// number of larger ones (keys differ).  All threads call it.
+// The `keep` largest of list[0 .. n), sorted, to the front of the list: each
+// key's rank is the number of larger ones (keys differ).  Warp-wide; `tmp`
+// holds `keep` keys.
 __device__ __forceinline__ int cut(uint64_t *list, int n, int keep, uint64_t *tmp) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) {
         const uint64_t key = list[i];
         int rank = 0;
-        int j = 0;
-        for (; j + 4 <= n && rank < keep; j += 4)
-            rank += (list[j] > key) + (list[j + 1] > key) + (list[j + 2] > key) + (list[j + 3] > key);
-        if (j + 4 > n)
-            for (; j < n; ++j) rank += list[j] > key;
+        for (int j = 0; j < n; ++j) rank += list[j] > key;
         if (rank < keep) tmp[rank] = key;
     }
-    __syncthreads();
+    __syncwarp();
     const int m = min(n, keep);
-    for (int i = threadIdx.x; i < m; i += NT) list[i] = tmp[i];
-    __syncthreads();
+    for (int i = lane; i < m; i += 32) list[i] = tmp[i];
+    __syncwarp();
     return m;
 }
 
+// Offer vector `raw` (elements at VEC ..) of every lane in `lanes` to the
+// warp's list: eight lanes (four of float32) look at one element each.
 template <typename T>
-__global__ void __launch_bounds__(NT) beam_part_impl(const __grid_constant__ BeamArgs A) {
+__device__ __noinline__ void offer(const uint4 raw, int at, uint32_t lanes, uint64_t *list, int &count, uint64_t &bound, int keep,
+                                   uint64_t *tmp, unsigned long long *s_bound) {
+    constexpr int VEC = Store<T>::VEC;
+    const int lane = threadIdx.x & 31;
+    while (lanes) {
+        const int src = __ffs(lanes) - 1;
+        lanes &= lanes - 1;
+        const uint32_t x = __shfl_sync(FULL, raw.x, src), y = __shfl_sync(FULL, raw.y, src), z = __shfl_sync(FULL, raw.z, src),
+                       w = __shfl_sync(FULL, raw.w, src);
+        const int v0 = __shfl_sync(FULL, at, src) * VEC;
+        const int e = lane & (VEC - 1), word = VEC == 8 ? e >> 1 : e;
+        const uint32_t u = word == 0 ? x : word == 1 ? y : word == 2 ? z : w;
+        const float f = __uint_as_float(VEC == 4 ? u : (e & 1) ? u & 0xffff0000u : u << 16);
+        const uint64_t key = make_key(f, v0 + e);
+        const uint32_t in = __ballot_sync(FULL, lane < VEC && f > -INFINITY && key >= bound);
+        if (!in) continue;
+        if (count + VEC > CAP) {
+            count = cut(list, count, keep, tmp);
+            if (count == keep) {
+                bound = list[keep - 1];
+                if (lane == 0) atomicMax(s_bound, static_cast<unsigned long long>(bound));
+            }
+        }
+        // (a key that the bound has passed meanwhile does no harm)
+        if ((in >> lane) & 1u) list[count + __popc(in & ((1u << lane) - 1u))] = key;
+        count += __popc(in);
+    }
+    __syncwarp();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_constant__ BeamArgs A) {
     constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
-    __shared__ uint64_t list[CAP];
-    __shared__ uint64_t tmp[BEAM_MAX_K];
-    __shared__ uint64_t tops[NT];
-    __shared__ int s_count, s_bad;
-    __shared__ float s_m[NT / 32];
-    __shared__ double s_s[NT / 32];
+    __shared__ uint64_t lists[NW][CAP];
+    __shared__ uint64_t tmps[NW][BEAM_MAX_K];  // (also the threads' maxima, at first)
+    __shared__ unsigned long long s_bound;
+    __shared__ int s_bad, s_n[NW];
+    __shared__ float s_m[NW];
+    __shared__ float s_s[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / A.parts, part = blockIdx.x - row * A.parts;
     const int b = row / A.W;
@@ -159,40 +171,49 @@ __global__ void __launch_bounds__(NT) beam_part_impl(const __grid_constant__ Bea
         // a dead beam, or a sequence that the join flags: its logits are not read
         if (tid == 0) {
             A.part_max[slot] = -INFINITY;
-            A.part_sum[slot] = 0.0;
+            A.part_sum[slot] = 0.f;
             A.part_flag[slot] = 0;
         }
         for (int i = tid; i < A.KL; i += NT) cv[i] = -1;
         return;
     }
-    // k in two floats: a row's sum is corrected for the rounding of k (below)
-    const double kd = 1.4426950408889634 / static_cast<double>(temp);
-    const float k = static_cast<float>(kd), dk = static_cast<float>(kd - static_cast<double>(k));
+    // log2(e) / T in two floats, k + dk: a row's sum is corrected for the
+    // rounding of k (below).  log2(e) = LOG2E + LOG2E_LO.
+    constexpr float LOG2E_LO = 1.9259629911266175e-8f;
+    const float k = LOG2E / temp, dk = (fmaf(-k, temp, LOG2E) + LOG2E_LO) / temp;
     const unsigned char *base = static_cast<const unsigned char *>(A.logits) + static_cast<size_t>(row) * A.V * ES;
     const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base) & 15u);
     const int j0 = part * (A.part_elems / VEC);
     const int j1 = min((A.V + VEC - 1) / VEC, j0 + A.part_elems / VEC);
-    if (tid == 0) s_count = s_bad = 0;
+    const int whole = min(A.V / VEC, j1);  // vectors without a tail
+    if (tid == 0) s_bad = 0;
 
     // sums of e_i = 2^(z_i k - mk) and of e_i z_i, where mk = m k rounded
     float m = -INFINITY, mk = 0.f, s = 0.f, s1 = 0.f;
     const uint64_t K2 = f2pack(k, k);
-    uint64_t bound = static_cast<uint64_t>(order_bits(-INFINITY)) << 32;
+    uint64_t bound = 0;
     int count = 0;
-    for (int j = j0; j < j1; j += NT * UN) {
-        uint4 raw[UN];
-        int at[UN];
-        float top = -INFINITY;
+    // vectors j, j + NT, ..: the next four are on their way while four are worked on
+    auto fetch = [&](int j, uint4 (&raw)[UN]) {
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            at[u] = j + u * NT + tid;
-            raw[u] = at[u] < j1 ? row_vec<T>(base, sh, at[u], A.V) : minus_inf_vec<T>();
+            const int at = j + u * NT + tid;
+            raw[u] = at < whole ? row_vec<T>(base, sh, at) : at < j1 ? row_tail<T>(base, at, A.V) : minus_inf_vec<T>();
         }
+    };
+    uint4 ahead[UN];
+    fetch(j0, ahead);
+    for (int j = j0; j < j1; j += NT * UN) {
+        uint4 raw[UN];
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) raw[u] = ahead[u];
+        if (j + NT * UN < j1) fetch(j + NT * UN, ahead);
 #pragma unroll
         for (int u = 0; u < UN; ++u) top = max_nan(top, Store<T>::vmax(raw[u]));
         if (!(top <= m)) {  // a new maximum of this thread, or NaN
             if (!(top < INFINITY)) {
-                s_bad = 1;  // the join flags the sequence; nothing of this thread counts
+                s_bad = 1;  // the join flags the sequence; nothing of this round counts
 #pragma unroll
                 for (int u = 0; u < UN; ++u) raw[u] = minus_inf_vec<T>();
                 top = -INFINITY;
@@ -233,42 +254,68 @@ __global__ void __launch_bounds__(NT) beam_part_impl(const __grid_constant__ Bea
         }
         if (j == j0) {
             // the KL-th largest of the threads' maxima: KL logits are at least as large
+            uint64_t *tops = &tmps[0][0];
             const uint64_t mine = (static_cast<uint64_t>(order_bits(top)) << 32) | static_cast<uint32_t>(tid);
             tops[tid] = mine;
             __syncthreads();
             int rank = 0;
+#pragma unroll 8
             for (int i = 0; i < NT; ++i) rank += tops[i] > mine;
-            if (rank == A.KL - 1) tmp[0] = static_cast<uint64_t>(order_bits(top)) << 32;
-            __syncthreads();
-            bound = tmp[0];
-        }
-        // offer this round's logits; cut the list and do the round again when it overflows
-        for (int dup = 0;;) {
-            offer<T>(raw, at, bound, list, &s_count, dup);
-            __syncthreads();
-            count = s_count;
-            __syncthreads();
-            if (count <= CAP) break;
-            dup = cut(list, CAP, A.KL, tmp);
-            bound = list[dup - 1];
-            if (tid == 0) s_count = dup;
+            if (rank == A.KL - 1) s_bound = static_cast<uint64_t>(order_bits(top)) << 32;
             __syncthreads();
         }
+        // (a bound that is read late is a lower bound all the same)
+        bound = max(bound, static_cast<uint64_t>(*static_cast<volatile unsigned long long *>(&s_bound)));
+        bound = __shfl_sync(FULL, bound, 0);
+        const float zb = order_float(static_cast<uint32_t>(bound >> 32));
+        if (__any_sync(FULL, top >= zb)) {
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const uint32_t lanes = __ballot_sync(FULL, Store<T>::vmax(raw[u]) >= zb);
+                if (lanes) offer<T>(raw[u], j + u * NT + tid, lanes, lists[warp], count, bound, A.KL, tmps[warp], &s_bound);
+            }
+        }
     }
-    __syncthreads();
-    const int n = cut(list, count, A.KL, tmp);
-    for (int i = tid; i < A.KL; i += NT) {
-        cz[i] = i < n ? order_float(static_cast<uint32_t>(list[i] >> 32)) : -INFINITY;
-        cv[i] = i < n ? static_cast<int>(~static_cast<uint32_t>(list[i])) : -1;
-    }
+    count = cut(lists[warp], count, A.KL, tmps[warp]);
+    if (lane == 0) s_n[warp] = count;
     float top = warp_allmax(m);
     if (lane == 0) s_m[warp] = top;
     __syncthreads();
+    // the warps' lists, each sorted, to one: the rank of a key is its place in
+    // its own list plus the larger ones of the others
+    for (int i = tid; i < NW * A.KL; i += NT) {
+        const int w = i / A.KL, e = i - w * A.KL;
+        if (e >= s_n[w]) continue;
+        const uint64_t key = lists[w][e];
+        int rank = e;
+#pragma unroll
+        for (int o = 0; o < NW; ++o) {
+            if (o == w) continue;
+            int lo = 0, hi = s_n[o];  // first place whose key is smaller
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (lists[o][mid] > key)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            rank += lo;
+            if (rank >= A.KL) break;
+        }
+        if (rank < A.KL) {
+            cz[rank] = order_float(static_cast<uint32_t>(key >> 32));
+            cv[rank] = static_cast<int>(~static_cast<uint32_t>(key));
+        }
+    }
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) total += s_n[w];
+    for (int i = total + tid; i < A.KL; i += NT) cv[i] = -1;
     top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, s_m[w]);
-    // 2^((z_i - m) kd) = e_i 2^(z_i dk + mk - m kd), and the second factor is
-    // 1 + (z_i dk + mk - m kd) ln 2 to within its square (1e-12)
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w]);
+    // 2^((z_i - m) (k + dk)) = e_i 2^(z_i dk + mk - m (k + dk)), and the second
+    // factor is 1 + (z_i dk + mk - m (k + dk)) ln 2 to within its square (1e-12)
     float sum = 0.f;
     if (m > -INFINITY) {
         const float off = -fmaf(m, k, -mk) - m * dk;
@@ -278,8 +325,8 @@ __global__ void __launch_bounds__(NT) beam_part_impl(const __grid_constant__ Bea
     if (lane == 0) s_s[warp] = sum;
     __syncthreads();
     if (tid == 0) {
-        double t = 0.0;
-        for (int w = 0; w < NT / 32; ++w) t += s_s[w];
+        float t = 0.f;
+        for (int w = 0; w < NW; ++w) t += s_s[w];
         A.part_max[slot] = top;
         A.part_sum[slot] = t;
         A.part_flag[slot] = s_bad;
@@ -294,39 +341,59 @@ __device__ __forceinline__ long long order_double(double x) {
 
 // One CTA per sequence: thread i holds the head of sorted list i = (beam,
 // part); each round takes the best head (equal scores: the smaller list, and
-// so the smaller beam and index) and moves its list on.
+// so the smaller beam and index) and moves its list on.  The lists come to
+// shared memory first, all at once: a round is short, a load is not.
 __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ BeamArgs A) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float s_max[BEAM_MAX_W];
     __shared__ double s_off[BEAM_MAX_W];  // scores[w] - ln sum
     __shared__ int s_flag;
-    __shared__ long long s_key[2][NT / 32];
-    __shared__ int s_who[2][NT / 32];
+    __shared__ long long s_key[2][NW];
+    __shared__ int s_who[2][NW];
+    __shared__ float s_z[SMEM_CAND];
+    __shared__ int s_v[SMEM_CAND];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
     const int lists = A.W * A.parts;
     const float temp = __ldg(A.temp + b);
     const bool bad_temp = !(temp > 0.f) || temp == INFINITY;
     if (tid == 0) s_flag = bad_temp ? F_BAD_TEMP : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const size_t cand0 = static_cast<size_t>(b) * lists * A.KL;
+    const int n = lists * A.KL;
+    const bool shared = n <= SMEM_CAND;
+    if (shared) {
+#pragma unroll 4
+        for (int i = tid; i < n; i += NT) {
+            s_z[i] = A.cand_z[cand0 + i];
+            s_v[i] = A.cand_v[cand0 + i];
+        }
+    }
     __syncthreads();
-    if (tid < A.W) {
-        const int row = b * A.W + tid;
+    for (int w = warp; w < A.W; w += NW) {  // a warp per beam, a lane per part
+        const int row = b * A.W + w;
         const float score = __ldg(A.scores + row);
         const size_t p0 = static_cast<size_t>(row) * A.parts;
+        const float k = LOG2E / temp;
         float top = -INFINITY;
         int bad = 0;
-        for (int p = 0; p < A.parts; ++p) {
+        for (int p = lane; p < A.parts; p += 32) {
             top = fmaxf(top, A.part_max[p0 + p]);
             bad |= A.part_flag[p0 + p];
         }
-        const float k = LOG2E / temp;
-        double sum = 0.0;
-        for (int p = 0; p < A.parts; ++p)
-            if (A.part_max[p0 + p] > -INFINITY) sum += A.part_sum[p0 + p] * ex2((A.part_max[p0 + p] - top) * k);
-        s_max[tid] = top;
-        // a dead beam has no candidates; a live one with no finite logit is an error
-        const bool dead = score == -INFINITY;
-        s_off[tid] = dead || top == -INFINITY ? 0.0 : static_cast<double>(score) - log(sum);
-        if (!bad_temp && (bad || !(score < INFINITY) || (!dead && top == -INFINITY))) atomicOr(&s_flag, F_NONFINITE);
+        top = warp_allmax(top);
+        bad = __reduce_or_sync(FULL, bad);
+        float sum = 0.f;
+        for (int p = lane; p < A.parts; p += 32) {
+            const float m = A.part_max[p0 + p];
+            if (m > -INFINITY) sum += A.part_sum[p0 + p] * ex2((m - top) * k);
+        }
+        sum = warp_allsum(sum);
+        if (lane == 0) {
+            // a dead beam has no candidates; a live one with no finite logit is an error
+            const bool dead = score == -INFINITY;
+            s_max[w] = top;
+            s_off[w] = dead || top == -INFINITY ? 0.0 : static_cast<double>(score) - log(static_cast<double>(sum));
+            if (!bad_temp && (bad || !(score < INFINITY) || (!dead && top == -INFINITY))) atomicOr(&s_flag, F_NONFINITE);
+        }
     }
     __syncthreads();
     const int flag = s_flag;
@@ -343,16 +410,16 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
     constexpr long long NONE = -0x7fffffffffffffffll - 1;
     const double inv_t = 1.0 / static_cast<double>(temp);
     const int w = tid / A.parts;
-    const size_t at = (static_cast<size_t>(b) * lists + tid) * A.KL;
     int pos = 0, v = -1;
     double x = 0.0;
     long long key = NONE;
     auto load = [&]() {
         key = NONE;
         if (tid >= lists || pos >= A.KL) return;
-        v = A.cand_v[at + pos];
+        const int at = tid * A.KL + pos;
+        v = shared ? s_v[at] : A.cand_v[cand0 + at];
         if (v < 0) return;
-        x = s_off[w] + static_cast<double>(A.cand_z[at + pos] - s_max[w]) * inv_t;
+        x = s_off[w] + static_cast<double>((shared ? s_z[at] : A.cand_z[cand0 + at]) - s_max[w]) * inv_t;
         key = order_double(x);
     };
     load();
@@ -376,7 +443,7 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
         top = NONE;
         who = -1;
 #pragma unroll
-        for (int u = 0; u < NT / 32; ++u)
+        for (int u = 0; u < NW; ++u)
             if (s_key[i & 1][u] > top) {
                 top = s_key[i & 1][u];
                 who = s_who[i & 1][u];

@@ -72,7 +72,7 @@ struct BeamArgs {
     int parts;            // parts each row is cut into
     int part_elems;       // elements of one part (a multiple of the 16-byte vector)
     float *part_max;      // [B * W, parts] maximum of z
-    double *part_sum;     // [B * W, parts] sum of 2^((z - max) k)
+    float *part_sum;      // [B * W, parts] sum of 2^((z - max) k)
     int *part_flag;       // [B * W, parts]
     float *cand_z;        // [B * W, parts, KL] candidates, best first
     int *cand_v;          // their vocabulary indices (-1: none)
@@ -81,7 +81,7 @@ struct BeamArgs {
     int32_t *flags;             // [B] or null
 };
 
-constexpr int BEAM_THREADS = 256;
+constexpr int BEAM_THREADS = 256, BEAM_PER_SM = 4;
 const void *beam_part_func(int dtype);
 const void *beam_join_func();
 

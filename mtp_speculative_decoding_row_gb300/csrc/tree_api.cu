@@ -294,7 +294,7 @@ namespace {
 struct BeamPlan {
     int KL = 0, parts = 0, part_elems = 0;
     size_t n = 0;  // parts of all rows
-    size_t bytes() const { return n * (8 + 8 + static_cast<size_t>(KL) * 8); }
+    size_t bytes() const { return n * (12 + static_cast<size_t>(KL) * 8); }
 };
 
 int beam_sizes(int dtype, int B, int W, int V, int K) {
@@ -311,14 +311,30 @@ int beam_plan(int dtype, int B, int W, int V, int K, BeamPlan &p) {
     const int vec = dtype == MTP_DTYPE_F32 ? 4 : 8;
     const int per_sm = resident(dev, beam_part_func(dtype), 0, BEAM_THREADS);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
-    // as many parts as fill the GPU once, of at least one round of a CTA
-    // each; the join holds one list per thread
-    const long long rows = static_cast<long long>(B) * W;
-    long long parts = (static_cast<long long>(sms) * per_sm + rows - 1) / (rows > 0 ? rows : 1);
-    const long long vecs = (V + vec - 1) / vec, round = BEAM_THREADS * 4;
-    if (parts > (vecs + round - 1) / round) parts = (vecs + round - 1) / round;
-    if (parts > BEAM_THREADS / W) parts = BEAM_THREADS / W;
-    if (parts < 1) parts = 1;
+    // Parts of at least one round of a CTA each, and no more lists than the
+    // join has threads.  Few rows: as many parts as fill the GPU once.  Many:
+    // the number of parts (up to 8) that leaves the least of the last wave
+    // idle; a part costs about half a round beside its rounds.
+    const long long rows = static_cast<long long>(B > 0 ? B : 1) * W;
+    const long long vecs = (V + vec - 1) / vec, round = BEAM_THREADS * 4, slots = static_cast<long long>(sms) * per_sm;
+    long long most = (vecs + round - 1) / round;
+    if (most > BEAM_THREADS / W) most = BEAM_THREADS / W;
+    if (most < 1) most = 1;
+    long long parts = slots / rows;
+    if (parts < 8) {
+        double best = 0.0;
+        long long pick = 1;
+        for (long long c = 1; c <= 8 && c <= most; ++c) {
+            const long long waves = (rows * c + slots - 1) / slots;
+            const double cost = static_cast<double>(waves) * (static_cast<double>(vecs) / (c * round) + 0.5);
+            if (c == 1 || cost < best) {
+                best = cost;
+                pick = c;
+            }
+        }
+        parts = pick;
+    }
+    if (parts > most) parts = most;
     const long long each = (vecs + parts - 1) / parts;
     p.parts = static_cast<int>((vecs + each - 1) / each);
     p.part_elems = static_cast<int>(each * vec);
@@ -360,11 +376,11 @@ extern "C" int mtp_beam_select(const void *logits, mtp_dtype dtype, const float 
     A.parts = p.parts;
     A.part_elems = p.part_elems;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    A.part_sum = reinterpret_cast<double *>(ws);
-    A.part_max = reinterpret_cast<float *>(ws + p.n * 8);
-    A.part_flag = reinterpret_cast<int *>(ws + p.n * 12);
-    A.cand_z = reinterpret_cast<float *>(ws + p.n * 16);
-    A.cand_v = reinterpret_cast<int *>(ws + p.n * 16 + p.n * p.KL * 4);
+    A.part_sum = reinterpret_cast<float *>(ws);
+    A.part_max = reinterpret_cast<float *>(ws + p.n * 4);
+    A.part_flag = reinterpret_cast<int *>(ws + p.n * 8);
+    A.cand_z = reinterpret_cast<float *>(ws + p.n * 12);
+    A.cand_v = reinterpret_cast<int *>(ws + p.n * 12 + p.n * p.KL * 4);
     A.tokens = tokens;
     A.parents = parents;
     A.best = out_scores;
