@@ -34,7 +34,7 @@ constexpr int NT = BEAM_THREADS;
 constexpr int UN = 4;        // vectors of a thread per round
 constexpr int NW = NT / 32;
 constexpr int CAP = 192;     // candidates held by a warp
-constexpr int SMEM_CAND = 4096;  // candidates that the join holds in shared memory
+constexpr int SMEM_CAND = 2048;  // candidates that the join holds in shared memory
 
 // Order-preserving bits of a float (the two zeros are equal).
 __device__ __forceinline__ uint32_t order_bits(float z) {
@@ -254,14 +254,32 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         }
         if (j == j0) {
             // the KL-th largest of the threads' maxima: KL logits are at least as large
-            uint64_t *tops = &tmps[0][0];
-            const uint64_t mine = (static_cast<uint64_t>(order_bits(top)) << 32) | static_cast<uint32_t>(tid);
-            tops[tid] = mine;
+            // (each warp sorts its own; a value's rank is its lane plus the
+            // larger ones of the other warps, equal ones of lower warps too)
+            uint32_t(*tops)[32] = reinterpret_cast<uint32_t(*)[32]>(tmps);
+            uint32_t mine = order_bits(top);
+#pragma unroll
+            for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+                for (int d = size >> 1; d > 0; d >>= 1) {
+                    const uint32_t o = __shfl_xor_sync(FULL, mine, d);
+                    const bool falling = (lane & size) == 0, low = (lane & d) == 0;
+                    mine = falling == low ? max(mine, o) : min(mine, o);
+                }
+            tops[warp][lane] = mine;
             __syncthreads();
-            int rank = 0;
-#pragma unroll 8
-            for (int i = 0; i < NT; ++i) rank += tops[i] > mine;
-            if (rank == A.KL - 1) s_bound = static_cast<uint64_t>(order_bits(top)) << 32;
+            int rank = lane;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                if (w == warp) continue;
+                const uint32_t limit = w < warp ? mine : mine + 1;  // count values >= limit
+                int lo = 0;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    if (tops[w][lo + d - 1] >= limit) lo += d;
+                rank += lo + (lo == 31 && tops[w][31] >= limit ? 1 : 0);
+            }
+            if (rank == A.KL - 1) s_bound = static_cast<uint64_t>(mine) << 32;
             __syncthreads();
         }
         // (a bound that is read late is a lower bound all the same)
@@ -339,60 +357,60 @@ __device__ __forceinline__ long long order_double(double x) {
     return u < 0 ? u ^ 0x7fffffffffffffffll : u;
 }
 
-// One CTA per sequence: thread i holds the head of sorted list i = (beam,
-// part); each round takes the best head (equal scores: the smaller list, and
-// so the smaller beam and index) and moves its list on.  The lists come to
-// shared memory first, all at once: a round is short, a load is not.
+// One CTA per sequence.  All threads turn the lists' candidates into scores;
+// then one warp merges the sorted lists (beam after beam, part after part),
+// eight of them to a lane: each round takes the best head -- equal scores: the
+// smaller list, and so the smaller beam and index -- and moves its list on.
+// A round is a few warp-wide reductions, with no barrier and no load from
+// global memory.
 __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ BeamArgs A) {
+    constexpr long long NONE = -0x7fffffffffffffffll - 1;
+    constexpr int PER = NT / 32;  // lists of a lane
     __shared__ float s_max[BEAM_MAX_W];
     __shared__ double s_off[BEAM_MAX_W];  // scores[w] - ln sum
     __shared__ int s_flag;
-    __shared__ long long s_key[2][NW];
-    __shared__ int s_who[2][NW];
-    __shared__ float s_z[SMEM_CAND];
+    __shared__ long long s_key[SMEM_CAND];
     __shared__ int s_v[SMEM_CAND];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
     const int lists = A.W * A.parts;
     const float temp = __ldg(A.temp + b);
     const bool bad_temp = !(temp > 0.f) || temp == INFINITY;
+    const double inv_t = 1.0 / static_cast<double>(temp);
     if (tid == 0) s_flag = bad_temp ? F_BAD_TEMP : 0;
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t cand0 = static_cast<size_t>(b) * lists * A.KL;
     const int n = lists * A.KL;
     const bool shared = n <= SMEM_CAND;
-    if (shared) {
-#pragma unroll 4
-        for (int i = tid; i < n; i += NT) {
-            s_z[i] = A.cand_z[cand0 + i];
-            s_v[i] = A.cand_v[cand0 + i];
-        }
+    float z0 = 0.f;  // the first candidate of this thread is on its way during the statistics
+    int v0 = -1;
+    if (shared && tid < n) {
+        z0 = A.cand_z[cand0 + tid];
+        v0 = A.cand_v[cand0 + tid];
     }
-    __syncthreads();
     for (int w = warp; w < A.W; w += NW) {  // a warp per beam, a lane per part
         const int row = b * A.W + w;
         const float score = __ldg(A.scores + row);
         const size_t p0 = static_cast<size_t>(row) * A.parts;
         const float k = LOG2E / temp;
-        float top = -INFINITY;
+        float top = -INFINITY, sum = 0.f;
         int bad = 0;
         for (int p = lane; p < A.parts; p += 32) {
-            top = fmaxf(top, A.part_max[p0 + p]);
+            const float m = A.part_max[p0 + p], s = A.part_sum[p0 + p];
             bad |= A.part_flag[p0 + p];
+            const float up = fmaxf(top, m);
+            if (up > -INFINITY) sum = sum * ex2((top - up) * k) + s * ex2((m - up) * k);
+            top = up;
         }
-        top = warp_allmax(top);
+        const float all = warp_allmax(top);
+        sum = warp_allsum(top > -INFINITY ? sum * ex2((top - all) * k) : 0.f);
         bad = __reduce_or_sync(FULL, bad);
-        float sum = 0.f;
-        for (int p = lane; p < A.parts; p += 32) {
-            const float m = A.part_max[p0 + p];
-            if (m > -INFINITY) sum += A.part_sum[p0 + p] * ex2((m - top) * k);
-        }
-        sum = warp_allsum(sum);
         if (lane == 0) {
             // a dead beam has no candidates; a live one with no finite logit is an error
             const bool dead = score == -INFINITY;
-            s_max[w] = top;
-            s_off[w] = dead || top == -INFINITY ? 0.0 : static_cast<double>(score) - log(static_cast<double>(sum));
-            if (!bad_temp && (bad || !(score < INFINITY) || (!dead && top == -INFINITY))) atomicOr(&s_flag, F_NONFINITE);
+            s_max[w] = all;
+            s_off[w] = dead || all == -INFINITY ? 0.0 : static_cast<double>(score) - log(static_cast<double>(sum));
+            if (!bad_temp && (bad || !(score < INFINITY) || (!dead && all == -INFINITY))) atomicOr(&s_flag, F_NONFINITE);
         }
     }
     __syncthreads();
@@ -407,58 +425,68 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
         }
         return;
     }
-    constexpr long long NONE = -0x7fffffffffffffffll - 1;
-    const double inv_t = 1.0 / static_cast<double>(temp);
-    const int w = tid / A.parts;
-    int pos = 0, v = -1;
-    double x = 0.0;
-    long long key = NONE;
-    auto load = [&]() {
-        key = NONE;
-        if (tid >= lists || pos >= A.KL) return;
-        const int at = tid * A.KL + pos;
-        v = shared ? s_v[at] : A.cand_v[cand0 + at];
-        if (v < 0) return;
-        x = s_off[w] + static_cast<double>((shared ? s_z[at] : A.cand_z[cand0 + at]) - s_max[w]) * inv_t;
-        key = order_double(x);
+    const int beam_cand = A.parts * A.KL;
+    auto key_of = [&](int i, float z, int v) {
+        const int w = i / beam_cand;
+        return v < 0 ? NONE : order_double(s_off[w] + static_cast<double>(z - s_max[w]) * inv_t);
     };
-    load();
-    for (int i = 0; i < A.K; ++i) {
-        long long top = key;
-        int who = tid;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_down_sync(FULL, top, d);
-            const int ow = __shfl_down_sync(FULL, who, d);
-            if (lane + d < 32 && o > top) {  // the lower lane keeps a tie
-                top = o;
-                who = ow;
+    if (shared) {
+        for (int i = tid; i < n; i += NT) {
+            if (i != tid) {
+                z0 = A.cand_z[cand0 + i];
+                v0 = A.cand_v[cand0 + i];
             }
-        }
-        if (lane == 0) {
-            s_key[i & 1][warp] = top;
-            s_who[i & 1][warp] = who;
+            s_key[i] = key_of(i, z0, v0);
+            s_v[i] = v0;
         }
         __syncthreads();
-        top = NONE;
-        who = -1;
+    }
+    if (warp != 0) return;
+    long long head[PER];
+    int pos[PER];
+    auto load = [&](int list, int at) {
+        if (list >= lists || at >= A.KL) return NONE;
+        const int i = list * A.KL + at;
+        return shared ? s_key[i] : key_of(i, A.cand_z[cand0 + i], A.cand_v[cand0 + i]);
+    };
 #pragma unroll
-        for (int u = 0; u < NW; ++u)
-            if (s_key[i & 1][u] > top) {
-                top = s_key[i & 1][u];
-                who = s_who[i & 1][u];
+    for (int q = 0; q < PER; ++q) {
+        head[q] = load(lane * PER + q, 0);
+        pos[q] = 0;
+    }
+    for (int i = 0; i < A.K; ++i) {
+        long long mine = head[0];
+        int q0 = 0;
+#pragma unroll
+        for (int q = 1; q < PER; ++q)
+            if (head[q] > mine) {
+                mine = head[q];
+                q0 = q;
             }
-        if (who == tid) {
-            tokens[i] = v;
-            parents[i] = w;
-            best[i] = static_cast<float>(x);
-            ++pos;
-            load();
-        }
-        if (who < 0 && tid == 0) {  // fewer candidates than K: the rest is empty
+        const uint64_t u = static_cast<uint64_t>(mine) ^ 0x8000000000000000ull;
+        const uint32_t hi = static_cast<uint32_t>(u >> 32), lo = static_cast<uint32_t>(u);
+        const uint32_t top = __reduce_max_sync(FULL, hi);
+        const uint32_t low = __reduce_max_sync(FULL, hi == top ? lo : 0u);
+        const int who = __ffs(__ballot_sync(FULL, hi == top && lo == low)) - 1;
+        if (lane != who) continue;
+        if (mine == NONE) {  // fewer candidates than K: the rest is empty
             tokens[i] = parents[i] = -1;
             best[i] = -INFINITY;
+            continue;
         }
+        const int list = lane * PER + q0;
+        int at = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (q == q0) at = pos[q]++;
+        const int c = list * A.KL + at;
+        tokens[i] = shared ? s_v[c] : A.cand_v[cand0 + c];
+        parents[i] = list / A.parts;
+        best[i] = static_cast<float>(__longlong_as_double(mine < 0 ? mine ^ 0x7fffffffffffffffll : mine));
+        const long long next = load(list, at + 1);
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (q == q0) head[q] = next;
     }
 }
 

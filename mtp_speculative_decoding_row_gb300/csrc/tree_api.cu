@@ -314,7 +314,7 @@ int beam_plan(int dtype, int B, int W, int V, int K, BeamPlan &p) {
     // Parts of at least one round of a CTA each, and no more lists than the
     // join has threads.  Few rows: as many parts as fill the GPU once.  Many:
     // the number of parts (up to 8) that leaves the least of the last wave
-    // idle; a part costs about half a round beside its rounds.
+    // idle; a part costs about three and a half rounds beside its own.
     const long long rows = static_cast<long long>(B > 0 ? B : 1) * W;
     const long long vecs = (V + vec - 1) / vec, round = BEAM_THREADS * 4, slots = static_cast<long long>(sms) * per_sm;
     long long most = (vecs + round - 1) / round;
@@ -326,7 +326,7 @@ int beam_plan(int dtype, int B, int W, int V, int K, BeamPlan &p) {
         long long pick = 1;
         for (long long c = 1; c <= 8 && c <= most; ++c) {
             const long long waves = (rows * c + slots - 1) / slots;
-            const double cost = static_cast<double>(waves) * (static_cast<double>(vecs) / (c * round) + 0.5);
+            const double cost = static_cast<double>(waves) * (static_cast<double>(vecs) / (c * round) + 3.5);
             if (c == 1 || cost < best) {
                 best = cost;
                 pick = c;
