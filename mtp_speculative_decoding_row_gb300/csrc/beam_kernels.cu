@@ -11,13 +11,13 @@
 //
 // Candidates are 64-bit keys: the logit's bits in an order-preserving form,
 // then the complement of the index, so one integer comparison orders by value
-// and then by smaller index.  The K-th largest of the threads' maxima over
-// their first 4 vectors bounds the K-th best from below; the rest is compared
-// with that bound 4 vectors at a time, and few pass.  Each warp keeps a list
-// of its own, so nothing waits for another warp while the row streams by; a
-// list that is full is cut to its K best, and the bound rises for all warps.
-// What bounds the kernel is the row's bytes: the exponentials take about half
-// of the time of the loads.
+// and then by smaller index.  The K-th largest of the threads' running maxima
+// bounds the K-th best from below; vectors are compared with that bound four
+// at a time, and few pass.  The bound is taken again whenever twice as much of
+// the row has been seen, so that about K pass in between; a candidate costs as
+// much as 500 elements of the sums (with the first bound alone the kernel took
+// 81 us at 512 rows of 151936).  Each warp keeps a list of its own; one that
+// is full is cut to its K best, and the bound rises for all warps.
 //
 // Rows may start on any element.  A vector is always elements [8 j, 8 j + 8)
 // (4 j of float32) of the row, put together from two aligned loads where the
@@ -119,10 +119,11 @@ __device__ __forceinline__ int cut(uint64_t *list, int n, int keep, uint64_t *tm
 }
 
 // Offer vector `raw` (elements at VEC ..) of every lane in `lanes` to the
-// warp's list: eight lanes (four of float32) look at one element each.
+// warp's list of `count`: eight lanes (four of float32) look at one element
+// each.  Returns the list's new length; a cut raises *s_bound.
 template <typename T>
-__device__ __noinline__ void offer(const uint4 raw, int at, uint32_t lanes, uint64_t *list, int &count, uint64_t &bound, int keep,
-                                   uint64_t *tmp, unsigned long long *s_bound) {
+__device__ __noinline__ int offer(const uint4 raw, int at, uint32_t lanes, uint64_t *list, int count, uint64_t bound, int keep,
+                                  uint64_t *tmp, unsigned long long *s_bound) {
     constexpr int VEC = Store<T>::VEC;
     const int lane = threadIdx.x & 31;
     while (lanes) {
@@ -138,24 +139,55 @@ __device__ __noinline__ void offer(const uint4 raw, int at, uint32_t lanes, uint
         const uint32_t in = __ballot_sync(FULL, lane < VEC && f > -INFINITY && key >= bound);
         if (!in) continue;
         if (count + VEC > CAP) {
-            count = cut(list, count, keep, tmp);
-            if (count == keep) {
-                bound = list[keep - 1];
-                if (lane == 0) atomicMax(s_bound, static_cast<unsigned long long>(bound));
-            }
+            count = cut(list, count, keep, tmp);  // CAP - VEC >= keep: the list has `keep` keys
+            bound = max(bound, list[keep - 1]);
+            if (lane == 0) atomicMax(s_bound, static_cast<unsigned long long>(bound));
         }
         // (a key that the bound has passed meanwhile does no harm)
         if ((in >> lane) & 1u) list[count + __popc(in & ((1u << lane) - 1u))] = key;
         count += __popc(in);
     }
     __syncwarp();
+    return count;
+}
+
+// The keep-th largest of the block's values, as order-preserving bits, raises
+// *s_bound: each warp sorts its own, and a value's rank is its lane plus the
+// larger ones of the other warps (of equal ones those of lower warps).
+__device__ __noinline__ void raise_bound(float value, int keep, uint32_t (*tops)[32], unsigned long long *s_bound) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t mine = order_bits(value);
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int d = size >> 1; d > 0; d >>= 1) {
+            const uint32_t o = __shfl_xor_sync(FULL, mine, d);
+            const bool falling = (lane & size) == 0, low = (lane & d) == 0;
+            mine = falling == low ? max(mine, o) : min(mine, o);
+        }
+    tops[warp][lane] = mine;
+    __syncthreads();
+    int rank = lane;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w == warp) continue;
+        const uint32_t limit = w < warp ? mine : mine + 1;  // count values >= limit
+        int lo = 0;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            if (tops[w][lo + d - 1] >= limit) lo += d;
+        rank += lo + (lo == 31 && tops[w][31] >= limit ? 1 : 0);
+    }
+    if (rank == keep - 1) atomicMax(s_bound, static_cast<unsigned long long>(mine) << 32);
+    __syncthreads();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_constant__ BeamArgs A) {
     constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
     __shared__ uint64_t lists[NW][CAP];
-    __shared__ uint64_t tmps[NW][BEAM_MAX_K];  // (also the threads' maxima, at first)
+    __shared__ uint64_t tmps[NW][BEAM_MAX_K];
+    __shared__ uint32_t tops[NW][32];
     __shared__ unsigned long long s_bound;
     __shared__ int s_bad, s_n[NW];
     __shared__ float s_m[NW];
@@ -186,13 +218,15 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     const int j0 = part * (A.part_elems / VEC);
     const int j1 = min((A.V + VEC - 1) / VEC, j0 + A.part_elems / VEC);
     const int whole = min(A.V / VEC, j1);  // vectors without a tail
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) {
+        s_bad = 0;
+        s_bound = 0;
+    }
 
     // sums of e_i = 2^(z_i k - mk) and of e_i z_i, where mk = m k rounded
     float m = -INFINITY, mk = 0.f, s = 0.f, s1 = 0.f;
     const uint64_t K2 = f2pack(k, k);
-    uint64_t bound = 0;
-    int count = 0;
+    int count = 0, again = j0;
     // vectors j, j + NT, ..: the next four are on their way while four are worked on
     auto fetch = [&](int j, uint4 (&raw)[UN]) {
 #pragma unroll
@@ -252,45 +286,20 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
             f2unpack(acc1, a0, a1);
             s1 += a0 + a1;
         }
-        if (j == j0) {
-            // the KL-th largest of the threads' maxima: KL logits are at least as large
-            // (each warp sorts its own; a value's rank is its lane plus the
-            // larger ones of the other warps, equal ones of lower warps too)
-            uint32_t(*tops)[32] = reinterpret_cast<uint32_t(*)[32]>(tmps);
-            uint32_t mine = order_bits(top);
-#pragma unroll
-            for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-                for (int d = size >> 1; d > 0; d >>= 1) {
-                    const uint32_t o = __shfl_xor_sync(FULL, mine, d);
-                    const bool falling = (lane & size) == 0, low = (lane & d) == 0;
-                    mine = falling == low ? max(mine, o) : min(mine, o);
-                }
-            tops[warp][lane] = mine;
-            __syncthreads();
-            int rank = lane;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                if (w == warp) continue;
-                const uint32_t limit = w < warp ? mine : mine + 1;  // count values >= limit
-                int lo = 0;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    if (tops[w][lo + d - 1] >= limit) lo += d;
-                rank += lo + (lo == 31 && tops[w][31] >= limit ? 1 : 0);
-            }
-            if (rank == A.KL - 1) s_bound = static_cast<uint64_t>(mine) << 32;
-            __syncthreads();
+        if (j >= again) {
+            if (j == j0) __syncthreads();  // (s_bound is set)
+            raise_bound(m, A.KL, tops, &s_bound);
+            again = j + (j - j0 + NT * UN);
         }
         // (a bound that is read late is a lower bound all the same)
-        bound = max(bound, static_cast<uint64_t>(*static_cast<volatile unsigned long long *>(&s_bound)));
-        bound = __shfl_sync(FULL, bound, 0);
+        const uint64_t bound = __shfl_sync(FULL, *static_cast<volatile unsigned long long *>(&s_bound), 0);
         const float zb = order_float(static_cast<uint32_t>(bound >> 32));
         if (__any_sync(FULL, top >= zb)) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 const uint32_t lanes = __ballot_sync(FULL, Store<T>::vmax(raw[u]) >= zb);
-                if (lanes) offer<T>(raw[u], j + u * NT + tid, lanes, lists[warp], count, bound, A.KL, tmps[warp], &s_bound);
+                if (lanes)
+                    count = offer<T>(raw[u], j + u * NT + tid, lanes, lists[warp], count, bound, A.KL, tmps[warp], &s_bound);
             }
         }
     }
