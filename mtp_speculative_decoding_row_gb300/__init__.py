@@ -121,6 +121,7 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False):
     lib.mtp_status_string.argtypes = [I]
     lib.mtp_status_string.restype = ctypes.c_char_p
     _lib = lib
+    tree.unbind()
     return lib
 
 

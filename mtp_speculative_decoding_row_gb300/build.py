@@ -10,6 +10,10 @@ is newer than the library.
 (``-DMTP_DEBUG``: the device primitives check their shared-memory, bulk-copy,
 DSMEM and TMEM accesses and print a line starting with ``MTP_DEBUG`` for
 any that fails) in its own object folder; the tests load it explicitly.
+
+``csrc/binding.cpp`` -- the argument marshalling of the tree-draft operators,
+a Python extension against the installed torch's headers -- is compiled by the
+host compiler beside them, to ``_binding.so`` in the package.
 """
 from __future__ import annotations
 
@@ -27,6 +31,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmtprs.so")
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build", "debug")
 DEBUG_LIB = os.path.join(PKG, "libmtprs_debug.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -57,12 +63,54 @@ def is_stale(debug: bool = False) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def _binding_inputs():
+    return [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def binding_is_stale() -> bool:
+    return not os.path.exists(BINDING) or any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in _binding_inputs())
+
+
+def _binding_command(out: str):
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), BINDING_SRC, "-o", out,
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+
+
+def _start_binding():
+    """Start compiling the binding if it is stale: (command, log, process, temporary output) or None."""
+    if not binding_is_stale():
+        return None
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    tmp, log = BINDING + f".tmp{os.getpid()}", os.path.join(BUILD_DIR, "binding.log")
+    cmd = _binding_command(tmp)
+    return cmd, log, subprocess.Popen(cmd, stdout=open(log, "w"), stderr=subprocess.STDOUT), tmp
+
+
+def _finish_binding(job) -> None:
+    if job is None:
+        return
+    cmd, log, p, tmp = job
+    if p.wait() != 0:
+        raise RuntimeError("the binding did not compile:\n" + " ".join(cmd) + "\n" + open(log).read())
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile and link libmtprs.so (debug: libmtprs_debug.so) if needed;
     returns its path."""
     lib = DEBUG_LIB if debug else LIB
     bdir = DEBUG_BUILD_DIR if debug else BUILD_DIR
+    binding = _start_binding()
     if not force and not is_stale(debug):
+        _finish_binding(binding)
         return lib
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -75,6 +123,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         objs.append(obj)
         cmd = [cc, *flags, "-c", src, "-o", obj]
         procs.append((cmd, log, subprocess.Popen(cmd, stdout=open(log, "w"), stderr=subprocess.STDOUT)))
+    _finish_binding(binding)
     failed = []
     for cmd, log, p in procs:
         if p.wait() != 0:

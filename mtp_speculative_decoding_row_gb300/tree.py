@@ -3,13 +3,13 @@
 selection, beam reordering and the commit of an accepted path.
 
 Argument marshalling only, like the package's other entry points.  These calls
-sit between the small launches of a decoding loop, so the checks are kept
-short: each tensor is looked at once, and the two calls with many arguments
-pass them as one packed struct.
+sit between the small launches of a decoding loop, so the checks of their
+tensors and the call of the library are native (``csrc/binding.cpp``); here
+missing outputs are allocated and the stream is chosen.
 """
 from __future__ import annotations
 
-import functools
+import os
 import struct
 from typing import NamedTuple, Optional
 
@@ -17,8 +17,12 @@ import mtp_speculative_decoding_row_gb300 as _m
 
 MAX_NODES, MAX_BEAMS, MAX_SELECT = 64, 64, 64
 
+# the C structs as they lie in memory (for callers of the C ABI through ctypes)
 _ATTN = struct.Struct("@13Pq15q9if")
-_COMMIT = struct.Struct("@15P16q9i4x")  # (as the C structs lie in memory)
+_COMMIT = struct.Struct("@15P16q9i4x")
+
+_NOT_BOUND = -1
+_native = None
 
 
 class TreeAttentionResult(NamedTuple):
@@ -47,37 +51,41 @@ class CommitResult(NamedTuple):
     row_flags: "object"   # [B] int32
 
 
-def _shape(t, name, dtype, shape, index):
-    """The pointer of a contiguous tensor of this dtype and shape on device `index`."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the device of the other tensors")
-    return t.data_ptr()
+def _binding():
+    """The native marshalling module; raises if it was not built."""
+    global _native
+    if _native is None:
+        _m._torch()  # (its libraries come first)
+        if not os.path.exists(_m._build.BINDING):
+            raise ImportError(f"{_m._build.BINDING} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import _binding as native
+
+        _native = native
+    return _native
 
 
-def _strided(t, name, dtype, shape, index):
-    """As _shape, but only the last dimension has to be contiguous: (pointer, strides of the others)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the device of the other tensors")
-    return t.data_ptr(), s[:-1]
+def _bind(lib) -> None:
+    """Tell the marshalling module where the functions of `lib` are."""
+    import ctypes
+
+    names = ("mtp_tree_attention", "mtp_tree_attention_workspace", "mtp_beam_select", "mtp_beam_select_workspace",
+             "mtp_beam_reorder", "mtp_tree_commit")
+    _binding().bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
 
 
-def _dims(t, name, n):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
-    return t.shape
+def unbind() -> None:
+    """Another library was loaded: the next call looks its functions up."""
+    if _native is not None:
+        _native.bind(0, 0, 0, 0, 0, 0)
+
+
+def _call(name, index, args):
+    rc = getattr(_binding(), name)(*args)
+    if rc == _NOT_BOUND:
+        _bind(_m.load_library())
+        rc = getattr(_binding(), name)(*args)
+    if rc:
+        raise _m.MTPError("mtp_" + name, rc)
 
 
 class _on:
@@ -85,10 +93,8 @@ class _on:
 
     __slots__ = ("guard",)
 
-    def __init__(self, torch, index, name):
-        if index < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+    def __init__(self, torch, index):
+        self.guard = None if index < 0 or torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -99,23 +105,28 @@ class _on:
             self.guard.__exit__(*exc)
 
 
-def _launch_stream(torch, dev, stream, *mine):
+def _raw(torch, index, stream, mine=()):
     """The raw stream of a call; tensors allocated for it here are tied to a
     stream that is not the current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
     for t in mine:
-        if t is not None:
+        if t is not None and t.is_cuda:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-@functools.lru_cache(maxsize=1024)
-def _attn_workspace(index, *sizes):
-    n = _m.load_library().mtp_tree_attention_workspace(_ATTN.pack(*([0] * 14), *([0] * 15), *sizes, 1.0))
+def _scratch(torch, like, stream, size, *args):
+    """Workspace for a call on a given stream (None: allocated natively, on
+    the current one)."""
+    if stream is None or not like.is_cuda:
+        return None
+    n = getattr(_m.load_library(), size)(*args)
     if n < 0:
-        raise _m.MTPError("mtp_tree_attention_workspace", _m.MTP_ERR_INVALID_ARG)
-    return n
+        raise _m.MTPError(size, _m.MTP_ERR_INVALID_ARG)
+    ws = torch.empty((n,), dtype=torch.uint8, device=like.device)
+    ws.record_stream(stream)
+    return ws
 
 
 def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len, parents=None, n_nodes=None, *,
@@ -132,66 +143,28 @@ def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
     with_lse, or where `out` has it) and row_flags [B]; rows of nodes >=
     n_nodes are left as they were (undefined in outputs allocated here)."""
     torch = _m._torch()
-    B, T, Hq, D = _dims(q, "q", 4)
-    Hkv = _dims(k_new, "k_new", 4)[2]
-    pages, page_size = _dims(k_cache, "k_cache", 4)[:2]
-    max_pages = _dims(page_table, "page_table", 2)[1]
-    dt, dev = q.dtype, q.device
-    code = _m._dtype_code(q)
-    i32 = torch.int32
-    if Hkv < 1 or Hq % Hkv != 0 or Hq < 1:
-        raise ValueError(f"q has {Hq} heads: not a multiple of the {Hkv} of k_new")
-    if not 1 <= T <= MAX_NODES:
-        raise ValueError(f"trees have 1 to {MAX_NODES} nodes, got {T}")
-    if not 1 <= D <= 256:
-        raise ValueError(f"heads have 1 to 256 elements, got {D}")
-    if scale is None:
-        scale = D ** -0.5
-    elif not 0.0 < scale < 1e30:
-        raise ValueError(f"scale must be positive, got {scale}")
     index = q.get_device()
-    if out is not None:
-        pl = _shape(out.lse, "out.lse", torch.float32, (B, T, Hq), index) if out.lse is not None else 0
-        pf = _shape(out.row_flags, "out.row_flags", i32, (B,), index) if out.row_flags is not None else 0
-        po = _shape(out.out, "out.out", dt, (B, T, Hq, D), index)
-        if with_lse and not pl:
-            raise ValueError("mtp_tree_attention: with_lse needs out.lse")
-    pq, sq = _strided(q, "q", dt, (B, T, Hq, D), index)
-    pk, sk = _strided(k_new, "k_new", dt, (B, T, Hkv, D), index)
-    pv, sv = _strided(v_new, "v_new", dt, (B, T, Hkv, D), index)
-    pkc, skc = _strided(k_cache, "k_cache", dt, (pages, page_size, Hkv, D), index)
-    pvc, svc = _strided(v_cache, "v_cache", dt, (pages, page_size, Hkv, D), index)
-    pt = _shape(page_table, "page_table", i32, (B, max_pages), index)
-    pc = _shape(cache_len, "cache_len", i32, (B,), index)
-    pp = _shape(parents, "parents", i32, (B, T), index) if parents is not None else 0
-    pn = _shape(n_nodes, "n_nodes", i32, (B,), index) if n_nodes is not None else 0
-    with _on(torch, index, "q"):
+    if out is not None and with_lse and out.lse is None:
+        raise ValueError("mtp_tree_attention: with_lse needs out.lse")
+    with _on(torch, index):
         mine = ()
         if out is None:
-            out = TreeAttentionResult(torch.empty((B, T, Hq, D), dtype=dt, device=dev),
-                                      torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if with_lse else None,
-                                      torch.empty((B,), dtype=i32, device=dev))
-            mine = out
-            po, pf = out.out.data_ptr(), out.row_flags.data_ptr()
-            pl = out.lse.data_ptr() if with_lse else 0
-        sizes = (code, B, T, Hq, Hkv, D, pages, page_size, max_pages)
-        nbytes = _attn_workspace(index, *sizes)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
-        raw = _launch_stream(torch, dev, stream, ws, *mine)
-        rc = _m.load_library().mtp_tree_attention(
-            _ATTN.pack(pq, pk, pv, pkc, pvc, pt, pc, pp, pn, po, pl, pf, ws.data_ptr(), nbytes, *sq, *sk, *sv, *skc, *svc, *sizes,
-                       scale), raw)
-    if rc:
-        raise _m.MTPError("mtp_tree_attention", rc)
+            if q.dim() != 4:
+                raise ValueError(f"q must have 4 dimensions, got {tuple(q.shape)}")
+            dev = q.device
+            out = mine = TreeAttentionResult(torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                             torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None,
+                                             torch.empty(q.shape[:1], dtype=torch.int32, device=dev))
+        ws = None
+        if stream is not None and q.dim() == 4 and k_new.dim() == 4 and k_cache.dim() == 4 and page_table.dim() == 2:
+            ws = _scratch(torch, q, stream, "mtp_tree_attention_workspace",
+                          _ATTN.pack(*([0] * 29), _m._dtype_code(q), *q.shape[:3], k_new.shape[2], q.shape[3], *k_cache.shape[:2],
+                                     page_table.shape[1], 1.0))
+        _call("tree_attention", index,
+              (q, k_new, v_new, k_cache, v_cache, page_table, cache_len, parents, n_nodes,
+               q.shape[-1] ** -0.5 if scale is None else scale, out.out, out.lse, out.row_flags, ws,
+               _raw(torch, index, stream, mine)))
     return out
-
-
-@functools.lru_cache(maxsize=1024)
-def _beam_workspace(index, code, B, W, V, K):
-    n = _m.load_library().mtp_beam_select_workspace(code, B, W, V, K)
-    if n < 0:
-        raise _m.MTPError("mtp_beam_select_workspace", _m.MTP_ERR_INVALID_ARG)
-    return n
 
 
 def mtp_beam_select(logits, scores, temperature, K: int, *, out: Optional[BeamResult] = None, stream=None) -> BeamResult:
@@ -200,34 +173,19 @@ def mtp_beam_select(logits, scores, temperature, K: int, *, out: Optional[BeamRe
     bfloat16), scores [B, W] float32 (-inf: a dead beam), temperature [B]
     float32.  Returns tokens, parents and scores [B, K], best first."""
     torch = _m._torch()
-    B, W, V = _dims(logits, "logits", 3)
-    code = _m._dtype_code(logits)
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
-    if not 1 <= W <= MAX_BEAMS:
-        raise ValueError(f"1 to {MAX_BEAMS} beams, got {W}")
-    if not 1 <= K <= MAX_SELECT or K > W * V:
-        raise ValueError(f"K must be 1 to {MAX_SELECT} and at most W V, got {K}")
     index = logits.get_device()
-    if out is not None:
-        po = (_shape(out.tokens, "out.tokens", i32, (B, K), index), _shape(out.parents, "out.parents", i32, (B, K), index),
-              _shape(out.scores, "out.scores", f32, (B, K), index),
-              _shape(out.row_flags, "out.row_flags", i32, (B,), index) if out.row_flags is not None else 0)
-    pz = _shape(logits, "logits", logits.dtype, (B, W, V), index)
-    ps = _shape(scores, "scores", f32, (B, W), index)
-    pt = _shape(temperature, "temperature", f32, (B,), index)
-    with _on(torch, index, "logits"):
+    with _on(torch, index):
         mine = ()
         if out is None:
-            out = BeamResult(torch.empty((B, K), dtype=i32, device=dev), torch.empty((B, K), dtype=i32, device=dev),
-                             torch.empty((B, K), dtype=f32, device=dev), torch.empty((B,), dtype=i32, device=dev))
-            mine = out
-            po = tuple(t.data_ptr() for t in out)
-        nbytes = _beam_workspace(index, code, B, W, V, K)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
-        raw = _launch_stream(torch, dev, stream, ws, *mine)
-        rc = _m.load_library().mtp_beam_select(pz, code, ps, pt, B, W, V, K, *po, ws.data_ptr(), nbytes, raw)
-    if rc:
-        raise _m.MTPError("mtp_beam_select", rc)
+            B, dev, i32 = logits.shape[0], logits.device, torch.int32
+            k = max(int(K), 0)
+            out = mine = BeamResult(torch.empty((B, k), dtype=i32, device=dev), torch.empty((B, k), dtype=i32, device=dev),
+                                    torch.empty((B, k), dtype=torch.float32, device=dev), torch.empty((B,), dtype=i32, device=dev))
+        ws = None
+        if stream is not None and logits.dim() == 3:
+            ws = _scratch(torch, logits, stream, "mtp_beam_select_workspace", _m._dtype_code(logits), *logits.shape, int(K))
+        _call("beam_select", index, (logits, scores, temperature, K, out.tokens, out.parents, out.scores, out.row_flags, ws,
+                                     _raw(torch, index, stream, mine)))
     return out
 
 
@@ -237,33 +195,18 @@ def mtp_beam_reorder(states, parents, *, out: Optional[ReorderResult] = None, st
     int32; returns states [N0, B, K, ...] with out[n, b, k] = states[n, b,
     parents[b, k]], zeros for a parent outside [0, W)."""
     torch = _m._torch()
-    if states.dim() < 3:
-        raise ValueError(f"states must be [N0, B, W, ...], got {tuple(states.shape)}")
-    N0, B, W = states.shape[:3]
-    K = _dims(parents, "parents", 2)[1]
-    dev, dt, i32 = states.device, states.dtype, torch.int32
-    if W < 1 or K < 1:
-        raise ValueError(f"at least one beam and one place are needed, got W = {W}, K = {K}")
     index = states.get_device()
-    shape = (N0, B, K, *states.shape[3:])
-    if out is not None:
-        pd = _shape(out.states, "out.states", dt, shape, index)
-        pf = _shape(out.row_flags, "out.row_flags", i32, (B,), index) if out.row_flags is not None else 0
-    ps = _shape(states, "states", dt, states.shape, index)
-    pp = _shape(parents, "parents", i32, (B, K), index)
-    row = states.element_size()
-    for n in shape[3:]:
-        row *= n
-    with _on(torch, index, "states"):
+    with _on(torch, index):
         mine = ()
         if out is None:
-            out = ReorderResult(torch.empty(shape, dtype=dt, device=dev), torch.zeros((B,), dtype=i32, device=dev))
-            mine = out
-            pd, pf = out.states.data_ptr(), out.row_flags.data_ptr()
-        raw = _launch_stream(torch, dev, stream, *mine)
-        rc = _m.load_library().mtp_beam_reorder(ps, pp, N0, B, W, K, row, pd, pf, raw)
-    if rc:
-        raise _m.MTPError("mtp_beam_reorder", rc)
+            if states.dim() < 3 or parents.dim() != 2:
+                raise ValueError(f"states must be [N0, B, W, ...] and parents [B, K], got {tuple(states.shape)} and "
+                                 f"{tuple(parents.shape)}")
+            dev = states.device
+            out = mine = ReorderResult(
+                torch.empty((*states.shape[:2], parents.shape[1], *states.shape[3:]), dtype=states.dtype, device=dev),
+                torch.zeros((states.shape[1],), dtype=torch.int32, device=dev))
+        _call("beam_reorder", index, (states, parents, out.states, out.row_flags, _raw(torch, index, stream, mine)))
     return out
 
 
@@ -279,48 +222,16 @@ def mtp_tree_commit(tokens, target_tokens, parents=None, k_new=None, v_new=None,
     one layer; written in place), page_table [B, max_pages], cache_len [B],
     n_nodes [B] (None: T)."""
     torch = _m._torch()
-    i32 = torch.int32
-    B, T = _dims(tokens, "tokens", 2)
-    if not 1 <= T <= MAX_NODES:
-        raise ValueError(f"trees have 1 to {MAX_NODES} nodes, got {T}")
-    for t, name in ((k_new, "k_new"), (v_new, "v_new"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"),
-                    (cache_len, "cache_len")):
-        if t is None:
-            raise ValueError(f"{name} is required")
-    dt = k_new.dtype
-    code = _m._dtype_code(k_new)
-    if k_new.dim() == 4:
-        k_new, v_new, k_cache, v_cache = k_new[None], v_new[None], k_cache[None], v_cache[None]
-    layers, _, _, Hkv, D = _dims(k_new, "k_new", 5)
-    pages, page_size = _dims(k_cache, "k_cache", 5)[1:3]
-    max_pages = _dims(page_table, "page_table", 2)[1]
-    index, dev = tokens.get_device(), tokens.device
-    if out is not None:
-        po = (_shape(out.tokens, "out.tokens", i32, (B, T), index), _shape(out.accept_len, "out.accept_len", i32, (B,), index),
-              _shape(out.path, "out.path", i32, (B, T), index), _shape(out.cache_len, "out.cache_len", i32, (B,), index),
-              _shape(out.row_flags, "out.row_flags", i32, (B,), index) if out.row_flags is not None else 0)
-    pt = _shape(tokens, "tokens", i32, (B, T), index)
-    pg = _shape(target_tokens, "target_tokens", i32, (B, T), index)
-    pp = _shape(parents, "parents", i32, (B, T), index) if parents is not None else 0
-    pn = _shape(n_nodes, "n_nodes", i32, (B,), index) if n_nodes is not None else 0
-    pk, sk = _strided(k_new, "k_new", dt, (layers, B, T, Hkv, D), index)
-    pv, sv = _strided(v_new, "v_new", dt, (layers, B, T, Hkv, D), index)
-    pkc, skc = _strided(k_cache, "k_cache", dt, (layers, pages, page_size, Hkv, D), index)
-    pvc, svc = _strided(v_cache, "v_cache", dt, (layers, pages, page_size, Hkv, D), index)
-    pta = _shape(page_table, "page_table", i32, (B, max_pages), index)
-    pc = _shape(cache_len, "cache_len", i32, (B,), index)
-    if out is not None and po[3] == pc and B:
-        raise ValueError("out.cache_len must not be cache_len itself")
-    with _on(torch, index, "tokens"):
+    index = tokens.get_device()
+    with _on(torch, index):
         mine = ()
         if out is None:
-            e = lambda *s: torch.empty(s, dtype=i32, device=dev)  # noqa: E731
-            out = mine = CommitResult(e(B, T), e(B), e(B, T), e(B), e(B))
-            po = tuple(t.data_ptr() for t in out)
-        raw = _launch_stream(torch, dev, stream, *mine)
-        rc = _m.load_library().mtp_tree_commit(
-            _COMMIT.pack(pt, pg, pp, pn, pta, pc, pk, pv, pkc, pvc, po[0], po[1], po[2], po[3], po[4], *sk, *sv, *skc, *svc, code,
-                         layers, B, T, Hkv, D, pages, page_size, max_pages), raw)
-    if rc:
-        raise _m.MTPError("mtp_tree_commit", rc)
+            if tokens.dim() != 2:
+                raise ValueError(f"tokens must have 2 dimensions, got {tuple(tokens.shape)}")
+            e = lambda s: torch.empty(s, dtype=torch.int32, device=tokens.device)  # noqa: E731
+            n = tokens.shape[:1]
+            out = mine = CommitResult(e(tokens.shape), e(n), e(tokens.shape), e(n), e(n))
+        _call("tree_commit", index,
+              (tokens, target_tokens, parents, k_new, v_new, k_cache, v_cache, page_table, cache_len, n_nodes, out.tokens,
+               out.accept_len, out.path, out.cache_len, out.row_flags, _raw(torch, index, stream, mine)))
     return out

@@ -15,6 +15,11 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 i32 = torch.int32
 
 
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mtp_build.build()
+
+
 @pytest.fixture(autouse=True)
 def no_launch(monkeypatch, request):
     if "lib" in request.fixturenames:
