@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     const size_t slot = static_cast<size_t>(row) * A.parts + part;
     float *cz = A.cand_z + slot * A.KL;
     int *cv = A.cand_v + slot * A.KL;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float temp = __ldg(A.temp + b), score = __ldg(A.scores + row);
     if (!(temp > 0.f) || temp == INFINITY || !(score < INFINITY) || score == -INFINITY) {
         // a dead beam, or a sequence that the join flags: its logits are not read
@@ -382,12 +384,13 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
     __shared__ int s_v[SMEM_CAND];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
     const int lists = A.W * A.parts;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float temp = __ldg(A.temp + b);
     const bool bad_temp = !(temp > 0.f) || temp == INFINITY;
     const double inv_t = 1.0 / static_cast<double>(temp);
     if (tid == 0) s_flag = bad_temp ? F_BAD_TEMP : 0;
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t cand0 = static_cast<size_t>(b) * lists * A.KL;
     const int n = lists * A.KL;
     const bool shared = n <= SMEM_CAND;

@@ -69,9 +69,10 @@ int resident(int dev, const void *func, uint32_t smem, int threads) {
     return n;
 }
 
-// `after`: a kernel that waits for the launch before it itself
-// (griddepcontrol.wait), so that its CTAs may be set up while that one ends.
-int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream, bool after = false,
+// Every kernel here waits for the launches before it itself
+// (griddepcontrol.wait) before it touches memory, and lets the next one's CTAs
+// be set up early, so all are launched programmatically.
+int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream,
            const void *map1 = nullptr, const void *map2 = nullptr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -82,7 +83,7 @@ int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = after ? 1 : 0;
+    cfg.numAttrs = 1;
     void *kargs[] = {const_cast<void *>(args), const_cast<void *>(map1), const_cast<void *>(map2)};
     return cudaLaunchKernelExC(&cfg, func, kargs) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
@@ -281,10 +282,9 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.qrows = p.qrows;
     A.slots = p.slots;
     A.per_page = p.per_page;
-    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, false, &kmap, &vmap);
+    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, &kmap, &vmap);
     if (e != MTP_OK || !p.joins()) return e;
-    return launch(attn_join_func(a.dtype, a.D), dim3(p.groups * p.mtiles, ((p.rows < p.bm ? p.rows : p.bm) + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A,
-                  stream, true);
+    return launch(attn_join_func(a.dtype, a.D), dim3(p.groups * p.mtiles, ((p.rows < p.bm ? p.rows : p.bm) + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A, stream);
 }
 
 // ------------------------------------------------------- beam selection --
@@ -387,7 +387,7 @@ extern "C" int mtp_beam_select(const void *logits, mtp_dtype dtype, const float 
     A.flags = row_flags;
     const int e = launch(beam_part_func(dtype), dim3(static_cast<unsigned>(p.n)), BEAM_THREADS, 0, &A, stream);
     if (e != MTP_OK) return e;
-    return launch(beam_join_func(), dim3(B), BEAM_THREADS, 0, &A, stream, true);
+    return launch(beam_join_func(), dim3(B), BEAM_THREADS, 0, &A, stream);
 }
 
 // --------------------------------------------------- reorder and commit ----

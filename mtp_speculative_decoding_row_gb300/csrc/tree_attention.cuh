@@ -72,71 +72,68 @@ struct AttnPiece {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == prefix + 1; }
 };
 
-__device__ __forceinline__ long long attn_lo(long long W, int g, int groups) { return W * g / groups; }
+// Groups that have tiles: none of their ranges is empty.
+__device__ __forceinline__ int attn_groups(const TreeAttnArgs &A, long long W) {
+    return W < A.groups ? static_cast<int>(W) : A.groups;
+}
+// The first tile of group g's range (a 64-bit division only where it is needed).
+__device__ __forceinline__ long long attn_lo(long long W, int g, int groups) {
+    const unsigned long long x = static_cast<unsigned long long>(W) * g;
+    return x >> 32 ? static_cast<long long>(x / groups) : static_cast<uint32_t>(x) / static_cast<uint32_t>(groups);
+}
 
-// The walk over a group's pieces.  start() finds the first one (all threads
-// of the block call it; `scan` is shared memory of NT / 32 long longs, two at least), next()
-// steps on.
+// The walk over a group's pieces.  start() finds the first one, in every warp
+// by itself (a lane takes a stretch of the sequences): a barrier would cost
+// more than the second reading of a few lengths.
 struct AttnWalk {
-    long long W = 0, lo = 0, hi = 0, at = 0;  // all tiles, this group's range, the next tile
-    int groups = 0;                           // groups that have tiles: no range of theirs is empty
-    int b = 0, h = 0, tile = 0;               // where `at` is
+    long long hi = 0, at = 0;    // the end of this group's range, the next tile
+    int b = 0, h = 0, tile = 0;  // where `at` is
     int len = 0, prefix = 0;
+    bool begins = true;          // no piece was taken yet
 
-    template <int NT>
-    __device__ __forceinline__ void start(const TreeAttnArgs &A, int g, long long *scan) {
-        const int tid = threadIdx.x;
-        const int per = (A.B + NT - 1) / NT;
-        const int b0 = min(A.B, tid * per), b1 = min(A.B, b0 + per);
+    // Returns the number of all tiles.
+    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
+        const int lane = threadIdx.x & 31;
+        const int per = (A.B + 31) / 32;
+        const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
         long long sum = 0;
         bool bad;
-        for (int i = b0; i < b1; ++i) sum += static_cast<long long>(attn_prefix_tiles(A, attn_len(A, i, bad)) + 1) * A.Hkv;
-        // inclusive scan of the threads' sums
-        const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll 4
+        for (int i = b0; i < b1; ++i) sum += attn_prefix_tiles(A, attn_len(A, i, bad)) + 1;
+        sum *= A.Hkv;
         long long inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long o = __shfl_up_sync(FULL, inc, d);
             if (lane >= d) inc += o;
         }
-        if (lane == 31) scan[warp] = inc;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int w = 0; w < NT / 32; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-        __syncthreads();
-        W = total;
-        groups = W < A.groups ? static_cast<int>(W) : A.groups;
-        lo = attn_lo(W, min(g, groups), groups);
+        const long long W = __shfl_sync(FULL, inc, 31);
+        const int groups = attn_groups(A, W);
+        const long long lo = attn_lo(W, min(g, groups), groups);
         hi = attn_lo(W, min(g + 1, groups), groups);
         at = lo;
-        const long long from = before + inc - sum;
-        if (lo < hi && lo >= from && lo < from + sum) {
-            long long x = lo - from;
-            for (int i = b0; i < b1; ++i) {
-                const int n = attn_len(A, i, bad), p = attn_prefix_tiles(A, n);
-                const long long unit = static_cast<long long>(p + 1) * A.Hkv;
-                if (x < unit) {
-                    scan[0] = i;
-                    scan[1] = x;
-                    break;
-                }
+        const long long from = inc - sum;
+        const uint32_t own = __ballot_sync(FULL, lo < hi && lo >= from && lo < inc);
+        if (own == 0) return W;  // no tiles for this group
+        long long x = lo - from;
+        int i = b0;
+        if ((own >> lane) & 1u) {
+            for (;; ++i) {
+                len = attn_len(A, i, bad);
+                prefix = attn_prefix_tiles(A, len);
+                const long long unit = static_cast<long long>(prefix + 1) * A.Hkv;
+                if (x < unit) break;  // (x lies in this lane's stretch)
                 x -= unit;
             }
         }
-        __syncthreads();
-        if (lo < hi) {
-            b = static_cast<int>(scan[0]);
-            len = attn_len(A, b, bad);
-            prefix = attn_prefix_tiles(A, len);
-            h = static_cast<int>(scan[1] / (prefix + 1));
-            tile = static_cast<int>(scan[1] - static_cast<long long>(h) * (prefix + 1));
-        } else {
-            b = h = tile = len = prefix = 0;
-        }
-        __syncthreads();
+        const int src = __ffs(own) - 1;
+        b = __shfl_sync(FULL, i, src);
+        len = __shfl_sync(FULL, len, src);
+        prefix = __shfl_sync(FULL, prefix, src);
+        const int first = __shfl_sync(FULL, static_cast<int>(x), src);  // < Hkv (prefix + 1)
+        h = first / (prefix + 1);
+        tile = first - h * (prefix + 1);
+        return W;
     }
 
     // The next piece, or false at the end of the range.
@@ -146,7 +143,8 @@ struct AttnWalk {
         p.h = h;
         p.len = len;
         p.prefix = prefix;
-        p.first = at == lo;
+        p.first = begins;
+        begins = false;
         p.t0 = tile;
         const long long left = hi - at;
         p.t1 = static_cast<int>(tile + left < prefix + 1 ? tile + left : prefix + 1);
@@ -172,18 +170,25 @@ __device__ __forceinline__ size_t attn_slot(const TreeAttnArgs &A, int group, in
     return (static_cast<size_t>(group) * A.mtiles + mtile) * 2 + (first ? 0 : 1);
 }
 
+// Programmatic launches: what the kernels before this one in the stream wrote
+// may be read after pdl_wait(); the next kernel's CTAs may be set up from
+// pdl_next() on (they wait in turn).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Tell the join about the unit that begins in this group and goes on in the
 // next ones (at most one does): {b, h, parts, slot of the first part}.
-__device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, const AttnWalk &w, bool any,
+__device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, long long W, long long hi,
                                                 const AttnPiece &last) {
     int *d = A.desc + static_cast<size_t>(g) * ATTN_DESC;
-    if (!any || last.t0 != 0 || last.t1 == last.prefix + 1) {
+    if (last.t0 != 0 || last.t1 == 0 || last.t1 == last.prefix + 1) {  // (t1 = 0: the group had no piece)
         d[2] = 0;
         return;
     }
-    const long long end = w.hi + (last.prefix + 1 - last.t1);  // one past the unit's last tile
+    const long long end = hi + (last.prefix + 1 - last.t1);  // one past the unit's last tile
+    const int groups = attn_groups(A, W);
     int n = 1;
-    while (g + n < w.groups && attn_lo(w.W, g + n, w.groups) < end) ++n;
+    while (g + n < groups && attn_lo(W, g + n, groups) < end) ++n;
     d[0] = last.b;
     d[1] = last.h;
     d[3] = last.first ? 0 : 1;

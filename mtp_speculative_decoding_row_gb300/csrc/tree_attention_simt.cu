@@ -65,7 +65,6 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     float *sl = sm + BM;                          // [BM] sum
     float *sf = sl + BM;                          // [BM] factor of the old rows
     uint64_t *smask = reinterpret_cast<uint64_t *>(sf + BM);  // [MAX_NODES]
-    long long *scan = reinterpret_cast<long long *>(smask + MAX_NODES);  // [NT / 32]
     __shared__ int s_flag;
 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -73,12 +72,12 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
     const bool vec = A.vec != 0;
 
+    pdl_wait();
+    pdl_next();
     AttnWalk walk;
-    walk.start<NT>(A, group, scan);
+    const long long W = walk.start(A, group);
     AttnPiece pc, last = {};
-    bool any = false;
     while (walk.next(A, pc)) {
-        any = true;
         last = pc;
         const int b = pc.b, h = pc.h;
         bool bad_len, bad_nodes;
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         }
         __syncthreads();
     }
-    if (mtile == 0 && tid == 0) attn_write_desc(A, group, walk, any, last);
+    if (mtile == 0 && tid == 0) attn_write_desc(A, group, W, walk.hi, last);
 }
 
 // Join one unit that begins in group blockIdx.x / mtiles and goes on in the
@@ -283,7 +282,8 @@ constexpr int JOIN_AHEAD = 4;
 
 template <typename T, int NQ>
 __global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
+    pdl_next();
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
     const int4 d = *reinterpret_cast<const int4 *>(A.desc + static_cast<size_t>(group) * ATTN_DESC);
     const int b = d.x, h = d.y, parts = d.z;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_
 uint32_t attn_simt_smem(int D) {
     const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
     const size_t f = static_cast<size_t>(BM) * (dp + 4) + BN * (dp + 4) + BN * dp + BM * (BN + 4) + 3 * BM;
-    return static_cast<uint32_t>(f * 4 + MAX_NODES * 8 + (NT / 32) * 8);
+    return static_cast<uint32_t>(f * 4 + MAX_NODES * 8);
 }
 
 const void *attn_simt_func(int dtype, int D) {

@@ -67,8 +67,6 @@ struct Control {
     uint64_t mask[4][MAX_NODES];
     uint64_t poison[4];
     int flag[4];
-    long long scan[12];
-    AttnWalk begin;
     float m[2][128], l[2][128];   // KEYS: the groups' statistics
     uint32_t tmem;
     int dead;
@@ -234,12 +232,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
     const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
 
-    AttnWalk walk;
-    walk.start<NT>(A, group, ctl.scan);
-    if (walk.at >= walk.hi) {  // no tiles for this group
-        if (mtile == 0 && tid == 0) A.desc[static_cast<size_t>(group) * ATTN_DESC + 2] = 0;
-        return;
-    }
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < A.slots; ++i) {
             mbar_init(smem_addr(&ctl.full[2 * i]), 1);
@@ -266,7 +258,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&vmap);
     }
-    if (warp == 1) tmem_alloc(&ctl.tmem, TMEM_COLS);
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(&ctl.tmem, TMEM_COLS);
+    }
     // Rows of the query tile that no query fills.  (The product reads 128 rows
     // of each block whatever qrows is: what lies behind them gives rows that
     // nobody looks at.)
@@ -280,7 +275,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     __syncthreads();
     tmem_fence_after_sync();
     const uint32_t tmem = ctl.tmem;
-    if (tid == 0) ctl.begin = walk;  // read at the end, by the same thread
+    pdl_wait();  // (what was done so far reads nothing that another kernel writes)
+    pdl_next();
+    AttnWalk walk;
+    const long long W = walk.start(A, group);
+    const AttnWalk begin = walk;
     bool ok = (sq & 1023u) == 0u;    // the swizzle counts on it
     AttnPiece pc;
 
@@ -736,14 +735,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
     }
-    if (mtile == 0 && tid == 0) {
-        AttnWalk w = ctl.begin;
+    if (mtile == 0 && warp == 0) {
+        AttnWalk w = begin;
         AttnPiece last = {};
         while (w.next(A, pc)) {
             last = pc;
-            if (ctl.dead && A.flags) atomicOr(A.flags + pc.b, F_TIMEOUT);
+            if (ctl.dead && A.flags && lane == 0) atomicOr(A.flags + pc.b, F_TIMEOUT);
         }
-        attn_write_desc(A, group, w, true, last);
+        if (lane == 0) attn_write_desc(A, group, W, w.hi, last);
     }
     tmem_fence_after_sync();
     __syncthreads();

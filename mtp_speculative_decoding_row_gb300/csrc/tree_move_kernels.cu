@@ -40,6 +40,8 @@ constexpr int RT = REORDER_THREADS, RU = REORDER_UNROLL;
 template <int WIDTH>
 __global__ void __launch_bounds__(RT) reorder_impl(const __grid_constant__ ReorderArgs A) {
     using W = typename Word<WIDTH>::type;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long rows = static_cast<long long>(A.N0) * A.B * A.K, words = A.bytes / WIDTH;
     for (long long y = blockIdx.y; y < rows; y += gridDim.y) {
         const long long nb = y / A.K;
@@ -80,6 +82,8 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
     __shared__ int s_count, s_flag;
     const int b = blockIdx.x, tid = threadIdx.x;
     const int T = A.T;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int n = A.nodes ? __ldg(A.nodes + b) : T;
     const int len = __ldg(A.len + b);
     int flag = 0;
