@@ -67,6 +67,8 @@ struct Control {
     uint64_t mask[4][MAX_NODES];
     uint64_t poison[4];
     int flag[4];
+    long long W;
+    AttnWalk begin;
     float m[2][128], l[2][128];   // KEYS: the groups' statistics
     uint32_t tmem;
     int dead;
@@ -101,23 +103,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// -inf in the columns of block c that the row does not see.
-template <bool TREE>
-__device__ __forceinline__ void mask_block(uint32_t (&s)[32], int c, int valid, uint64_t see) {
-    if (TREE) {
-        const uint32_t w = static_cast<uint32_t>(see >> (32 * c));
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (!((w >> i) & 1u)) s[i] = 0xff800000u;
-    } else if (valid < 32 * (c + 1)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= valid) s[i] = 0xff800000u;
-    }
-}
-
-// Weights of one block of scores, stored as bfloat16 in 16 columns at p_addr;
-// their sum goes to acc.
+// Weights of one block of 32 scores, stored as bfloat16 in 16 columns at
+// p_addr; their sum goes to acc.
 __device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2, uint64_t N2, uint64_t (&acc)[2], uint32_t p_addr) {
     uint32_t p[16];
 #pragma unroll
@@ -132,21 +119,67 @@ __device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2
     tmem_st16(p_addr, p);
 }
 
-__device__ __forceinline__ void max_block(const uint32_t (&s)[32], float (&t)[4]) {
+// The maximum of one block; with `masked`, of the columns in `see`, and -inf
+// is written over the others.
+__device__ __forceinline__ void max_block(uint32_t (&s)[32], float (&t)[4], bool masked, uint32_t see, uint32_t s_addr) {
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1u)) s[i] = 0xff800000u;
+        __syncwarp();
+        tmem_st32(s_addr, s);
+    }
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
         t[(i >> 1) & 3] = max3(t[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
 }
 
-// Softmax of one score tile: CH blocks of 32 columns, of which a row sees the
-// first `valid` or, of a tree tile, those in `see`.  Two blocks are in
-// registers at a time; of four, the last two are read a second time for their
-// weights, while those of the first two are worked on (168 registers a thread
-// do not hold a row of 128 scores and what else is needed).  Block c's weights
-// go to columns 16 c .. of the tile, over scores that have been read.
-template <int CH, bool TREE>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int valid, uint64_t see,
-                                             bool first, float &m, float &l, uint32_t o_bar, uint32_t o_phase, bool &ok) {
+// The row's reference maximum for a tile whose largest score is `top` (in
+// units of log2 e); the accumulator is rescaled where it has to be.
+__device__ __forceinline__ void rescale(float top, bool first, float &m, float &l, uint32_t o_addr, int ocols, uint32_t o_bar,
+                                        uint32_t o_phase, bool &ok) {
+    if (first) {
+        m = top;
+        l = 0.f;
+        return;
+    }
+    const bool up = top > m + RESCALE;
+    if (!__any_sync(FULL, up)) return;
+    ok = mbar_wait_bounded(o_bar, o_phase) && ok;  // the products before this tile
+    __syncwarp();
+    tmem_fence_after_sync();
+    const float f = up ? ex2(m - top) : 1.f;
+    if (up) m = top;
+    l *= f;
+#pragma unroll 1
+    for (int c = 0; c < ocols; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st32(o_addr + c, o);
+        tmem_wait_st();
+    }
+}
+
+__device__ __forceinline__ float sum4(const uint64_t (&acc)[2]) {
+    float a0, a1, b0, b1;
+    f2unpack(acc[0], a0, a1);
+    f2unpack(acc[1], b0, b1);
+    return (a0 + a1) + (b0 + b1);
+}
+
+// Softmax of a score tile of CH blocks of 32 columns, all of which the row
+// sees.  Two blocks are in registers at a time; of four, the last two are read
+// a second time for their weights while those of the first two are worked on
+// (168 registers a thread do not hold 128 scores and what else is needed).
+// Block c's weights go to columns 16 c .. of the tile, over scores that have
+// been read.
+template <int CH>
+__device__ __forceinline__ void softmax_full(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, bool first, float &m,
+                                             float &l, uint32_t o_bar, uint32_t o_phase, bool &ok) {
     uint32_t s[2][32];
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     __syncwarp();  // TMEM accesses are warp-wide, and the lanes may have left a wait one by one
@@ -154,65 +187,60 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
         tmem_ld32(s_addr + 64, s[0]);
         tmem_ld32(s_addr + 96, s[1]);
         tmem_wait_ld32(s);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            mask_block<TREE>(s[c], c + 2, valid, see);
-            max_block(s[c], t);
-        }
+        max_block(s[0], t, false, 0u, 0u);
+        max_block(s[1], t, false, 0u, 0u);
     }
-#pragma unroll
-    for (int c = 0; c < (CH == 1 ? 1 : 2); ++c) tmem_ld32(s_addr + 32 * c, s[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < (CH == 1 ? 1 : 2); ++c) {
-        tmem_use32(s[c]);
-        mask_block<TREE>(s[c], c, valid, see);
-        max_block(s[c], t);
-    }
-    const float top = max3(t[0], t[1], fmaxf(t[2], t[3])) * scale;
-    if (first) {
-        m = top;
-        l = 0.f;
-    } else {
-        const bool up = top > m + RESCALE;
-        if (__any_sync(FULL, up)) {
-            ok = mbar_wait_bounded(o_bar, o_phase) && ok;  // the products before this tile
-            __syncwarp();
-            tmem_fence_after_sync();
-            const float f = up ? ex2(m - top) : 1.f;
-            if (up) m = top;
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < ocols; c += 32) {
-                uint32_t o[32];
-                __syncwarp();
-                tmem_ld32(o_addr + c, o);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(o_addr + c, o);
-                tmem_wait_st();
-            }
-        }
-    }
+    tmem_ld32(s_addr, s[0]);
+    tmem_ld32(s_addr + 32, s[1]);
+    tmem_wait_ld32(s);
+    max_block(s[0], t, false, 0u, 0u);
+    max_block(s[1], t, false, 0u, 0u);
+    rescale(max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
     const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
     uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+    __syncwarp();
     weigh_block(s[0], K2, N2, acc, s_addr);
     if (CH == 4) tmem_ld32(s_addr + 64, s[0]);
-    if (CH >= 2) weigh_block(s[1], K2, N2, acc, s_addr + 16);
+    weigh_block(s[1], K2, N2, acc, s_addr + 16);
     if (CH == 4) {
         tmem_wait_ld32(s[0]);
         tmem_ld32(s_addr + 96, s[1]);
-        mask_block<TREE>(s[0], 2, valid, see);
         weigh_block(s[0], K2, N2, acc, s_addr + 32);
         tmem_wait_ld32(s[1]);
-        mask_block<TREE>(s[1], 3, valid, see);
         weigh_block(s[1], K2, N2, acc, s_addr + 48);
     }
-    float a0, a1, b0, b1;
-    f2unpack(acc[0], a0, a1);
-    f2unpack(acc[1], b0, b1);
-    l += (a0 + a1) + (b0 + b1);
+    l += sum4(acc);
+    tmem_wait_st();
+}
+
+// The same for the other tiles, of `blocks` blocks: the row sees the columns
+// in lo (the first 64) and hi.  One short loop for all of them: the warps of
+// an SM run five different programs at once, and unrolled by kind of tile they
+// did not fit in its instruction cache.
+__device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int blocks, uint64_t lo,
+                                             uint64_t hi, bool first, float &m, float &l, uint32_t o_bar, uint32_t o_phase,
+                                             bool &ok) {
+    uint32_t s[32];
+    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int c = 0; c < blocks; ++c) {
+        __syncwarp();
+        tmem_ld32(s_addr + 32 * c, s);
+        tmem_wait_ld32(s);
+        max_block(s, t, true, static_cast<uint32_t>((c < 2 ? lo : hi) >> (32 * (c & 1))), s_addr + 32 * c);
+    }
+    tmem_wait_st();
+    rescale(max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
+    const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
+    uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll 1
+    for (int c = 0; c < blocks; ++c) {
+        __syncwarp();
+        tmem_ld32(s_addr + 32 * c, s);
+        tmem_wait_ld32(s);
+        weigh_block(s, K2, N2, acc, s_addr + 16 * c);
+    }
+    l += sum4(acc);
     tmem_wait_st();
 }
 
@@ -278,8 +306,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     pdl_wait();  // (what was done so far reads nothing that another kernel writes)
     pdl_next();
     AttnWalk walk;
-    const long long W = walk.start(A, group);
-    const AttnWalk begin = walk;
+    {
+        const long long W = walk.start(A, group);
+        if (tid == 0) {  // for the end
+            ctl.W = W;
+            ctl.begin = walk;
+        }
+    }
     bool ok = (sq & 1023u) == 0u;    // the swizzle counts on it
     AttnPiece pc;
 
@@ -573,34 +606,35 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 // the product before this one into the accumulator
                 const uint32_t o_bar = smem_addr(&ctl.o_done[MODE == ONE ? buf ^ 1 : wg]);
                 const uint32_t o_phase = ((MODE == ONE ? buf ? count0 : count1 : count0) - 1) & 1;
-                if (t == pc.prefix) {
+                int valid = C::BN;
+                uint64_t lo = ~0ull, hi = ~0ull;
+                const bool tree = t == pc.prefix;
+                if (tree) {
                     ok = mbar_wait_bounded(smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
-                    const uint64_t see = live && node < n ? ctl.mask[np & 3][node] : 0ull;
-                    if (busy) {
-                        if (n <= 32)
-                            softmax_tile<1, true>(s_addr, o_addr, D, A.scale_log2, 0, see, first, m, l, o_bar, o_phase, ok);
-                        else
-                            softmax_tile<2, true>(s_addr, o_addr, D, A.scale_log2, 0, see, first, m, l, o_bar, o_phase, ok);
-                    }
+                    lo = live && node < n ? ctl.mask[np & 3][node] : 0ull;
                 } else {
-                    int pos, valid;
+                    int pos;
                     attn_tile(A, pc.len, t, pos, valid);
-                    if (busy)
-                        softmax_tile<C::BN / 32, false>(s_addr, o_addr, D, A.scale_log2, valid, 0ull, first, m, l, o_bar, o_phase,
-                                                        ok);
-                    const int end = round16(valid);
+                    if (valid < 64) lo = (1ull << valid) - 1ull;
+                    hi = valid > 64 ? (valid < 128 ? (1ull << (valid - 64)) - 1ull : ~0ull) : 0ull;
+                }
+                if (busy && !tree && valid == C::BN)
+                    softmax_full<C::BN / 32>(s_addr, o_addr, D, A.scale_log2, first, m, l, o_bar, o_phase, ok);
+                else if (busy)
+                    softmax_part(s_addr, o_addr, D, A.scale_log2, tree ? max(n + 31, 32) >> 5 : (valid + 31) >> 5, lo, hi, first, m,
+                                 l, o_bar, o_phase, ok);
+                if (!tree && (valid & 15)) {
                     // What lies behind the last key meets a weight of 0: it has
                     // to be a number.  (ROWS: each group sees to it for its own
                     // product; both write the same.)
-                    if (valid < end) {
-                        ok = mbar_wait_bounded(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
-                        for (int i = wt; i < (end - valid) * (D / 8); i += 128) {
-                            const int j = valid + i / (D / 8), u = i % (D / 8);
-                            *reinterpret_cast<uint4 *>(ring + vr.slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async();
+                    const int end = round16(valid);
+                    ok = mbar_wait_bounded(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
+                    for (int i = wt; i < (end - valid) * (D / 8); i += 128) {
+                        const int j = valid + i / (D / 8), u = i % (D / 8);
+                        *reinterpret_cast<uint4 *>(ring + vr.slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
+                            make_uint4(0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async();
                 }
                 first = false;
                 tmem_fence_before_sync();
@@ -736,13 +770,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
     }
     if (mtile == 0 && warp == 0) {
-        AttnWalk w = begin;
+        AttnWalk w = ctl.begin;
         AttnPiece last = {};
         while (w.next(A, pc)) {
             last = pc;
             if (ctl.dead && A.flags && lane == 0) atomicOr(A.flags + pc.b, F_TIMEOUT);
         }
-        if (lane == 0) attn_write_desc(A, group, W, w.hi, last);
+        if (lane == 0) attn_write_desc(A, group, ctl.W, w.hi, last);
     }
     tmem_fence_after_sync();
     __syncthreads();
