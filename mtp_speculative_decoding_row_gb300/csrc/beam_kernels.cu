@@ -225,26 +225,16 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         s_bound = 0;
     }
 
-    // sums of e_i = 2^(z_i k - mk) and of e_i z_i, where mk = m k rounded
-    float m = -INFINITY, mk = 0.f, s = 0.f, s1 = 0.f;
+    // s: the sum of e_i = 2^(z_i k - mk), where mk = m k rounded.  se and s1: the
+    // sums of e_i and of e_i z_i over every fourth vector; their ratio says
+    // where the row's weight lies, which is all that the correction for dk needs
+    // to know (it is below 3e-7 of a score to begin with).
+    float m = -INFINITY, mk = 0.f, s = 0.f, se = 0.f, s1 = 0.f;
     const uint64_t K2 = f2pack(k, k);
     int count = 0, again = j0;
-    // vectors j, j + NT, ..: the next four are on their way while four are worked on
-    auto fetch = [&](int j, uint4 (&raw)[UN]) {
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int at = j + u * NT + tid;
-            raw[u] = at < whole ? row_vec<T>(base, sh, at) : at < j1 ? row_tail<T>(base, at, A.V) : minus_inf_vec<T>();
-        }
-    };
-    uint4 ahead[UN];
-    fetch(j0, ahead);
-    for (int j = j0; j < j1; j += NT * UN) {
-        uint4 raw[UN];
+    // one round: vectors j + tid, j + tid + NT, .. of the row
+    auto round = [&](int j, uint4 (&raw)[UN]) {
         float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < UN; ++u) raw[u] = ahead[u];
-        if (j + NT * UN < j1) fetch(j + NT * UN, ahead);
 #pragma unroll
         for (int u = 0; u < UN; ++u) top = max_nan(top, Store<T>::vmax(raw[u]));
         if (!(top <= m)) {  // a new maximum of this thread, or NaN
@@ -258,32 +248,36 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
                 m = top;
                 mk = top * k;
                 s *= f;
+                se *= f;
                 s1 *= f;
             }
         }
         if (m > -INFINITY) {
             const uint64_t N2 = f2pack(-mk, -mk);
-            uint64_t acc = f2pack(0.f, 0.f), acc1 = acc;
+            uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)}, acc1 = f2pack(0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
                 for (int e = 0; e < VEC / 2; ++e) {
-                    // -inf becomes the lowest finite number: e = 0 then, and e z = 0
-                    uint64_t z2;
-                    if (ES == 2)
-                        z2 = bf16pair_f2(bmax2_nan(w[e], 0xff7fff7fu));
-                    else
-                        z2 = f2pack(fmaxf(__uint_as_float(w[2 * e & 3]), -3.0e38f), fmaxf(__uint_as_float(w[(2 * e + 1) & 3]), -3.0e38f));
+                    const uint64_t z2 = ES == 2 ? bf16pair_f2(w[e])
+                                                : f2pack(__uint_as_float(w[2 * e & 3]), __uint_as_float(w[(2 * e + 1) & 3]));
                     float d0, d1;
                     f2unpack(f2fma(z2, K2, N2), d0, d1);
                     const uint64_t e2 = f2pack(ex2(d0), ex2(d1));
-                    acc = f2add(acc, e2);
-                    acc1 = f2fma(e2, z2, acc1);
+                    acc[u != 0] = f2add(acc[u != 0], e2);
+                    if (u == 0) {  // -inf becomes the lowest finite number: e = 0 then, and e z = 0
+                        float z0, z1;
+                        f2unpack(z2, z0, z1);
+                        acc1 = f2fma(e2, f2pack(fmaxf(z0, -3.0e38f), fmaxf(z1, -3.0e38f)), acc1);
+                    }
                 }
             }
             float a0, a1;
-            f2unpack(acc, a0, a1);
+            f2unpack(acc[0], a0, a1);
+            se += a0 + a1;
+            s += a0 + a1;
+            f2unpack(acc[1], a0, a1);
             s += a0 + a1;
             f2unpack(acc1, a0, a1);
             s1 += a0 + a1;
@@ -304,6 +298,31 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
                     count = offer<T>(raw[u], j + u * NT + tid, lanes, lists[warp], count, bound, A.KL, tmps[warp], &s_bound);
             }
         }
+    };
+    // vectors of a round; whole rounds of aligned rows need no test
+    const uint4 *fast = reinterpret_cast<const uint4 *>(base) + tid;
+    auto fetch = [&](int j, uint4 (&raw)[UN]) {
+        if (sh == 0 && j + NT * UN <= whole) {
+#pragma unroll
+            for (int u = 0; u < UN; ++u) raw[u] = __ldg(fast + j + u * NT);
+        } else {
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const int at = j + u * NT + tid;
+                raw[u] = at < whole ? row_vec<T>(base, sh, at) : at < j1 ? row_tail<T>(base, at, A.V) : minus_inf_vec<T>();
+            }
+        }
+    };
+    // the next round's vectors are on their way while one is worked on
+    constexpr int STEP = NT * UN;
+    uint4 one[UN], two[UN];
+    fetch(j0, one);
+    for (int j = j0; j < j1; j += 2 * STEP) {
+        if (j + STEP < j1) fetch(j + STEP, two);
+        round(j, one);
+        if (j + STEP >= j1) break;
+        if (j + 2 * STEP < j1) fetch(j + 2 * STEP, one);
+        round(j + STEP, two);
     }
     count = cut(lists[warp], count, A.KL, tmps[warp]);
     if (lane == 0) s_n[warp] = count;
@@ -347,8 +366,8 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     // factor is 1 + (z_i dk + mk - m (k + dk)) ln 2 to within its square (1e-12)
     float sum = 0.f;
     if (m > -INFINITY) {
-        const float off = -fmaf(m, k, -mk) - m * dk;
-        sum = fmaf(LN2, fmaf(off, s, dk * s1), s) * ex2((m - top) * k);
+        const float off = -fmaf(m, k, -mk) - m * dk, where = se > 0.f ? s1 / se : m;
+        sum = fmaf(LN2 * (off + dk * where), s, s) * ex2((m - top) * k);
     }
     sum = warp_allsum(sum);
     if (lane == 0) s_s[warp] = sum;

@@ -195,22 +195,51 @@ __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, lo
     d[2] = n;
 }
 
-// Ancestor mask of node i (itself included); sets bad for a parent that is
-// not a node before i.  A null `up` is a chain: node i sees nodes 0 .. i.
-__device__ __forceinline__ uint64_t attn_mask(const int32_t *up, int i, bool &bad) {
-    if (!up) return (2ull << i) - 1ull;
-    uint64_t m = 0;
-    int j = i;
-    for (int step = 0; step < MAX_NODES && j >= 0; ++step) {
-        m |= 1ull << j;
-        const int p = __ldg(up + j);
-        if (p >= j || p < -1) {
-            bad = true;
-            break;
-        }
-        j = p;
+// Ancestor masks of a tree's n nodes (a node's own bit included) into `mask`,
+// by one warp, two nodes to a lane; a null `up` is a chain.  Each round a node
+// takes over the mask of the farthest ancestor it knows of and that one's own,
+// so six rounds reach any of 64 -- not a chain of loads as deep as the tree.
+// Returns F_BAD_ID (in some lane) for a parent that is not a node before its
+// child.  `above` is scratch of MAX_NODES ints.
+__device__ __forceinline__ int attn_masks(const int32_t *up, int n, uint64_t *mask, int *above) {
+    const int lane = threadIdx.x & 31;
+    int flag = 0;
+    if (!up) {
+        for (int i = lane; i < n; i += 32) mask[i] = (2ull << i) - 1ull;
+        __syncwarp();
+        return 0;
     }
-    return m;
+    for (int i = lane; i < n; i += 32) {
+        int p = __ldg(up + i);
+        if (p >= i || p < -1) {
+            flag = F_BAD_ID;
+            p = -1;
+        }
+        above[i] = p;
+        mask[i] = 1ull << i;
+    }
+    __syncwarp();
+    for (int reach = 1; reach < n; reach <<= 1) {
+        uint64_t m[2];
+        int a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = lane + 32 * e, p = i < n ? above[i] : -1;
+            m[e] = p < 0 ? 0ull : mask[p];
+            a[e] = p < 0 ? -1 : above[p];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = lane + 32 * e;
+            if (i < n) {
+                mask[i] |= m[e];
+                above[i] = a[e];
+            }
+        }
+        __syncwarp();
+    }
+    return flag;
 }
 
 // Flags that one thread of `nt` finds in its share of sequence b's page table.

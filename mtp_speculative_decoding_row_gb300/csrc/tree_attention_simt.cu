@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     float *sl = sm + BM;                          // [BM] sum
     float *sf = sl + BM;                          // [BM] factor of the old rows
     uint64_t *smask = reinterpret_cast<uint64_t *>(sf + BM);  // [MAX_NODES]
-    __shared__ int s_flag;
+    __shared__ int s_flag, s_above[MAX_NODES];
 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
@@ -87,11 +87,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         if (tid == 0) s_flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
         __syncthreads();
         int bad = attn_check_pages(A, b, pc.len, tid, NT);
-        if (tid < n) {
-            bool bad_up = false;
-            smask[tid] = attn_mask(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, tid, bad_up);
-            if (bad_up) bad |= F_BAD_ID;
-        }
+        if (tid < 32) bad |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, smask, s_above);
         if (bad) atomicOr(&s_flag, bad);
         {
             const int r = tid >> 3;  // 8 threads a row

@@ -67,6 +67,7 @@ struct Control {
     uint64_t mask[4][MAX_NODES];
     uint64_t poison[4];
     int flag[4];
+    int above[MAX_NODES];
     long long W;
     AttnWalk begin;
     float m[2][128], l[2][128];   // KEYS: the groups' statistics
@@ -474,11 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 if (!ok) break;
             }
             int flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
-            for (int i = lane; i < n; i += 32) {
-                bool bad_up = false;
-                ctl.mask[np & 3][i] = attn_mask(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, i, bad_up);
-                if (bad_up) flag |= F_BAD_ID;
-            }
+            flag |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, ctl.mask[np & 3], ctl.above);
             mbar_arrive(smem_addr(&ctl.masks[np & 3]));
             for (int t = pc.t0; t < min(pc.t1, pc.prefix); ++t) {
                 r.step();
