@@ -13,10 +13,10 @@
 // then the complement of the index, so one integer comparison orders by value
 // and then by smaller index.  The K-th largest of the threads' running maxima
 // bounds the K-th best from below; vectors are compared with that bound four
-// at a time, and few pass.  The bound is taken again whenever twice as much of
-// the row has been seen, so that about K pass in between; a candidate costs as
-// much as 500 elements of the sums (with the first bound alone the kernel took
-// 81 us at 512 rows of 151936).  Each warp keeps a list of its own; one that
+// at a time, and few pass.  The bound is taken again whenever three times as much
+// of the row has been seen; a candidate costs as much as 500 elements of the
+// sums (with the first bound alone the kernel took 81 us at 512 rows of
+// 151936).  Each warp keeps a list of its own; one that
 // is full is cut to its K best, and the bound rises for all warps.
 //
 // Rows may start on any element.  A vector is always elements [8 j, 8 j + 8)
@@ -230,7 +230,6 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     // where the row's weight lies, which is all that the correction for dk needs
     // to know (it is below 3e-7 of a score to begin with).
     float m = -INFINITY, mk = 0.f, s = 0.f, se = 0.f, s1 = 0.f;
-    const uint64_t K2 = f2pack(k, k);
     int count = 0, again = j0;
     // one round: vectors j + tid, j + tid + NT, .. of the row
     auto round = [&](int j, uint4 (&raw)[UN]) {
@@ -253,39 +252,28 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
             }
         }
         if (m > -INFINITY) {
-            const uint64_t N2 = f2pack(-mk, -mk);
-            uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)}, acc1 = f2pack(0.f, 0.f);
+            // (four sums, in plain instructions: packed pairs cost more in moves
+            // than they save)
+            float a[4] = {0.f, 0.f, 0.f, 0.f}, a1 = 0.f;
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
-                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                float z[VEC];
+                Store<T>::unpack(raw[u], z);
 #pragma unroll
-                for (int e = 0; e < VEC / 2; ++e) {
-                    const uint64_t z2 = ES == 2 ? bf16pair_f2(w[e])
-                                                : f2pack(__uint_as_float(w[2 * e & 3]), __uint_as_float(w[(2 * e + 1) & 3]));
-                    float d0, d1;
-                    f2unpack(f2fma(z2, K2, N2), d0, d1);
-                    const uint64_t e2 = f2pack(ex2(d0), ex2(d1));
-                    acc[u != 0] = f2add(acc[u != 0], e2);
-                    if (u == 0) {  // -inf becomes the lowest finite number: e = 0 then, and e z = 0
-                        float z0, z1;
-                        f2unpack(z2, z0, z1);
-                        acc1 = f2fma(e2, f2pack(fmaxf(z0, -3.0e38f), fmaxf(z1, -3.0e38f)), acc1);
-                    }
+                for (int e = 0; e < VEC; ++e) {
+                    const float x = ex2(fmaf(z[e], k, -mk));
+                    a[e & 3] += x;
+                    if (u == 0) a1 = fmaf(x, fmaxf(z[e], -3.0e38f), a1);  // (-inf: 0 times a finite number)
                 }
+                if (u == 0) se += (a[0] + a[1]) + (a[2] + a[3]);
             }
-            float a0, a1;
-            f2unpack(acc[0], a0, a1);
-            se += a0 + a1;
-            s += a0 + a1;
-            f2unpack(acc[1], a0, a1);
-            s += a0 + a1;
-            f2unpack(acc1, a0, a1);
-            s1 += a0 + a1;
+            s += (a[0] + a[1]) + (a[2] + a[3]);
+            s1 += a1;
         }
         if (j >= again) {
             if (j == j0) __syncthreads();  // (s_bound is set)
             raise_bound(m, A.KL, tops, &s_bound);
-            again = j + (j - j0 + NT * UN);
+            again = j + 2 * (j - j0) + 2 * NT * UN;
         }
         // (a bound that is read late is a lower bound all the same)
         const uint64_t bound = __shfl_sync(FULL, *static_cast<volatile unsigned long long *>(&s_bound), 0);
