@@ -13,7 +13,8 @@
 // then the complement of the index, so one integer comparison orders by value
 // and then by smaller index.  The K-th largest of the threads' running maxima
 // bounds the K-th best from below; vectors are compared with that bound four
-// at a time, and few pass.  The bound is taken again whenever three times as much
+// at a time, and the indices of the few that pass are put aside: looking at
+// them at once, in the midst of the loop, took a third of the kernel's time.  The bound is taken again whenever three times as much
 // of the row has been seen; a candidate costs as much as 500 elements of the
 // sums (with the first bound alone the kernel took 81 us at 512 rows of
 // 151936).  Each warp keeps a list of its own; one that
@@ -33,7 +34,8 @@ namespace {
 constexpr int NT = BEAM_THREADS;
 constexpr int UN = 4;        // vectors of a thread per round
 constexpr int NW = NT / 32;
-constexpr int CAP = 192;     // candidates held by a warp
+constexpr int CAP = 384;     // candidates held by a warp: BEAM_MAX_K and a warp's vectors of 8 at least
+constexpr int QUEUE = 256;   // vectors put aside by a warp: two rounds' at least
 constexpr int SMEM_CAND = 2048;  // candidates that the join holds in shared memory
 
 // Order-preserving bits of a float (the two zeros are equal).
@@ -118,67 +120,53 @@ __device__ __forceinline__ int cut(uint64_t *list, int n, int keep, uint64_t *tm
     return m;
 }
 
-// Offer vector `raw` (elements at VEC ..) of every lane in `lanes` to the
-// warp's list of `count`: eight lanes (four of float32) look at one element
-// each.  Returns the list's new length; a cut raises *s_bound.
+// Look at the `queued` vectors that a warp has put aside: their elements that
+// reach the bound join the warp's list of `count`.  Returns the list's new
+// length; a cut raises *s_bound.
 template <typename T>
-__device__ __noinline__ int offer(const uint4 raw, int at, uint32_t lanes, uint64_t *list, int count, uint64_t bound, int keep,
-                                  uint64_t *tmp, unsigned long long *s_bound) {
+__device__ __noinline__ int drain(const unsigned char *row, uint32_t sh, int whole, int V, const int *queue, int queued, uint64_t *list,
+                                  int count, int keep, uint64_t *tmp, unsigned long long *s_bound) {
     constexpr int VEC = Store<T>::VEC;
     const int lane = threadIdx.x & 31;
-    while (lanes) {
-        const int src = __ffs(lanes) - 1;
-        lanes &= lanes - 1;
-        const uint32_t x = __shfl_sync(FULL, raw.x, src), y = __shfl_sync(FULL, raw.y, src), z = __shfl_sync(FULL, raw.z, src),
-                       w = __shfl_sync(FULL, raw.w, src);
-        const int v0 = __shfl_sync(FULL, at, src) * VEC;
-        const int e = lane & (VEC - 1), word = VEC == 8 ? e >> 1 : e;
-        const uint32_t u = word == 0 ? x : word == 1 ? y : word == 2 ? z : w;
-        const float f = __uint_as_float(VEC == 4 ? u : (e & 1) ? u & 0xffff0000u : u << 16);
-        const uint64_t key = make_key(f, v0 + e);
-        const uint32_t in = __ballot_sync(FULL, lane < VEC && f > -INFINITY && key >= bound);
-        if (!in) continue;
-        if (count + VEC > CAP) {
-            count = cut(list, count, keep, tmp);  // CAP - VEC >= keep: the list has `keep` keys
-            bound = max(bound, list[keep - 1]);
-            if (lane == 0) atomicMax(s_bound, static_cast<unsigned long long>(bound));
-        }
-        // (a key that the bound has passed meanwhile does no harm)
-        if ((in >> lane) & 1u) list[count + __popc(in & ((1u << lane) - 1u))] = key;
-        count += __popc(in);
-    }
     __syncwarp();
+    for (int i0 = 0; i0 < queued; i0 += 32) {
+        uint64_t bound = __shfl_sync(FULL, *static_cast<volatile unsigned long long *>(s_bound), 0);
+        if (count + 32 * VEC > CAP) {
+            count = cut(list, count, keep, tmp);
+            if (count == keep) {
+                bound = max(bound, list[keep - 1]);
+                if (lane == 0) atomicMax(s_bound, static_cast<unsigned long long>(bound));
+            }
+        }
+        const int at = i0 + lane < queued ? queue[i0 + lane] : -1;
+        const uint4 raw = at < 0 ? minus_inf_vec<T>() : at < whole ? row_vec<T>(row, sh, at) : row_tail<T>(row, at, V);
+        float z[VEC];
+        Store<T>::unpack(raw, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const uint64_t key = make_key(z[e], at * VEC + e);
+            const bool take = key >= bound && z[e] > -INFINITY;  // (not of a round that had a NaN: it may lie in this vector)
+            const uint32_t in = __ballot_sync(FULL, take);
+            if (take) list[count + __popc(in & ((1u << lane) - 1u))] = key;
+            count += __popc(in);
+        }
+        __syncwarp();
+    }
     return count;
 }
 
-// The keep-th largest of the block's values, as order-preserving bits, raises
-// *s_bound: each warp sorts its own, and a value's rank is its lane plus the
-// larger ones of the other warps (of equal ones those of lower warps).
-__device__ __noinline__ void raise_bound(float value, int keep, uint32_t (*tops)[32], unsigned long long *s_bound) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t mine = order_bits(value);
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int d = size >> 1; d > 0; d >>= 1) {
-            const uint32_t o = __shfl_xor_sync(FULL, mine, d);
-            const bool falling = (lane & size) == 0, low = (lane & d) == 0;
-            mine = falling == low ? max(mine, o) : min(mine, o);
-        }
-    tops[warp][lane] = mine;
-    __syncthreads();
-    int rank = lane;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w == warp) continue;
-        const uint32_t limit = w < warp ? mine : mine + 1;  // count values >= limit
-        int lo = 0;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            if (tops[w][lo + d - 1] >= limit) lo += d;
-        rank += lo + (lo == 31 && tops[w][31] >= limit ? 1 : 0);
-    }
-    if (rank == keep - 1) atomicMax(s_bound, static_cast<unsigned long long>(mine) << 32);
+// A lower bound of the keep-th largest of the block's values (for bfloat16 the
+// value itself) raises *s_bound: its leading bits one by one, by counting the
+// values that reach them.
+template <int BITS>
+__device__ __forceinline__ void raise_bound(float value, int keep, unsigned long long *s_bound) {
+    const uint32_t mine = order_bits(value);
+    uint32_t at = 0;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit >= (1u << (32 - BITS)); bit >>= 1)
+        if (__syncthreads_count(mine >= (at | bit)) >= keep) at |= bit;
+    // (not below -inf: what lies there is no number)
+    if (threadIdx.x == 0) atomicMax(s_bound, static_cast<unsigned long long>(max(at, order_bits(-INFINITY))) << 32);
     __syncthreads();
 }
 
@@ -187,7 +175,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
     __shared__ uint64_t lists[NW][CAP];
     __shared__ uint64_t tmps[NW][BEAM_MAX_K];
-    __shared__ uint32_t tops[NW][32];
+    __shared__ int queue[NW][QUEUE];
     __shared__ unsigned long long s_bound;
     __shared__ int s_bad, s_n[NW];
     __shared__ float s_m[NW];
@@ -230,7 +218,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     // where the row's weight lies, which is all that the correction for dk needs
     // to know (it is below 3e-7 of a score to begin with).
     float m = -INFINITY, mk = 0.f, s = 0.f, se = 0.f, s1 = 0.f;
-    int count = 0, again = j0;
+    int count = 0, queued = 0, again = j0;
     // one round: vectors j + tid, j + tid + NT, .. of the row
     auto round = [&](int j, uint4 (&raw)[UN]) {
         float top = -INFINITY;
@@ -271,8 +259,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
             s1 += a1;
         }
         if (j >= again) {
-            if (j == j0) __syncthreads();  // (s_bound is set)
-            raise_bound(m, A.KL, tops, &s_bound);
+            raise_bound<ES == 2 ? 16 : 20>(m, A.KL, &s_bound);
             again = j + 2 * (j - j0) + 2 * NT * UN;
         }
         // (a bound that is read late is a lower bound all the same)
@@ -281,9 +268,14 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         if (__any_sync(FULL, top >= zb)) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
-                const uint32_t lanes = __ballot_sync(FULL, Store<T>::vmax(raw[u]) >= zb);
-                if (lanes)
-                    count = offer<T>(raw[u], j + u * NT + tid, lanes, lists[warp], count, bound, A.KL, tmps[warp], &s_bound);
+                const bool take = Store<T>::vmax(raw[u]) >= zb;
+                const uint32_t in = __ballot_sync(FULL, take);
+                if (take) queue[warp][queued + __popc(in & ((1u << lane) - 1u))] = j + u * NT + tid;
+                queued += __popc(in);
+            }
+            if (queued > QUEUE - 32 * UN) {
+                count = drain<T>(base, sh, whole, A.V, queue[warp], queued, lists[warp], count, A.KL, tmps[warp], &s_bound);
+                queued = 0;
             }
         }
     };
@@ -312,40 +304,30 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         if (j + 2 * STEP < j1) fetch(j + 2 * STEP, one);
         round(j + STEP, two);
     }
-    count = cut(lists[warp], count, A.KL, tmps[warp]);
+    count = drain<T>(base, sh, whole, A.V, queue[warp], queued, lists[warp], count, A.KL, tmps[warp], &s_bound);
+    if (count > 2 * BEAM_MAX_K) count = cut(lists[warp], count, A.KL, tmps[warp]);
     if (lane == 0) s_n[warp] = count;
     float top = warp_allmax(m);
     if (lane == 0) s_m[warp] = top;
     __syncthreads();
-    // the warps' lists, each sorted, to one: the rank of a key is its place in
-    // its own list plus the larger ones of the others
-    for (int i = tid; i < NW * A.KL; i += NT) {
-        const int w = i / A.KL, e = i - w * A.KL;
-        if (e >= s_n[w]) continue;
-        const uint64_t key = lists[w][e];
-        int rank = e;
+    // the warps' lists to one: a key's place is the number of larger ones
+    int ends[NW], total = 0;
 #pragma unroll
-        for (int o = 0; o < NW; ++o) {
-            if (o == w) continue;
-            int lo = 0, hi = s_n[o];  // first place whose key is smaller
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (lists[o][mid] > key)
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            rank += lo;
-            if (rank >= A.KL) break;
+    for (int w = 0; w < NW; ++w) ends[w] = total += s_n[w];
+    for (int i = tid; i < total; i += NT) {
+        int w = 0;
+        for (; i >= ends[w]; ++w) {
         }
+        const uint64_t key = lists[w][i - (ends[w] - s_n[w])];
+        int rank = 0;
+        for (int o = 0; o < NW && rank < A.KL; ++o)
+#pragma unroll 4
+            for (int e = 0; e < s_n[o]; ++e) rank += lists[o][e] > key;
         if (rank < A.KL) {
             cz[rank] = order_float(static_cast<uint32_t>(key >> 32));
             cv[rank] = static_cast<int>(~static_cast<uint32_t>(key));
         }
     }
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) total += s_n[w];
     for (int i = total + tid; i < A.KL; i += NT) cv[i] = -1;
     top = -INFINITY;
 #pragma unroll
