@@ -45,7 +45,10 @@ bool device_sms(int &dev, int &sms) {
         (void)cudaGetLastError();
         return false;
     }
-    g_devices.push_back({dev, sms});
+    try {
+        g_devices.push_back({dev, sms});
+    } catch (...) {  // out of memory: asked again next time
+    }
     return true;
 }
 
@@ -65,7 +68,10 @@ int resident(int dev, const void *func, uint32_t smem, int threads) {
         (void)cudaGetLastError();
         n = 0;
     }
-    g_funcs.push_back({dev, func, smem, n});
+    try {
+        g_funcs.push_back({dev, func, smem, n});
+    } catch (...) {
+    }
     return n;
 }
 
@@ -146,6 +152,7 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
     p.mtiles = (p.rows + p.bm - 1) / p.bm;
     p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
+    if (p.max_tiles * a.Hkv > 0x7fffffffll) return MTP_ERR_INVALID_ARG;  // tiles of a sequence are counted in 32 bits
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
     const long long all = p.max_tiles * a.Hkv * (a.B > 0 ? a.B : 1);
     if (groups > all) groups = all;

@@ -108,6 +108,9 @@ ATTN = [
     ("bf16", 1, 6, 5, 1, 33, 16, [50], "random", None),
     ("bf16", 1, 2, 8, 2, 128, 16, [5003], "chain", None),
     ("bf16", 1, 64, 32, 1, 64, 64, [2000], "random", None),
+    ("bf16", 2, 64, 8, 1, 256, 32, [100, 64], "random", None),      # 512 rows of one key head
+    ("bf16", 1, 64, 40, 1, 64, 64, [130], "random", [61]),           # 2560 rows: ten row tiles
+    ("bf16", 2, 3, 128, 2, 128, 16, [77, 300], "random", None),
     ("f32", 1, 1, 4, 2, 64, 16, [0], "chain", None),
     ("f32", 4, 7, 8, 2, 64, 16, [1, 64, 65, 400], "random", [7, 1, 0, 5]),
     ("f32", 2, 64, 4, 1, 128, 24, [200, 77], "random", None),
@@ -123,7 +126,7 @@ def test_tree_attention(case):
     run_attention(attn_case(sum(lens) + T, dtype, B, T, Hq, Hkv, D, ps, lens, tree, nodes))
 
 
-@pytest.mark.parametrize("seed", range(24))
+@pytest.mark.parametrize("seed", range(40))
 def test_tree_attention_random(seed):
     rng = random.Random(1000 + seed)
     B, T, Hkv = rng.randint(1, 6), rng.choice([1, 2, 3, 5, 8, 16, 31, 64]), rng.choice([1, 2, 3])
