@@ -78,6 +78,7 @@ __device__ __forceinline__ int attn_groups(const TreeAttnArgs &A, long long W) {
 }
 // The first tile of group g's range (a 64-bit division only where it is needed).
 __device__ __forceinline__ long long attn_lo(long long W, int g, int groups) {
+    if (W == groups) return g;
     const unsigned long long x = static_cast<unsigned long long>(W) * g;
     return x >> 32 ? static_cast<long long>(x / groups) : static_cast<uint32_t>(x) / static_cast<uint32_t>(groups);
 }

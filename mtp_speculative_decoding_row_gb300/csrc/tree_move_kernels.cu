@@ -92,13 +92,10 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
         n = 0;
     }
     if (len < 0 || len > static_cast<long long>(A.max_pages) * A.page_size) flag = F_BAD_ID;
-    const int32_t *tok = A.tokens + static_cast<size_t>(b) * T, *tgt = A.target + static_cast<size_t>(b) * T;
-    if (tid < n) {
-        s_target[tid] = __ldg(tgt + tid);
-        s_token[tid] = __ldg(tok + tid);
-    }
-    __syncthreads();
+    const size_t o = static_cast<size_t>(b) * T;
     if (tid < 32) {
+        // everything that the walk needs, two nodes to a lane, loaded at once:
+        // what bounds a block is the number of loads that wait for another
         int up[2], mine[2];
         bool bad = false;
 #pragma unroll
@@ -107,12 +104,28 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
             up[e] = -2;
             mine[e] = 0;
             if (i < n) {
-                up[e] = A.parents ? __ldg(A.parents + static_cast<size_t>(b) * T + i) : i - 1;
-                mine[e] = s_token[i];
+                mine[e] = __ldg(A.tokens + o + i);
+                up[e] = A.parents ? __ldg(A.parents + o + i) : i - 1;
+                s_target[i] = __ldg(A.target + o + i);
+                s_token[i] = mine[e];
                 bad |= up[e] >= i || up[e] < -1 || (i == 0 && up[e] != -1);
             }
         }
+        // where tokens len, len + 1, .. go (as far as the table reaches)
+        int page[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long pos = static_cast<long long>(len) + tid + 32 * e;
+            page[e] = -1;
+            if (flag == 0 && tid + 32 * e < n && pos < static_cast<long long>(A.max_pages) * A.page_size) {
+                const int at = static_cast<int>(pos) / A.page_size;
+                page[e] = __ldg(A.table + static_cast<size_t>(b) * A.max_pages + at);
+                s_page[tid + 32 * e] = page[e];
+                s_off[tid + 32 * e] = static_cast<int>(pos) - at * A.page_size;
+            }
+        }
         if (__any_sync(FULL, bad)) flag |= F_BAD_ID;
+        __syncwarp();
         int count = 0;
         if (n > 0 && !flag) {
             int cur = 0;
@@ -125,16 +138,10 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
                 if (!(lo | hi)) break;
                 cur = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);  // a child comes after its parent: at most T steps
             }
-            if (len + static_cast<long long>(count) > static_cast<long long>(A.max_pages) * A.page_size) flag = F_BAD_ID;
-        }
-        __syncwarp();
-        // where the path goes
-        for (int j = tid; j < count && !flag; j += 32) {
-            const int pos = len + j, page = pos / A.page_size;
-            const int pid = __ldg(A.table + static_cast<size_t>(b) * A.max_pages + page);
-            if (pid < 0 || pid >= A.num_pages) flag = F_BAD_ID;
-            s_page[j] = pid;
-            s_off[j] = pos - page * A.page_size;
+            // no room for the path, or a page that is none
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (tid + 32 * e < count && (page[e] < 0 || page[e] >= A.num_pages)) flag |= F_BAD_ID;
         }
         flag = __reduce_or_sync(FULL, flag);
         if (flag) count = 0;
@@ -146,7 +153,6 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
     __syncthreads();
     const int count = s_count;
     if (blockIdx.y == 0) {
-        const size_t o = static_cast<size_t>(b) * T;
         for (int j = tid; j < T; j += COMMIT_THREADS) {
             A.path[o + j] = j < count ? s_path[j] : -1;
             A.out[o + j] = j + 1 < count ? s_token[s_path[j + 1]] : j + 1 == count ? s_target[s_path[j]] : -1;
