@@ -26,7 +26,8 @@
 //          of a piece their maxima, sums and outputs are joined
 //   ONE    heads of 256: TMEM holds one accumulator, so one group works, with
 //          two score buffers (the products of tile j + 1 run under the softmax
-//          of tile j)
+//          of tile j); warp 1 issues the products with the keys, warp 2 those
+//          with the values
 // The output accumulator is rescaled only when a row's maximum has risen by
 // more than 2^8 since the last time: until then the weights are taken
 // relative to the older maximum, which changes nothing but their scale.
@@ -186,7 +187,7 @@ __device__ __forceinline__ float sum4(const uint64_t (&acc)[2]) {
 // Block c's weights go to columns 16 c .. of the tile, over scores that have
 // been read.  The first half of them is announced as soon as it is there: the
 // product over those keys runs while the other half is made (trees of 64
-// nodes: 290 -> 261 us).
+// nodes: 290 -> 275 us).
 template <int CH>
 __device__ __forceinline__ void softmax_full(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, bool first, float &m,
                                              float &l, uint32_t o_bar, uint32_t o_phase, uint32_t half_bar, bool &ok) {
@@ -373,14 +374,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
             }
         }
-    } else if (warp <= C::GROUPS) {
+    } else if (warp < 3) {
         // -------------------------------------------------- products ----
         Ring r(A.slots);
-        const int g = warp - 1;      // the group of softmax warps; ONE: both score buffers
+        const int g = MODE == ONE ? 0 : warp - 1;  // the group of softmax warps
         const int qi = MODE == ROWS ? g : 0;
         const uint64_t qdesc = umma_desc(sq + qi * C::CH * qblock);
         uint32_t q_phase = 0;
-        int count0 = 0, count1 = 0;  // score tiles of buffer 0 and 1 (KEYS, ROWS: of the group, in count0)
+        int count = 0, other = 0;  // uses of the group's score buffer (ONE: of both buffers)
         // O += P V of a tile: its buffer, the use of it, its slot of the ring
         auto pv = [&](int buf, int use, const Ring &at, int steps, bool first) {
             ok = mbar_wait_bounded(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
@@ -427,11 +428,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         while (ok && walk.next(A, pc)) {
             bool bad;
             const int n = attn_nodes(A, pc.b, bad);
-            ok = mbar_wait_bounded(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
-            q_phase ^= 1u;
+            if (MODE != ONE || warp == 1) {
+                ok = mbar_wait_bounded(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
+                q_phase ^= 1u;
+            }
             // the tile whose weights' product is still to be issued
             bool have = false, old_first = false;
-            int old_steps = 0, old_buf = 0;
+            int old_steps = 0;
             Ring old(A.slots);
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
                 const Ring kr = r;
@@ -444,30 +447,32 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     valid = n > 0 ? n : 1;
                 else
                     attn_tile(A, pc.len, t, pos, valid);
-                const uint32_t idesc = umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false);
                 const int buf = MODE == ONE ? (t - pc.t0) & 1 : g;
-                // One buffer: its last weights have to be used before new scores
-                // go there.  Two: the scores first, unless their keys are not
-                // there yet.
-                if (have && (MODE != ONE || !__all_sync(FULL, mbar_test_wait(smem_addr(&ctl.full[kr.full()]), kr.phase())))) {
-                    pv(old_buf, MODE == ONE && old_buf ? count1 : count0, old, old_steps, old_first);
-                    have = false;
+                int &uses = MODE == ONE && buf ? other : count;
+                if (MODE == ONE && warp == 2) {  // the values' products
+                    ++uses;
+                    pv(buf, uses, vr, round16(valid) / 16, t == pc.t0);
+                    continue;
+                }
+                // the buffer's last weights have to be used before new scores go there
+                if (MODE == ONE) {
+                    if (uses > 0) ok = mbar_wait_bounded(smem_addr(&ctl.o_done[buf]), (uses - 1) & 1) && ok;
+                } else if (have) {
+                    pv(buf, uses, old, old_steps, old_first);
                 }
                 ok = mbar_wait_bounded(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
-                qk(buf, kr.slot, idesc);
-                if (MODE == ONE && have)
-                    pv(old_buf, old_buf ? count1 : count0, old, old_steps, old_first);
-                if (MODE == ONE && buf)
-                    ++count1;
-                else
-                    ++count0;
+                qk(buf, kr.slot, umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false));
+                ++uses;
                 have = true;
                 old_first = MODE == KEYS ? t - pc.t0 < 2 : t == pc.t0;
                 old = vr;
                 old_steps = round16(valid) / 16;
-                old_buf = buf;
+            }
+            if (MODE == ONE && warp == 2) {
+                ok = __all_sync(FULL, ok);
+                continue;
             }
             // all scores of the piece are on their way: its queries may go
             if (elect_one()) {
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     mbar_arrive(smem_addr(&ctl.q_empty[qi]));
             }
             __syncwarp();
-            if (ok && have) pv(old_buf, MODE == ONE && old_buf ? count1 : count0, old, old_steps, old_first);
+            if (MODE != ONE && ok && have) pv(g, count, old, old_steps, old_first);
         }
     } else if (warp == 3) {
         // --------------------------------------- new keys and values ----
