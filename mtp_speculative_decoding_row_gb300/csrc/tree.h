@@ -28,6 +28,7 @@ struct TreeAttnArgs {
     int rows;                // T * G: query rows of one (sequence, key head)
     int mtiles;              // row tiles of BM rows
     int groups;              // CTAs / mtiles: each group of CTAs walks one range of key tiles
+    int whole;               // units are not split: the groups share them out, not the tiles
     int bm;                  // query rows of one tile
     int ktile;               // keys of one tile
     int per_page;            // tiles of one page where pages are larger than a tile and no multiple of it, else 0

@@ -104,7 +104,8 @@ struct AttnPlan {
     int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0;
-    bool joins() const { return max_tiles > 1 && groups > 1; }
+    bool whole = false;       // units are not split
+    bool joins() const { return !whole && max_tiles > 1 && groups > 1; }
     size_t bytes() const { return joins() ? part_bytes + desc_bytes : desc_bytes; }
 };
 
@@ -154,7 +155,12 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
     if (p.max_tiles * a.Hkv > 0x7fffffffll) return MTP_ERR_INVALID_ARG;  // tiles of a sequence are counted in 32 bits
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
-    const long long all = p.max_tiles * a.Hkv * (a.B > 0 ? a.B : 1);
+    // Units of few tiles are not split, unless there are so many of them that
+    // their sizes should be evened out: a join takes as long as about six tiles
+    // on the tensor cores (5 us), or two of the other kernel.
+    const long long units = static_cast<long long>(a.Hkv) * (a.B > 0 ? a.B : 1);
+    p.whole = p.max_tiles <= (umma ? 6 : 2) && units <= 2 * groups;
+    const long long all = p.whole ? units : p.max_tiles * units;
     if (groups > all) groups = all;
     p.groups = static_cast<int>(groups < 1 ? 1 : groups);
     p.part_bytes = attn_slot_floats(p.bm, a.D) * 4 * 2 * p.groups * p.mtiles;
@@ -285,6 +291,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.mtiles = p.mtiles;
     A.groups = p.groups;
     A.bm = p.bm;
+    A.whole = p.whole;
     A.ktile = p.ktile;
     A.qrows = p.qrows;
     A.slots = p.slots;

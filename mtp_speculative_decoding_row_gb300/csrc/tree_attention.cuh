@@ -16,7 +16,9 @@
 // the lengths are, and a launch fits any lengths (a captured graph too).  A
 // unit that lies in several groups' ranges is joined afterwards from its
 // parts' running maxima, sums and unnormalised rows, in the order of the
-// groups: the result does not depend on which CTA ran first.
+// groups: the result does not depend on which CTA ran first.  Where no unit can
+// have more than a few tiles, whole units are dealt out instead and nothing is
+// joined: the second launch takes as long as several tiles.
 #pragma once
 
 #include "common.cuh"
@@ -92,15 +94,29 @@ struct AttnWalk {
     int len = 0, prefix = 0;
     bool begins = true;          // no piece was taken yet
 
-    // Returns the number of all tiles.
+    // Returns the number of all tiles (of all units where they are not split;
+    // hi and at count units then).
     __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
+        if (A.whole) {
+            const long long units = static_cast<long long>(A.B) * A.Hkv;
+            at = attn_lo(units, min(g, A.groups), A.groups);
+            hi = attn_lo(units, min(g + 1, A.groups), A.groups);
+            b = static_cast<int>(at / A.Hkv);
+            h = static_cast<int>(at - static_cast<long long>(b) * A.Hkv);
+            if (at < hi) read(A);
+            return units;
+        }
         const int lane = threadIdx.x & 31;
         const int per = (A.B + 31) / 32;
         const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
         long long sum = 0;
         bool bad;
 #pragma unroll 4
-        for (int i = b0; i < b1; ++i) sum += attn_prefix_tiles(A, attn_len(A, i, bad)) + 1;
+        for (int i = b0; i < b1; ++i) {
+            len = attn_len(A, i, bad);
+            prefix = attn_prefix_tiles(A, len);
+            sum += prefix + 1;
+        }
         sum *= A.Hkv;
         long long inc = sum;
 #pragma unroll
@@ -120,8 +136,10 @@ struct AttnWalk {
         int i = b0;
         if ((own >> lane) & 1u) {
             for (;; ++i) {
-                len = attn_len(A, i, bad);
-                prefix = attn_prefix_tiles(A, len);
+                if (per > 1) {  // (one sequence to a lane: they are here)
+                    len = attn_len(A, i, bad);
+                    prefix = attn_prefix_tiles(A, len);
+                }
                 const long long unit = static_cast<long long>(prefix + 1) * A.Hkv;
                 if (x < unit) break;  // (x lies in this lane's stretch)
                 x -= unit;
@@ -137,6 +155,12 @@ struct AttnWalk {
         return W;
     }
 
+    __device__ __forceinline__ void read(const TreeAttnArgs &A) {
+        bool bad;
+        len = attn_len(A, b, bad);
+        prefix = attn_prefix_tiles(A, len);
+    }
+
     // The next piece, or false at the end of the range.
     __device__ __forceinline__ bool next(const TreeAttnArgs &A, AttnPiece &p) {
         if (at >= hi) return false;
@@ -147,6 +171,15 @@ struct AttnWalk {
         p.first = begins;
         begins = false;
         p.t0 = tile;
+        if (A.whole) {
+            p.t1 = prefix + 1;
+            if (++at < hi && ++h == A.Hkv) {
+                h = 0;
+                ++b;
+                read(A);
+            }
+            return true;
+        }
         const long long left = hi - at;
         p.t1 = static_cast<int>(tile + left < prefix + 1 ? tile + left : prefix + 1);
         at += p.t1 - p.t0;
@@ -156,9 +189,7 @@ struct AttnWalk {
             if (++h == A.Hkv) {
                 h = 0;
                 ++b;
-                bool bad;
-                len = attn_len(A, b, bad);
-                prefix = attn_prefix_tiles(A, len);
+                read(A);
             }
         }
         return true;
@@ -181,6 +212,7 @@ __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch
 // next ones (at most one does): {b, h, parts, slot of the first part}.
 __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, long long W, long long hi,
                                                 const AttnPiece &last) {
+    if (A.whole) return;
     int *d = A.desc + static_cast<size_t>(g) * ATTN_DESC;
     if (last.t0 != 0 || last.t1 == 0 || last.t1 == last.prefix + 1) {  // (t1 = 0: the group had no piece)
         d[2] = 0;
