@@ -366,7 +366,8 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  *   projection and the cache may have its heads outside its tokens)
  *   out [B, T, Hq, D] dtype, lse [B, T, Hq] float32 or NULL, contiguous
  *   row_flags [B] or NULL.
- * Requirements: 1 <= T <= MTP_MAX_NODES, Hq a multiple of Hkv, 1 <= D <= 256,
+ * Requirements: 1 <= T <= MTP_MAX_NODES, Hq a multiple of Hkv (at most
+ * 4096 times), 1 <= D <= 256,
  * 0 < scale, max_pages * page_size < 2^31 - 2^16 (else MTP_ERR_INVALID_ARG);
  * pointers aligned to their elements (else MTP_ERR_MISALIGNED).  Scores, softmax statistics
  * and outputs are accumulated in float32; with bfloat16 storage the softmax

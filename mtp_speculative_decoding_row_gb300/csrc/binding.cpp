@@ -170,8 +170,8 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                       page = kc.size(1), most = table.size(1);
         const at::ScalarType dt = q.scalar_type();
         s.dtype = dtype_code(q);
-        if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0)
-            value_error("q has " + std::to_string(Hq) + " heads: not a multiple of the " + std::to_string(Hkv) + " of k_new");
+        if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 4096)
+            value_error("q has " + std::to_string(Hq) + " heads: not a multiple (up to 4096) of the " + std::to_string(Hkv) + " of k_new");
         if (T < 1 || T > MTP_MAX_NODES)
             value_error("trees have 1 to " + std::to_string(MTP_MAX_NODES) + " nodes, got " + std::to_string(T));
         if (D < 1 || D > 256) value_error("heads have 1 to 256 elements, got " + std::to_string(D));

@@ -24,6 +24,7 @@ struct TreeAttnArgs {
     int32_t *desc;           // ATTN_DESC ints per group: the unit to join (see tree_attention.cuh)
     int64_t qs[3], ks[3], vs[3], kcs[3], vcs[3];  // element strides: (b, t, h) and (page, token, head)
     int B, T, Hq, Hkv, D, G;
+    uint32_t g_inverse;      // ceil(2^32 / G); 0 for G = 1
     int num_pages, page_size, max_pages;
     int rows;                // T * G: query rows of one (sequence, key head)
     int mtiles;              // row tiles of BM rows

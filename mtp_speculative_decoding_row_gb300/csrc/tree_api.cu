@@ -111,7 +111,7 @@ struct AttnPlan {
 
 int attn_sizes(const mtp_tree_attention_args &a) {
     if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
-    if (a.B < 0 || a.T < 1 || a.T > MTP_MAX_NODES || a.Hkv < 1 || a.Hq < 1 || a.Hq % a.Hkv != 0 || a.D < 1 || a.D > 256 ||
+    if (a.B < 0 || a.T < 1 || a.T > MTP_MAX_NODES || a.Hkv < 1 || a.Hq < 1 || a.Hq % a.Hkv != 0 || a.Hq / a.Hkv > 4096 || a.D < 1 || a.D > 256 ||
         a.num_pages < 1 || a.page_size < 1 || a.max_pages < 1 || !(a.scale > 0.f) || a.scale > 1e30f)
         return MTP_ERR_INVALID_ARG;
     if (static_cast<long long>(a.max_pages) * a.page_size > 0x7fff0000ll || a.B > (1 << 20) || a.Hq > (1 << 16))
@@ -268,6 +268,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.Hkv = a.Hkv;
     A.D = a.D;
     A.G = a.Hq / a.Hkv;
+    A.g_inverse = A.G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + A.G - 1) / A.G);
     A.num_pages = a.num_pages;
     A.page_size = a.page_size;
     A.max_pages = a.max_pages;

@@ -44,6 +44,12 @@ __device__ __forceinline__ int attn_nodes(const TreeAttnArgs &A, int b, bool &ba
     return bad ? 0 : n;
 }
 
+// The node of query row r = node G + head: r / G by multiplication (r < 64 G and
+// G <= 4096, so r G < 2^32 and the quotient is exact).
+__device__ __forceinline__ int node_of(const TreeAttnArgs &A, int r) {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(r), A.g_inverse)) + (A.G == 1 ? r : 0);
+}
+
 // Tiles of cached keys of a sequence of `len` tokens.  Tiles follow one another
 // every ktile keys -- whole pages, or equal parts of one -- except where pages
 // are larger than a tile and no multiple of it (per_page > 0): there every

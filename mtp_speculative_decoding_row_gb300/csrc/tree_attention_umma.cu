@@ -96,6 +96,14 @@ struct Ring {
     __device__ __forceinline__ uint32_t phase() const { return (lap >> 1) & 1; }  // its parity
 };
 
+// Wait for an mbarrier's phase, 2 s at most.  The first tries are inline, the
+// rest is one function for all of the kernel's waits: every byte of code counts
+// here (see softmax_part).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) { return mbar_wait_spin(bar, parity); }
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+}
+
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
 
 // The largest of three (NaN only if all are).
@@ -147,7 +155,7 @@ __device__ __forceinline__ void rescale(float top, bool first, float &m, float &
     }
     const bool up = top > m + RESCALE;
     if (!__any_sync(FULL, up)) return;
-    ok = mbar_wait_bounded(o_bar, o_phase) && ok;  // the products before this tile
+    ok = wait_for(o_bar, o_phase) && ok;  // the products before this tile
     __syncwarp();
     tmem_fence_after_sync();
     const float f = up ? ex2(m - top) : 1.f;
@@ -257,6 +265,23 @@ __device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, i
     tmem_wait_st();
 }
 
+// Values that are not finite, of the nodes in `seen`, added to columns c0 .. c1
+// of one finished row (`part`: of a partial result): the products took them as
+// zeros.
+__device__ __noinline__ void add_far_values(float *part, bf16_t *out, const bf16_t *v, int64_t stride, uint64_t seen, int c0, int c1) {
+    for (; seen; seen &= seen - 1) {
+        const bf16_t *row = v + (__ffsll(static_cast<long long>(seen)) - 1) * stride;
+        for (int c = c0; c < c1; ++c) {
+            const float x = __uint_as_float(static_cast<uint32_t>(row[c].bits) << 16);
+            if (fabsf(x) < INFINITY) continue;
+            if (part)
+                part[c] += x;
+            else
+                out[c].bits = static_cast<uint16_t>(bf16x2(__uint_as_float(static_cast<uint32_t>(out[c].bits) << 16) + x, 0.f));
+        }
+    }
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     attn_umma_impl(const __grid_constant__ TreeAttnArgs A, const __grid_constant__ CUtensorMap kmap,
@@ -339,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
                 if (t == pc.prefix) {  // the loaders fill these two slots once they are free
                     for (int i = 0; i < 2; ++i) {
-                        if (r.lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
+                        if (r.lap) ok = wait_for(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                         r.step();
                     }
                     ok = __all_sync(FULL, ok);
@@ -354,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 const int mine = lane < pages ? attn_page(A, pc.b, page0 + lane) : 0;  // at most BN / 8 pages
                 for (int kv = 0; kv < 2; ++kv) {
                     // (the first use of every slot needs no wait)
-                    if (r.lap) ok = mbar_wait_bounded(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
+                    if (r.lap) ok = wait_for(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                     ok = __all_sync(FULL, ok);
                     if (!ok) break;
                     const uint32_t full = smem_addr(&ctl.full[r.full()]), dst = ring0 + r.slot * C::SLOT;
@@ -384,8 +409,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         int count = 0, other = 0;  // uses of the group's score buffer (ONE: of both buffers)
         // O += P V of a tile: its buffer, the use of it, its slot of the ring
         auto pv = [&](int buf, int use, const Ring &at, int steps, bool first) {
-            ok = mbar_wait_bounded(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
-            ok = mbar_wait_bounded(smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
+            ok = wait_for(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
+            ok = wait_for(smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
             ok = __all_sync(FULL, ok);
             if (!ok) return;
             tmem_fence_after_sync();
@@ -399,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     if (k < steps) step(k);
             }
             __syncwarp();
-            ok = mbar_wait_bounded(smem_addr(&ctl.p_full[buf]), (use - 1) & 1) && ok;
+            ok = wait_for(smem_addr(&ctl.p_full[buf]), (use - 1) & 1) && ok;
             ok = __all_sync(FULL, ok);
             if (!ok) return;
             tmem_fence_after_sync();
@@ -429,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             bool bad;
             const int n = attn_nodes(A, pc.b, bad);
             if (MODE != ONE || warp == 1) {
-                ok = mbar_wait_bounded(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
+                ok = wait_for(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
                 q_phase ^= 1u;
             }
             // the tile whose weights' product is still to be issued
@@ -456,11 +481,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
                 // the buffer's last weights have to be used before new scores go there
                 if (MODE == ONE) {
-                    if (uses > 0) ok = mbar_wait_bounded(smem_addr(&ctl.o_done[buf]), (uses - 1) & 1) && ok;
+                    if (uses > 0) ok = wait_for(smem_addr(&ctl.o_done[buf]), (uses - 1) & 1) && ok;
                 } else if (have) {
                     pv(buf, uses, old, old_steps, old_first);
                 }
-                ok = mbar_wait_bounded(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
+                ok = wait_for(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
                 qk(buf, kr.slot, umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false));
@@ -494,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             attn_len(A, b, bad_len);
             const int n = attn_nodes(A, b, bad_nodes);
             if (np >= 4) {
-                ok = mbar_wait_bounded(smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
+                ok = wait_for(smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
@@ -507,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             }
             uint64_t poison = 0;
             if (pc.t1 > pc.prefix) {
-                ok = mbar_wait_bounded(smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
+                ok = wait_for(smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
                 ++grants;
                 for (int kv = 0; kv < 2; ++kv) {
                     unsigned char *dst = ring + r.slot * C::SLOT;
@@ -519,15 +544,16 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     // is not finite (its rows get it later).
                     const int fill = (kv ? round16(n > 0 ? n : 1) : n) * (D / 8);
                     if (ok) {
-                        for (int i0 = lane; i0 < fill; i0 += 32 * 8) {
-                            uint4 y[8];
+#pragma unroll 1
+                        for (int i0 = lane; i0 < fill; i0 += 32 * 4) {
+                            uint4 y[4];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 4; ++e) {
                                 const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
                                 y[e] = j < n ? __ldg(reinterpret_cast<const uint4 *>(src + j * st[1]) + u) : make_uint4(0u, 0u, 0u, 0u);
                             }
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 4; ++e) {
                                 const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
                                 if (i0 + 32 * e >= fill) break;
                                 if (kv) {
@@ -570,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const int lrow = wt + (MODE == ROWS ? 128 * wg : 0);  // row of the CTA's tile
         const bool live = lrow < rows;
         const bool busy = lrow - lane < rows;           // the warp has rows
-        const int rr = row0 + lrow, node = rr / A.G;
+        const int rr = row0 + lrow, node = node_of(A, rr);
         const uint32_t o_addr = lanes + C::O_COL + (MODE == ONE ? 0 : wg * D);
         const int qi = MODE == ROWS ? wg : 0;
         Ring r(A.slots);
@@ -579,20 +605,21 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         // The queries of piece `np` into shared memory, by the threads that
         // arrive on q_full[qi], once the scores of the piece before are done.
         auto load_q = [&](const AttnPiece &p, int np) {
-            constexpr int LOAD = MODE == KEYS ? 256 : 128, AHEAD = 8;
+            constexpr int LOAD = MODE == KEYS ? 256 : 128, AHEAD = 4;
             const int lt = MODE == KEYS ? tid - 128 : wt;
             const int q0 = MODE == ROWS ? 128 * wg : 0, vecs = max(0, min(rows - q0, 128)) * (D / 8);
             const bf16_t *src = static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2];
             bool waited = np == 0;
+#pragma unroll 1
             for (int i0 = lt; i0 < vecs || !waited; i0 += LOAD * AHEAD) {
                 uint4 x[AHEAD];
 #pragma unroll
                 for (int e = 0; e < AHEAD; ++e) {
-                    const int i = i0 + e * LOAD, row = row0 + q0 + i / (D / 8), t = row / A.G;
+                    const int i = i0 + e * LOAD, row = row0 + q0 + i / (D / 8), t = node_of(A, row);
                     if (i < vecs) x[e] = __ldg(reinterpret_cast<const uint4 *>(src + t * A.qs[1] + (row - t * A.G) * A.qs[2]) + i % (D / 8));
                 }
                 if (!waited) {
-                    ok = mbar_wait_bounded(smem_addr(&ctl.q_empty[qi]), (np - 1) & 1) && ok;
+                    ok = wait_for(smem_addr(&ctl.q_empty[qi]), (np - 1) & 1) && ok;
                     waited = true;
                 }
 #pragma unroll
@@ -606,9 +633,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             mbar_arrive(smem_addr(&ctl.q_full[qi]));
             ok = __all_sync(FULL, ok);
         };
-        bool more = walk.next(A, pc);
-        if (more) load_q(pc, 0);
-        for (int np = 0; ok && more; ++np) {
+        // (a turn before the first piece loads its queries: this way there is one
+        // copy of load_q)
+        AttnPiece next;
+        bool more = true;
+        for (int np = -1; ok && more; ++np) {
+            pc = next;
+            if (np < 0) {
+                more = walk.next(A, next);
+                if (more) load_q(next, 0);
+                continue;
+            }
             const int b = pc.b, h = pc.h;
             bool bad;
             const int n = attn_nodes(A, b, bad);
@@ -622,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 const int buf = MODE == ONE ? (t - pc.t0) & 1 : wg;
                 const int use = MODE == ONE && buf ? count1 : count0;
                 const uint32_t s_addr = lanes + buf * C::S_COL;
-                ok = mbar_wait_bounded(smem_addr(&ctl.s_full[buf]), use & 1) && ok;
+                ok = wait_for(smem_addr(&ctl.s_full[buf]), use & 1) && ok;
                 tmem_fence_after_sync();
                 // the product before this one into the accumulator
                 const uint32_t o_bar = smem_addr(&ctl.o_done[MODE == ONE ? buf ^ 1 : wg]);
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 uint64_t lo = ~0ull, hi = ~0ull;
                 const bool tree = t == pc.prefix;
                 if (tree) {
-                    ok = mbar_wait_bounded(smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
+                    ok = wait_for(smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
                     lo = live && node < n ? ctl.mask[np & 3][node] : 0ull;
                 } else {
                     int pos;
@@ -654,7 +689,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     // to be a number.  (ROWS: each group sees to it for its own
                     // product; both write the same.)
                     const int end = round16(valid);
-                    ok = mbar_wait_bounded(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
+                    ok = wait_for(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
                     for (int i = wt; i < (end - valid) * (D / 8); i += 128) {
                         const int j = valid + i / (D / 8), u = i % (D / 8);
                         *reinterpret_cast<uint4 *>(ring + vr.slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
@@ -673,15 +708,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 ok = __all_sync(FULL, ok);
             }
             if (!ok) break;
-            AttnPiece next;
             more = walk.next(A, next);
             if (more) load_q(next, np + 1);
             // ------------------------------------------------ results ----
-            ok = mbar_wait_bounded(smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
+            ok = wait_for(smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
             if (!first) {
                 const int buf = MODE == ONE ? (pc.t1 - 1 - pc.t0) & 1 : wg;
                 const int use = MODE == ONE && buf ? count1 : count0;
-                ok = mbar_wait_bounded(smem_addr(&ctl.o_done[buf]), (use - 1) & 1) && ok;
+                ok = wait_for(smem_addr(&ctl.o_done[buf]), (use - 1) & 1) && ok;
             }
             ok = __all_sync(FULL, ok);
             if (!ok) break;
@@ -695,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             tmem_fence_before_sync();
             if (MODE == KEYS) {
                 mbar_arrive(smem_addr(&ctl.stats));
-                ok = mbar_wait_bounded(smem_addr(&ctl.stats), join_phase) && ok;
+                ok = wait_for(smem_addr(&ctl.stats), join_phase) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
@@ -739,17 +773,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     } else {
                         tmem_wait_ld32(o);
                     }
-                    if (seen) {  // values that are not finite, of nodes that this row sees
-                        const bf16_t *v = static_cast<const bf16_t *>(A.v_new) + b * A.vs[0] + h * A.vs[2];
-                        for (int j = 0; j < n; ++j) {
-                            if (!((seen >> j) & 1ull)) continue;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = __uint_as_float(static_cast<uint32_t>(v[j * A.vs[1] + c + i].bits) << 16);
-                                if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                            }
-                        }
-                    }
                     if (!mine) continue;
                     if (whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16_t *>(A.out) + at * D + c);
@@ -766,6 +789,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                         for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
+                if (mine && seen)
+                    add_far_values(whole ? nullptr : slot + 2 * BM + static_cast<size_t>(lrow) * D,
+                                   static_cast<bf16_t *>(A.out) + at * D, static_cast<const bf16_t *>(A.v_new) + b * A.vs[0] + h * A.vs[2],
+                                   A.vs[1], seen, c0, c1);
                 if (mine && c0 == 0 && c1 > 0) {
                     if (!whole) {
                         slot[lrow] = m;
@@ -779,11 +806,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             mbar_arrive(smem_addr(&ctl.done[np & 3]));
             if (MODE == KEYS) {  // the next piece's products may write the accumulators
                 mbar_arrive(smem_addr(&ctl.joined));
-                ok = mbar_wait_bounded(smem_addr(&ctl.joined), join_phase) && ok;
+                ok = wait_for(smem_addr(&ctl.joined), join_phase) && ok;
                 join_phase ^= 1u;
                 ok = __all_sync(FULL, ok);
             }
-            pc = next;
         }
     }
     // ---------------------------------------------------------- the end ----

@@ -72,6 +72,13 @@ def test_tree_attention_refusals(new, error, text):
         mtp.mtp_tree_attention(**attn_args(**new))
 
 
+def test_tree_attention_most_heads_of_one_key_head():
+    a = attn_args(q=torch.zeros(2, 3, 4097, 8), k_new=torch.zeros(2, 3, 1, 8), v_new=torch.zeros(2, 3, 1, 8),
+                  k_cache=torch.zeros(5, 16, 1, 8), v_cache=torch.zeros(5, 16, 1, 8))
+    with pytest.raises(ValueError, match="up to 4096"):
+        mtp.mtp_tree_attention(**a)
+
+
 @pytest.mark.parametrize("new, error, text", [
     (dict(logits=torch.zeros(2, 3, 10, dtype=torch.float64)), TypeError, "float32 or bfloat16"),
     (dict(logits=torch.zeros(2, 30)), ValueError, "dimensions"),
