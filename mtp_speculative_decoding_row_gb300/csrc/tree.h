@@ -33,7 +33,7 @@ struct TreeAttnArgs {
     int bm;                  // query rows of one tile
     int ktile;               // keys of one tile
     int per_page;            // tiles of one page where pages are larger than a tile and no multiple of it, else 0
-    int qrows, slots;        // tensor-core kernel: query rows in shared memory (a multiple of 8), slots of its ring
+    int qrows, qbufs, slots; // tensor-core kernel: query rows in shared memory (a multiple of 8), buffers for them, slots of its ring
     float scale_log2;        // scale * log2(e)
     int vec;                 // SIMT kernel: 16-byte loads are aligned
 };
@@ -52,7 +52,7 @@ uint32_t attn_simt_smem(int D);
 constexpr uint32_t UMMA_SMEM = 232448;  // 227 KB per CTA
 struct UmmaPlan {
     const void *func;
-    int threads, bm, qrows, slots;
+    int threads, bm, qrows, qbufs, slots;
     uint32_t smem;
 };
 UmmaPlan attn_umma_plan(int D, int rows);

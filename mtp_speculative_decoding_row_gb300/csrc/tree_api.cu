@@ -101,7 +101,7 @@ bool good_dtype(int d) { return d == MTP_DTYPE_F32 || d == MTP_DTYPE_BF16; }
 struct AttnPlan {
     const void *func = nullptr;
     uint32_t smem = 0;
-    int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, slots = 0;
+    int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0;
     bool whole = false;       // units are not split
@@ -138,6 +138,7 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
         p.threads = u.threads;
         p.bm = u.bm;
         p.qrows = u.qrows;
+        p.qbufs = u.qbufs;
         p.slots = u.slots;
         const int bn = attn_umma_bn(a.D);
         p.per_page = a.page_size > bn && a.page_size % bn != 0 ? (a.page_size + bn - 1) / bn : 0;
@@ -295,6 +296,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.whole = p.whole;
     A.ktile = p.ktile;
     A.qrows = p.qrows;
+    A.qbufs = p.qbufs;
     A.slots = p.slots;
     A.per_page = p.per_page;
     const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, &kmap, &vmap);

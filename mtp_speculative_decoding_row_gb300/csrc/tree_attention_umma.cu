@@ -282,15 +282,28 @@ __device__ __noinline__ void add_far_values(float *part, bf16_t *out, const bf16
     }
 }
 
+// Start copies of `rows` query rows from row `row` on, by `threads` threads, this
+// being number i.
+template <int D>
+__device__ __noinline__ void copy_queries(const bf16_t *q, const TreeAttnArgs &A, int row, int rows, uint32_t dst, int i, int threads) {
+    constexpr int VECS = D / 8;
+#pragma unroll 1
+    for (; i < rows * VECS; i += threads) {
+        const int r = i / VECS, u = i % VECS, t = node_of(A, row + r);
+        cp_async16(dst + (u >> 3) * A.qrows * 128 + sw128(r, u & 7), q + t * A.qs[1] + (row + r - t * A.G) * A.qs[2] + 8 * u);
+    }
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     attn_umma_impl(const __grid_constant__ TreeAttnArgs A, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D, MODE>;
     constexpr int NT = C::NT, BM = MODE == ROWS ? 256 : 128;
-    // queries (blocks of 64 elements x qrows rows; in ROWS mode twice), ring, control
+    // queries (blocks of 64 elements x qrows rows, once or twice), ring, control
     extern __shared__ __align__(1024) unsigned char smem[];
-    const uint32_t qblock = A.qrows * 128, qbytes = qblock * C::CH * (MODE == ROWS ? 2 : 1);
+    const int qbufs = MODE == ROWS ? 2 : A.qbufs;  // ROWS: one for each group
+    const uint32_t qblock = A.qrows * 128, qbytes = qblock * C::CH * qbufs;
     Control &ctl = *reinterpret_cast<Control *>(smem + qbytes + C::SLOT * A.slots);
     unsigned char *ring = smem + qbytes;
     const uint32_t sq = smem_addr(smem), ring0 = sq + qbytes;
@@ -332,10 +345,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     // Rows of the query tile that no query fills.  (The product reads 128 rows
     // of each block whatever qrows is: what lies behind them gives rows that
     // nobody looks at.)
-    for (int i = tid; i < (A.qrows * (MODE == ROWS ? 2 : 1) - rows) * (D / 8); i += NT) {
-        const int r = rows + i / (D / 8), u = i % (D / 8);
-        *reinterpret_cast<uint4 *>(smem + ((r >> 7) * C::CH + (u >> 3)) * qblock + sw128(r & 127, u & 7)) =
-            make_uint4(0u, 0u, 0u, 0u);
+    for (int buf = 0; buf < qbufs; ++buf) {
+        const int used = MODE == ROWS ? max(0, min(rows - 128 * buf, 128)) : rows;
+        for (int i = tid; i < (A.qrows - used) * (D / 8); i += NT) {
+            const int r = used + i / (D / 8), u = i % (D / 8);
+            *reinterpret_cast<uint4 *>(smem + (buf * C::CH + (u >> 3)) * qblock + sw128(r, u & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     fence_proxy_async();
     tmem_fence_before_sync();
@@ -403,8 +418,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         // -------------------------------------------------- products ----
         Ring r(A.slots);
         const int g = MODE == ONE ? 0 : warp - 1;  // the group of softmax warps
-        const int qi = MODE == ROWS ? g : 0;
-        const uint64_t qdesc = umma_desc(sq + qi * C::CH * qblock);
+        int qi = MODE == ROWS ? g : 0;
         uint32_t q_phase = 0;
         int count = 0, other = 0;  // uses of the group's score buffer (ONE: of both buffers)
         // O += P V of a tile: its buffer, the use of it, its slot of the ring
@@ -440,6 +454,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         auto qk = [&](int buf, int slot, uint32_t idesc) {
             tmem_fence_after_sync();
             if (elect_one()) {
+                const uint64_t qdesc = umma_desc(sq + qi * C::CH * qblock);
                 const uint64_t k = umma_desc(ring0 + slot * C::SLOT);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
@@ -455,7 +470,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             const int n = attn_nodes(A, pc.b, bad);
             if (MODE != ONE || warp == 1) {
                 ok = wait_for(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
-                q_phase ^= 1u;
             }
             // the tile whose weights' product is still to be issued
             bool have = false, old_first = false;
@@ -507,6 +521,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     mbar_arrive(smem_addr(&ctl.q_empty[qi]));
             }
             __syncwarp();
+            if (MODE != ROWS && A.qbufs == 2) {
+                q_phase ^= static_cast<uint32_t>(qi);
+                qi ^= 1;
+            } else {
+                q_phase ^= 1u;
+            }
             if (MODE != ONE && ok && have) pv(g, count, old, old_steps, old_first);
         }
     } else if (warp == 3) {
@@ -598,52 +618,32 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const bool busy = lrow - lane < rows;           // the warp has rows
         const int rr = row0 + lrow, node = node_of(A, rr);
         const uint32_t o_addr = lanes + C::O_COL + (MODE == ONE ? 0 : wg * D);
-        const int qi = MODE == ROWS ? wg : 0;
         Ring r(A.slots);
         int count0 = 0, count1 = 0;                     // uses of the group's score buffer (ONE: of both)
         uint32_t join_phase = 0;
-        // The queries of piece `np` into shared memory, by the threads that
-        // arrive on q_full[qi], once the scores of the piece before are done.
-        auto load_q = [&](const AttnPiece &p, int np) {
-            constexpr int LOAD = MODE == KEYS ? 256 : 128, AHEAD = 4;
-            const int lt = MODE == KEYS ? tid - 128 : wt;
-            const int q0 = MODE == ROWS ? 128 * wg : 0, vecs = max(0, min(rows - q0, 128)) * (D / 8);
-            const bf16_t *src = static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2];
-            bool waited = np == 0;
-#pragma unroll 1
-            for (int i0 = lt; i0 < vecs || !waited; i0 += LOAD * AHEAD) {
-                uint4 x[AHEAD];
-#pragma unroll
-                for (int e = 0; e < AHEAD; ++e) {
-                    const int i = i0 + e * LOAD, row = row0 + q0 + i / (D / 8), t = node_of(A, row);
-                    if (i < vecs) x[e] = __ldg(reinterpret_cast<const uint4 *>(src + t * A.qs[1] + (row - t * A.G) * A.qs[2]) + i % (D / 8));
-                }
-                if (!waited) {
-                    ok = wait_for(smem_addr(&ctl.q_empty[qi]), (np - 1) & 1) && ok;
-                    waited = true;
-                }
-#pragma unroll
-                for (int e = 0; e < AHEAD; ++e) {
-                    const int i = i0 + e * LOAD, row = i / (D / 8), u = i % (D / 8);
-                    if (i < vecs && ok)
-                        *reinterpret_cast<uint4 *>(smem + (qi * C::CH + (u >> 3)) * qblock + sw128(row, u & 7)) = x[e];
-                }
-            }
-            fence_proxy_async();
-            mbar_arrive(smem_addr(&ctl.q_full[qi]));
+        // The queries of piece `np`: copies into shared memory are started, by the
+        // threads that arrive on q_full, once the scores of the piece before that
+        // were in this buffer are done.
+        const int depth = MODE == ROWS ? 1 : A.qbufs;
+        auto copy_q = [&](const AttnPiece &p, int np) {
+            const int qi = MODE == ROWS ? wg : np & (depth - 1);
+            if (np >= depth) ok = wait_for(smem_addr(&ctl.q_empty[qi]), (np / depth - 1) & 1) && ok;
+            const int q0 = MODE == ROWS ? 128 * wg : 0;
             ok = __all_sync(FULL, ok);
+            if (ok)
+                copy_queries<D>(static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2], A,
+                                row0 + q0, min(rows - q0, 128), sq + qi * C::CH * qblock, MODE == KEYS ? tid - 128 : wt,
+                                MODE == KEYS ? 256 : 128);
         };
-        // (a turn before the first piece loads its queries: this way there is one
-        // copy of load_q)
-        AttnPiece next;
+        // (the turn before the first piece only loads its queries)
+        AttnPiece next = {};
         bool more = true;
         for (int np = -1; ok && more; ++np) {
             pc = next;
-            if (np < 0) {
-                more = walk.next(A, next);
-                if (more) load_q(next, 0);
-                continue;
-            }
+            more = walk.next(A, next);
+            // with two buffers the next queries are copied during this piece
+            const bool early = np < 0 || depth == 2;
+            if (more && early) copy_q(next, np + 1);
             const int b = pc.b, h = pc.h;
             bool bad;
             const int n = attn_nodes(A, b, bad);
@@ -708,8 +708,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 ok = __all_sync(FULL, ok);
             }
             if (!ok) break;
-            more = walk.next(A, next);
-            if (more) load_q(next, np + 1);
+            if (more) {
+                if (!early) copy_q(next, np + 1);
+                cp_async_wait_all();
+                fence_proxy_async();
+                mbar_arrive(smem_addr(&ctl.q_full[MODE == ROWS ? wg : (np + 1) & (depth - 1)]));
+                if (!ok) break;
+            }
+            if (np < 0) continue;
             // ------------------------------------------------ results ----
             ok = wait_for(smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
             if (!first) {
@@ -852,15 +858,26 @@ auto pick(int D, int mode, F f) {
 
 int attn_umma_bn(int D) { return D == 256 ? 64 : 128; }
 
+// Two buffers of queries where they fit beside at least six slots of the ring
+// (or as many as go in with one buffer).
 UmmaPlan attn_umma_plan(int D, int rows) {
     UmmaPlan p;
     const int mode = D == 256 ? ONE : rows > 128 ? ROWS : KEYS;
     p.bm = mode == ROWS ? 256 : 128;
     p.qrows = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
-    const uint32_t q = static_cast<uint32_t>(p.qrows) * D * 2 * (mode == ROWS ? 2 : 1);
+    uint32_t q = static_cast<uint32_t>(p.qrows) * D * 2 * (mode == ROWS ? 2 : 1);
     const uint32_t slot = static_cast<uint32_t>(attn_umma_bn(D)) * D * 2;
-    p.slots = static_cast<int>((UMMA_SMEM - sizeof(Control) - q) / slot);
-    if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
+    auto fit = [&](uint32_t queries) {
+        const int n = static_cast<int>((UMMA_SMEM - sizeof(Control) - queries) / slot);
+        return n < MAX_SLOTS ? n : MAX_SLOTS;
+    };
+    p.slots = fit(q);
+    p.qbufs = 1;
+    if (mode != ROWS && (fit(2 * q) >= 6 || fit(2 * q) == p.slots)) {
+        p.qbufs = 2;
+        p.slots = fit(2 * q);
+        q *= 2;
+    }
     // the product reads 128 rows of every block of queries
     p.smem = q + p.slots * slot + static_cast<uint32_t>(sizeof(Control));
     p.func = pick(D, mode, [](auto, auto f) { return reinterpret_cast<const void *>(f); });
