@@ -15,15 +15,21 @@
 //               piece, and checks its page table
 //   warps 4 ..  softmax: a thread has one row of a score tile, so the running
 //               maximum and sum need no exchange.  Weights go back to TMEM as
-//               bfloat16 over the scores they came from.  The same warps load
-//               the next piece's queries while the last products run.
+//               bfloat16 over the scores they came from.  The same warps copy
+//               the next piece's queries while this one is worked on.
 // The softmax of a tile takes longer than its copy or its products, so two
 // score tiles are worked on at a time by two groups of four warps, each with
 // its own accumulator in TMEM:
 //   ROWS   more than 128 query rows: one group has rows 0 - 127, the other
 //          128 - 255, and a key tile is copied once for both
-//   KEYS   up to 128 rows: the groups take turns at the key tiles; at the end
+//   KEYS   33 to 128 rows: the groups take turns at the key tiles; at the end
 //          of a piece their maxima, sums and outputs are joined
+//   FEW    up to 32 rows: as KEYS, but those rows would lie in the lanes of one
+//          warp and leave three idle, so each warp of a group gets the scores
+//          of a quarter of the keys (64 sequences of 768 tokens, 16 rows: 74 ->
+//          68 us; one of 131072, 32 rows: 97 -> 94 us).  They exchange the
+//          maximum of each tile; weights go through shared memory, because in
+//          TMEM a warp reaches its own lanes only
 //   ONE    heads of 256: TMEM holds one accumulator, so one group works, with
 //          two score buffers (the products of tile j + 1 run under the softmax
 //          of tile j); warp 1 issues the products with the keys, warp 2 those
@@ -46,13 +52,15 @@ namespace {
 constexpr int LOADERS = 32;
 constexpr float RESCALE = 8.f;  // rescale when the maximum rose by this many powers of two
 constexpr int MAX_SLOTS = 14;
-enum Mode { ONE = 0, KEYS = 1, ROWS = 2 };
+enum Mode { ONE = 0, KEYS = 1, ROWS = 2, FEW = 3 };
 
 template <int D, int MODE>
 struct Cfg {
     static constexpr int NT = MODE == ONE ? 256 : 384;
     static constexpr int BN = D == 256 ? 64 : 128;
     static constexpr int CH = D / 64;                      // 64-element blocks of a row
+    static constexpr bool TURNS = MODE == KEYS || MODE == FEW;  // the groups take turns at the key tiles
+    static constexpr uint32_t P = MODE == FEW ? 16384 : 0; // weights in shared memory: 32 rows for each group
     static constexpr int GROUPS = MODE == ONE ? 1 : 2;     // of softmax warps
     static constexpr uint32_t SLOT = BN * D * 2;           // a key or value tile
     static constexpr uint32_t S_COL = 128;                 // score buffers at columns 0 and 128
@@ -64,6 +72,7 @@ struct Control {
     uint64_t full[2 * MAX_SLOTS], empty[MAX_SLOTS], s_full[2], p_half[2], p_full[2], o_done[2], q_full[2], q_empty[2];
     uint64_t grant[8];            // two slots of the ring are the loader's to fill (at most slots / 2 at a time)
     uint64_t masks[4], ready[4], done[4];  // a piece's masks are there; all that the loader found out is; it has been read
+    uint64_t tops[2];             // FEW: the maxima of a tile's quarters are there
     uint64_t stats, joined;       // KEYS: both groups' statistics are there; both have read the accumulators
     uint64_t mask[4][MAX_NODES];
     uint64_t poison[4];
@@ -71,6 +80,7 @@ struct Control {
     int above[MAX_NODES];
     long long W;
     AttnWalk begin;
+    float top[2][2][4][32];       // FEW: group, even and odd tiles, quarter, row
     float m[2][128], l[2][128];   // KEYS: the groups' statistics
     uint32_t tmem;
     int dead;
@@ -113,10 +123,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Weights of one block of 32 scores, stored as bfloat16 in 16 columns at
-// p_addr; their sum goes to acc.
-__device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2, uint64_t N2, uint64_t (&acc)[2], uint32_t p_addr) {
-    uint32_t p[16];
+// Weights of one block of 32 scores, two to a register; their sum goes to acc.
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint64_t K2, uint64_t N2, uint64_t (&acc)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
         float a, b;
@@ -126,6 +134,12 @@ __device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2
         acc[(i >> 1) & 1] = f2add(acc[(i >> 1) & 1], f2pack(a, b));
         p[i / 2] = bf16x2(a, b);
     }
+}
+
+// The same, stored as bfloat16 in 16 columns at p_addr.
+__device__ __forceinline__ void weigh_block(const uint32_t (&s)[32], uint64_t K2, uint64_t N2, uint64_t (&acc)[2], uint32_t p_addr) {
+    uint32_t p[16];
+    weights(s, K2, N2, acc, p);
     tmem_st16(p_addr, p);
 }
 
@@ -145,9 +159,10 @@ __device__ __forceinline__ void max_block(uint32_t (&s)[32], float (&t)[4], bool
 }
 
 // The row's reference maximum for a tile whose largest score is `top` (in
-// units of log2 e); the accumulator is rescaled where it has to be.
+// units of log2 e); the accumulator (if this warp has one) is rescaled where it
+// has to be.
 __device__ __forceinline__ void rescale(float top, bool first, float &m, float &l, uint32_t o_addr, int ocols, uint32_t o_bar,
-                                        uint32_t o_phase, bool &ok) {
+                                        uint32_t o_phase, bool &ok, bool has = true) {
     if (first) {
         m = top;
         l = 0.f;
@@ -155,12 +170,13 @@ __device__ __forceinline__ void rescale(float top, bool first, float &m, float &
     }
     const bool up = top > m + RESCALE;
     if (!__any_sync(FULL, up)) return;
-    ok = wait_for(o_bar, o_phase) && ok;  // the products before this tile
-    __syncwarp();
-    tmem_fence_after_sync();
     const float f = up ? ex2(m - top) : 1.f;
     if (up) m = top;
     l *= f;
+    if (!has) return;
+    ok = wait_for(o_bar, o_phase) && ok;  // the products before this tile
+    __syncwarp();
+    tmem_fence_after_sync();
 #pragma unroll 1
     for (int c = 0; c < ocols; c += 32) {
         uint32_t o[32];
@@ -265,6 +281,53 @@ __device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, i
     tmem_wait_st();
 }
 
+// FEW: a quarter of a score tile of at most 32 rows, by one of a group's four
+// warps.  `any`: there are keys in it, of which the row sees those in `see`.
+// The four share the row's maximum; each keeps the sum of its own weights.
+// Weights go to shared memory at p (128-byte rows, swizzled).
+__device__ __forceinline__ void softmax_quarter(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int quarter, bool any,
+                                                uint32_t see, bool live, bool first, float &m, float &l, uint32_t o_bar,
+                                                uint32_t o_phase, bool used, float (&tops)[4][32], uint32_t top_bar,
+                                                uint32_t top_phase, unsigned char *p, int prows, bool &ok) {
+    const int lane = threadIdx.x & 31;
+    uint32_t s[32];
+    float top = -INFINITY;
+    if (any) {
+        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        __syncwarp();
+        tmem_ld32(s_addr, s);
+        tmem_wait_ld32(s);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1u)) s[i] = 0xff800000u;
+        max_block(s, t, false, 0u, 0u);
+        if (live) top = max3(t[0], t[1], fmaxf(t[2], t[3])) * scale;
+    }
+    tops[quarter][lane] = top;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(top_bar);
+    ok = wait_for(top_bar, top_phase) && ok;
+    top = fmaxf(max3(tops[0][lane], tops[1][lane], tops[2][lane]), tops[3][lane]);
+    rescale(top, first, m, l, o_addr, ocols, o_bar, o_phase, ok, quarter == 0);
+    if (any) {
+        const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
+        uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+        uint32_t w[16];
+        weights(s, K2, N2, acc, w);
+        l += sum4(acc);
+        // (the product that read the weights before these is done: its scores'
+        // successors are here)
+        if (used) ok = wait_for(o_bar, o_phase) && ok;
+        if (lane < prows && ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(p + (quarter >> 1) * 4096 + sw128(lane, (quarter & 1) * 4 + j)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+        fence_proxy_async();
+    }
+}
+
 // Values that are not finite, of the nodes in `seen`, added to columns c0 .. c1
 // of one finished row (`part`: of a partial result): the products took them as
 // zeros.
@@ -300,13 +363,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                    const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D, MODE>;
     constexpr int NT = C::NT, BM = MODE == ROWS ? 256 : 128;
-    // queries (blocks of 64 elements x qrows rows, once or twice), ring, control
+    // FEW: weights; queries (blocks of 64 elements x qrows rows, once or twice), ring, control
     extern __shared__ __align__(1024) unsigned char smem[];
     const int qbufs = MODE == ROWS ? 2 : A.qbufs;  // ROWS: one for each group
     const uint32_t qblock = A.qrows * 128, qbytes = qblock * C::CH * qbufs;
-    Control &ctl = *reinterpret_cast<Control *>(smem + qbytes + C::SLOT * A.slots);
-    unsigned char *ring = smem + qbytes;
-    const uint32_t sq = smem_addr(smem), ring0 = sq + qbytes;
+    unsigned char *queries = smem + C::P;
+    Control &ctl = *reinterpret_cast<Control *>(queries + qbytes + C::SLOT * A.slots);
+    unsigned char *ring = queries + qbytes;
+    const uint32_t sq = smem_addr(queries), ring0 = sq + qbytes;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
     const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
@@ -320,10 +384,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_half[i]), 128);
-            mbar_init(smem_addr(&ctl.p_full[i]), 128);
+            mbar_init(smem_addr(&ctl.p_full[i]), MODE == FEW ? 4 : 128);
+            mbar_init(smem_addr(&ctl.tops[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
-            mbar_init(smem_addr(&ctl.q_full[i]), MODE == KEYS ? 256 : 128);  // ROWS: a group's own rows
-            mbar_init(smem_addr(&ctl.q_empty[i]), MODE == KEYS ? 2 : 1);
+            mbar_init(smem_addr(&ctl.q_full[i]), C::TURNS ? 256 : 128);  // ROWS: a group's own rows
+            mbar_init(smem_addr(&ctl.q_empty[i]), C::TURNS ? 2 : 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&ctl.grant[i]), 1);
         for (int i = 0; i < 4; ++i) {
@@ -349,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const int used = MODE == ROWS ? max(0, min(rows - 128 * buf, 128)) : rows;
         for (int i = tid; i < (A.qrows - used) * (D / 8); i += NT) {
             const int r = used + i / (D / 8), u = i % (D / 8);
-            *reinterpret_cast<uint4 *>(smem + (buf * C::CH + (u >> 3)) * qblock + sw128(r, u & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(queries + (buf * C::CH + (u >> 3)) * qblock + sw128(r, u & 7)) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
     fence_proxy_async();
@@ -423,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         int count = 0, other = 0;  // uses of the group's score buffer (ONE: of both buffers)
         // O += P V of a tile: its buffer, the use of it, its slot of the ring
         auto pv = [&](int buf, int use, const Ring &at, int steps, bool first) {
-            ok = wait_for(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
+            if (MODE != FEW) ok = wait_for(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
             ok = wait_for(smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
             ok = __all_sync(FULL, ok);
             if (!ok) return;
@@ -431,8 +496,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             constexpr int HALF = C::BN / 32;  // steps of 16 keys in half a tile
             const uint64_t v = umma_desc(ring0 + at.slot * C::SLOT, C::BN * 128);
             const uint32_t o = tmem + C::O_COL + (MODE == ONE ? 0 : g * D), p = tmem + buf * C::S_COL;
-            auto step = [&](int k) { umma_ts(o, p + 8 * k, v + k * (2048 >> 4), umma_idesc(D, true), !(first && k == 0)); };
-            if (elect_one()) {
+            const uint64_t shared_p = umma_desc(sq - C::P + g * 8192);
+            auto step = [&](int k) {
+                if (MODE == FEW)
+                    umma_ss(o, shared_p + (((k >> 2) * 4096 + (k & 3) * 32) >> 4), v + k * (2048 >> 4), umma_idesc(D, true), !(first && k == 0));
+                else
+                    umma_ts(o, p + 8 * k, v + k * (2048 >> 4), umma_idesc(D, true), !(first && k == 0));
+            };
+            if (MODE != FEW && elect_one()) {
 #pragma unroll
                 for (int k = 0; k < HALF; ++k)
                     if (k < steps) step(k);
@@ -444,22 +515,30 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             tmem_fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int k = HALF; k < 2 * HALF; ++k)
+                for (int k = MODE == FEW ? 0 : HALF; k < 2 * HALF; ++k)
                     if (k < steps) step(k);
                 umma_commit(smem_addr(&ctl.o_done[buf]));
                 umma_commit(smem_addr(&ctl.empty[at.slot]));
             }
             __syncwarp();
         };
-        auto qk = [&](int buf, int slot, uint32_t idesc) {
+        // S = Q K^T of the first `keys` keys of a tile.  FEW: quarter by quarter,
+        // the queries' first row 32 rows further down the tile each time, so that
+        // each quarter's scores end in the lanes of another warp.  (The rows
+        // before and behind the queries give scores that nobody looks at.)
+        auto qk = [&](int buf, int slot, int keys) {
             tmem_fence_after_sync();
             if (elect_one()) {
                 const uint64_t qdesc = umma_desc(sq + qi * C::CH * qblock);
                 const uint64_t k = umma_desc(ring0 + slot * C::SLOT);
+#pragma unroll 1
+                for (int part = 0; part < (MODE == FEW ? keys : 1); part += 32) {
+                    const uint32_t idesc = umma_idesc(MODE == FEW ? min(32, keys - part) : keys, false);
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    umma_ss(tmem + buf * C::S_COL, qdesc + (((i >> 2) * qblock + (i & 3) * 32) >> 4),
-                            k + (((i >> 2) * (C::BN * 128) + (i & 3) * 32) >> 4), idesc, i > 0);
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_ss(tmem + buf * C::S_COL + part, qdesc + (((i >> 2) * qblock + (i & 3) * 32) >> 4) - part * 128 / 16,
+                                k + (((i >> 2) * (C::BN * 128) + (i & 3) * 32 + part * 128) >> 4), idesc, i > 0);
+                }
                 umma_commit(smem_addr(&ctl.s_full[buf]));
                 umma_commit(smem_addr(&ctl.empty[slot]));
             }
@@ -480,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 r.step();
                 const Ring vr = r;
                 r.step();
-                if (MODE == KEYS && ((t - pc.t0) & 1) != g) continue;
+                if (C::TURNS && ((t - pc.t0) & 1) != g) continue;
                 int pos, valid;
                 if (t == pc.prefix)
                     valid = n > 0 ? n : 1;
@@ -502,10 +581,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 ok = wait_for(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
-                qk(buf, kr.slot, umma_idesc(t == pc.prefix ? round16(valid) : C::BN, false));
+                qk(buf, kr.slot, t == pc.prefix ? round16(valid) : C::BN);
                 ++uses;
                 have = true;
-                old_first = MODE == KEYS ? t - pc.t0 < 2 : t == pc.t0;
+                old_first = C::TURNS ? t - pc.t0 < 2 : t == pc.t0;
                 old = vr;
                 old_steps = round16(valid) / 16;
             }
@@ -613,14 +692,15 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const int wt = (tid - 128) & 127;               // this thread's row
         const int part = warp & 3;                      // its 32 TMEM lanes
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * part) << 16);
-        const int lrow = wt + (MODE == ROWS ? 128 * wg : 0);  // row of the CTA's tile
+        const int quarter = wt >> 5;                     // FEW: of the keys of a tile
+        const int lrow = MODE == FEW ? lane : wt + (MODE == ROWS ? 128 * wg : 0);  // row of the CTA's tile
         const bool live = lrow < rows;
-        const bool busy = lrow - lane < rows;           // the warp has rows
+        const bool busy = MODE == FEW ? quarter == 0 : lrow - lane < rows;  // the warp has rows of the accumulator
         const int rr = row0 + lrow, node = node_of(A, rr);
         const uint32_t o_addr = lanes + C::O_COL + (MODE == ONE ? 0 : wg * D);
         Ring r(A.slots);
         int count0 = 0, count1 = 0;                     // uses of the group's score buffer (ONE: of both)
-        uint32_t join_phase = 0;
+        uint32_t join_phase = 0, top_phase = 0;
         // The queries of piece `np`: copies into shared memory are started, by the
         // threads that arrive on q_full, once the scores of the piece before that
         // were in this buffer are done.
@@ -632,8 +712,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             ok = __all_sync(FULL, ok);
             if (ok)
                 copy_queries<D>(static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2], A,
-                                row0 + q0, min(rows - q0, 128), sq + qi * C::CH * qblock, MODE == KEYS ? tid - 128 : wt,
-                                MODE == KEYS ? 256 : 128);
+                                row0 + q0, min(rows - q0, 128), sq + qi * C::CH * qblock, C::TURNS ? tid - 128 : wt,
+                                C::TURNS ? 256 : 128);
         };
         // (the turn before the first piece only loads its queries)
         AttnPiece next = {};
@@ -653,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 r.step();  // the keys' slot
                 const Ring vr = r;
                 r.step();
-                if (MODE == KEYS && ((t - pc.t0) & 1) != wg) continue;
+                if (C::TURNS && ((t - pc.t0) & 1) != wg) continue;
                 const int buf = MODE == ONE ? (t - pc.t0) & 1 : wg;
                 const int use = MODE == ONE && buf ? count1 : count0;
                 const uint32_t s_addr = lanes + buf * C::S_COL;
@@ -675,7 +755,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     hi = valid > 64 ? (valid < 128 ? (1ull << (valid - 64)) - 1ull : ~0ull) : 0ull;
                 }
                 bool half = true;  // the first half was announced
-                if (busy && !tree && valid == C::BN)
+                if (MODE == FEW) {
+                    softmax_quarter(s_addr + 32 * quarter, o_addr, D, A.scale_log2, quarter, 32 * quarter < (tree ? max(n, 1) : valid),
+                                    static_cast<uint32_t>((quarter < 2 ? lo : hi) >> (32 * (quarter & 1))), live, first, m, l, o_bar,
+                                    o_phase, use > 0, ctl.top[wg][top_phase], smem_addr(&ctl.tops[wg]), top_phase,
+                                    smem + wg * 8192, A.qrows, ok);
+                    top_phase ^= 1u;
+                } else if (busy && !tree && valid == C::BN)
                     softmax_full<C::BN / 32>(s_addr, o_addr, D, A.scale_log2, first, m, l, o_bar, o_phase,
                                              smem_addr(&ctl.p_half[buf]), ok);
                 else {
@@ -699,8 +785,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
                 first = false;
                 tmem_fence_before_sync();
-                if (!half) mbar_arrive(smem_addr(&ctl.p_half[buf]));
-                mbar_arrive(smem_addr(&ctl.p_full[buf]));
+                if (MODE == FEW) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl.p_full[buf]));
+                } else {
+                    if (!half) mbar_arrive(smem_addr(&ctl.p_half[buf]));
+                    mbar_arrive(smem_addr(&ctl.p_full[buf]));
+                }
                 if (MODE == ONE && buf)
                     ++count1;
                 else
@@ -727,26 +818,32 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             if (!ok) break;
             // KEYS: o = f0 o0 + f1 o1, each group for half of the columns
             float f0 = 1.f, f1 = 0.f;
-            const bool two = MODE == KEYS && pc.t1 - pc.t0 > 1;  // the second group had tiles
-            if (two) {
+            const bool two = C::TURNS && pc.t1 - pc.t0 > 1;  // the second group had tiles
+            if (two || MODE == FEW) {
                 ctl.m[wg][wt] = m;
                 ctl.l[wg][wt] = l;
             }
             tmem_fence_before_sync();
-            if (MODE == KEYS) {
+            if (C::TURNS) {
                 mbar_arrive(smem_addr(&ctl.stats));
                 ok = wait_for(smem_addr(&ctl.stats), join_phase) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
             tmem_fence_after_sync();
+            // the sum over a group's weights (FEW: the four warps' sums)
+            auto sum_of = [&](int of) {
+                const float *x = ctl.l[of];
+                return MODE == FEW ? (x[lane] + x[lane + 32]) + (x[lane + 64] + x[lane + 96]) : x[wt];
+            };
+            if (MODE == FEW && !two) l = sum_of(0);
             if (two) {
                 const float m0 = ctl.m[0][wt], m1 = ctl.m[1][wt];
                 m = fmaxf(m0, m1);
                 const float ref = m == -INFINITY ? 0.f : m;
                 f0 = ex2(m0 - ref);
                 f1 = ex2(m1 - ref);
-                l = f0 * ctl.l[0][wt] + f1 * ctl.l[1][wt];
+                l = f0 * sum_of(0) + f1 * sum_of(1);
             }
             const int flag = ctl.flag[np & 3];
             if (A.flags && tid == 128 && h == 0 && mtile == 0) A.flags[b] = flag;
@@ -761,7 +858,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             float *slot = A.part + attn_slot(A, group, mtile, pc.first) * attn_slot_floats(BM, D);
             const float inv = 1.f / l;
             // columns of this group (a piece of one tile: the first group had it, and has all)
-            const int c0 = two ? wg * (D / 2) : 0, c1 = two ? c0 + D / 2 : MODE == KEYS && wg == 1 ? 0 : D;
+            const int c0 = two ? wg * (D / 2) : 0, c1 = two ? c0 + D / 2 : C::TURNS && wg == 1 ? 0 : D;
             if (busy) {
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
@@ -810,7 +907,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             }
             tmem_fence_before_sync();
             mbar_arrive(smem_addr(&ctl.done[np & 3]));
-            if (MODE == KEYS) {  // the next piece's products may write the accumulators
+            if (C::TURNS) {  // the next piece's products may write the accumulators
                 mbar_arrive(smem_addr(&ctl.joined));
                 ok = wait_for(smem_addr(&ctl.joined), join_phase) && ok;
                 join_phase ^= 1u;
@@ -850,9 +947,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
 namespace {
 template <typename F>
 auto pick(int D, int mode, F f) {
-    return D == 64    ? mode == ROWS ? f(Cfg<64, ROWS>{}, attn_umma_impl<64, ROWS>) : f(Cfg<64, KEYS>{}, attn_umma_impl<64, KEYS>)
-           : D == 128 ? mode == ROWS ? f(Cfg<128, ROWS>{}, attn_umma_impl<128, ROWS>) : f(Cfg<128, KEYS>{}, attn_umma_impl<128, KEYS>)
-                      : f(Cfg<256, ONE>{}, attn_umma_impl<256, ONE>);
+    if (D == 256) return f(Cfg<256, ONE>{}, attn_umma_impl<256, ONE>);
+    if (D == 128)
+        return mode == ROWS   ? f(Cfg<128, ROWS>{}, attn_umma_impl<128, ROWS>)
+               : mode == KEYS ? f(Cfg<128, KEYS>{}, attn_umma_impl<128, KEYS>)
+                              : f(Cfg<128, FEW>{}, attn_umma_impl<128, FEW>);
+    return mode == ROWS   ? f(Cfg<64, ROWS>{}, attn_umma_impl<64, ROWS>)
+           : mode == KEYS ? f(Cfg<64, KEYS>{}, attn_umma_impl<64, KEYS>)
+                          : f(Cfg<64, FEW>{}, attn_umma_impl<64, FEW>);
 }
 }  // namespace
 
@@ -862,13 +964,14 @@ int attn_umma_bn(int D) { return D == 256 ? 64 : 128; }
 // (or as many as go in with one buffer).
 UmmaPlan attn_umma_plan(int D, int rows) {
     UmmaPlan p;
-    const int mode = D == 256 ? ONE : rows > 128 ? ROWS : KEYS;
+    const int mode = D == 256 ? ONE : rows > 128 ? ROWS : rows > 32 ? KEYS : FEW;
     p.bm = mode == ROWS ? 256 : 128;
     p.qrows = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
     uint32_t q = static_cast<uint32_t>(p.qrows) * D * 2 * (mode == ROWS ? 2 : 1);
     const uint32_t slot = static_cast<uint32_t>(attn_umma_bn(D)) * D * 2;
+    const uint32_t p_bytes = mode == FEW ? Cfg<64, FEW>::P : 0;
     auto fit = [&](uint32_t queries) {
-        const int n = static_cast<int>((UMMA_SMEM - sizeof(Control) - queries) / slot);
+        const int n = static_cast<int>((UMMA_SMEM - sizeof(Control) - p_bytes - queries) / slot);
         return n < MAX_SLOTS ? n : MAX_SLOTS;
     };
     p.slots = fit(q);
@@ -879,7 +982,7 @@ UmmaPlan attn_umma_plan(int D, int rows) {
         q *= 2;
     }
     // the product reads 128 rows of every block of queries
-    p.smem = q + p.slots * slot + static_cast<uint32_t>(sizeof(Control));
+    p.smem = p_bytes + q + p.slots * slot + static_cast<uint32_t>(sizeof(Control));
     p.func = pick(D, mode, [](auto, auto f) { return reinterpret_cast<const void *>(f); });
     p.threads = pick(D, mode, [](auto c, auto) { return decltype(c)::NT; });
     return p;
