@@ -30,6 +30,7 @@ struct TreeAttnArgs {
     int mtiles;              // row tiles of BM rows
     int groups;              // CTAs / mtiles: each group of CTAs walks one range of key tiles
     int whole;               // units are not split: the groups share them out, not the tiles
+    int extra;               // what a unit counts for beside its tiles, in tiles (see AttnWalk)
     int bm;                  // query rows of one tile
     int ktile;               // keys of one tile
     int per_page;            // tiles of one page where pages are larger than a tile and no multiple of it, else 0
@@ -50,6 +51,7 @@ const void *attn_simt_func(int dtype, int D);
 uint32_t attn_simt_smem(int D);
 // Tensor-core kernel (csrc/tree_attention_umma.cu): bfloat16, D 64, 128, 256.
 constexpr uint32_t UMMA_SMEM = 232448;  // 227 KB per CTA
+constexpr int UMMA_EXTRA = 3;
 struct UmmaPlan {
     const void *func;
     int threads, bm, qrows, qbufs, slots;

@@ -295,6 +295,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.bm = p.bm;
     A.whole = p.whole;
     A.ktile = p.ktile;
+    A.extra = umma ? UMMA_EXTRA : 0;
     A.qrows = p.qrows;
     A.qbufs = p.qbufs;
     A.slots = p.slots;

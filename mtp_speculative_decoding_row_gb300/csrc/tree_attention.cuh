@@ -98,6 +98,7 @@ struct AttnWalk {
     long long hi = 0, at = 0;    // the end of this group's range, the next tile
     int b = 0, h = 0, tile = 0;  // where `at` is
     int len = 0, prefix = 0;
+    int extra = 0;               // a unit ends with so many tiles that are none (see start)
     bool begins = true;          // no piece was taken yet
 
     // Returns the number of all tiles (of all units where they are not split;
@@ -130,7 +131,18 @@ struct AttnWalk {
             const long long o = __shfl_up_sync(FULL, inc, d);
             if (lane >= d) inc += o;
         }
-        const long long W = __shfl_sync(FULL, inc, 31);
+        // On the tensor cores the start and end of a piece take the time of
+        // about three tiles: where there are tiles enough, that is counted.  (A
+        // sequence without a cache is Hkv pieces of one tile each, which one
+        // group would get otherwise.  16 sequences of 1333 to 4000 tokens and
+        // an empty one: 59 -> 45 us.  In the other kernel a piece costs little
+        // beside its tiles: 1000 tokens of 32 sequences took 152 us without
+        // and 177 us with three tiles.)
+        const long long real = __shfl_sync(FULL, inc, 31);
+        if (real >= 4ll * A.groups) extra = A.extra;
+        const long long W = real + static_cast<long long>(A.B) * A.Hkv * extra;
+        inc += static_cast<long long>(b1) * A.Hkv * extra;
+        sum += static_cast<long long>(b1 - b0) * A.Hkv * extra;
         const int groups = attn_groups(A, W);
         const long long lo = attn_lo(W, min(g, groups), groups);
         hi = attn_lo(W, min(g + 1, groups), groups);
@@ -146,7 +158,7 @@ struct AttnWalk {
                     len = attn_len(A, i, bad);
                     prefix = attn_prefix_tiles(A, len);
                 }
-                const long long unit = static_cast<long long>(prefix + 1) * A.Hkv;
+                const long long unit = static_cast<long long>(prefix + 1 + extra) * A.Hkv;
                 if (x < unit) break;  // (x lies in this lane's stretch)
                 x -= unit;
             }
@@ -155,9 +167,13 @@ struct AttnWalk {
         b = __shfl_sync(FULL, i, src);
         len = __shfl_sync(FULL, len, src);
         prefix = __shfl_sync(FULL, prefix, src);
-        const int first = __shfl_sync(FULL, static_cast<int>(x), src);  // < Hkv (prefix + 1)
-        h = first / (prefix + 1);
-        tile = first - h * (prefix + 1);
+        const int first = __shfl_sync(FULL, static_cast<int>(x), src);  // < Hkv (prefix + 1 + extra)
+        h = first / (prefix + 1 + extra);
+        tile = first - h * (prefix + 1 + extra);
+        if (tile > prefix) {  // the range begins behind a unit's tiles
+            at += prefix + 1 + extra - tile;
+            step(A);
+        }
         return W;
     }
 
@@ -165,6 +181,17 @@ struct AttnWalk {
         bool bad;
         len = attn_len(A, b, bad);
         prefix = attn_prefix_tiles(A, len);
+    }
+
+    // On to the next unit, if the range has it.
+    __device__ __forceinline__ void step(const TreeAttnArgs &A) {
+        if (at >= hi) return;
+        tile = 0;
+        if (++h == A.Hkv) {
+            h = 0;
+            ++b;
+            read(A);
+        }
     }
 
     // The next piece, or false at the end of the range.
@@ -190,13 +217,9 @@ struct AttnWalk {
         p.t1 = static_cast<int>(tile + left < prefix + 1 ? tile + left : prefix + 1);
         at += p.t1 - p.t0;
         tile = p.t1;
-        if (tile == prefix + 1 && at < hi) {
-            tile = 0;
-            if (++h == A.Hkv) {
-                h = 0;
-                ++b;
-                read(A);
-            }
+        if (tile == prefix + 1) {
+            at += extra;
+            step(A);
         }
         return true;
     }
@@ -224,7 +247,7 @@ __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, lo
         d[2] = 0;
         return;
     }
-    const long long end = hi + (last.prefix + 1 - last.t1);  // one past the unit's last tile
+    const long long end = hi + (last.prefix + 1 - last.t1);  // one past the unit's last tile (the range ended inside of the unit)
     const int groups = attn_groups(A, W);
     int n = 1;
     while (g + n < groups && attn_lo(W, g + n, groups) < end) ++n;

@@ -259,6 +259,16 @@ def test_tree_attention_batch_of_many_and_padded():
     run_attention(attn_case(8, "bf16", B, 2, 2, 1, 64, 16, lens, "random", nodes))
 
 
+@pytest.mark.parametrize("dtype, T, Hq, D", [("bf16", 1, 8, 64), ("bf16", 4, 64, 128), ("bf16", 9, 32, 64), ("bf16", 2, 16, 256),
+                                              ("f32", 2, 16, 64)])
+def test_tree_attention_many_uneven(dtype, T, Hq, D):
+    """More tiles than four for every CTA, whose split counts the units too:
+    runs of sequences without a cache, single tokens and longer ones."""
+    rng = random.Random(D + T)
+    lens = [0] * 9 + [700] + [rng.choice([0, 1, 16, 128, 129, rng.randint(200, 699)]) for _ in range(34)] + [640, 0, 0, 0]
+    run_attention(attn_case(71, dtype, len(lens), T, Hq, 8, D, 32, lens))
+
+
 @pytest.mark.parametrize("dtype, T, D", [("bf16", 3, 128), ("bf16", 33, 64), ("f32", 3, 64)])
 def test_tree_attention_is_repeatable(dtype, T, D):
     """The split of long sequences joins in a fixed order: the same bits every time."""
