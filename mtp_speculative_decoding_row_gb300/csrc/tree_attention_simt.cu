@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
     const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
     const bool vec = A.vec != 0;
+    const bool works = 4 * (tid >> 5) < rows;  // a warp has rows 4 w .. 4 w + 3 from the scores to the output
 
     pdl_wait();
     pdl_next();
@@ -129,98 +130,100 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                 }
             }
             __syncthreads();
-            // scores of rows 2 ty, 2 ty + 1 against keys tx + 16 i
-            float s[2][4];
+            if (works) {
+                // scores of rows 2 ty, 2 ty + 1 against keys tx + 16 i
+                float s[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
-            const float *q0 = sq + 2 * ty * KS;
+                    for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+                const float *q0 = sq + 2 * ty * KS;
 #pragma unroll 4
-            for (int d = 0; d < DP; d += 4) {
-                const float4 a0 = *reinterpret_cast<const float4 *>(q0 + d);
-                const float4 a1 = *reinterpret_cast<const float4 *>(q0 + KS + d);
+                for (int d = 0; d < DP; d += 4) {
+                    const float4 a0 = *reinterpret_cast<const float4 *>(q0 + d);
+                    const float4 a1 = *reinterpret_cast<const float4 *>(q0 + KS + d);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 k = *reinterpret_cast<const float4 *>(sk + (tx + 16 * c) * KS + d);
-                    s[0][c] = fmaf(a0.x, k.x, fmaf(a0.y, k.y, fmaf(a0.z, k.z, fmaf(a0.w, k.w, s[0][c]))));
-                    s[1][c] = fmaf(a1.x, k.x, fmaf(a1.y, k.y, fmaf(a1.z, k.z, fmaf(a1.w, k.w, s[1][c]))));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * ty + i;
-                const uint64_t see = tree && r < rows && (row0 + r) / A.G < n ? smask[(row0 + r) / A.G] : 0ull;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int j = tx + 16 * c;
-                    const bool on = tree ? ((see >> j) & 1ull) != 0 : j < valid;
-                    sp[r * (BN + 4) + j] = on ? s[i][c] : -INFINITY;
-                }
-            }
-            __syncthreads();
-            {  // softmax: 8 threads a row
-                const int r = tid >> 3, l = tid & 7;
-                float *p = sp + r * (BN + 4);
-                float x[8], top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = p[l + 8 * i];
-                    top = max_nan(top, x[i]);
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 k = *reinterpret_cast<const float4 *>(sk + (tx + 16 * c) * KS + d);
+                        s[0][c] = fmaf(a0.x, k.x, fmaf(a0.y, k.y, fmaf(a0.z, k.z, fmaf(a0.w, k.w, s[0][c]))));
+                        s[1][c] = fmaf(a1.x, k.x, fmaf(a1.y, k.y, fmaf(a1.z, k.z, fmaf(a1.w, k.w, s[1][c]))));
+                    }
                 }
 #pragma unroll
-                for (int d = 1; d < 8; d <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, d));
-                const float m0 = sm[r], m1 = max_nan(m0, top);
-                const float ref = m1 == -INFINITY ? 0.f : m1 * A.scale_log2;
-                float sum = 0.f;
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 2 * ty + i;
+                    const uint64_t see = tree && r < rows && (row0 + r) / A.G < n ? smask[(row0 + r) / A.G] : 0ull;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = exp2f(fmaf(x[i], A.scale_log2, -ref));
-                    p[l + 8 * i] = x[i];
-                    sum += x[i];
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = tx + 16 * c;
+                        const bool on = tree ? ((see >> j) & 1ull) != 0 : j < valid;
+                        sp[r * (BN + 4) + j] = on ? s[i][c] : -INFINITY;
+                    }
                 }
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL, sum, d);
                 __syncwarp();
-                if (l == 0) {
-                    const float f = m0 == -INFINITY ? 0.f : exp2f(fmaf(m0, A.scale_log2, -ref));
-                    sf[r] = f;
-                    sl[r] = sl[r] * f + sum;
-                    sm[r] = m1;
-                }
-            }
-            __syncthreads();
-            {  // outputs of rows 2 ty, 2 ty + 1, columns 64 c + 4 tx ..
-                const float f0 = sf[2 * ty], f1 = sf[2 * ty + 1];
-                uint64_t see0 = ~0ull, see1 = ~0ull;
-                if (tree) {  // a node that a row does not see never reaches it, not even as 0 times infinity
-                    const int r = row0 + 2 * ty, t0 = r / A.G, t1 = (r + 1) / A.G;
-                    see0 = 2 * ty < rows && t0 < n ? smask[t0] : 0ull;
-                    see1 = 2 * ty + 1 < rows && t1 < n ? smask[t1] : 0ull;
-                }
+                {  // softmax: 8 threads a row
+                    const int r = tid >> 3, l = tid & 7;
+                    float *p = sp + r * (BN + 4);
+                    float x[8], top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < DC * 4; ++c) {
-                    acc[0][c] *= f0;
-                    acc[1][c] *= f1;
-                }
-                const float *p0 = sp + 2 * ty * (BN + 4), *p1 = p0 + BN + 4;
-                for (int j = 0; j < valid; ++j) {
-                    const float w0 = p0[j], w1 = p1[j];
-                    const bool on0 = (see0 >> j) & 1ull, on1 = (see1 >> j) & 1ull;
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = p[l + 8 * i];
+                        top = max_nan(top, x[i]);
+                    }
 #pragma unroll
-                    for (int c = 0; c < DC; ++c) {
-                        const float4 v = *reinterpret_cast<const float4 *>(sv + j * DP + 64 * c + 4 * tx);
-                        if (on0) {
-                            acc[0][4 * c] = fmaf(w0, v.x, acc[0][4 * c]);
-                            acc[0][4 * c + 1] = fmaf(w0, v.y, acc[0][4 * c + 1]);
-                            acc[0][4 * c + 2] = fmaf(w0, v.z, acc[0][4 * c + 2]);
-                            acc[0][4 * c + 3] = fmaf(w0, v.w, acc[0][4 * c + 3]);
-                        }
-                        if (on1) {
-                            acc[1][4 * c] = fmaf(w1, v.x, acc[1][4 * c]);
-                            acc[1][4 * c + 1] = fmaf(w1, v.y, acc[1][4 * c + 1]);
-                            acc[1][4 * c + 2] = fmaf(w1, v.z, acc[1][4 * c + 2]);
-                            acc[1][4 * c + 3] = fmaf(w1, v.w, acc[1][4 * c + 3]);
+                    for (int d = 1; d < 8; d <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, d));
+                    const float m0 = sm[r], m1 = max_nan(m0, top);
+                    const float ref = m1 == -INFINITY ? 0.f : m1 * A.scale_log2;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = exp2f(fmaf(x[i], A.scale_log2, -ref));
+                        p[l + 8 * i] = x[i];
+                        sum += x[i];
+                    }
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL, sum, d);
+                    __syncwarp();
+                    if (l == 0) {
+                        const float f = m0 == -INFINITY ? 0.f : exp2f(fmaf(m0, A.scale_log2, -ref));
+                        sf[r] = f;
+                        sl[r] = sl[r] * f + sum;
+                        sm[r] = m1;
+                    }
+                }
+                __syncwarp();
+                {  // outputs of rows 2 ty, 2 ty + 1, columns 64 c + 4 tx ..
+                    const float f0 = sf[2 * ty], f1 = sf[2 * ty + 1];
+                    uint64_t see0 = ~0ull, see1 = ~0ull;
+                    if (tree) {  // a node that a row does not see never reaches it, not even as 0 times infinity
+                        const int r = row0 + 2 * ty, t0 = r / A.G, t1 = (r + 1) / A.G;
+                        see0 = 2 * ty < rows && t0 < n ? smask[t0] : 0ull;
+                        see1 = 2 * ty + 1 < rows && t1 < n ? smask[t1] : 0ull;
+                    }
+#pragma unroll
+                    for (int c = 0; c < DC * 4; ++c) {
+                        acc[0][c] *= f0;
+                        acc[1][c] *= f1;
+                    }
+                    const float *p0 = sp + 2 * ty * (BN + 4), *p1 = p0 + BN + 4;
+                    for (int j = 0; j < valid; ++j) {
+                        const float w0 = p0[j], w1 = p1[j];
+                        const bool on0 = (see0 >> j) & 1ull, on1 = (see1 >> j) & 1ull;
+#pragma unroll
+                        for (int c = 0; c < DC; ++c) {
+                            const float4 v = *reinterpret_cast<const float4 *>(sv + j * DP + 64 * c + 4 * tx);
+                            if (on0) {
+                                acc[0][4 * c] = fmaf(w0, v.x, acc[0][4 * c]);
+                                acc[0][4 * c + 1] = fmaf(w0, v.y, acc[0][4 * c + 1]);
+                                acc[0][4 * c + 2] = fmaf(w0, v.z, acc[0][4 * c + 2]);
+                                acc[0][4 * c + 3] = fmaf(w0, v.w, acc[0][4 * c + 3]);
+                            }
+                            if (on1) {
+                                acc[1][4 * c] = fmaf(w1, v.x, acc[1][4 * c]);
+                                acc[1][4 * c + 1] = fmaf(w1, v.y, acc[1][4 * c + 1]);
+                                acc[1][4 * c + 2] = fmaf(w1, v.z, acc[1][4 * c + 2]);
+                                acc[1][4 * c + 3] = fmaf(w1, v.w, acc[1][4 * c + 3]);
+                            }
                         }
                     }
                 }
