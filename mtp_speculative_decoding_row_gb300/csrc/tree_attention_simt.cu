@@ -206,7 +206,29 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                         acc[1][c] *= f1;
                     }
                     const float *p0 = sp + 2 * ty * (BN + 4), *p1 = p0 + BN + 4;
-                    for (int j = 0; j < valid; ++j) {
+                    int j = 0;
+                    if (!tree) {  // four keys at a time
+#pragma unroll 2
+                        for (; j + 4 <= valid; j += 4) {
+                            const float4 wa = *reinterpret_cast<const float4 *>(p0 + j), wb = *reinterpret_cast<const float4 *>(p1 + j);
+                            const float w0[4] = {wa.x, wa.y, wa.z, wa.w}, w1[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                for (int c = 0; c < DC; ++c) {
+                                    const float4 v = *reinterpret_cast<const float4 *>(sv + (j + e) * DP + 64 * c + 4 * tx);
+                                    acc[0][4 * c] = fmaf(w0[e], v.x, acc[0][4 * c]);
+                                    acc[0][4 * c + 1] = fmaf(w0[e], v.y, acc[0][4 * c + 1]);
+                                    acc[0][4 * c + 2] = fmaf(w0[e], v.z, acc[0][4 * c + 2]);
+                                    acc[0][4 * c + 3] = fmaf(w0[e], v.w, acc[0][4 * c + 3]);
+                                    acc[1][4 * c] = fmaf(w1[e], v.x, acc[1][4 * c]);
+                                    acc[1][4 * c + 1] = fmaf(w1[e], v.y, acc[1][4 * c + 1]);
+                                    acc[1][4 * c + 2] = fmaf(w1[e], v.z, acc[1][4 * c + 2]);
+                                    acc[1][4 * c + 3] = fmaf(w1[e], v.w, acc[1][4 * c + 3]);
+                                }
+                        }
+                    }
+                    for (; j < valid; ++j) {
                         const float w0 = p0[j], w1 = p1[j];
                         const bool on0 = (see0 >> j) & 1ull, on1 = (see1 >> j) & 1ull;
 #pragma unroll
