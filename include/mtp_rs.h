@@ -338,7 +338,8 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  * The calls below that need scratch memory take it from the caller
  * (`workspace`, 16-byte aligned, its size from the function of the same name
  * with _workspace); its contents before and after a call mean nothing.  Calls
- * that may run at the same time need workspaces of their own.
+ * that may run at the same time need workspaces of their own, and no output
+ * may overlap an input (but for the cache of mtp_tree_commit).
  */
 #define MTP_MAX_NODES 64    /* nodes of a tree */
 #define MTP_MAX_BEAMS 64    /* beams of a sequence in mtp_beam_select */
@@ -367,10 +368,9 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  *   out [B, T, Hq, D] dtype, lse [B, T, Hq] float32 or NULL, contiguous
  *   row_flags [B] or NULL.
  * Requirements: 1 <= T <= MTP_MAX_NODES, Hq a multiple of Hkv (at most
- * 4096 times), 1 <= D <= 256,
- * 0 < scale, max_pages * page_size < 2^31 - 2^16 (else MTP_ERR_INVALID_ARG);
- * pointers aligned to their elements (else MTP_ERR_MISALIGNED).  Scores, softmax statistics
- * and outputs are accumulated in float32; with bfloat16 storage the softmax
+ * 4096 times), 1 <= D <= 256, 0 < scale, max_pages * page_size < 2^31 - 2^16
+ * (else MTP_ERR_INVALID_ARG); pointers aligned to their elements (else
+ * MTP_ERR_MISALIGNED).  Scores, softmax statistics and outputs are accumulated in float32; with bfloat16 storage the softmax
  * weights are rounded to bfloat16 for their product with the values (the
  * weights' sum is not).
  */
@@ -412,8 +412,8 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  *   MTP_ROW_BAD_TEMP)
  *   tokens, parents [B, K] int32, out_scores [B, K] float32 (required),
  *   row_flags [B] or NULL; a flagged sequence (a score or a read logit NaN or
- *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and parents -1
- *   and scores NaN.
+ *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and
+ *   parents -1 and scores NaN.
  * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24
  * (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  Scores are
  * formed and compared in float64.
@@ -429,7 +429,8 @@ int64_t mtp_beam_select_workspace(mtp_dtype dtype, int B, int W, int V, int K);
  * bytes.  states [N0, B, W, row], out [N0, B, K, row], contiguous, not
  * overlapping (MTP_ERR_INVALID_ARG).  A parent outside [0, W) -- the empty
  * places of mtp_beam_select -- gives a row of zeros and flags the sequence
- * MTP_ROW_BAD_ID.  row_flags [B] or NULL.
+ * MTP_ROW_BAD_ID (where there are no bytes to move, nothing is flagged).
+ * row_flags [B] or NULL.
  */
 int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, int W, int K, int64_t row_bytes, void *out,
                      int32_t *row_flags, mtp_stream_t stream);
@@ -455,14 +456,15 @@ int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, 
  * For every layer, the keys and values of the path's nodes go to tokens
  * cache_len, cache_len + 1, .. of the sequence; nothing else of the cache is
  * written.  A sequence of no nodes, or a flagged one (also: no room in the
- * page table for the path, a target token < 0 on it), has accept_len -1, tokens and path -1,
- * new_len = cache_len, and its cache stays as it was.
+ * page table for the path, a target token < 0 on it), has accept_len -1,
+ * tokens and path -1, new_len = cache_len, and its cache stays as it was.
  *
  *   k_new, v_new [layers, B, T, Hkv, D], k_cache, v_cache [layers, num_pages,
  *   page_size, Hkv, D] dtype, D contiguous, strides in elements; layers = 0
  *   writes no cache (all four may be NULL).  The pages that the path goes to
  *   must belong to one sequence only, and the new keys and values must not
- *   overlap the cache.  new_len must not be cache_len itself.
+ *   overlap the cache.  new_len must not be cache_len itself.  At most 2^30
+ *   elements of keys in the T nodes of one sequence and layer.
  */
 typedef struct mtp_tree_commit_args {
     const int32_t *tokens, *target_tokens; /* [B, T] */

@@ -14,11 +14,12 @@
 // and then by smaller index.  The K-th largest of the threads' running maxima
 // bounds the K-th best from below; vectors are compared with that bound four
 // at a time, and the indices of the few that pass are put aside: looking at
-// them at once, in the midst of the loop, took a third of the kernel's time.  The bound is taken again whenever three times as much
-// of the row has been seen; a candidate costs as much as 500 elements of the
-// sums (with the first bound alone the kernel took 81 us at 512 rows of
-// 151936).  Each warp keeps a list of its own; one that
-// is full is cut to its K best, and the bound rises for all warps.
+// them at once, in the midst of the loop, took a third of the kernel's time.
+// The bound is taken again whenever three times as much of the row has been
+// seen; a candidate costs as much as 500 elements of the sums (with the first
+// bound alone the kernel took 81 us at 512 rows of 151936).  Each warp keeps a
+// list of its own; one that is full is cut to its K best, and the bound rises
+// for all warps.
 //
 // Rows may start on any element.  A vector is always elements [8 j, 8 j + 8)
 // (4 j of float32) of the row, put together from two aligned loads where the

@@ -209,7 +209,8 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor hold;
         s.workspace = workspace(a[13], bytes, q, hold, s.workspace_bytes);
         const mtp_stream_t stream = stream_of(a[14]);
-        return call([&] { return fn.attention(&s, stream); });
+        const auto f = fn.attention;  // (another thread may bind meanwhile)
+        return call([&] { return f(&s, stream); });
     });
 }
 
@@ -247,7 +248,8 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int64_t have = 0;
         void *ws = workspace(a[8], bytes, z, hold, have);
         const mtp_stream_t stream = stream_of(a[9]);
-        return call([&] { return fn.select(pz, dt, scores, temp, b, w, v, k, tokens, parents, best, flags, ws, have, stream); });
+        const auto f = fn.select;
+        return call([&] { return f(pz, dt, scores, temp, b, w, v, k, tokens, parents, best, flags, ws, have, stream); });
     });
 }
 
@@ -280,9 +282,10 @@ PyObject *beam_reorder(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (d > 0x7fffffff) value_error("a dimension is too large");
         if (!fn.reorder) return NOT_BOUND;
         const mtp_stream_t stream = stream_of(a[4]);
+        const auto f = fn.reorder;
         return call([&] {
-            return fn.reorder(x.data_ptr(), parents, static_cast<int>(N0), static_cast<int>(B), static_cast<int>(W),
-                              static_cast<int>(K), row, out.data_ptr(), flags, stream);
+            return f(x.data_ptr(), parents, static_cast<int>(N0), static_cast<int>(B), static_cast<int>(W),
+                     static_cast<int>(K), row, out.data_ptr(), flags, stream);
         });
     });
 }
@@ -346,7 +349,8 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.max_pages = static_cast<int>(most);
         if (!fn.commit) return NOT_BOUND;
         const mtp_stream_t stream = stream_of(a[15]);
-        return call([&] { return fn.commit(&s, stream); });
+        const auto f = fn.commit;
+        return call([&] { return f(&s, stream); });
     });
 }
 

@@ -415,7 +415,12 @@ extern "C" int mtp_beam_reorder(const void *states, const int32_t *parents, int 
     if (N0 < 0 || B < 0 || W < 1 || K < 1 || row_bytes < 0 || row_bytes > (1ll << 40)) return MTP_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(N0) * B * K;
     if (static_cast<long long>(N0) * B > (1ll << 31) / K) return MTP_ERR_INVALID_ARG;
-    if (rows == 0 || row_bytes == 0) return MTP_OK;
+    if (rows == 0 || row_bytes == 0) {  // nothing is moved: nothing is flagged
+        if (row_flags && B > 0 &&
+            cudaMemsetAsync(row_flags, 0, static_cast<size_t>(B) * sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return MTP_ERR_CUDA;
+        return MTP_OK;
+    }
     if (!states || !parents || !out) return MTP_ERR_INVALID_ARG;
     const uintptr_t s0 = reinterpret_cast<uintptr_t>(states), d0 = reinterpret_cast<uintptr_t>(out);
     const uintptr_t s1 = s0 + static_cast<uintptr_t>(N0) * B * W * row_bytes, d1 = d0 + static_cast<uintptr_t>(rows) * row_bytes;
@@ -438,6 +443,7 @@ extern "C" int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t st
         a.max_pages < 1 || static_cast<long long>(a.max_pages) * a.page_size > 0x7fff0000ll)
         return MTP_ERR_INVALID_ARG;
     if (a.layers > 0 && (a.Hkv < 1 || a.D < 1 || a.D > 4096 || a.Hkv > 65536)) return MTP_ERR_INVALID_ARG;
+    if (a.layers > 0 && static_cast<long long>(a.T) * a.Hkv * a.D > (1ll << 30)) return MTP_ERR_INVALID_ARG;  // words of a path, in 32 bits
     if (a.B == 0) return MTP_OK;
     if (!a.tokens || !a.target_tokens || !a.page_table || !a.cache_len || !a.out_tokens || !a.accept_len || !a.path ||
         !a.new_len || (a.layers > 0 && (!a.k_new || !a.v_new || !a.k_cache || !a.v_cache)))

@@ -205,7 +205,7 @@ def mtp_beam_reorder(states, parents, *, out: Optional[ReorderResult] = None, st
             dev = states.device
             out = mine = ReorderResult(
                 torch.empty((*states.shape[:2], parents.shape[1], *states.shape[3:]), dtype=states.dtype, device=dev),
-                torch.zeros((states.shape[1],), dtype=torch.int32, device=dev))
+                torch.empty((states.shape[1],), dtype=torch.int32, device=dev))
         _call("beam_reorder", index, (states, parents, out.states, out.row_flags, _raw(torch, index, stream, mine)))
     return out
 

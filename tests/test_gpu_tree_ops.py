@@ -513,6 +513,29 @@ def test_beam_reorder_unaligned_and_bad_parents():
             assert torch.equal(r.states[:, b, k], want)
 
 
+def test_beam_reorder_flags_on_another_stream():
+    """The flags are the kernel's alone: nothing that the call queues on the
+    current stream, busy here, writes them later."""
+    states = torch.randn(1, 2, 3, 8, device="cuda")
+    parents = torch.tensor([[0, 3], [1, 2]], dtype=i32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    r = mtp.mtp_beam_reorder(states, parents, stream=side)
+    torch.cuda.synchronize()
+    assert r.row_flags.tolist() == [mtp.ROW_BAD_ID, 0]
+    assert torch.equal(r.states[0, 1], states[0, 1, 1:])
+
+
+@pytest.mark.parametrize("shape", [(0, 2, 3, 4), (2, 2, 3, 0)])
+def test_beam_reorder_no_bytes(shape):
+    flags = torch.full((2,), 9, dtype=i32, device="cuda")
+    states = torch.zeros(shape, device="cuda")
+    out = mtp.ReorderResult(torch.empty_like(states), flags)
+    r = mtp.mtp_beam_reorder(states, torch.zeros(2, 3, dtype=i32, device="cuda"), out=out)
+    assert r.row_flags.tolist() == [0, 0]
+
+
 def test_beam_reorder_overlap_is_refused():
     x = torch.zeros(1, 2, 4, 8, device="cuda")
     up = torch.zeros(2, 4, dtype=i32, device="cuda")

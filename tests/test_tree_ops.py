@@ -216,3 +216,15 @@ def test_host_validation_of_tree_commit(lib):
         assert call(**bad) == 1, bad
     assert call(k_new=(1 << 20) + 1) == 3
     assert call(B=0, ptr=0) == 0
+
+
+def test_tree_commit_most_elements(lib):
+    """A path's words are counted in 32 bits."""
+    p = [1 << 20] * 15
+
+    def call(T, Hkv, D, B):
+        return lib.mtp_tree_commit(tree._COMMIT.pack(*p, *([64] * 16), 1, 1, B, T, Hkv, D, 5, 16, 2), None)
+
+    assert call(64, 65536, 512, 2) == 1
+    assert call(64, 65536, 4096, 2) == 1
+    assert call(64, 65536, 256, 0) == 0
