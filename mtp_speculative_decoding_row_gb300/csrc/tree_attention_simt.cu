@@ -9,7 +9,14 @@
 // registers, the running maximum m and sum l of the softmax per row
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
 //   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j       (s in units of log2 e),
-// all in float32.
+// all in float32.  A warp has four rows from their scores to their output, so
+// only the tile itself needs barriers.  The next tile's keys are on their way
+// while this one's weights and outputs are formed, its values while the next
+// scores are: one tile of shared memory each, so that two CTAs fit an SM (64
+// ragged sequences of up to 2500 tokens, 16 rows, float32: 89 -> 68 us; 128
+// without the four rows to a warp and the values four at a time).  What bounds
+// it: two thirds of the issue slots are empty while warps wait for shared
+// memory and for each other; memory runs at a fifth of its rate.
 #include "tree_attention.cuh"
 
 namespace mtp {
@@ -45,6 +52,23 @@ __device__ __forceinline__ void row_to_smem(float *dst, const void *p, int64_t o
     } else {
         for (int c = l; c < DP; c += nl) dst[c] = c < D ? ld1<T>(p, off + c) : 0.f;
     }
+}
+
+// The same of a key or value: in float32 whole vectors are copied
+// asynchronously (a group is to be committed and waited for).
+template <typename T, int DP>
+__device__ __forceinline__ void row_async(float *dst, const void *p, int64_t off, int D, int l, int nl, bool vec) {
+    if constexpr (Store<T>::ES == 4) {
+        if (vec) {
+            for (int c = l; c < DP / 4; c += nl)
+                if (4 * c < D)
+                    cp_async16(smem_addr(dst + 4 * c), static_cast<const float *>(p) + off + 4 * c);
+                else
+                    *reinterpret_cast<float4 *>(dst + 4 * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            return;
+        }
+    }
+    row_to_smem<T, DP>(dst, p, off, D, l, nl, vec);
 }
 
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
@@ -87,6 +111,26 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         const int rows_n = bad_nodes ? A.rows : n * A.G;  // rows that are written
         if (tid == 0) s_flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
         __syncthreads();
+        // This thread's part of the keys or of the values of tile t, one row for
+        // four threads; `pid`: the row's page.
+        auto page_of = [&](int t) {
+            const int pos = t * BN + (tid >> 2);
+            return t < pc.t1 && t < pc.prefix && pos < pc.len ? attn_page(A, b, pos / A.page_size) : 0;
+        };
+        auto fetch = [&](bool values, int t, int pid) {
+            const int j = tid >> 2;
+            if (t < pc.t1 && j < (t == pc.prefix ? n : min(BN, pc.len - t * BN))) {
+                const int off = (t * BN + j) % A.page_size;
+                const int64_t *cs = values ? A.vcs : A.kcs, *ns = values ? A.vs : A.ks;
+                const int64_t from = t == pc.prefix ? b * ns[0] + j * ns[1] + h * ns[2] : pid * cs[0] + off * cs[1] + h * cs[2];
+                const void *src = t == pc.prefix ? (values ? A.v_new : A.k_new) : (values ? A.v_cache : A.k_cache);
+                row_async<T, DP>(values ? sv + j * DP : sk + j * KS, src, from, A.D, tid & 3, 4, vec);
+            }
+            cp_async_commit();
+        };
+        int pid = page_of(pc.t0);
+        fetch(false, pc.t0, pid);
+        fetch(true, pc.t0, pid);
         int bad = attn_check_pages(A, b, pc.len, tid, NT);
         if (tid < 32) bad |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, smask, s_above);
         if (bad) atomicOr(&s_flag, bad);
@@ -112,23 +156,8 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         for (int t = pc.t0; t < pc.t1; ++t) {
             const bool tree = t == pc.prefix;
             const int valid = tree ? n : min(BN, pc.len - t * BN);
-            {
-                const int j = tid >> 2, l = tid & 3;  // 4 threads a key
-                if (j < valid) {
-                    int64_t ko, vo;
-                    if (tree) {
-                        ko = b * A.ks[0] + j * A.ks[1] + h * A.ks[2];
-                        vo = b * A.vs[0] + j * A.vs[1] + h * A.vs[2];
-                    } else {
-                        const int pos = t * BN + j, page = pos / A.page_size, off = pos - page * A.page_size;
-                        const int64_t pid = attn_page(A, b, page);
-                        ko = pid * A.kcs[0] + off * A.kcs[1] + h * A.kcs[2];
-                        vo = pid * A.vcs[0] + off * A.vcs[1] + h * A.vcs[2];
-                    }
-                    row_to_smem<T, DP>(sk + j * KS, tree ? A.k_new : A.k_cache, ko, A.D, l, 4, vec);
-                    row_to_smem<T, DP>(sv + j * DP, tree ? A.v_new : A.v_cache, vo, A.D, l, 4, vec);
-                }
-            }
+            pid = page_of(t + 1);
+            cp_async_wait<1>();  // the keys
             __syncthreads();
             if (works) {
                 // scores of rows 2 ty, 2 ty + 1 against keys tx + 16 i
@@ -160,7 +189,11 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                         sp[r * (BN + 4) + j] = on ? s[i][c] : -INFINITY;
                     }
                 }
-                __syncwarp();
+            }
+            cp_async_wait<0>();  // the values
+            __syncthreads();
+            fetch(false, t + 1, pid);  // the next keys: on their way from here on
+            if (works) {
                 {  // softmax: 8 threads a row
                     const int r = tid >> 3, l = tid & 7;
                     float *p = sp + r * (BN + 4);
@@ -251,6 +284,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                 }
             }
             __syncthreads();
+            fetch(true, t + 1, pid);
         }
 
         const int flag = s_flag;

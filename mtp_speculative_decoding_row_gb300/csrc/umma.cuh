@@ -145,10 +145,4 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return r;
 }
 
-// 16-byte asynchronous copy to shared memory (completion by cp_async_wait_all
-// of the issuing thread).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 }  // namespace mtp
