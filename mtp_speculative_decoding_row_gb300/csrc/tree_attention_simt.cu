@@ -329,14 +329,17 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 // next groups: with m the largest of the parts' maxima, o = sum_i 2^(m_i - m)
 // o_i / sum_i 2^(m_i - m) l_i, the parts in the order of their keys.  A warp
 // takes one row and lane i the columns 4 i ..; the maxima and sums of 32 parts
-// are loaded by the 32 lanes at once and handed round, and four parts' rows are
-// on their way at a time: what bounds this kernel is the time of a load, not
-// their number (a row of 20 parts read one after the other took 30 us), so it
-// also keeps its registers few and many warps on an SM.
-constexpr int JOIN_AHEAD = 4;
+// are loaded by the 32 lanes at once and handed round, and the rows of several
+// parts are on their way at a time: what bounds this kernel is the time of a
+// load, not their number (a row of 20 parts read one after the other took 30
+// us).  bfloat16 has many rows of few parts: four at a time, few registers and
+// many warps on an SM (trees of 64 nodes: 262 us, with eight 267, with sixteen
+// 278).  float32 has more and smaller CTAs, so more parts: sixteen (4 sequences
+// of 2501: 22.0 us with four, 20.3 with eight, 19.6 with sixteen).
 
 template <typename T, int NQ>
-__global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
+__global__ void __launch_bounds__(JOIN_THREADS, Store<T>::ES == 4 ? 5 : 10) attn_join_impl(const __grid_constant__ TreeAttnArgs A) {
+    constexpr int AHEAD = Store<T>::ES == 4 ? 16 / NQ : 4;
     pdl_wait();
     pdl_next();
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
@@ -367,10 +370,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_
             l = fmaf(w, s[A.bm + r], l);
         }
         const int here = min(32, parts - k0);
-        for (int i0 = 0; i0 < here; i0 += JOIN_AHEAD) {
-            float4 x[JOIN_AHEAD][NQ];
+        for (int i0 = 0; i0 < here; i0 += AHEAD) {
+            float4 x[AHEAD][NQ];
 #pragma unroll
-            for (int i = 0; i < JOIN_AHEAD; ++i)
+            for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     const int c = 4 * lane + 128 * q;
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 10) attn_join_impl(const __grid_
                         x[i][q] = make_float4(s[0], c + 1 < A.D ? s[1] : 0.f, c + 2 < A.D ? s[2] : 0.f, c + 3 < A.D ? s[3] : 0.f);
                 }
 #pragma unroll
-            for (int i = 0; i < JOIN_AHEAD; ++i) {
+            for (int i = 0; i < AHEAD; ++i) {
                 const float wi = __shfl_sync(FULL, w, (i0 + i) & 31);
                 if (i0 + i >= here) continue;
 #pragma unroll
