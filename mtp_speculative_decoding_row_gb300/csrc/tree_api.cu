@@ -156,11 +156,17 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
     if (p.max_tiles * a.Hkv > 0x7fffffffll) return MTP_ERR_INVALID_ARG;  // tiles of a sequence are counted in 32 bits
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
-    // Units of few tiles are not split, unless there are so many of them that
-    // their sizes should be evened out: a join takes as long as about six tiles
-    // on the tensor cores (5 us), or two of the other kernel.
+    // Units are not split where that costs less.  Whole, the CTAs take them in
+    // `waves` of max_tiles; split, all have the same number of tiles, and a
+    // join and the ends of the pieces take as long as about six tiles on the
+    // tensor cores, two of the other kernel.  (Whole against split: one token
+    // after 256 8.3 and 13 us; 128 units of 1000 tokens 17 and 26 us, 512 of
+    // 1000 65 and 73.)  The lengths are not known here: beyond 16 tiles, or
+    // four waves, one long unit could cost more than it saves.
     const long long units = static_cast<long long>(a.Hkv) * (a.B > 0 ? a.B : 1);
-    p.whole = p.max_tiles <= (umma ? 6 : 2) && units <= 2 * groups;
+    const long long waves = (units + groups - 1) / (groups > 0 ? groups : 1);
+    p.whole = umma ? p.max_tiles <= 16 && waves <= 4 && (waves * groups - units) * p.max_tiles <= 6 * groups
+                   : p.max_tiles <= 2 && waves <= 2;
     const long long all = p.whole ? units : p.max_tiles * units;
     if (groups > all) groups = all;
     p.groups = static_cast<int>(groups < 1 ? 1 : groups);

@@ -269,6 +269,14 @@ def test_tree_attention_many_uneven(dtype, T, Hq, D):
     run_attention(attn_case(71, dtype, len(lens), T, Hq, 8, D, 32, lens))
 
 
+@pytest.mark.parametrize("T, Hq, D", [(1, 8, 64), (3, 16, 128), (9, 32, 64), (2, 16, 256)])
+def test_tree_attention_many_uneven_split(T, Hq, D):
+    """The same with lengths that are too many tiles to be left whole."""
+    rng = random.Random(T)
+    lens = [0] * 5 + [2300] + [rng.choice([0, 1, 128, 129, rng.randint(500, 2299)]) for _ in range(16)] + [1408, 0]
+    run_attention(attn_case(72, "bf16", len(lens), T, Hq, 8, D, 32, lens))
+
+
 @pytest.mark.parametrize("dtype, T, D", [("bf16", 3, 128), ("bf16", 33, 64), ("f32", 3, 64)])
 def test_tree_attention_is_repeatable(dtype, T, D):
     """The split of long sequences joins in a fixed order: the same bits every time."""
