@@ -15,8 +15,8 @@
 // scores are: one tile of shared memory each, so that two CTAs fit an SM (64
 // ragged sequences of up to 2500 tokens, 16 rows, float32: 89 -> 68 us; 128
 // without the four rows to a warp and the values four at a time).  What bounds
-// it: two thirds of the issue slots are empty while warps wait for shared
-// memory and for each other; memory runs at a fifth of its rate.
+// it: half of the issue slots, and as many empty while warps wait for shared
+// memory and for each other (28 rows); memory runs at 14 % of its rate.
 #include "tree_attention.cuh"
 
 namespace mtp {
