@@ -31,6 +31,8 @@
 // row is not aligned, so the order of the sums -- and with it the last bit of
 // a normaliser -- does not depend on where a row lies: equal rows get equal
 // scores and their ties go to the smaller beam.
+#include <cfloat>
+
 #include "common.cuh"
 #include "tree.h"
 
@@ -126,8 +128,8 @@ __device__ __forceinline__ int cut(uint64_t *list, int n, int keep, uint64_t *tm
     return m;
 }
 
-// Look at the `queued` vectors that a warp has put aside: their elements that
-// reach the bound join the warp's list of `count`.  Returns the list's new
+// Look at the `queued` vectors that a warp has put aside, all of them in its
+// part: their elements that reach the bound join the warp's list of `count`.  Returns the list's new
 // length; a cut raises *s_bound.
 template <typename T>
 __device__ __noinline__ int drain(const unsigned char *row, uint32_t sh, int whole, int V, const int *queue, int queued, uint64_t *list,
@@ -267,7 +269,10 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         }
         // (a bound that is read late is a lower bound all the same)
         const uint64_t bound = __shfl_sync(FULL, *static_cast<volatile unsigned long long *>(&s_bound), 0);
-        const float zb = order_float(static_cast<uint32_t>(bound >> 32));
+        // Vectors of -inf alone are never put aside: they hold no candidate, and
+        // what stands in for vectors behind the part's end is such a one (drain()
+        // would read the next part's logits for it, candidates of two parts then).
+        const float zb = fmaxf(order_float(static_cast<uint32_t>(bound >> 32)), -FLT_MAX);
         if (__any_sync(FULL, top >= zb)) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {

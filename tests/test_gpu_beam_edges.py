@@ -36,3 +36,99 @@ def test_one_bad_logit_in_every_vector_of_the_first_rounds(dtype, bad):
         torch.cuda.synchronize()
         assert r.row_flags.tolist() == [mtp.ROW_NONFINITE] * B + [0]
         assert (r.tokens[:B] == -1).all() and r.tokens[B].tolist() == [0, 1, 2]
+
+
+def exact_scores(z, scores, T):
+    """[B, W, V] float64: scores[w] + ln softmax(z_w / T)(v), from the
+    difference to the row's largest logit, so that it holds at any T."""
+    x = z.double()
+    x = (x - x.amax(2, keepdim=True)) / T.double()[:, None, None]
+    x = x - x.exp().sum(2, keepdim=True).log() + scores.double()[:, :, None]
+    return x.masked_fill((scores == -math.inf)[:, :, None] | z.isneginf(), -math.inf)
+
+
+def check_exact(z, scores, T, K, r):
+    """Every returned candidate is looked up in the 64-bit scores.
+
+    Within a beam the order is that of the logits, equal ones by index, and
+    must be met exactly.  A score is off by at most tol: exponents x = (z -
+    max) log2(e) / T by three roundings, 3 |x| 2^-24, which changes a sum that
+    holds 2^0 by at most 3 max(x 2^-x) 2^-24 ln 2 < 2^-23 per term's share, x
+    itself of terms that weigh (x < 24) by 2^-18; powers 2^-21; sums of fewer
+    than 256 terms in a row 2^-16 at the very worst and far less here (100,000
+    elements over 256 threads and four sums each: 2^-18); with the output's own
+    rounding 2^-16 + 2^-23 |score|.  Between beams candidates closer than two
+    such errors may come in either order."""
+    exact = exact_scores(z, scores, T)
+    B, W, V = z.shape
+    for b in range(B):
+        tok, par, val = r.tokens[b].tolist(), r.parents[b].tolist(), r.scores[b].tolist()
+        n = min(K, int((exact[b] > -math.inf).sum()))
+        assert all(p == (-1, -1, -math.inf) for p in zip(tok[n:], par[n:], val[n:])), (b, n, tok, par)
+        assert all(0 <= t < V for t in tok[:n]) and all(0 <= p < W for p in par[:n]), (b, tok, par)
+        got = [exact[b, p, t].item() for p, t in zip(par[:n], tok[:n])]
+        tol = [2.0 ** -16 + 2.0 ** -23 * abs(s) for s in got]
+        for s, v, e in zip(got, val, tol):
+            v32 = torch.tensor(s).float().item()
+            assert v == v32 or abs(v - s) <= e, (b, s, v)
+        for i in range(n - 1):
+            assert got[i] >= got[i + 1] - tol[i] - tol[i + 1], (b, i, got[i], got[i + 1])
+        for w in range(W):
+            mine = [t for t, p in zip(tok[:n], par[:n]) if p == w]
+            if scores[b, w] == -math.inf:
+                assert not mine
+                continue
+            order = torch.sort(z[b, w].double() + 0.0, descending=True, stable=True).indices[:len(mine) + 1].tolist()
+            assert mine == order[:len(mine)], (b, w, mine, order)
+            if n == K and n > 0 and len(order) > len(mine):
+                left = exact[b, w, order[-1]].item()
+                assert left <= got[-1] + tol[-1] + 2.0 ** -16 + 2.0 ** -23 * abs(left), (b, w, left, got[-1])
+
+
+def select(z, scores, T, K):
+    r = mtp.mtp_beam_select(z.cuda(), scores.cuda(), T.cuda(), K)
+    torch.cuda.synchronize()
+    assert r.row_flags.tolist() == [0] * z.shape[0]
+    r = mtp.BeamResult(*(t.cpu() for t in r))
+    check_exact(z, scores, T, K, r)
+    return r
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [10007, 24576])
+def test_three_tokens_left_at_every_border(dtype, V):
+    """All but three neighbouring tokens masked, the three at every place
+    where a vector, and so a part of a row, may begin."""
+    vec, B, K = (8 if dtype == "bf16" else 4), 64, 6
+    lse = math.log(math.e + math.e ** 2 + math.e ** 3)
+    starts = list(range(vec, V - 1, vec))
+    for s0 in range(0, len(starts), B):
+        at = torch.tensor((starts[s0:s0 + B] * B)[:B], device="cuda")
+        z = torch.full((B, 1, V), -math.inf, dtype=DTYPES[dtype], device="cuda")
+        for d in (-1, 0, 1):
+            z[torch.arange(B), 0, at + d] = 2.0 + d
+        r = mtp.mtp_beam_select(z, torch.zeros(B, 1, device="cuda"), torch.ones(B, device="cuda"), K)
+        want = torch.stack([at + 1, at, at - 1] + [torch.full_like(at, -1)] * 3, 1)
+        assert torch.equal(r.tokens.long(), want), (s0, r.tokens, want)
+        assert (r.scores[:, :3] - torch.tensor([3 - lse, 2 - lse, 1 - lse], device="cuda")).abs().max() < 1e-5
+        assert (r.scores[:, 3:] == -math.inf).all() and (r.row_flags == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B, W, V, left", [(1, 1, 5003, 3), (1, 4, 151936, 50), (1, 1, 151936, 8), (16, 5, 50257, 50), (3, 2, 20011, 200),
+                                           (1, 64, 9001, 2), (40, 16, 4099, 40)])
+def test_few_tokens_left(dtype, B, W, V, left):
+    """Grammar masks and top-k filters: -inf but for a few tokens at random."""
+    for seed in range(6):
+        g = torch.Generator().manual_seed(1000 * V + seed)
+        z = torch.full((B, W, V), -math.inf)
+        at = torch.randint(V, (B, W, left), generator=g)
+        z.scatter_(2, at, torch.randn(B, W, left, generator=g) * 3)
+        z = z.to(DTYPES[dtype])
+        select(z, -torch.rand(B, W, generator=g).cumsum(1), 0.5 + torch.rand(B, generator=g), min(64, W * V, 1 + 13 * seed))
+
+
+def test_three_tokens_of_one_row():
+    z = torch.full((1, 1, 5003), -math.inf)
+    z[0, 0, 2510:2513] = torch.tensor([3.0, 2.0, 1.0])
+    assert select(z, torch.zeros(1, 1), torch.ones(1), 6).tokens.tolist() == [[2510, 2511, 2512, -1, -1, -1]]
