@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     __shared__ uint64_t tmps[NW][BEAM_MAX_K];
     __shared__ int queue[NW][QUEUE];
     __shared__ unsigned long long s_bound;
-    __shared__ int s_n[NW];
+    __shared__ int s_bad, s_n[NW];
     __shared__ float s_m[NW];
     __shared__ float s_s[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -216,14 +216,17 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     const int j0 = part * (A.part_elems / VEC);
     const int j1 = min((A.V + VEC - 1) / VEC, j0 + A.part_elems / VEC);
     const int whole = min(A.V / VEC, j1);  // vectors without a tail
-    if (tid == 0) s_bound = 0;  // (its first reader and writer come behind the barriers of raise_bound)
+    if (tid == 0) {
+        s_bound = 0;
+        s_bad = 0;
+    }
 
     // s: the sum of e_i = 2^(z_i k - mk), where mk = m k rounded.  se and s1: the
     // sums of e_i and of e_i z_i over every fourth vector; their ratio says
     // where the row's weight lies, which is all that the correction for dk needs
     // to know (it is below 3e-7 of a score to begin with).
     float m = -INFINITY, mk = 0.f, s = 0.f, se = 0.f, s1 = 0.f;
-    int bad = 0, count = 0, queued = 0, again = j0;
+    int count = 0, queued = 0, again = j0;
     // one round: vectors j + tid, j + tid + NT, .. of the row
     auto round = [&](int j, uint4 (&raw)[UN]) {
         float top = -INFINITY;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         for (int u = 0; u < UN; ++u) top = max_nan(top, Store<T>::vmax(raw[u]));
         if (!(top <= m)) {  // a new maximum of this thread, or NaN
             if (!(top < INFINITY)) {
-                bad = 1;  // the join flags the sequence; nothing of this round counts
+                s_bad = 1;  // the join flags the sequence; nothing of this round counts
 #pragma unroll
                 for (int u = 0; u < UN; ++u) raw[u] = minus_inf_vec<T>();
                 top = -INFINITY;
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     constexpr int STEP = NT * UN;
     uint4 one[UN], two[UN];
     fetch(j0, one);
+    __syncthreads();  // s_bad and s_bound are set (a thread that met a NaN before could be overwritten)
     for (int j = j0; j < j1; j += 2 * STEP) {
         if (j + STEP < j1) fetch(j + STEP, two);
         round(j, one);
@@ -349,13 +353,13 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     }
     sum = warp_allsum(sum);
     if (lane == 0) s_s[warp] = sum;
-    bad = __syncthreads_or(bad);
+    __syncthreads();
     if (tid == 0) {
         float t = 0.f;
         for (int w = 0; w < NW; ++w) t += s_s[w];
         A.part_max[slot] = top;
         A.part_sum[slot] = t;
-        A.part_flag[slot] = bad;
+        A.part_flag[slot] = s_bad;
     }
 }
 
