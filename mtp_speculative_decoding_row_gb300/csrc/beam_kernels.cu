@@ -178,6 +178,10 @@ __device__ __forceinline__ void raise_bound(float value, int keep, unsigned long
     __syncthreads();
 }
 
+// k = log2(e) / T; the largest float where that is beyond it (a difference of
+// two logits is then 0 or far beyond any weight, whichever of the two k is).
+__device__ __forceinline__ float exponent_scale(float temp) { return fminf(LOG2E / temp, FLT_MAX); }
+
 template <typename T>
 __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_constant__ BeamArgs A) {
     constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     // log2(e) / T in two floats, k + dk: a row's sum is corrected for the
     // rounding of k (below).  log2(e) = LOG2E + LOG2E_LO.
     constexpr float LOG2E_LO = 1.9259629911266175e-8f;
-    const float k = LOG2E / temp, dk = (fmaf(-k, temp, LOG2E) + LOG2E_LO) / temp;
+    const float k = exponent_scale(temp), dk = k < FLT_MAX ? (fmaf(-k, temp, LOG2E) + LOG2E_LO) / temp : 0.f;
     const unsigned char *base = static_cast<const unsigned char *>(A.logits) + static_cast<size_t>(row) * A.V * ES;
     const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base) & 15u);
     const int j0 = part * (A.part_elems / VEC);
@@ -221,11 +225,14 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
         s_bad = 0;
     }
 
-    // s: the sum of e_i = 2^(z_i k - mk), where mk = m k rounded.  se and s1: the
-    // sums of e_i and of e_i z_i over every fourth vector; their ratio says
-    // where the row's weight lies, which is all that the correction for dk needs
-    // to know (it is below 3e-7 of a score to begin with).
-    float m = -INFINITY, mk = 0.f, s = 0.f, se = 0.f, s1 = 0.f;
+    // s: the sum of e_i = 2^((z_i - m) k): the difference first, so that the
+    // exponents that weigh are small and exact to 2^-23 of themselves at any
+    // temperature (z_i k - m k loses what a low temperature leaves of it: m k has
+    // half a unit of error at 2^24).  se and s1: the sums of e_i and of e_i (z_i
+    // - m) over every fourth vector; their ratio says where the row's weight
+    // lies, which is all that the correction for dk needs to know (it is below
+    // 3e-7 of a score to begin with).
+    float m = -INFINITY, s = 0.f, se = 0.f, s1 = 0.f;
     int count = 0, queued = 0, again = j0;
     // one round: vectors j + tid, j + tid + NT, .. of the row
     auto round = [&](int j, uint4 (&raw)[UN]) {
@@ -239,12 +246,11 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
                 for (int u = 0; u < UN; ++u) raw[u] = minus_inf_vec<T>();
                 top = -INFINITY;
             } else {
-                const float f = m == -INFINITY ? 0.f : ex2(mk - top * k);
+                const float gap = m - top, f = ex2(gap * k);  // (m = -inf at first: f = 0)
+                s1 = f > 0.f ? f * fmaf(se, gap, s1) : 0.f;
                 m = top;
-                mk = top * k;
                 s *= f;
                 se *= f;
-                s1 *= f;
             }
         }
         if (m > -INFINITY) {
@@ -257,9 +263,9 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
                 Store<T>::unpack(raw[u], z);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float x = ex2(fmaf(z[e], k, -mk));
+                    const float d = z[e] - m, x = ex2(d * k);
                     a[e & 3] += x;
-                    if (u == 0) a1 = fmaf(x, fmaxf(z[e], -3.0e38f), a1);  // (-inf: 0 times a finite number)
+                    if (u == 0) a1 = fmaf(x, fmaxf(d, -FLT_MAX), a1);  // (-inf: 0 times a finite number)
                 }
                 if (u == 0) se += (a[0] + a[1]) + (a[2] + a[3]);
             }
@@ -344,13 +350,13 @@ __global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_part_impl(const __grid_c
     top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w]);
-    // 2^((z_i - m) (k + dk)) = e_i 2^(z_i dk + mk - m (k + dk)), and the second
-    // factor is 1 + (z_i dk + mk - m (k + dk)) ln 2 to within its square (1e-12)
+    // The thread's share of sum_i 2^((z_i - top) (k + dk)) is s 2^((m - top) k)
+    // 2^(((m - top) + d) dk), d the mean of z_i - m over its weight (the spread of
+    // z_i dk about its mean changes the sum by its square: 1e-12).  A share below
+    // 2^-200 is none.
     float sum = 0.f;
-    if (m > -INFINITY) {
-        const float off = -fmaf(m, k, -mk) - m * dk, where = se > 0.f ? s1 / se : m;
-        sum = fmaf(LN2 * (off + dk * where), s, s) * ex2((m - top) * k);
-    }
+    const float gap = (m - top) * k;
+    if (gap > -200.f) sum = s * ex2(fmaf((m - top) + (se > 0.f ? s1 / se : 0.f), dk, gap));
     sum = warp_allsum(sum);
     if (lane == 0) s_s[warp] = sum;
     __syncthreads();
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
         const int row = b * A.W + w;
         const float score = __ldg(A.scores + row);
         const size_t p0 = static_cast<size_t>(row) * A.parts;
-        const float k = LOG2E / temp;
+        const float k = exponent_scale(temp);
         float top = -INFINITY, sum = 0.f;
         int bad = 0;
         for (int p = lane; p < A.parts; p += 32) {

@@ -132,3 +132,42 @@ def test_three_tokens_of_one_row():
     z = torch.full((1, 1, 5003), -math.inf)
     z[0, 0, 2510:2513] = torch.tensor([3.0, 2.0, 1.0])
     assert select(z, torch.zeros(1, 1), torch.ones(1), 6).tokens.tolist() == [[2510, 2511, 2512, -1, -1, -1]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [100.0, 1e-2, 1e-3, 1e-4, 1e-5, 3e-6, 1e-6, 1e-7, 1e-9, 1e-20, 1e-37, 4e-39, 1e-44])
+def test_any_temperature(dtype, T):
+    """Down to what stands for greedy: rows with one dominating logit of either
+    sign, rows of small numbers, and rows of two equal best ones."""
+    g = torch.Generator().manual_seed(7)
+    W, V = 6, 20011
+    z = torch.randn(4, W, V, generator=g) * 3
+    top = torch.randint(V, (W,), generator=g)
+    z[0] -= 200                                    # negative rows
+    for w in range(W):
+        z[0, w, top[w]] = -10.0 - 6.3 * w
+        z[1, w, top[w]] = 10.0 + 6.3 * w
+    z[2] *= 1e-6
+    z[3, :, 17] = z[3, :, 19000] = 39.7
+    z = z.to(DTYPES[dtype])
+    scores = -torch.rand(4, W, generator=g).cumsum(1)
+    r = select(z, scores, torch.full((4,), T), 12)
+    if T < 1e-3:  # each beam's best first, in the order of the beams
+        first = torch.sort(z[1].double(), descending=True, stable=True, dim=1).indices[:, 0]
+        assert r.tokens[1, :W].tolist() == first.tolist() and r.parents[1, :W].tolist() == list(range(W))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0])
+def test_masks_of_the_lowest_value(dtype, T):
+    """A mask of the type's lowest number: a row of nothing else is uniform."""
+    low = torch.finfo(DTYPES[dtype]).min
+    V = 9001
+    z = torch.full((3, 2, V), low, dtype=DTYPES[dtype])
+    z[1, 0, 5000], z[1, 0, 77] = 1.5, 1.0
+    z[1, 1, 8000] = -2.0
+    z[2] = torch.randn(2, V).to(z.dtype)
+    z[2, :, ::3] = low
+    r = select(z, torch.tensor([[0.0, -1.0]] * 3), torch.full((3,), T), 3)
+    assert r.tokens[0].tolist() == [0, 1, 2] and r.parents[0].tolist() == [0, 0, 0]
+    assert abs(r.scores[0, 0].item() + math.log(V)) < 1e-5
