@@ -415,8 +415,10 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and
  *   parents -1 and scores NaN.
  * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24
- * (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  Scores are
- * formed and compared in float64.
+ * (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  A row's sum of
+ * exponentials is a float32 sum (relative error below 2^-16 for V <= 2^18); with
+ * its logarithm, scores are formed and compared in float64 and
+ * rounded to float32 at the end.
  */
 int mtp_beam_select(const void *logits, mtp_dtype dtype, const float *scores, const float *temperature, int B, int W, int V,
                     int K, int32_t *tokens, int32_t *parents, float *out_scores, int32_t *row_flags, void *workspace,

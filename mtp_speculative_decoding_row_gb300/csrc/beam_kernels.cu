@@ -5,9 +5,10 @@
 // Every logit is read once.  A row is cut into parts, one CTA each; a part
 // yields its maximum, its sum of 2^((z - max) k) with k = log2(e) / T, and
 // its own K best logits (within a row the order of the scores is that of the
-// logits).  A second launch turns the parts' candidates into scores in
-// float64 -- candidates of two beams may lie closer than float32 tells apart
-// -- and merges the sorted lists.
+// logits).  A second launch turns the parts' candidates into scores -- each
+// logit's difference to its row's maximum, over T, less the logarithm of the
+// float32 sum, in float64, because candidates may lie closer than float32 tells
+// apart -- and merges the sorted lists.
 //
 // Candidates are 64-bit keys: the logit's bits in an order-preserving form,
 // then the complement of the index, so one integer comparison orders by value
@@ -447,7 +448,8 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
     const int beam_cand = A.parts * A.KL;
     auto key_of = [&](int i, float z, int v) {
         const int w = i / beam_cand;
-        return v < 0 ? NONE : order_double(s_off[w] + static_cast<double>(z - s_max[w]) * inv_t);
+        // (the difference in float64 too: in float32 neighbouring logits fall together beside a large one)
+        return v < 0 ? NONE : order_double(s_off[w] + (static_cast<double>(z) - static_cast<double>(s_max[w])) * inv_t);
     };
     if (shared) {
         for (int i = tid; i < n; i += NT) {

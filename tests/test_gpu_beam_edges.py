@@ -171,3 +171,17 @@ def test_masks_of_the_lowest_value(dtype, T):
     r = select(z, torch.tensor([[0.0, -1.0]] * 3), torch.full((3,), T), 3)
     assert r.tokens[0].tolist() == [0, 1, 2] and r.parents[0].tolist() == [0, 0, 0]
     assert abs(r.scores[0, 0].item() + math.log(V)) < 1e-5
+
+
+@pytest.mark.parametrize("V", [20011, 151936])
+def test_neighbouring_logits_beside_a_large_one(V):
+    """Logits of one row that differ by less than a float32 difference to the
+    row's largest can tell, the larger one in a later part."""
+    z = torch.full((2, 1, V), -100.0)
+    z[:, 0, 3] = 12.0
+    for b in range(2):
+        for i, at in enumerate(range(100, V, V // 7)):
+            z[b, 0, at] = 1.0 + i * 2.0 ** -23
+    z[1, 0, 3] = 3e4
+    r = select(z, torch.zeros(2, 1), torch.ones(2), 8)
+    assert r.tokens[0].tolist() == r.tokens[1].tolist() == [3] + sorted(range(100, V, V // 7), reverse=True)[:7]
