@@ -403,8 +403,8 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  * mtp_beam_select -- the K best continuations of a sequence's W beams (one
  * level of a draft tree, or one step of beam search): over w < W, v < V
  *   score(w, v) = scores[b,w] + ln softmax(logits[b,w] / T_b)(v),
- * the K largest, best first; equal scores go to the smaller beam, then the
- * smaller token.  A continuation of probability 0 is never selected: where
+ * the K largest, best first; equal scores go to the smaller beam, then (within
+ * a beam the order is that of the logits) the smaller token.  A continuation of probability 0 is never selected: where
  * fewer than K are left the rest has token and parent -1 and score -inf.  A
  * beam with score -inf is dead: its logits are not read.
  *

@@ -33,6 +33,7 @@
 // a normaliser -- does not depend on where a row lies: equal rows get equal
 // scores and their ties go to the smaller beam.
 #include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tree.h"
@@ -381,8 +382,13 @@ __device__ __forceinline__ long long order_double(double x) {
 // eight of them to a lane: each round takes the best head -- equal scores: the
 // smaller list, and so the smaller beam and index -- and moves its list on.
 // A round is a few warp-wide reductions, with no barrier and no load from
-// global memory.
-__global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ BeamArgs A) {
+// global memory.  Where float64 may not tell the scores of two different logits
+// of a beam apart (a temperature of 10^12, logits of 10^-12 below one of 10),
+// equal scores are looked at by beam, logit and list.  (Doing so always: one
+// sequence of 4 rows 16.3 us instead of 15.3.)  No more registers than the first
+// kernel has: a CTA fits in as soon as one of that kernel's has ended (with 88 of
+// them 64 sequences of 8 rows took 66.5 us instead of 64.5).
+__global__ void __launch_bounds__(NT, BEAM_PER_SM) beam_join_impl(const __grid_constant__ BeamArgs A) {
     constexpr long long NONE = -0x7fffffffffffffffll - 1;
     constexpr int PER = NT / 32;  // lists of a lane
     __shared__ float s_max[BEAM_MAX_W];
@@ -451,16 +457,29 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
         // (the difference in float64 too: in float32 neighbouring logits fall together beside a large one)
         return v < 0 ? NONE : order_double(s_off[w] + (static_cast<double>(z) - static_cast<double>(s_max[w])) * inv_t);
     };
+    // Different logits lie at least 2^-24 of the larger one apart, and a score is
+    // formed by three roundings of 2^-53 of it or of s_off: where |z| / T is below
+    // 2^-26 of these, two scores may be one number.  (By the exponents: float64
+    // arithmetic is slow here.)
+    const int exp_t = static_cast<int>(__float_as_uint(temp) >> 23);
+    auto coarse = [&](int i, long long key, float z) {
+        const int exp_z = static_cast<int>((__float_as_uint(z) >> 23) & 0xffu);
+        const int of_key = static_cast<int>((key < 0 ? ~key : key) >> 52), of_off = (__double2hiint(s_off[i / beam_cand]) >> 20) & 0x7ff;
+        return key != NONE && z != 0.f && (exp_z == 0 ? -24 : exp_z) - max(exp_t, 1) < max(of_key, of_off) - 1023 - 24;
+    };
+    bool careful = !shared;
     if (shared) {
         for (int i = tid; i < n; i += NT) {
             if (i != tid) {
                 z0 = A.cand_z[cand0 + i];
                 v0 = A.cand_v[cand0 + i];
             }
-            s_key[i] = key_of(i, z0, v0);
+            const long long key = key_of(i, z0, v0);
+            careful |= coarse(i, key, z0);
+            s_key[i] = key;
             s_v[i] = v0;
         }
-        __syncthreads();
+        careful = __syncthreads_or(careful);
     }
     if (warp != 0) return;
     long long head[PER];
@@ -475,40 +494,66 @@ __global__ void __launch_bounds__(NT) beam_join_impl(const __grid_constant__ Bea
         head[q] = load(lane * PER + q, 0);
         pos[q] = 0;
     }
-    for (int i = 0; i < A.K; ++i) {
-        long long mine = head[0];
-        int q0 = 0;
+    auto merge = [&](auto looks) {
+        for (int i = 0; i < A.K; ++i) {
+            long long mine = head[0];
+            int q0 = 0;
 #pragma unroll
-        for (int q = 1; q < PER; ++q)
-            if (head[q] > mine) {
-                mine = head[q];
-                q0 = q;
+            for (int q = 1; q < PER; ++q)
+                if (head[q] > mine) {
+                    mine = head[q];
+                    q0 = q;
+                }
+            const uint64_t u = static_cast<uint64_t>(mine) ^ 0x8000000000000000ull;
+            const uint32_t hi = static_cast<uint32_t>(u >> 32), lo = static_cast<uint32_t>(u);
+            const uint32_t top = __reduce_max_sync(FULL, hi);
+            const uint32_t low = __reduce_max_sync(FULL, hi == top ? lo : 0u);
+            const uint32_t same = __ballot_sync(FULL, hi == top && lo == low);
+            int who = __ffs(same) - 1;
+            if constexpr (decltype(looks)::value) {
+                // of the smallest beam with this score the largest logit
+                const int beam = __shfl_sync(FULL, (lane * PER + q0) / A.parts, who);
+                uint32_t zb = 0u;
+                if ((same >> lane) & 1u && mine != NONE) {
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) {
+                        const int list = lane * PER + q;
+                        if (head[q] != mine || list / A.parts != beam) continue;
+                        const uint32_t o = order_bits(A.cand_z[cand0 + list * A.KL + pos[q]]);
+                        if (o > zb) {
+                            zb = o;
+                            q0 = q;
+                        }
+                    }
+                }
+                const uint32_t most = __reduce_max_sync(FULL, zb);
+                who = __ffs(__ballot_sync(FULL, zb == most)) - 1;
             }
-        const uint64_t u = static_cast<uint64_t>(mine) ^ 0x8000000000000000ull;
-        const uint32_t hi = static_cast<uint32_t>(u >> 32), lo = static_cast<uint32_t>(u);
-        const uint32_t top = __reduce_max_sync(FULL, hi);
-        const uint32_t low = __reduce_max_sync(FULL, hi == top ? lo : 0u);
-        const int who = __ffs(__ballot_sync(FULL, hi == top && lo == low)) - 1;
-        if (lane != who) continue;
-        if (mine == NONE) {  // fewer candidates than K: the rest is empty
-            tokens[i] = parents[i] = -1;
-            best[i] = -INFINITY;
-            continue;
+            if (lane != who) continue;
+            if (mine == NONE) {  // fewer candidates than K: the rest is empty
+                tokens[i] = parents[i] = -1;
+                best[i] = -INFINITY;
+                continue;
+            }
+            const int list = lane * PER + q0;
+            int at = 0;
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+                if (q == q0) at = pos[q]++;
+            const int c = list * A.KL + at;
+            tokens[i] = shared ? s_v[c] : A.cand_v[cand0 + c];
+            parents[i] = list / A.parts;
+            best[i] = static_cast<float>(__longlong_as_double(mine < 0 ? mine ^ 0x7fffffffffffffffll : mine));
+            const long long next = load(list, at + 1);
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+                if (q == q0) head[q] = next;
         }
-        const int list = lane * PER + q0;
-        int at = 0;
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            if (q == q0) at = pos[q]++;
-        const int c = list * A.KL + at;
-        tokens[i] = shared ? s_v[c] : A.cand_v[cand0 + c];
-        parents[i] = list / A.parts;
-        best[i] = static_cast<float>(__longlong_as_double(mine < 0 ? mine ^ 0x7fffffffffffffffll : mine));
-        const long long next = load(list, at + 1);
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            if (q == q0) head[q] = next;
-    }
+    };
+    if (careful)
+        merge(std::true_type{});
+    else
+        merge(std::false_type{});
 }
 
 }  // namespace

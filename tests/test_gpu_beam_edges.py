@@ -135,7 +135,7 @@ def test_three_tokens_of_one_row():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T", [100.0, 1e-2, 1e-3, 1e-4, 1e-5, 3e-6, 1e-6, 1e-7, 1e-9, 1e-20, 1e-37, 4e-39, 1e-44])
+@pytest.mark.parametrize("T", [1e30, 100.0, 1e-2, 1e-3, 1e-4, 1e-5, 3e-6, 1e-6, 1e-7, 1e-9, 1e-20, 1e-37, 4e-39, 1e-44])
 def test_any_temperature(dtype, T):
     """Down to what stands for greedy: rows with one dominating logit of either
     sign, rows of small numbers, and rows of two equal best ones."""
@@ -185,3 +185,17 @@ def test_neighbouring_logits_beside_a_large_one(V):
     z[1, 0, 3] = 3e4
     r = select(z, torch.zeros(2, 1), torch.ones(2), 8)
     assert r.tokens[0].tolist() == r.tokens[1].tolist() == [3] + sorted(range(100, V, V // 7), reverse=True)[:7]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_whose_scores_float64_does_not_tell_apart(dtype):
+    """The larger logit comes first wherever in the row, and the smaller beam
+    before it."""
+    V, W = 30011, 3
+    z = torch.full((2, W, V), -50.0)
+    z[0] = 2.0 ** -126 * torch.randint(1, 100, (W, V), generator=torch.Generator().manual_seed(3))
+    for i, at in enumerate(range(50, V, 2000)):
+        z[1, :, at] = (1 + i) * 2.0 ** -100
+    z[1, :, 5] = 1.0
+    r = select(z.to(DTYPES[dtype]), torch.zeros(2, W), torch.tensor([1.0, 1.0]), 40)
+    assert r.parents[0].tolist() == [0] * 40
