@@ -199,3 +199,25 @@ def test_logits_whose_scores_float64_does_not_tell_apart(dtype):
     z[1, :, 5] = 1.0
     r = select(z.to(DTYPES[dtype]), torch.zeros(2, W), torch.tensor([1.0, 1.0]), 40)
     assert r.parents[0].tolist() == [0] * 40
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B, W, V, K", [(1, 1, 1, 1), (3, 4, 3, 12), (2, 5, 50257, 64), (1, 4, 151936, 8), (1, 64, 257, 64), (20, 8, 2048, 16),
+                                        (70, 3, 8191, 33), (1, 2, 32000, 64), (9, 16, 20011, 32)])
+@pytest.mark.parametrize("spread", [0.02, 3.0])
+def test_returned_candidates_have_the_scores_they_claim(dtype, B, W, V, K, spread):
+    """The ordinary sizes, every returned token looked up; a spread of 0.02
+    leaves bfloat16 few different values and float32 close ones."""
+    g = torch.Generator().manual_seed(V * K)
+    z = (torch.randn(B, W, V, generator=g) * spread).to(DTYPES[dtype])
+    select(z, -torch.rand(B, W, generator=g).cumsum(1), 0.2 + 2 * torch.rand(B, generator=g), K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_equal_rows_and_rising_rows(dtype):
+    g = torch.Generator().manual_seed(5)
+    z = torch.empty(3, 4, 40003)
+    z[0] = torch.randint(0, 4, (40003,), generator=g).float()
+    z[1] = torch.linspace(-20, 20, 40003)
+    z[2] = torch.linspace(20, -20, 40003)
+    select(z.to(DTYPES[dtype]), torch.zeros(3, 4), torch.ones(3), 64)
