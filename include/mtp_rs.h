@@ -359,7 +359,9 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  * Rows of nodes >= n_nodes[b] are left as they were.  A node that a row does
  * not see never reaches its output, not even where its value is infinite or
  * NaN; nor do rows of a page behind the sequence's last token.  A flagged
- * sequence gets NaN rows.
+ * sequence gets NaN rows; where an on-chip wait gave up, the rows that were lost
+ * are NaN and their sequences flagged MTP_ROW_TIMEOUT (replays of a captured
+ * call may show that flag once more in the replay after).
  *
  *   q [B, T, Hq, D], k_new and v_new [B, T, Hkv, D], k_cache and v_cache
  *   [num_pages, page_size, Hkv, D]: elements of `dtype`, D contiguous, the
@@ -547,11 +549,13 @@ typedef struct mtp_tuning {
     int pair_l2_mb;          /* streaming row-pair kernel: the same cap for sequences; 0 = no cap */
     int row_streams;         /* cluster-resident row kernel: sequences in flight per CTA, 1 or 2; 0 = planner */
     /* Fault injection for tests of the bounded waits (both 0 in normal use).
-     * They act on the TMEM-resident TV kernel only. */
+     * They act on the TMEM-resident TV kernel and on the tensor-core kernel of
+     * mtp_tree_attention only. */
     int fault_wait_us;       /* limit of every on-chip wait in microseconds; 0 = 2 s */
     int fault_skip_position; /* 1 + the position whose first exchange push the cluster's first warp
                                 skips: every wait on it gives up, and that position and the later ones
-                                of its cluster come back flagged MTP_ROW_TIMEOUT; 0 = none */
+                                of its cluster come back flagged MTP_ROW_TIMEOUT; tree attention: 1 +
+                                the CTA whose loader leaves out the first of its signals; 0 = none */
 } mtp_tuning;
 
 /* Set (t != NULL) or clear (t == NULL) the overrides; affects calls made

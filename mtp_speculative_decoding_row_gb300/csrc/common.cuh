@@ -127,15 +127,15 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // Wait for an mbarrier phase with plain try_wait (the hardware suspends the
 // thread inside each try_wait for a while, so polling costs few issue
-// slots); the clock is read every 32 polls and the wait gives up after 2 s.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity) {
+// slots); the clock is read every 32 polls and the wait gives up after limit_ns.
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > 2000000000ull) return false;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
 

@@ -37,6 +37,11 @@ struct TreeAttnArgs {
     int qrows, qbufs, slots; // tensor-core kernel: query rows in shared memory (a multiple of 8), buffers for them, slots of its ring
     float scale_log2;        // scale * log2(e)
     int vec;                 // SIMT kernel: 16-byte loads are aligned
+    // tensor-core kernel: how a wait that gave up is reported (see put_flag)
+    unsigned long long *late;   // [B], workspace
+    unsigned long long number;  // the call's
+    uint32_t wait_us;           // limit of every wait
+    int fault_cta;              // 1 + a CTA whose loader leaves out a signal (tests), else 0
 };
 
 constexpr int ATTN_DESC = 4;

@@ -3,6 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <chrono>
 #include <cstdint>
 #include <mutex>
 #include <vector>
@@ -103,10 +105,10 @@ struct AttnPlan {
     uint32_t smem = 0;
     int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
-    size_t part_bytes = 0, desc_bytes = 0;
+    size_t part_bytes = 0, desc_bytes = 0, late_bytes = 0;
     bool whole = false;       // units are not split
     bool joins() const { return !whole && max_tiles > 1 && groups > 1; }
-    size_t bytes() const { return joins() ? part_bytes + desc_bytes : desc_bytes; }
+    size_t bytes() const { return desc_bytes + late_bytes + (joins() ? part_bytes : 0); }
 };
 
 int attn_sizes(const mtp_tree_attention_args &a) {
@@ -173,7 +175,20 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     p.part_bytes = attn_slot_floats(p.bm, a.D) * 4 * 2 * p.groups * p.mtiles;
     p.part_bytes = (p.part_bytes + 15) / 16 * 16;
     p.desc_bytes = static_cast<size_t>(p.groups) * ATTN_DESC * sizeof(int32_t);
+    p.late_bytes = umma ? (static_cast<size_t>(a.B) * 8 + 15) / 16 * 16 : 0;
     return MTP_OK;
+}
+
+// 64 bits that no other call has and that no memory holds by chance (the mixing
+// is the finaliser of the SplitMix64 generator).
+unsigned long long call_number() {
+    static std::atomic<unsigned long long> count{
+        static_cast<unsigned long long>(std::chrono::high_resolution_clock::now().time_since_epoch().count()) ^
+        (static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(&g_mu)) << 20)};
+    unsigned long long x = count.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
+    x = (x ^ (x >> 30)) * 0xbf58476d1ce4e5b9ull;
+    x = (x ^ (x >> 27)) * 0x94d049bb133111ebull;
+    return x ^ (x >> 31);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -294,7 +309,15 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     if (pc != MTP_OK) return pc;
     if (a.workspace_bytes < static_cast<int64_t>(p.bytes())) return MTP_ERR_INVALID_ARG;
     A.desc = static_cast<int32_t *>(a.workspace);
-    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
+    A.late = reinterpret_cast<unsigned long long *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
+    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes + p.late_bytes);
+    if (umma) {
+        mtp_tuning tuning;
+        (void)mtp_get_tuning(&tuning);
+        A.number = call_number();
+        A.wait_us = tuning.fault_wait_us > 0 ? static_cast<uint32_t>(tuning.fault_wait_us) : 2000000u;
+        A.fault_cta = tuning.fault_skip_position;
+    }
     A.rows = p.rows;
     A.mtiles = p.mtiles;
     A.groups = p.groups;

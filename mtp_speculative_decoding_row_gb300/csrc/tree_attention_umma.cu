@@ -112,12 +112,13 @@ struct Ring {
     __device__ __forceinline__ uint32_t phase() const { return (lap >> 1) & 1; }  // its parity
 };
 
-// Wait for an mbarrier's phase, 2 s at most.  The first tries are inline, the
-// rest is one function for all of the kernel's waits: every byte of code counts
-// here (see softmax_part).
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) { return mbar_wait_spin(bar, parity); }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+// Wait for an mbarrier's phase, A.wait_us at most (2 s but for tests).  The first
+// tries are inline, the rest is one function for all of the kernel's waits:
+// every byte of code counts here (see softmax_part).  Lanes may differ in what
+// they get back, so it is put to the vote before it decides where a warp goes.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t us) { return mbar_wait_spin(bar, parity, us * 1000ull); }
+__device__ __forceinline__ bool wait_for(const TreeAttnArgs &A, uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, A.wait_us);
 }
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
@@ -167,7 +168,7 @@ __device__ __forceinline__ void max_block(uint32_t (&s)[32], float (&t)[4], bool
 // The row's reference maximum for a tile whose largest score is `top` (in
 // units of log2 e); the accumulator (if this warp has one) is rescaled where it
 // has to be.
-__device__ __forceinline__ void rescale(float top, bool first, float &m, float &l, uint32_t o_addr, int ocols, uint32_t o_bar,
+__device__ __forceinline__ void rescale(const TreeAttnArgs &A, float top, bool first, float &m, float &l, uint32_t o_addr, int ocols, uint32_t o_bar,
                                         uint32_t o_phase, bool &ok, bool has = true) {
     if (first) {
         m = top;
@@ -180,7 +181,7 @@ __device__ __forceinline__ void rescale(float top, bool first, float &m, float &
     if (up) m = top;
     l *= f;
     if (!has) return;
-    ok = wait_for(o_bar, o_phase) && ok;  // the products before this tile
+    ok = wait_for(A, o_bar, o_phase) && ok;  // the products before this tile
     __syncwarp();
     tmem_fence_after_sync();
 #pragma unroll 1
@@ -219,7 +220,7 @@ __device__ __forceinline__ float sum4(const uint64_t (&acc)[2]) {
 // product over those keys runs while the other half is made (trees of 64
 // nodes: 290 -> 275 us).
 template <int CH>
-__device__ __forceinline__ void softmax_full(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, bool first, float &m,
+__device__ __forceinline__ void softmax_full(const TreeAttnArgs &A, uint32_t s_addr, uint32_t o_addr, int ocols, float scale, bool first, float &m,
                                              float &l, uint32_t o_bar, uint32_t o_phase, uint32_t half_bar, bool &ok) {
     uint32_t s[2][32];
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -236,7 +237,7 @@ __device__ __forceinline__ void softmax_full(uint32_t s_addr, uint32_t o_addr, i
     tmem_wait_ld32(s);
     max_block(s[0], t, false, 0u, 0u);
     max_block(s[1], t, false, 0u, 0u);
-    rescale(max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
+    rescale(A, max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
     const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
     uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
     __syncwarp();
@@ -260,7 +261,7 @@ __device__ __forceinline__ void softmax_full(uint32_t s_addr, uint32_t o_addr, i
 // in lo (the first 64) and hi.  One short loop for all of them: the warps of
 // an SM run five different programs at once, and unrolled by kind of tile they
 // did not fit in its instruction cache.
-__device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int blocks, uint64_t lo,
+__device__ __forceinline__ void softmax_part(const TreeAttnArgs &A, uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int blocks, uint64_t lo,
                                              uint64_t hi, bool first, float &m, float &l, uint32_t o_bar, uint32_t o_phase,
                                              bool &ok) {
     uint32_t s[32];
@@ -273,7 +274,7 @@ __device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, i
         max_block(s, t, true, static_cast<uint32_t>((c < 2 ? lo : hi) >> (32 * (c & 1))), s_addr + 32 * c);
     }
     tmem_wait_st();
-    rescale(max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
+    rescale(A, max3(t[0], t[1], fmaxf(t[2], t[3])) * scale, first, m, l, o_addr, ocols, o_bar, o_phase, ok);
     const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
     uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll 1
@@ -291,7 +292,7 @@ __device__ __forceinline__ void softmax_part(uint32_t s_addr, uint32_t o_addr, i
 // warps.  `any`: there are keys in it, of which the row sees those in `see`.
 // The four share the row's maximum; each keeps the sum of its own weights.
 // Weights go to shared memory at p (128-byte rows, swizzled).
-__device__ __forceinline__ void softmax_quarter(uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int quarter, bool any,
+__device__ __forceinline__ void softmax_quarter(const TreeAttnArgs &A, uint32_t s_addr, uint32_t o_addr, int ocols, float scale, int quarter, bool any,
                                                 uint32_t see, bool live, bool first, float &m, float &l, uint32_t o_bar,
                                                 uint32_t o_phase, bool used, float (&tops)[4][32], uint32_t top_bar,
                                                 uint32_t top_phase, unsigned char *p, int prows, bool &ok) {
@@ -312,9 +313,9 @@ __device__ __forceinline__ void softmax_quarter(uint32_t s_addr, uint32_t o_addr
     tops[quarter][lane] = top;
     __syncwarp();
     if (lane == 0) mbar_arrive(top_bar);
-    ok = wait_for(top_bar, top_phase) && ok;
+    ok = wait_for(A, top_bar, top_phase) && ok;
     top = fmaxf(max3(tops[0][lane], tops[1][lane], tops[2][lane]), tops[3][lane]);
-    rescale(top, first, m, l, o_addr, ocols, o_bar, o_phase, ok, quarter == 0);
+    rescale(A, top, first, m, l, o_addr, ocols, o_bar, o_phase, ok, quarter == 0);
     if (any) {
         const uint64_t K2 = f2pack(scale, scale), N2 = m == -INFINITY ? f2pack(0.f, 0.f) : f2pack(-m, -m);
         uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
@@ -323,7 +324,7 @@ __device__ __forceinline__ void softmax_quarter(uint32_t s_addr, uint32_t o_addr
         l += sum4(acc);
         // (the product that read the weights before these is done: its scores'
         // successors are here)
-        if (used) ok = wait_for(o_bar, o_phase) && ok;
+        if (used) ok = wait_for(A, o_bar, o_phase) && ok;
         if (lane < prows && ok) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -360,6 +361,63 @@ __device__ __noinline__ void copy_queries(const bf16_t *q, const TreeAttnArgs &A
     for (; i < rows * VECS; i += threads) {
         const int r = i / VECS, u = i % VECS, t = node_of(A, row + r);
         cp_async16(dst + (u >> 3) * A.qrows * 128 + sw128(r, u & 7), q + t * A.qs[1] + (row + r - t * A.G) * A.qs[2] + 8 * u);
+    }
+}
+
+// The flags of a sequence are stored by the loader of one CTA, the one that has
+// the first tile of its first head and row tile.
+__device__ __forceinline__ bool flags_owner(const AttnPiece &p, int mtile) { return p.h == 0 && mtile == 0 && p.t0 == 0; }
+
+// A CTA that has given up may belong to another head, tile or row tile of the
+// sequence, and its report must not be lost whichever of the two comes first.
+// So it leaves the call's number in A.late[b] before it adds its bit to the flags,
+// and the owner looks there after its store: with a full fence between the two
+// on either side, one of them sees the other.  (A workspace holds anything; the
+// number is 64 random bits, another for each call.  A replayed graph has one
+// number for all replays: the owner takes away what it has seen, and a report
+// that came after it may show once more in the next replay.)
+__device__ __forceinline__ void put_flag(const TreeAttnArgs &A, int b, int flag) {
+    *const_cast<volatile int32_t *>(A.flags + b) = flag;
+    __threadfence();
+    volatile unsigned long long *late = A.late + b;
+    if (*late == A.number) {
+        atomicOr(A.flags + b, F_TIMEOUT);
+        *late = 0ull;
+    }
+}
+
+// By all threads of a CTA that has given up: its rows become NaN -- of a unit
+// that it shares with others its part's sum, from which the join makes NaN --
+// and its sequences are flagged.
+__device__ __noinline__ void give_up(const TreeAttnArgs &A, const AttnWalk &begin, int group, int mtile, int row0, int rows, int tid, int nt) {
+    AttnWalk w = begin;
+    AttnPiece p;
+    while (w.next(A, p)) {
+        bool bad;
+        const int n = attn_nodes(A, p.b, bad);
+        const int live = min(rows, (bad ? A.rows : n * A.G) - row0);
+        if (p.whole()) {
+            for (int r = 0; r < live; ++r) {
+                const int node = node_of(A, row0 + r), hq = p.h * A.G + row0 + r - node * A.G;
+                const size_t at = (static_cast<size_t>(p.b) * A.T + node) * A.Hq + hq;
+                for (int c = tid; c < A.D; c += nt) static_cast<uint16_t *>(A.out)[at * A.D + c] = 0x7fffu;
+                if (A.lse && tid == 0) A.lse[at] = NAN;
+            }
+        } else {
+            float *slot = A.part + attn_slot(A, group, mtile, p.first) * attn_slot_floats(A.bm, A.D);
+            for (int r = tid; r < live; r += nt) {
+                slot[r] = -INFINITY;
+                slot[A.bm + r] = NAN;
+            }
+        }
+        if (A.flags && tid == 0) {
+            atomicExch(A.late + p.b, A.number);
+            __threadfence();
+            if (flags_owner(p, mtile))
+                *const_cast<volatile int32_t *>(A.flags + p.b) = F_TIMEOUT;  // (in place of a flag that may never have been stored)
+            else
+                atomicOr(A.flags + p.b, F_TIMEOUT);
+        }
     }
 }
 
@@ -450,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             for (int t = pc.t0; t < pc.t1 && ok; ++t) {
                 if (t == pc.prefix) {  // the loaders fill these two slots once they are free
                     for (int i = 0; i < 2; ++i) {
-                        if (r.lap) ok = wait_for(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
+                        if (r.lap) ok = wait_for(A, smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                         r.step();
                     }
                     ok = __all_sync(FULL, ok);
@@ -465,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 const int mine = lane < pages ? attn_page(A, pc.b, page0 + lane) : 0;  // at most BN / 8 pages
                 for (int kv = 0; kv < 2; ++kv) {
                     // (the first use of every slot needs no wait)
-                    if (r.lap) ok = wait_for(smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
+                    if (r.lap) ok = wait_for(A, smem_addr(&ctl.empty[r.slot]), (r.lap - 1) & 1) && ok;
                     ok = __all_sync(FULL, ok);
                     if (!ok) break;
                     const uint32_t full = smem_addr(&ctl.full[r.full()]), dst = ring0 + r.slot * C::SLOT;
@@ -494,8 +552,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         int count = 0, other = 0;  // uses of the group's score buffer (ONE: of both buffers)
         // O += P V of a tile: its buffer, the use of it, its slot of the ring
         auto pv = [&](int buf, int use, const Ring &at, int steps, bool first) {
-            if (MODE != FEW) ok = wait_for(smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
-            ok = wait_for(smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
+            if (MODE != FEW) ok = wait_for(A, smem_addr(&ctl.p_half[buf]), (use - 1) & 1) && ok;
+            ok = wait_for(A, smem_addr(&ctl.full[at.full()]), at.phase()) && ok;
             ok = __all_sync(FULL, ok);
             if (!ok) return;
             tmem_fence_after_sync();
@@ -515,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     if (k < steps) step(k);
             }
             __syncwarp();
-            ok = wait_for(smem_addr(&ctl.p_full[buf]), (use - 1) & 1) && ok;
+            ok = wait_for(A, smem_addr(&ctl.p_full[buf]), (use - 1) & 1) && ok;
             ok = __all_sync(FULL, ok);
             if (!ok) return;
             tmem_fence_after_sync();
@@ -554,7 +612,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             bool bad;
             const int n = attn_nodes(A, pc.b, bad);
             if (MODE != ONE || warp == 1) {
-                ok = wait_for(smem_addr(&ctl.q_full[qi]), q_phase) && ok;
+                ok = wait_for(A, smem_addr(&ctl.q_full[qi]), q_phase) && ok;
+                ok = __all_sync(FULL, ok);
             }
             // the tile whose weights' product is still to be issued
             bool have = false, old_first = false;
@@ -580,11 +639,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
                 // the buffer's last weights have to be used before new scores go there
                 if (MODE == ONE) {
-                    if (uses > 0) ok = wait_for(smem_addr(&ctl.o_done[buf]), (uses - 1) & 1) && ok;
+                    if (uses > 0) ok = wait_for(A, smem_addr(&ctl.o_done[buf]), (uses - 1) & 1) && ok;
                 } else if (have) {
                     pv(buf, uses, old, old_steps, old_first);
                 }
-                ok = wait_for(smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
+                ok = wait_for(A, smem_addr(&ctl.full[kr.full()]), kr.phase()) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
                 qk(buf, kr.slot, t == pc.prefix ? round16(valid) : C::BN);
@@ -624,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             attn_len(A, b, bad_len);
             const int n = attn_nodes(A, b, bad_nodes);
             if (np >= 4) {
-                ok = wait_for(smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
+                ok = wait_for(A, smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
@@ -637,7 +696,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             }
             uint64_t poison = 0;
             if (pc.t1 > pc.prefix) {
-                ok = wait_for(smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
+                ok = wait_for(A, smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
                 ++grants;
                 for (int kv = 0; kv < 2; ++kv) {
                     unsigned char *dst = ring + r.slot * C::SLOT;
@@ -648,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     // at; the values behind them are zero, and so is one that
                     // is not finite (its rows get it later).
                     const int fill = (kv ? round16(n > 0 ? n : 1) : n) * (D / 8);
-                    if (ok) {
+                    {
 #pragma unroll 1
                         for (int i0 = lane; i0 < fill; i0 += 32 * 4) {
                             uint4 y[4];
@@ -689,8 +750,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 ctl.flag[np & 3] = flag;
                 ctl.poison[np & 3] = (static_cast<uint64_t>(phi) << 32) | plo;
             }
-            mbar_arrive(smem_addr(&ctl.ready[np & 3]));
-            ok = __all_sync(FULL, ok);
+            if (np > 0 || A.fault_cta != static_cast<int>(blockIdx.x) + 1) mbar_arrive(smem_addr(&ctl.ready[np & 3]));
+            if (A.flags && lane == 0 && flags_owner(pc, mtile)) put_flag(A, b, flag);
         }
     } else if (warp >= 4) {
         // --------------------------------------------------- softmax ----
@@ -713,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         const int depth = MODE == ROWS ? 1 : A.qbufs;
         auto copy_q = [&](const AttnPiece &p, int np) {
             const int qi = MODE == ROWS ? wg : np & (depth - 1);
-            if (np >= depth) ok = wait_for(smem_addr(&ctl.q_empty[qi]), (np / depth - 1) & 1) && ok;
+            if (np >= depth) ok = wait_for(A, smem_addr(&ctl.q_empty[qi]), (np / depth - 1) & 1) && ok;
             const int q0 = MODE == ROWS ? 128 * wg : 0;
             ok = __all_sync(FULL, ok);
             if (ok)
@@ -743,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 const int buf = MODE == ONE ? (t - pc.t0) & 1 : wg;
                 const int use = MODE == ONE && buf ? count1 : count0;
                 const uint32_t s_addr = lanes + buf * C::S_COL;
-                ok = wait_for(smem_addr(&ctl.s_full[buf]), use & 1) && ok;
+                ok = wait_for(A, smem_addr(&ctl.s_full[buf]), use & 1) && ok;
                 tmem_fence_after_sync();
                 // the product before this one into the accumulator
                 const uint32_t o_bar = smem_addr(&ctl.o_done[MODE == ONE ? buf ^ 1 : wg]);
@@ -752,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 uint64_t lo = ~0ull, hi = ~0ull;
                 const bool tree = t == pc.prefix;
                 if (tree) {
-                    ok = wait_for(smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
+                    ok = wait_for(A, smem_addr(&ctl.masks[np & 3]), (np >> 2) & 1) && ok;
                     lo = live && node < n ? ctl.mask[np & 3][node] : 0ull;
                 } else {
                     int pos;
@@ -762,18 +823,18 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 }
                 bool half = true;  // the first half was announced
                 if (MODE == FEW) {
-                    softmax_quarter(s_addr + 32 * quarter, o_addr, D, A.scale_log2, quarter, 32 * quarter < (tree ? max(n, 1) : valid),
+                    softmax_quarter(A, s_addr + 32 * quarter, o_addr, D, A.scale_log2, quarter, 32 * quarter < (tree ? max(n, 1) : valid),
                                     static_cast<uint32_t>((quarter < 2 ? lo : hi) >> (32 * (quarter & 1))), live, first, m, l, o_bar,
                                     o_phase, use > 0, ctl.top[wg][top_phase], smem_addr(&ctl.tops[wg]), top_phase,
                                     smem + wg * 8192, A.qrows, ok);
                     top_phase ^= 1u;
                 } else if (busy && !tree && valid == C::BN)
-                    softmax_full<C::BN / 32>(s_addr, o_addr, D, A.scale_log2, first, m, l, o_bar, o_phase,
+                    softmax_full<C::BN / 32>(A, s_addr, o_addr, D, A.scale_log2, first, m, l, o_bar, o_phase,
                                              smem_addr(&ctl.p_half[buf]), ok);
                 else {
                     half = false;
                     if (busy)
-                        softmax_part(s_addr, o_addr, D, A.scale_log2, tree ? max(n + 31, 32) >> 5 : (valid + 31) >> 5, lo, hi, first,
+                        softmax_part(A, s_addr, o_addr, D, A.scale_log2, tree ? max(n + 31, 32) >> 5 : (valid + 31) >> 5, lo, hi, first,
                                      m, l, o_bar, o_phase, ok);
                 }
                 if (!tree && (valid & 15)) {
@@ -781,7 +842,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                     // to be a number.  (ROWS: each group sees to it for its own
                     // product; both write the same.)
                     const int end = round16(valid);
-                    ok = wait_for(smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
+                    ok = wait_for(A, smem_addr(&ctl.full[vr.full()]), vr.phase()) && ok;
                     for (int i = wt; i < (end - valid) * (D / 8); i += 128) {
                         const int j = valid + i / (D / 8), u = i % (D / 8);
                         *reinterpret_cast<uint4 *>(ring + vr.slot * C::SLOT + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) =
@@ -814,11 +875,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             }
             if (np < 0) continue;
             // ------------------------------------------------ results ----
-            ok = wait_for(smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
+            ok = wait_for(A, smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
             if (!first) {
                 const int buf = MODE == ONE ? (pc.t1 - 1 - pc.t0) & 1 : wg;
                 const int use = MODE == ONE && buf ? count1 : count0;
-                ok = wait_for(smem_addr(&ctl.o_done[buf]), (use - 1) & 1) && ok;
+                ok = wait_for(A, smem_addr(&ctl.o_done[buf]), (use - 1) & 1) && ok;
             }
             ok = __all_sync(FULL, ok);
             if (!ok) break;
@@ -832,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             tmem_fence_before_sync();
             if (C::TURNS) {
                 mbar_arrive(smem_addr(&ctl.stats));
-                ok = wait_for(smem_addr(&ctl.stats), join_phase) && ok;
+                ok = wait_for(A, smem_addr(&ctl.stats), join_phase) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
@@ -852,7 +913,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 l = f0 * sum_of(0) + f1 * sum_of(1);
             }
             const int flag = ctl.flag[np & 3];
-            if (A.flags && tid == 128 && h == 0 && mtile == 0) A.flags[b] = flag;
             const uint64_t seen = pc.t1 == pc.prefix + 1 && live && node < n
                                       ? ctl.mask[np & 3][node] & ctl.poison[np & 3]
                                       : 0ull;
@@ -915,7 +975,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             mbar_arrive(smem_addr(&ctl.done[np & 3]));
             if (C::TURNS) {  // the next piece's products may write the accumulators
                 mbar_arrive(smem_addr(&ctl.joined));
-                ok = wait_for(smem_addr(&ctl.joined), join_phase) && ok;
+                ok = wait_for(A, smem_addr(&ctl.joined), join_phase) && ok;
                 join_phase ^= 1u;
                 ok = __all_sync(FULL, ok);
             }
@@ -927,17 +987,15 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     __syncthreads();
     if (ctl.dead) {
         // a wait gave up: let copies and products in flight end before the
-        // shared and tensor memory goes, and flag every sequence of the range
+        // shared and tensor memory goes
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
+        give_up(A, ctl.begin, group, mtile, row0, rows, tid, NT);
     }
     if (mtile == 0 && warp == 0) {
         AttnWalk w = ctl.begin;
         AttnPiece last = {};
-        while (w.next(A, pc)) {
-            last = pc;
-            if (ctl.dead && A.flags && lane == 0) atomicOr(A.flags + pc.b, F_TIMEOUT);
-        }
+        while (w.next(A, pc)) last = pc;
         if (lane == 0) attn_write_desc(A, group, ctl.W, w.hi, last);
     }
     tmem_fence_after_sync();

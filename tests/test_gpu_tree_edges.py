@@ -1,0 +1,73 @@
+"""Tree attention, reorder and commit on the GPU at the edges of their use:
+waits that run out, streams, graphs, page tables wider than the text."""
+import math
+import random
+
+import pytest
+import torch
+
+import mtp_speculative_decoding_row_gb300 as mtp
+from tests.test_gpu_tree_ops import attn_case, check_attention, on_gpu
+
+pytestmark = pytest.mark.gpu
+i32 = torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    from tests import gpu_util
+
+    gpu_util.ensure_library()
+
+
+# ------------------------------------------------------ waits that run out --
+
+def attend(g, B, T, Hq, D, fill=7.0):
+    """Outputs that were something else before, flags among them."""
+    out = mtp.TreeAttentionResult(torch.full((B, T, Hq, D), fill, dtype=torch.bfloat16, device="cuda"),
+                                  torch.full((B, T, Hq), fill, device="cuda"), torch.full((B,), 12345, dtype=i32, device="cuda"))
+    r = mtp.mtp_tree_attention(**g, out=out)
+    torch.cuda.synchronize()
+    return r
+
+
+@pytest.mark.parametrize("T, Hq, Hkv, D, ps, lens, ctas", [
+    (2, 8, 2, 64, 16, [40, 0, 300], (0, 1, 2, 3, 4, 5)),             # whole units, up to 32 rows
+    (8, 16, 2, 128, 32, [129, 500, 64], (0, 1, 3, 5)),               # 64 rows
+    (64, 16, 2, 128, 32, [129, 500], (0, 1, 2, 3, 4, 5, 6, 7)),      # 512 rows, two row tiles
+    (3, 8, 2, 256, 32, [100, 33], (0, 1, 2, 3)),                     # heads of 256
+    (2, 8, 2, 64, 16, [6000, 10, 2500], (0, 1, 60, 100, 140)),       # split units
+    (8, 16, 2, 128, 32, [5000, 4000], (0, 1, 50, 151)),
+    (64, 16, 2, 128, 32, [3000, 64], (0, 1, 40, 75, 101)),
+    (3, 8, 2, 256, 32, [4000, 33], (0, 70, 140)),
+])
+def test_a_wait_that_runs_out_is_reported(T, Hq, Hkv, D, ps, lens, ctas):
+    """The loader of one CTA leaves out a signal (test-only tuning fields), so
+    the waits of that CTA give up after 20 ms.  Whichever head, tile or row
+    tile it has: the call ends, every row is NaN or what it is without the
+    fault, a sequence with a row of the CTA is flagged MTP_ROW_TIMEOUT and no
+    other, and the next call is right again."""
+    B = len(lens)
+    x = attn_case(len(lens) + T, "bf16", B, T, Hq, Hkv, D, ps, lens, nodes=[T] + [max(1, T - 1)] * (B - 1))
+    g = on_gpu(x)
+    good = attend(g, B, T, Hq, D)
+    assert good.row_flags.tolist() == [0] * B
+    check_attention(x, good.out, None, good.lse, 7.0)
+    seen = 0
+    for cta in ctas:
+        with mtp.tuning(fault_wait_us=20000, fault_skip_position=1 + cta):
+            r = attend(g, B, T, Hq, D)
+        lost = r.out.isnan().all(3)                      # [B, T, Hq]
+        same = (r.out == good.out).all(3)
+        assert (lost | same).all(), cta
+        assert torch.equal(r.lse.isnan(), lost) and torch.equal(r.lse[~lost], good.lse[~lost])
+        hit = lost.flatten(1).any(1)
+        assert r.row_flags.tolist() == [mtp.ROW_TIMEOUT if h else 0 for h in hit.tolist()], cta
+        seen += int(hit.any())
+        if hit.any():
+            with pytest.raises(mtp.MTPError) as e:
+                mtp.check_row_flags(r.row_flags)
+            assert e.value.status == mtp.MTP_ERR_TIMEOUT
+    assert seen >= 2
+    again = attend(g, B, T, Hq, D)
+    assert torch.equal(again.out, good.out) and torch.equal(again.lse, good.lse) and again.row_flags.tolist() == [0] * B
