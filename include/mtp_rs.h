@@ -467,8 +467,10 @@ int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, 
  *   page_size, Hkv, D] dtype, D contiguous, strides in elements; layers = 0
  *   writes no cache (all four may be NULL).  The pages that the path goes to
  *   must belong to one sequence only, and the new keys and values must not
- *   overlap the cache.  new_len must not be cache_len itself.  At most 2^30
- *   elements of keys in the T nodes of one sequence and layer.
+ *   overlap the cache.  An output that overlaps tokens, target_tokens, parents,
+ *   n_nodes, page_table or cache_len (new_len = cache_len, say) is refused:
+ *   MTP_ERR_INVALID_ARG.  At most 2^30 elements of keys in the T nodes of one
+ *   sequence and layer, 32767 layers, 65536 heads of at most 4096 elements.
  */
 typedef struct mtp_tree_commit_args {
     const int32_t *tokens, *target_tokens; /* [B, T] */

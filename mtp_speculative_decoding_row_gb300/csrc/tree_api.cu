@@ -439,6 +439,17 @@ extern "C" int mtp_beam_select(const void *logits, mtp_dtype dtype, const float 
 
 // --------------------------------------------------- reorder and commit ----
 
+namespace {
+struct Ints {  // n 32-bit integers at p, or none
+    const int32_t *p;
+    long long n;
+    bool overlaps(const Ints &o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return p && o.p && a < b + static_cast<uintptr_t>(o.n) * 4 && b < a + static_cast<uintptr_t>(n) * 4;
+    }
+};
+}  // namespace
+
 extern "C" int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, int W, int K, int64_t row_bytes,
                                 void *out, int32_t *row_flags, mtp_stream_t stream) {
     if (N0 < 0 || B < 0 || W < 1 || K < 1 || row_bytes < 0 || row_bytes > (1ll << 40)) return MTP_ERR_INVALID_ARG;
@@ -517,6 +528,13 @@ extern "C" int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t st
         }
         low |= static_cast<uintptr_t>(A.row_bytes);
     }
+    // every block of a sequence reads its inputs, one of them writes the outputs
+    const long long each = a.B, nodes = each * a.T, table = each * a.max_pages;
+    const Ints in[] = {{a.tokens, nodes}, {a.target_tokens, nodes}, {a.parents, nodes}, {a.n_nodes, each}, {a.page_table, table}, {a.cache_len, each}};
+    const Ints out[] = {{a.out_tokens, nodes}, {a.path, nodes}, {a.accept_len, each}, {a.new_len, each}, {a.row_flags, each}};
+    for (const Ints &o : out)
+        for (const Ints &i : in)
+            if (o.overlaps(i)) return MTP_ERR_INVALID_ARG;
     const int width = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 2;
     return launch(commit_func(width), dim3(a.B, a.layers > 0 ? 2 * a.layers : 1), COMMIT_THREADS, 0, &A, stream);
 }
