@@ -465,7 +465,9 @@ int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, 
  *
  *   k_new, v_new [layers, B, T, Hkv, D], k_cache, v_cache [layers, num_pages,
  *   page_size, Hkv, D] dtype, D contiguous, strides in elements; layers = 0
- *   writes no cache (all four may be NULL).  The pages that the path goes to
+ *   is the verification alone: no cache is written, all four may be NULL, and
+ *   so may page_table (no room is looked for) and cache_len (new_len counts
+ *   from 0).  The pages that the path goes to
  *   must belong to one sequence only, and the new keys and values must not
  *   overlap the cache.  An output that overlaps tokens, target_tokens, parents,
  *   n_nodes, page_table or cache_len (new_len = cache_len, say) is refused:
@@ -476,8 +478,8 @@ typedef struct mtp_tree_commit_args {
     const int32_t *tokens, *target_tokens; /* [B, T] */
     const int32_t *parents;                /* [B, T] or NULL */
     const int32_t *n_nodes;                /* [B] or NULL */
-    const int32_t *page_table;             /* [B, max_pages] */
-    const int32_t *cache_len;              /* [B] */
+    const int32_t *page_table;             /* [B, max_pages], or NULL with layers = 0 */
+    const int32_t *cache_len;              /* [B], or NULL with layers = 0 */
     const void *k_new, *v_new;
     void *k_cache, *v_cache;
     int32_t *out_tokens, *accept_len, *path, *new_len, *row_flags;

@@ -301,18 +301,8 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t B = tokens.size(0), T = tokens.size(1);
         if (T < 1 || T > MTP_MAX_NODES)
             value_error("trees have 1 to " + std::to_string(MTP_MAX_NODES) + " nodes, got " + std::to_string(T));
-        const at::Tensor &k = tensor(a[3], "k_new"), &v = tensor(a[4], "v_new"), &kc = tensor(a[5], "k_cache"),
-                         &vc = tensor(a[6], "v_cache"), &table = tensor(a[7], "page_table");
         mtp_tree_commit_args s = {};
-        s.dtype = dtype_code(k);
-        const int one = k.dim() == 4 ? 1 : 0;  // without the layers' dimension
-        dims(k, "k_new", 5 - one);
-        dims(kc, "k_cache", 5 - one);
-        dims(table, "page_table", 2);
-        const int64_t layers = one ? 1 : k.size(0), Hkv = k.size(3 - one), D = k.size(4 - one), pages = kc.size(1 - one),
-                      page = kc.size(2 - one), most = table.size(1);
         const int index = index_of(tokens);
-        const at::ScalarType dt = k.scalar_type();
         s.out_tokens = static_cast<int32_t *>(whole(a[10], "out.tokens", at::kInt, {B, T}, index));
         s.accept_len = static_cast<int32_t *>(whole(a[11], "out.accept_len", at::kInt, {B}, index));
         s.path = static_cast<int32_t *>(whole(a[12], "out.path", at::kInt, {B, T}, index));
@@ -322,6 +312,32 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.target_tokens = static_cast<int32_t *>(whole(a[1], "target_tokens", at::kInt, {B, T}, index));
         s.parents = static_cast<int32_t *>(whole_or_null(a[2], "parents", at::kInt, {B, T}, index));
         s.n_nodes = static_cast<int32_t *>(whole_or_null(a[9], "n_nodes", at::kInt, {B}, index));
+        s.B = static_cast<int>(B);
+        s.T = static_cast<int>(T);
+        if (B > 0x7fffffff) value_error("a dimension is too large");
+        const auto launch = [&]() -> long {
+            if (s.new_len == s.cache_len && B > 0) value_error("out.cache_len must not be cache_len itself");
+            if (!fn.commit) return NOT_BOUND;
+            const mtp_stream_t stream = stream_of(a[15]);
+            const auto f = fn.commit;
+            return call([&] { return f(&s, stream); });
+        };
+        if (a[3] == Py_None && a[4] == Py_None && a[5] == Py_None && a[6] == Py_None) {  // the verification alone
+            if (a[7] != Py_None) value_error("page_table is of no use without k_new, v_new, k_cache and v_cache");
+            s.cache_len = static_cast<int32_t *>(whole_or_null(a[8], "cache_len", at::kInt, {B}, index));
+            on_gpu(index, "tokens");
+            return launch();
+        }
+        const at::Tensor &k = tensor(a[3], "k_new"), &v = tensor(a[4], "v_new"), &kc = tensor(a[5], "k_cache"),
+                         &vc = tensor(a[6], "v_cache"), &table = tensor(a[7], "page_table");
+        s.dtype = dtype_code(k);
+        const int one = k.dim() == 4 ? 1 : 0;  // without the layers' dimension
+        dims(k, "k_new", 5 - one);
+        dims(kc, "k_cache", 5 - one);
+        dims(table, "page_table", 2);
+        const int64_t layers = one ? 1 : k.size(0), Hkv = k.size(3 - one), D = k.size(4 - one), pages = kc.size(1 - one),
+                      page = kc.size(2 - one), most = table.size(1);
+        const at::ScalarType dt = k.scalar_type();
         if (one) {
             s.k_new = strided(k, "k_new", dt, {B, T, Hkv, D}, index, s.k_new_stride + 1);
             s.v_new = strided(v, "v_new", dt, {B, T, Hkv, D}, index, s.v_new_stride + 1);
@@ -336,21 +352,15 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.page_table = static_cast<int32_t *>(whole(a[7], "page_table", at::kInt, {B, most}, index));
         s.cache_len = static_cast<int32_t *>(whole(a[8], "cache_len", at::kInt, {B}, index));
         on_gpu(index, "tokens");
-        if (s.new_len == s.cache_len && B > 0) value_error("out.cache_len must not be cache_len itself");
-        for (int64_t x : {layers, B, Hkv, D, pages, page, most})
+        for (int64_t x : {layers, Hkv, D, pages, page, most})
             if (x > 0x7fffffff) value_error("a dimension is too large");
         s.layers = static_cast<int>(layers);
-        s.B = static_cast<int>(B);
-        s.T = static_cast<int>(T);
         s.Hkv = static_cast<int>(Hkv);
         s.D = static_cast<int>(D);
         s.num_pages = static_cast<int>(pages);
         s.page_size = static_cast<int>(page);
         s.max_pages = static_cast<int>(most);
-        if (!fn.commit) return NOT_BOUND;
-        const mtp_stream_t stream = stream_of(a[15]);
-        const auto f = fn.commit;
-        return call([&] { return f(&s, stream); });
+        return launch();
     });
 }
 

@@ -109,7 +109,7 @@ constexpr int REORDER_THREADS = 256, REORDER_UNROLL = 4, REORDER_BLOCK = REORDER
 
 struct CommitArgs {
     const int32_t *tokens, *target, *parents, *nodes;  // [B, T]; nodes [B] or null
-    const int32_t *table, *len;
+    const int32_t *table, *len;  // null where no cache is written: no pages to look at, lengths from 0
     const unsigned char *k_new, *v_new;
     unsigned char *k_cache, *v_cache;
     // byte strides: new (layer, b, t, h), cache (layer, page, token, head)

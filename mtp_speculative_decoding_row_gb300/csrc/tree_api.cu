@@ -479,14 +479,15 @@ extern "C" int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t st
     if (!args) return MTP_ERR_INVALID_ARG;
     const mtp_tree_commit_args &a = *args;
     if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
-    if (a.layers < 0 || a.layers > 32767 || a.B < 0 || a.T < 1 || a.T > MTP_MAX_NODES || a.num_pages < 1 || a.page_size < 1 ||
-        a.max_pages < 1 || static_cast<long long>(a.max_pages) * a.page_size > 0x7fff0000ll)
+    if (a.layers < 0 || a.layers > 32767 || a.B < 0 || a.T < 1 || a.T > MTP_MAX_NODES) return MTP_ERR_INVALID_ARG;
+    if ((a.layers > 0 || a.page_table) && (a.num_pages < 1 || a.page_size < 1 || a.max_pages < 1 ||
+                                           static_cast<long long>(a.max_pages) * a.page_size > 0x7fff0000ll))
         return MTP_ERR_INVALID_ARG;
     if (a.layers > 0 && (a.Hkv < 1 || a.D < 1 || a.D > 4096 || a.Hkv > 65536)) return MTP_ERR_INVALID_ARG;
     if (a.layers > 0 && static_cast<long long>(a.T) * a.Hkv * a.D > (1ll << 30)) return MTP_ERR_INVALID_ARG;  // words of a path, in 32 bits
     if (a.B == 0) return MTP_OK;
-    if (!a.tokens || !a.target_tokens || !a.page_table || !a.cache_len || !a.out_tokens || !a.accept_len || !a.path ||
-        !a.new_len || (a.layers > 0 && (!a.k_new || !a.v_new || !a.k_cache || !a.v_cache)))
+    if (!a.tokens || !a.target_tokens || !a.out_tokens || !a.accept_len || !a.path || !a.new_len ||
+        (a.layers > 0 && (!a.page_table || !a.cache_len || !a.k_new || !a.v_new || !a.k_cache || !a.v_cache)))
         return MTP_ERR_INVALID_ARG;
     const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
     CommitArgs A = {};

@@ -88,13 +88,13 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int n = A.nodes ? __ldg(A.nodes + b) : T;
-    const int len = __ldg(A.len + b);
+    const int len = A.len ? __ldg(A.len + b) : 0;
     int flag = 0;
     if (n < 0 || n > T) {
         flag = F_BAD_ID;
         n = 0;
     }
-    if (len < 0 || len > static_cast<long long>(A.max_pages) * A.page_size) flag = F_BAD_ID;
+    if (len < 0 || (A.table && len > static_cast<long long>(A.max_pages) * A.page_size)) flag = F_BAD_ID;
     const size_t o = static_cast<size_t>(b) * T;
     if (tid < 32) {
         // everything that the walk needs, two nodes to a lane, loaded at once:
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
         for (int e = 0; e < 2; ++e) {
             const long long pos = static_cast<long long>(len) + tid + 32 * e;
             page[e] = -1;
-            if (flag == 0 && tid + 32 * e < n && pos < static_cast<long long>(A.max_pages) * A.page_size) {
+            if (A.table && flag == 0 && tid + 32 * e < n && pos < static_cast<long long>(A.max_pages) * A.page_size) {
                 const int at = static_cast<int>(pos) / A.page_size;
                 page[e] = __ldg(A.table + static_cast<size_t>(b) * A.max_pages + at);
                 s_page[tid + 32 * e] = page[e];
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_impl(const __grid_const
             // no room for the path, or a page that is none
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (tid + 32 * e < count && (page[e] < 0 || page[e] >= A.num_pages)) flag |= F_BAD_ID;
+                if (A.table && tid + 32 * e < count && (page[e] < 0 || page[e] >= A.num_pages)) flag |= F_BAD_ID;
         }
         flag = __reduce_or_sync(FULL, flag);
         if (flag) count = 0;

@@ -220,7 +220,9 @@ def mtp_tree_commit(tokens, target_tokens, parents=None, k_new=None, v_new=None,
     is the root), k_new and v_new [layers, B, T, Hkv, D], k_cache and v_cache
     [layers, num_pages, page_size, Hkv, D] (without the layers' dimension for
     one layer; written in place), page_table [B, max_pages], cache_len [B],
-    n_nodes [B] (None: T)."""
+    n_nodes [B] (None: T).  Without keys, values, caches and table the tree is
+    verified alone: nothing is written but the outputs, whose cache_len counts
+    from `cache_len` or (None) from 0."""
     torch = _m._torch()
     index = tokens.get_device()
     with _on(torch, index):

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mtp_speculative_decoding_row_gb300 as mtp
-from tests.test_gpu_tree_ops import attn_case, check_attention, on_gpu
+from tests.test_gpu_tree_ops import attn_case, check_attention, check_commit, commit_case, on_gpu
 
 pytestmark = pytest.mark.gpu
 i32 = torch.int32
@@ -71,3 +71,32 @@ def test_a_wait_that_runs_out_is_reported(T, Hq, Hkv, D, ps, lens, ctas):
     assert seen >= 2
     again = attend(g, B, T, Hq, D)
     assert torch.equal(again.out, good.out) and torch.equal(again.lse, good.lse) and again.row_flags.tolist() == [0] * B
+
+
+# ------------------------------------------------------------------ commit --
+
+@pytest.mark.parametrize("T, nodes, tree", [(1, None, "chain"), (9, [9, 0, 4], "random"), (64, None, "chain"), (64, [64, 33, 1], "random")])
+@pytest.mark.parametrize("lens", [None, [0, 70, 5]])
+def test_verification_alone(T, nodes, tree, lens):
+    """Without keys, values, caches and table: the outputs of the whole call."""
+    x = commit_case(T, "bf16", 1, 3, T, 1, 16, 16, lens or [0, 0, 0], 0.9, nodes, tree)
+    g = on_gpu(x)
+    want = mtp.mtp_tree_commit(**g)
+    r = mtp.mtp_tree_commit(g["tokens"], g["target_tokens"], g["parents"], n_nodes=g["n_nodes"],
+                            cache_len=None if lens is None else g["cache_len"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(r, want))
+    check_commit(x, mtp.CommitResult(*(t.cpu() for t in r)), g["k_cache"], g["v_cache"])
+    assert r.row_flags.tolist() == [0, 0, 0]
+
+
+def test_verification_alone_flags():
+    t = torch.tensor([[3, 5, 6]] * 4, dtype=i32)
+    target = torch.tensor([[5, 6, 7], [5, -1, 7], [9, 0, 0], [5, 6, 7]], dtype=i32)
+    up = torch.tensor([[-1, 0, 1], [-1, 0, 1], [-1, 0, 1], [-1, 1, 0]], dtype=i32)
+    lens = torch.tensor([4, 4, -1, 4], dtype=i32)
+    r = mtp.mtp_tree_commit(t.cuda(), target.cuda(), up.cuda(), cache_len=lens.cuda())
+    torch.cuda.synchronize()
+    assert r.row_flags.tolist() == [0] + [mtp.ROW_BAD_ID] * 3
+    assert r.accept_len.tolist() == [2, -1, -1, -1] and r.cache_len.tolist() == [7, 4, -1, 4]
+    assert r.tokens.tolist() == [[5, 6, 7]] + [[-1] * 3] * 3
