@@ -110,18 +110,9 @@ void on_gpu(int index, const char *name) {
     if (index < 0) value_error(std::string(name) + " must be a CUDA tensor");
 }
 
-// Scratch memory on t's device: `given`, or (None) allocated here on the
-// current stream.  `hold` keeps it until the launch is done.
-void *workspace(PyObject *given, int64_t bytes, const at::Tensor &t, at::Tensor &hold, int64_t &have) {
-    if (given != Py_None) {
-        const at::Tensor &w = tensor(given, "workspace");
-        have = w.numel();
-        return w.data_ptr();
-    }
-    hold = at::empty({bytes}, t.options().dtype(at::kByte));
-    have = bytes;
-    return hold.data_ptr();
-}
+// Scratch memory on t's device, of the current stream, which is the call's; the
+// tensor keeps it until the launch is done.
+at::Tensor workspace(int64_t bytes, const at::Tensor &t) { return at::empty({bytes}, t.options().dtype(at::kByte)); }
 
 mtp_stream_t stream_of(PyObject *o) { return reinterpret_cast<mtp_stream_t>(PyLong_AsVoidPtr(o)); }
 
@@ -155,9 +146,9 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
 }
 
 // tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
-//   parents, n_nodes, scale, out, lse, row_flags, workspace, stream)
+//   parents, n_nodes, scale, out, lse, row_flags, stream)
 PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!count(n, 15)) return nullptr;
+    if (!count(n, 14)) return nullptr;
     return guarded([&]() -> long {
         const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"),
                          &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache"), &table = tensor(a[5], "page_table");
@@ -206,18 +197,19 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!fn.attention) return NOT_BOUND;
         const int64_t bytes = fn.attention_ws(&s);
         if (bytes < 0) return MTP_ERR_INVALID_ARG;
-        at::Tensor hold;
-        s.workspace = workspace(a[13], bytes, q, hold, s.workspace_bytes);
-        const mtp_stream_t stream = stream_of(a[14]);
+        const at::Tensor hold = workspace(bytes, q);
+        s.workspace = hold.data_ptr();
+        s.workspace_bytes = bytes;
+        const mtp_stream_t stream = stream_of(a[13]);
         const auto f = fn.attention;  // (another thread may bind meanwhile)
         return call([&] { return f(&s, stream); });
     });
 }
 
 // beam_select(logits, scores, temperature, K, tokens, parents, out_scores,
-//   row_flags, workspace, stream)
+//   row_flags, stream)
 PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!count(n, 10)) return nullptr;
+    if (!count(n, 9)) return nullptr;
     return guarded([&]() -> long {
         const at::Tensor &z = tensor(a[0], "logits");
         dims(z, "logits", 3);
@@ -244,12 +236,11 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const mtp_dtype dt = static_cast<mtp_dtype>(code);
         const int64_t bytes = fn.select_ws(dt, b, w, v, k);
         if (bytes < 0) return MTP_ERR_INVALID_ARG;
-        at::Tensor hold;
-        int64_t have = 0;
-        void *ws = workspace(a[8], bytes, z, hold, have);
-        const mtp_stream_t stream = stream_of(a[9]);
+        const at::Tensor hold = workspace(bytes, z);
+        void *ws = hold.data_ptr();
+        const mtp_stream_t stream = stream_of(a[8]);
         const auto f = fn.select;
-        return call([&] { return f(pz, dt, scores, temp, b, w, v, k, tokens, parents, best, flags, ws, have, stream); });
+        return call([&] { return f(pz, dt, scores, temp, b, w, v, k, tokens, parents, best, flags, ws, bytes, stream); });
     });
 }
 

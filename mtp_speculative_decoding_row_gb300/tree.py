@@ -79,7 +79,7 @@ def unbind() -> None:
         _native.bind(0, 0, 0, 0, 0, 0)
 
 
-def _call(name, index, args):
+def _call(name, args):
     rc = getattr(_binding(), name)(*args)
     if rc == _NOT_BOUND:
         _bind(_m.load_library())
@@ -89,44 +89,41 @@ def _call(name, index, args):
 
 
 class _on:
-    """The device of a call made current, where it is not."""
+    """The device and the stream of a call made current, where they are not.
 
-    __slots__ = ("guard",)
+    What is allocated inside -- outputs here, the workspace natively -- then
+    belongs to the stream that it is used on: memory of the caller's current
+    stream may still be written by work queued there before it was freed."""
 
-    def __init__(self, torch, index):
-        self.guard = None if index < 0 or torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+    __slots__ = ("guard", "caller")
+
+    def __init__(self, torch, index, stream):
+        self.guard = self.caller = None
+        if stream is not None and index >= 0:
+            if stream.device.index != index:
+                raise ValueError(f"stream must be on the device of the tensors, cuda:{index}, not {stream.device}")
+            self.caller = torch.cuda.current_stream(index)
+            self.guard = torch.cuda.stream(stream)
+        elif index >= 0 and torch._C._cuda_getDevice() != index:
+            self.guard = torch.cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
+        return self
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-
-def _raw(torch, index, stream, mine=()):
-    """The raw stream of a call; tensors allocated for it here are tied to a
-    stream that is not the current one."""
-    if stream is None:
+    def raw(self, torch, index, mine):
+        """The raw stream of the call.  Outputs allocated for it here will be
+        read, and may be freed, on the caller's stream: they are tied to both."""
+        if self.caller is not None:
+            for t in mine:
+                if t is not None:
+                    t.record_stream(self.caller)
         return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
-    for t in mine:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def _scratch(torch, like, stream, size, *args):
-    """Workspace for a call on a given stream (None: allocated natively, on
-    the current one)."""
-    if stream is None or not like.is_cuda:
-        return None
-    n = getattr(_m.load_library(), size)(*args)
-    if n < 0:
-        raise _m.MTPError(size, _m.MTP_ERR_INVALID_ARG)
-    ws = torch.empty((n,), dtype=torch.uint8, device=like.device)
-    ws.record_stream(stream)
-    return ws
 
 
 def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len, parents=None, n_nodes=None, *,
@@ -146,7 +143,7 @@ def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
     index = q.get_device()
     if out is not None and with_lse and out.lse is None:
         raise ValueError("mtp_tree_attention: with_lse needs out.lse")
-    with _on(torch, index):
+    with _on(torch, index, stream) as on:
         mine = ()
         if out is None:
             if q.dim() != 4:
@@ -155,15 +152,9 @@ def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
             out = mine = TreeAttentionResult(torch.empty(q.shape, dtype=q.dtype, device=dev),
                                              torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None,
                                              torch.empty(q.shape[:1], dtype=torch.int32, device=dev))
-        ws = None
-        if stream is not None and q.dim() == 4 and k_new.dim() == 4 and k_cache.dim() == 4 and page_table.dim() == 2:
-            ws = _scratch(torch, q, stream, "mtp_tree_attention_workspace",
-                          _ATTN.pack(*([0] * 29), _m._dtype_code(q), *q.shape[:3], k_new.shape[2], q.shape[3], *k_cache.shape[:2],
-                                     page_table.shape[1], 1.0))
-        _call("tree_attention", index,
+        _call("tree_attention",
               (q, k_new, v_new, k_cache, v_cache, page_table, cache_len, parents, n_nodes,
-               q.shape[-1] ** -0.5 if scale is None else scale, out.out, out.lse, out.row_flags, ws,
-               _raw(torch, index, stream, mine)))
+               q.shape[-1] ** -0.5 if scale is None else scale, out.out, out.lse, out.row_flags, on.raw(torch, index, mine)))
     return out
 
 
@@ -174,18 +165,15 @@ def mtp_beam_select(logits, scores, temperature, K: int, *, out: Optional[BeamRe
     float32.  Returns tokens, parents and scores [B, K], best first."""
     torch = _m._torch()
     index = logits.get_device()
-    with _on(torch, index):
+    with _on(torch, index, stream) as on:
         mine = ()
         if out is None:
             B, dev, i32 = logits.shape[0], logits.device, torch.int32
             k = max(int(K), 0)
             out = mine = BeamResult(torch.empty((B, k), dtype=i32, device=dev), torch.empty((B, k), dtype=i32, device=dev),
                                     torch.empty((B, k), dtype=torch.float32, device=dev), torch.empty((B,), dtype=i32, device=dev))
-        ws = None
-        if stream is not None and logits.dim() == 3:
-            ws = _scratch(torch, logits, stream, "mtp_beam_select_workspace", _m._dtype_code(logits), *logits.shape, int(K))
-        _call("beam_select", index, (logits, scores, temperature, K, out.tokens, out.parents, out.scores, out.row_flags, ws,
-                                     _raw(torch, index, stream, mine)))
+        _call("beam_select", (logits, scores, temperature, K, out.tokens, out.parents, out.scores, out.row_flags,
+                              on.raw(torch, index, mine)))
     return out
 
 
@@ -196,7 +184,7 @@ def mtp_beam_reorder(states, parents, *, out: Optional[ReorderResult] = None, st
     parents[b, k]], zeros for a parent outside [0, W)."""
     torch = _m._torch()
     index = states.get_device()
-    with _on(torch, index):
+    with _on(torch, index, stream) as on:
         mine = ()
         if out is None:
             if states.dim() < 3 or parents.dim() != 2:
@@ -206,7 +194,7 @@ def mtp_beam_reorder(states, parents, *, out: Optional[ReorderResult] = None, st
             out = mine = ReorderResult(
                 torch.empty((*states.shape[:2], parents.shape[1], *states.shape[3:]), dtype=states.dtype, device=dev),
                 torch.empty((states.shape[1],), dtype=torch.int32, device=dev))
-        _call("beam_reorder", index, (states, parents, out.states, out.row_flags, _raw(torch, index, stream, mine)))
+        _call("beam_reorder", (states, parents, out.states, out.row_flags, on.raw(torch, index, mine)))
     return out
 
 
@@ -225,7 +213,7 @@ def mtp_tree_commit(tokens, target_tokens, parents=None, k_new=None, v_new=None,
     from `cache_len` or (None) from 0."""
     torch = _m._torch()
     index = tokens.get_device()
-    with _on(torch, index):
+    with _on(torch, index, stream) as on:
         mine = ()
         if out is None:
             if tokens.dim() != 2:
@@ -233,7 +221,7 @@ def mtp_tree_commit(tokens, target_tokens, parents=None, k_new=None, v_new=None,
             e = lambda s: torch.empty(s, dtype=torch.int32, device=tokens.device)  # noqa: E731
             n = tokens.shape[:1]
             out = mine = CommitResult(e(tokens.shape), e(n), e(tokens.shape), e(n), e(n))
-        _call("tree_commit", index,
+        _call("tree_commit",
               (tokens, target_tokens, parents, k_new, v_new, k_cache, v_cache, page_table, cache_len, n_nodes, out.tokens,
-               out.accept_len, out.path, out.cache_len, out.row_flags, _raw(torch, index, stream, mine)))
+               out.accept_len, out.path, out.cache_len, out.row_flags, on.raw(torch, index, mine)))
     return out

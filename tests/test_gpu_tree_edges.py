@@ -100,3 +100,67 @@ def test_verification_alone_flags():
     assert r.row_flags.tolist() == [0] + [mtp.ROW_BAD_ID] * 3
     assert r.accept_len.tolist() == [2, -1, -1, -1] and r.cache_len.tolist() == [7, 4, -1, 4]
     assert r.tokens.tolist() == [[5, 6, 7]] + [[-1] * 3] * 3
+
+
+# ------------------------------------------------------- another stream --
+
+def calls():
+    """name -> (function of the keyword arguments, its inputs on the GPU)."""
+    torch.manual_seed(1)
+    attn = on_gpu(attn_case(5, "bf16", 2, 4, 8, 2, 64, 16, [3000, 40]))
+    whole = on_gpu(attn_case(6, "f32", 2, 4, 8, 2, 64, 16, [300, 40]))
+    z, scores, T = torch.randn(2, 3, 30011, device="cuda"), torch.zeros(2, 3, device="cuda"), torch.ones(2, device="cuda")
+    states, up = torch.randn(2, 2, 3, 64, device="cuda"), torch.tensor([[0, 2], [1, 1]], dtype=i32, device="cuda")
+    c = on_gpu(commit_case(7, "bf16", 2, 3, 9, 2, 16, 16, [3, 16, 40]))
+    return {
+        "attention": lambda **k: mtp.mtp_tree_attention(**attn, with_lse=True, **k),
+        "attention f32": lambda **k: mtp.mtp_tree_attention(**whole, with_lse=True, **k),
+        "select": lambda **k: mtp.mtp_beam_select(z, scores, T, 9, **k),
+        "reorder": lambda **k: mtp.mtp_beam_reorder(states, up, **k),
+        "commit": lambda **k: mtp.mtp_tree_commit(**c, **k),
+    }
+
+
+@pytest.mark.parametrize("name", ["attention", "attention f32", "select", "reorder", "commit"])
+def test_outputs_on_another_stream_are_nobody_elses(name):
+    """Memory freed on the current stream, whose work that writes it is still
+    queued, is not what a call on another stream gets for its outputs and
+    workspace."""
+    f = calls()[name]
+    want = [None if t is None else t.clone() for t in f()]
+    side = torch.cuda.Stream()
+    f(stream=side)
+    torch.cuda.synchronize()
+    sizes = [t.numel() * t.element_size() for t in want if t is not None] + [1 << k for k in range(4, 24)]
+    torch.cuda._sleep(100_000_000)
+    for n in sizes * 3:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xff)
+    r = f(stream=side)
+    side.synchronize()
+    kept = [None if t is None else t.cpu() for t in r]
+    torch.cuda.synchronize()
+    for t, k, w in zip(r, kept, want):
+        if t is not None:
+            assert torch.equal(t, w) and torch.equal(k, w.cpu())
+
+
+def test_outputs_freed_while_they_are_read():
+    """Outputs of a call on another stream, read on the current one and let go:
+    the next call on that stream does not write over them."""
+    f = calls()["reorder"]
+    want = f().states.clone()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            r = f(stream=side)
+        r = f(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(20_000_000)
+        got.append(r.states.clone())
+        del r
+        with torch.cuda.stream(side):
+            junk = [torch.full_like(want, 9.0) for _ in range(8)]
+        del junk
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
