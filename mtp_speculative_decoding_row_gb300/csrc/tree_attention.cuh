@@ -306,7 +306,7 @@ __device__ __forceinline__ int attn_masks(const int32_t *up, int n, uint64_t *ma
 
 // Flags that one thread of `nt` finds in its share of sequence b's page table.
 __device__ __forceinline__ int attn_check_pages(const TreeAttnArgs &A, int b, int len, int t, int nt) {
-    const int n = (len + A.page_size - 1) / A.page_size;
+    const int n = (static_cast<uint32_t>(len) + A.page_size - 1) / A.page_size;  // (the sum may pass 2^31)
     const int32_t *row = A.table + static_cast<size_t>(b) * A.max_pages;
     int bad = 0;
 #pragma unroll 8

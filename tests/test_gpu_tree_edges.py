@@ -164,3 +164,20 @@ def test_outputs_freed_while_they_are_read():
         del junk
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+# ------------------------------------------------------- pages and tables --
+
+def test_bad_page_of_a_very_large_page_size():
+    """Length and page size whose sum passes 2^31: the page is looked at."""
+    ps, n = 1_200_000_000, 1_100_000_000
+    cache = torch.zeros(1, ps, 1, 1, dtype=torch.bfloat16, device="cuda")
+    new = torch.ones(2, 1, 1, 1, dtype=torch.bfloat16, device="cuda")
+    r = mtp.mtp_tree_attention(new, new, new, cache, cache, torch.tensor([[0], [-1]], dtype=i32, device="cuda"),
+                               torch.tensor([n, n], dtype=i32, device="cuda"), with_lse=True)
+    torch.cuda.synchronize()
+    assert r.row_flags.tolist() == [0, mtp.ROW_BAD_ID]
+    assert r.out[1].isnan().all() and r.lse[1].isnan().all()
+    # n keys of score 0 and one of score 1; sums of float32 in a few thousand parts
+    want = math.log(n + math.e)
+    assert abs(r.lse[0].item() - want) < 1e-4 and 0 <= r.out[0].item() < 1e-6
