@@ -370,7 +370,8 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  *   out [B, T, Hq, D] dtype, lse [B, T, Hq] float32 or NULL, contiguous
  *   row_flags [B] or NULL.
  * Requirements: 1 <= T <= MTP_MAX_NODES, Hq a multiple of Hkv (at most
- * 4096 times), 1 <= D <= 256, 0 < scale, max_pages * page_size < 2^31 - 2^16
+ * 4096 times), Hq <= 2^16, B <= 2^20, 1 <= D <= 256, 0 < scale <= 1e30, at least
+ * one page and one column of the table, max_pages * page_size <= 2^31 - 2^16
  * (else MTP_ERR_INVALID_ARG); pointers aligned to their elements (else
  * MTP_ERR_MISALIGNED).  Scores, softmax statistics and outputs are accumulated in float32; with bfloat16 storage the softmax
  * weights are rounded to bfloat16 for their product with the values (the
@@ -416,8 +417,8 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  *   row_flags [B] or NULL; a flagged sequence (a score or a read logit NaN or
  *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and
  *   parents -1 and scores NaN.
- * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24
- * (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  A row's sum of
+ * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24,
+ * B <= 2^20 (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  A row's sum of
  * exponentials is a float32 sum (relative error below 2^-16 for V <= 2^18); with
  * its logarithm, scores are formed and compared in float64 and
  * rounded to float32 at the end.
@@ -434,7 +435,7 @@ int64_t mtp_beam_select_workspace(mtp_dtype dtype, int B, int W, int V, int K);
  * overlapping (MTP_ERR_INVALID_ARG).  A parent outside [0, W) -- the empty
  * places of mtp_beam_select -- gives a row of zeros and flags the sequence
  * MTP_ROW_BAD_ID (where there are no bytes to move, nothing is flagged).
- * row_flags [B] or NULL.
+ * row_flags [B] or NULL.  N0 B K <= 2^31, row_bytes <= 2^40.
  */
 int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, int W, int K, int64_t row_bytes, void *out,
                      int32_t *row_flags, mtp_stream_t stream);
@@ -451,7 +452,8 @@ int mtp_beam_reorder(const void *states, const int32_t *parents, int N0, int B, 
  * token after the current node, until there is none; the tokens that the
  * target drew are emitted, so whatever the tree holds the output follows the
  * target's distribution.  Nodes that continue the cached text (parent -1)
- * other than the root are never reached.
+ * other than the root are never reached.  (A chain verified by mtp_rs_verify:
+ * target_tokens = its tokens, n_nodes = its accept_len + 1, parents NULL.)
  *   out_tokens [B, T]: the accepted drafts, then the target's token after the
  *     last of them, then -1
  *   path [B, T]: the nodes of the path, the root first, then -1

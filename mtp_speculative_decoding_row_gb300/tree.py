@@ -161,8 +161,8 @@ def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
 def mtp_beam_select(logits, scores, temperature, K: int, *, out: Optional[BeamResult] = None, stream=None) -> BeamResult:
     """The K best continuations of each sequence's W beams (see
     mtp_beam_select in include/mtp_rs.h): logits [B, W, V] (float32 or
-    bfloat16), scores [B, W] float32 (-inf: a dead beam), temperature [B]
-    float32.  Returns tokens, parents and scores [B, K], best first."""
+    bfloat16, contiguous, starting on 16 bytes), scores [B, W] float32 (-inf: a
+    dead beam), temperature [B] float32.  Returns tokens, parents and scores [B, K], best first."""
     torch = _m._torch()
     index = logits.get_device()
     with _on(torch, index, stream) as on:

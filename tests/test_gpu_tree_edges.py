@@ -181,3 +181,93 @@ def test_bad_page_of_a_very_large_page_size():
     # n keys of score 0 and one of score 1; sums of float32 in a few thousand parts
     want = math.log(n + math.e)
     assert abs(r.lse[0].item() - want) < 1e-4 and 0 <= r.out[0].item() < 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, D, ps", [(1, 128, 16), (9, 64, 64), (40, 128, 24), (3, 256, 256)])
+def test_table_wider_than_the_text(dtype, T, D, ps):
+    """A table for the longest text a server allows, what lies behind a
+    sequence's pages no page numbers at all."""
+    x = attn_case(T + D, dtype, 3, T, 8, 2, D, ps, [0, 70, 333])
+    good = on_gpu(x)
+    plain = mtp.mtp_tree_attention(**good, with_lse=True)
+    check_attention(x, plain.out, None, plain.lse)
+    wide = torch.full((3, 8192 // ps), -7, dtype=i32)
+    wide[1::2] = 1 << 30
+    for b in range(3):
+        n = -(-int(x["cache_len"][b]) // ps)
+        wide[b, :n] = x["page_table"][b, :n]
+    r = mtp.mtp_tree_attention(**dict(good, page_table=wide.cuda()), with_lse=True)
+    torch.cuda.synchronize()
+    assert r.row_flags.tolist() == [0, 0, 0]
+    check_attention(x, r.out, None, r.lse)
+
+
+# ------------------------------------------------- graphs and the chain's way --
+
+def test_commit_and_reorder_graphs_and_streams():
+    """Captured once and replayed with other tokens, parents and lengths, and
+    the same on a given stream."""
+    x = commit_case(21, "bf16", 2, 3, 12, 2, 64, 16, [3, 16, 40], 0.7)
+    g = on_gpu(x)
+    first = {k: g[k].clone() for k in ("k_cache", "v_cache")}
+    states, up = torch.randn(2, 3, 4, 33, device="cuda"), torch.zeros(3, 4, dtype=i32, device="cuda")
+    mtp.mtp_tree_commit(**g)
+    mtp.mtp_beam_reorder(states, up)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = mtp.mtp_tree_commit(**g)
+        s = mtp.mtp_beam_reorder(states, up)
+    side = torch.cuda.Stream()
+    for seed in range(3):
+        y = commit_case(100 + seed, "bf16", 2, 3, 12, 2, 64, 16, [3, 16, 40], 0.7)
+        for k in ("tokens", "target_tokens", "parents"):
+            g[k].copy_(y[k])
+            x[k] = y[k]
+        x["cache_len"] = torch.tensor([seed, 40 - seed, 20], dtype=i32)
+        g["cache_len"].copy_(x["cache_len"])
+        up.copy_(torch.randint(0, 4, (3, 4)))
+        for run in (graph.replay, None):
+            for k in first:
+                g[k].copy_(first[k])
+            torch.cuda.synchronize()
+            if run:
+                run()
+                got, moved = r, s
+            else:
+                got, moved = mtp.mtp_tree_commit(**g, stream=side), mtp.mtp_beam_reorder(states, up, stream=side)
+            torch.cuda.synchronize()
+            check_commit(dict(x, k_cache=first["k_cache"].cpu(), v_cache=first["v_cache"].cpu()),
+                         mtp.CommitResult(*(t.cpu() for t in got)), g["k_cache"], g["v_cache"])
+            want = torch.stack([states[:, b, up[b].long()] for b in range(3)], 1)
+            assert torch.equal(moved.states, want) and got.row_flags.tolist() == moved.row_flags.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chain_verified_by_rejection_sampling_and_committed(dtype):
+    """mtp_rs_verify decides how many drafts of a chain stand; its tokens are
+    the commit's target tokens, and accept_len + 1 its nodes."""
+    B, gamma, V, Hkv, D, ps = 24, 5, 4099, 2, 64, 16
+    g = torch.Generator().manual_seed(11)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    target = torch.randn(B, gamma + 1, V, generator=g) * 2
+    draft = target[:, :gamma] + 0.4 * torch.randn(B, gamma, V, generator=g)
+    target, draft = target.to(dt), draft.to(dt)
+    ids = torch.distributions.Categorical(logits=draft.float()).sample().to(i32)
+    u = torch.rand(B, gamma + 1, generator=g)
+    bad = target.clone()
+    bad[5, 0, 7] = math.nan                       # a flagged sequence commits nothing
+    v = mtp.mtp_rs_verify(bad.cuda(), draft.cuda(), ids.cuda(), torch.ones(B).cuda(), u.cuda())
+    x = commit_case(31, dtype, 2, B, gamma + 1, Hkv, D, ps, [(7 * b) % 50 for b in range(B)], tree="chain")
+    x["tokens"] = torch.cat([torch.full((B, 1), 9, dtype=i32), ids], 1)
+    x["target_tokens"] = v.tokens.cpu()
+    x["n_nodes"] = v.accept_len.cpu() + 1
+    c = on_gpu(x)
+    r = mtp.mtp_tree_commit(c["tokens"], v.tokens, None, c["k_new"], c["v_new"], c["k_cache"], c["v_cache"], c["page_table"],
+                            c["cache_len"], v.accept_len + 1)
+    torch.cuda.synchronize()
+    check_commit(x, mtp.CommitResult(*(t.cpu() for t in r)), c["k_cache"], c["v_cache"])
+    assert torch.equal(r.accept_len, v.accept_len) and torch.equal(r.tokens, v.tokens)
+    assert r.row_flags.tolist() == [0] * B and v.accept_len.tolist()[5] == -1
+    assert len(set(v.accept_len.tolist())) > 3    # rejections at several places, and none
