@@ -9,12 +9,14 @@
 // registers, the running maximum m and sum l of the softmax per row
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
 //   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j       (s in units of log2 e),
-// all in float32.  A warp has four rows from their scores to their output, so
+// all in float32.  Each sum is made of shorter ones -- a score of two halves, an
+// output of its tiles' sums -- which halves the error (one token after 122070:
+// 1.3e-6 -> 6e-7 of the output) and costs 3 % (68 -> 70 us below).  A warp has four rows from their scores to their output, so
 // only the tile itself needs barriers.  The next tile's keys are on their way
 // while this one's weights and outputs are formed, its values while the next
 // scores are: one tile of shared memory each, so that two CTAs fit an SM (64
-// ragged sequences of up to 2500 tokens, 16 rows, float32: 89 -> 68 us; 128
-// without the four rows to a warp and the values four at a time).  What bounds
+// ragged sequences of up to 2500 tokens, 16 rows, float32: 89 -> 68 us, 70 with
+// the shorter sums; 128 without the four rows to a warp and the values four at a time).  What bounds
 // it: half of the issue slots, and as many empty while warps wait for shared
 // memory and for each other (28 rows); memory runs at 14 % of its rate.
 #include "tree_attention.cuh"
@@ -167,16 +169,29 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 #pragma unroll
                     for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
                 const float *q0 = sq + 2 * ty * KS;
+                // each half of the elements on its own: shorter sums lose less
+                float half[2][4] = {};
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
 #pragma unroll 4
-                for (int d = 0; d < DP; d += 4) {
-                    const float4 a0 = *reinterpret_cast<const float4 *>(q0 + d);
-                    const float4 a1 = *reinterpret_cast<const float4 *>(q0 + KS + d);
+                    for (int d = part * (DP / 2); d < (part + 1) * (DP / 2); d += 4) {
+                        const float4 a0 = *reinterpret_cast<const float4 *>(q0 + d);
+                        const float4 a1 = *reinterpret_cast<const float4 *>(q0 + KS + d);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float4 k = *reinterpret_cast<const float4 *>(sk + (tx + 16 * c) * KS + d);
-                        s[0][c] = fmaf(a0.x, k.x, fmaf(a0.y, k.y, fmaf(a0.z, k.z, fmaf(a0.w, k.w, s[0][c]))));
-                        s[1][c] = fmaf(a1.x, k.x, fmaf(a1.y, k.y, fmaf(a1.z, k.z, fmaf(a1.w, k.w, s[1][c]))));
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 k = *reinterpret_cast<const float4 *>(sk + (tx + 16 * c) * KS + d);
+                            s[0][c] = fmaf(a0.x, k.x, fmaf(a0.y, k.y, fmaf(a0.z, k.z, fmaf(a0.w, k.w, s[0][c]))));
+                            s[1][c] = fmaf(a1.x, k.x, fmaf(a1.y, k.y, fmaf(a1.z, k.z, fmaf(a1.w, k.w, s[1][c]))));
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float x = s[i][c];
+                            s[i][c] = part ? half[i][c] + x : 0.f;
+                            half[i][c] = x;
+                        }
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -206,7 +221,10 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 #pragma unroll
                     for (int d = 1; d < 8; d <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, d));
                     const float m0 = sm[r], m1 = max_nan(m0, top);
-                    const float ref = m1 == -INFINITY ? 0.f : m1 * A.scale_log2;
+                    // (the reference is the rounded product, in the weights and in the
+                    // factor of the old ones alike: the exact product in one of the two
+                    // would put them 2^-24 of a score's size apart at every new maximum)
+                    const float ref = m1 == -INFINITY ? 0.f : __fmul_rn(m1, A.scale_log2);
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -218,7 +236,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                     for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL, sum, d);
                     __syncwarp();
                     if (l == 0) {
-                        const float f = m0 == -INFINITY ? 0.f : exp2f(fmaf(m0, A.scale_log2, -ref));
+                        const float f = m0 == -INFINITY ? 0.f : exp2f(__fsub_rn(__fmul_rn(m0, A.scale_log2), ref));
                         sf[r] = f;
                         sl[r] = sl[r] * f + sum;
                         sm[r] = m1;
@@ -233,11 +251,13 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                         see0 = 2 * ty < rows && t0 < n ? smask[t0] : 0ull;
                         see1 = 2 * ty + 1 < rows && t1 < n ? smask[t1] : 0ull;
                     }
+                    // a tile's sums on their own first: one sum over all keys of a long
+                    // text would lose twice what the shorter ones do
+                    float add[2][DC * 4];
 #pragma unroll
-                    for (int c = 0; c < DC * 4; ++c) {
-                        acc[0][c] *= f0;
-                        acc[1][c] *= f1;
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int c = 0; c < DC * 4; ++c) add[i][c] = 0.f;
                     const float *p0 = sp + 2 * ty * (BN + 4), *p1 = p0 + BN + 4;
                     int j = 0;
                     if (!tree) {  // four keys at a time
@@ -250,14 +270,14 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 #pragma unroll
                                 for (int c = 0; c < DC; ++c) {
                                     const float4 v = *reinterpret_cast<const float4 *>(sv + (j + e) * DP + 64 * c + 4 * tx);
-                                    acc[0][4 * c] = fmaf(w0[e], v.x, acc[0][4 * c]);
-                                    acc[0][4 * c + 1] = fmaf(w0[e], v.y, acc[0][4 * c + 1]);
-                                    acc[0][4 * c + 2] = fmaf(w0[e], v.z, acc[0][4 * c + 2]);
-                                    acc[0][4 * c + 3] = fmaf(w0[e], v.w, acc[0][4 * c + 3]);
-                                    acc[1][4 * c] = fmaf(w1[e], v.x, acc[1][4 * c]);
-                                    acc[1][4 * c + 1] = fmaf(w1[e], v.y, acc[1][4 * c + 1]);
-                                    acc[1][4 * c + 2] = fmaf(w1[e], v.z, acc[1][4 * c + 2]);
-                                    acc[1][4 * c + 3] = fmaf(w1[e], v.w, acc[1][4 * c + 3]);
+                                    add[0][4 * c] = fmaf(w0[e], v.x, add[0][4 * c]);
+                                    add[0][4 * c + 1] = fmaf(w0[e], v.y, add[0][4 * c + 1]);
+                                    add[0][4 * c + 2] = fmaf(w0[e], v.z, add[0][4 * c + 2]);
+                                    add[0][4 * c + 3] = fmaf(w0[e], v.w, add[0][4 * c + 3]);
+                                    add[1][4 * c] = fmaf(w1[e], v.x, add[1][4 * c]);
+                                    add[1][4 * c + 1] = fmaf(w1[e], v.y, add[1][4 * c + 1]);
+                                    add[1][4 * c + 2] = fmaf(w1[e], v.z, add[1][4 * c + 2]);
+                                    add[1][4 * c + 3] = fmaf(w1[e], v.w, add[1][4 * c + 3]);
                                 }
                         }
                     }
@@ -268,18 +288,23 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                         for (int c = 0; c < DC; ++c) {
                             const float4 v = *reinterpret_cast<const float4 *>(sv + j * DP + 64 * c + 4 * tx);
                             if (on0) {
-                                acc[0][4 * c] = fmaf(w0, v.x, acc[0][4 * c]);
-                                acc[0][4 * c + 1] = fmaf(w0, v.y, acc[0][4 * c + 1]);
-                                acc[0][4 * c + 2] = fmaf(w0, v.z, acc[0][4 * c + 2]);
-                                acc[0][4 * c + 3] = fmaf(w0, v.w, acc[0][4 * c + 3]);
+                                add[0][4 * c] = fmaf(w0, v.x, add[0][4 * c]);
+                                add[0][4 * c + 1] = fmaf(w0, v.y, add[0][4 * c + 1]);
+                                add[0][4 * c + 2] = fmaf(w0, v.z, add[0][4 * c + 2]);
+                                add[0][4 * c + 3] = fmaf(w0, v.w, add[0][4 * c + 3]);
                             }
                             if (on1) {
-                                acc[1][4 * c] = fmaf(w1, v.x, acc[1][4 * c]);
-                                acc[1][4 * c + 1] = fmaf(w1, v.y, acc[1][4 * c + 1]);
-                                acc[1][4 * c + 2] = fmaf(w1, v.z, acc[1][4 * c + 2]);
-                                acc[1][4 * c + 3] = fmaf(w1, v.w, acc[1][4 * c + 3]);
+                                add[1][4 * c] = fmaf(w1, v.x, add[1][4 * c]);
+                                add[1][4 * c + 1] = fmaf(w1, v.y, add[1][4 * c + 1]);
+                                add[1][4 * c + 2] = fmaf(w1, v.z, add[1][4 * c + 2]);
+                                add[1][4 * c + 3] = fmaf(w1, v.w, add[1][4 * c + 3]);
                             }
                         }
+                    }
+#pragma unroll
+                    for (int c = 0; c < DC * 4; ++c) {
+                        acc[0][c] = fmaf(acc[0][c], f0, add[0][c]);
+                        acc[1][c] = fmaf(acc[1][c], f1, add[1][c]);
                     }
                 }
             }

@@ -271,3 +271,34 @@ def test_chain_verified_by_rejection_sampling_and_committed(dtype):
     assert torch.equal(r.accept_len, v.accept_len) and torch.equal(r.tokens, v.tokens)
     assert r.row_flags.tolist() == [0] * B and v.accept_len.tolist()[5] == -1
     assert len(set(v.accept_len.tolist())) > 3    # rejections at several places, and none
+
+
+# ------------------------------------------------------------- precision --
+
+@pytest.mark.parametrize("B, T, Hq, Hkv, D, L", [(1, 1, 8, 8, 64, 60013), (24, 1, 8, 8, 64, 1900), (2, 4, 8, 2, 128, 5001)])
+def test_float32_keeps_its_bits(B, T, Hq, Hkv, D, L):
+    """The error of all outputs together, relative to their size.  With random
+    values it is that of a weight, and u = 2^-24: a score of size 2, in two sums
+    of D / 2 roundings of at most u of it (uniform, so u / sqrt 3 each, on
+    partial sums of half its square on average), 2 u sqrt(D / 12) = 2.8e-7 or
+    3.9e-7; the exponent, up to 17, rounded once, 17 u ln 2 / sqrt 3 = 4.1e-7;
+    the power's two units, 1.2e-7; the output's sums of 64 and then of a few
+    hundred tiles, less than 2e-7: together below 6.5e-7.  The bound is half as
+    much again."""
+    x = attn_case(B + L, "f32", B, T, Hq, Hkv, D, 16, [L] * B, "chain")
+    g = on_gpu(x)
+    r = mtp.mtp_tree_attention(**g)
+    torch.cuda.synchronize()
+    far = size = 0.0
+    for b in range(B):
+        at = torch.arange(L, device="cuda")
+        page, row = g["page_table"][b].long()[at // 16], at % 16
+        K = torch.cat([g["k_cache"][page, row], g["k_new"][b]]).double()
+        V = torch.cat([g["v_cache"][page, row], g["v_new"][b]]).double()
+        q = g["q"][b].double().view(T, Hkv, Hq // Hkv, D)
+        s = torch.einsum("thgd,shd->thgs", q, K) * D ** -0.5
+        s[..., L:] += torch.full((T, T), -math.inf, device="cuda", dtype=torch.float64).triu(1)[:, None, None]
+        o = torch.einsum("thgs,shd->thgd", torch.softmax(s, -1), V).reshape(T, Hq, D)
+        far += (r.out[b].double() - o).square().sum().item()
+        size += o.square().sum().item()
+    assert math.sqrt(far / size) < 1e-6
