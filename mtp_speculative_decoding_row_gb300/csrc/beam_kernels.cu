@@ -22,10 +22,11 @@
 // list of its own; one that is full is cut to its K best, and the bound rises
 // for all warps.
 //
-// 512 rows of 151936 bfloat16 logits (64 sequences, 8 beams, K = 16) take 62
-// us, 2.5 TB/s; one sequence of 4 rows 14 us.  What bounds the first kernel is
-// issue: about 9 instructions a logit, 54 % of the slots, memory at 39 %; few
-// rows are bound by the chain of steps in both kernels.
+// 512 rows of 151936 bfloat16 logits (64 sequences, 8 beams, K = 16) take 64
+// us, 2.4 TB/s; one sequence of 4 rows 14.6 us.  Nothing of the first kernel is at
+// its limit: about 10 instructions a logit, 56 % of the issue slots, memory at 37
+// %, the rest waits for a round's loads and the bound's barriers; few rows are
+// bound by the chain of steps in both kernels.
 //
 // Rows may start on any element.  A vector is always elements [8 j, 8 j + 8)
 // (4 j of float32) of the row, put together from two aligned loads where the

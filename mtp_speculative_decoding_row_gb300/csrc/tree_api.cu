@@ -163,8 +163,10 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     // join and the ends of the pieces take as long as about six tiles on the
     // tensor cores, two of the other kernel.  (Whole against split: one token
     // after 256 8.3 and 13 us; 128 units of 1000 tokens 17 and 26 us, 512 of
-    // 1000 65 and 73.)  The lengths are not known here: beyond 16 tiles, or
-    // four waves, one long unit could cost more than it saves.
+    // 1000 65 and 73; all with a page table cut to the text.)  The lengths are not
+    // known here, only the table's width: beyond 16 tiles, or four waves, one
+    // long unit could cost more than it saves, so with a wide table short texts
+    // are split as well.
     const long long units = static_cast<long long>(a.Hkv) * (a.B > 0 ? a.B : 1);
     const long long waves = (units + groups - 1) / (groups > 0 ? groups : 1);
     p.whole = umma ? p.max_tiles <= 16 && waves <= 4 && (waves * groups - units) * p.max_tiles <= 6 * groups

@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
 // parts are on their way at a time: what bounds this kernel is the time of a
 // load, not their number (a row of 20 parts read one after the other took 30
 // us).  bfloat16 has many rows of few parts: four at a time, few registers and
-// many warps on an SM (trees of 64 nodes: 262 us, with eight 267, with sixteen
-// 278).  float32 has more and smaller CTAs, so more parts: sixteen (4 sequences
+// many warps on an SM (trees of 64 nodes: with four 262 us, with eight 267, with
+// sixteen 278).  float32 has more and smaller CTAs, so more parts: sixteen (4 sequences
 // of 2501: 22.0 us with four, 20.3 with eight, 19.6 with sixteen).
 
 template <typename T, int NQ>

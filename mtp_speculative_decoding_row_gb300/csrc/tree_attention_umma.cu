@@ -27,18 +27,18 @@
 //   FEW    up to 32 rows: as KEYS, but those rows would lie in the lanes of one
 //          warp and leave three idle, so each warp of a group gets the scores
 //          of a quarter of the keys (64 sequences of 768 tokens, 16 rows: 74 ->
-//          68 us; one of 131072, 32 rows: 97 -> 94 us).  They exchange the
+//          68 us; one of 131072, 32 rows: 3 % less).  They exchange the
 //          maximum of each tile; weights go through shared memory, because in
 //          TMEM a warp reaches its own lanes only
 //   ONE    heads of 256: TMEM holds one accumulator, so one group works, with
 //          two score buffers (the products of tile j + 1 run under the softmax
 //          of tile j); warp 1 issues the products with the keys, warp 2 those
 //          with the values
-// Measured: one token after 1000 12 us (latency: two launches and a chain of
-// dependent loads); 64 sequences of up to 8192, heads of 256, 131 us, and one
-// of 131072, 94 us (memory, at 0.81 and 0.84 of a copy's rate); trees of 64
-// nodes over 8 sequences of 16384, 262 us (the softmax warps; 0.55 of the
-// tensor cores' rate).
+// Measured, replayed in a graph: one token after 1000 12.4 us (latency: two
+// launches and a chain of dependent loads); 64 sequences of up to 8192, heads of
+// 256, 132 us, and one of 131072, 96 us (memory, at 0.81 of a copy's rate);
+// trees of 64 nodes over 8 sequences of 16384, 260 us (the softmax warps; 0.55 of
+// the tensor cores' rate).
 //
 // The output accumulator is rescaled only when a row's maximum has risen by
 // more than 2^8 since the last time: until then the weights are taken
