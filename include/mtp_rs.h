@@ -407,8 +407,10 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  * level of a draft tree, or one step of beam search): over w < W, v < V
  *   score(w, v) = scores[b,w] + ln softmax(logits[b,w] / T_b)(v),
  * the K largest, best first; equal scores go to the smaller beam, then (within
- * a beam the order is that of the logits) the smaller token.  A continuation of probability 0 is never selected: where
- * fewer than K are left the rest has token and parent -1 and score -inf.  A
+ * a beam the order is that of the logits) the smaller token.  A continuation of
+ * probability 0 (a logit of -inf) is never selected: where fewer than K are left
+ * the rest has token and parent -1 and score -inf.  (A score below float32's
+ * range, at temperatures near 0, is -inf as well, with its token and parent.)  A
  * beam with score -inf is dead: its logits are not read.
  *
  *   logits [B, W, V] dtype, scores [B, W] float32, temperature [B] (> 0, else
@@ -418,9 +420,9 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  *   +inf, a live beam of no finite logit: MTP_ROW_NONFINITE) has tokens and
  *   parents -1 and scores NaN.
  * Requirements: W <= MTP_MAX_BEAMS, K <= MTP_MAX_SELECT, K <= W V, V <= 2^24,
- * B <= 2^20 (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  A row's sum of
- * exponentials is a float32 sum (relative error below 2^-16 for V <= 2^18); with
- * its logarithm, scores are formed and compared in float64 and
+ * B <= 2^20 (else MTP_ERR_INVALID_ARG), a 16-byte aligned base (any V).  A
+ * row's sum of exponentials is a float32 sum (relative error below 2^-16 for V <=
+ * 2^18); with its logarithm, scores are formed and compared in float64 and
  * rounded to float32 at the end.
  */
 int mtp_beam_select(const void *logits, mtp_dtype dtype, const float *scores, const float *temperature, int B, int W, int V,

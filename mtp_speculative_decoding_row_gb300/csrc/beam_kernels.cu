@@ -132,8 +132,8 @@ __device__ __forceinline__ int cut(uint64_t *list, int n, int keep, uint64_t *tm
 }
 
 // Look at the `queued` vectors that a warp has put aside, all of them in its
-// part: their elements that reach the bound join the warp's list of `count`.  Returns the list's new
-// length; a cut raises *s_bound.
+// part: their elements that reach the bound join the warp's list of `count`.
+// Returns the list's new length; a cut raises *s_bound.
 template <typename T>
 __device__ __noinline__ int drain(const unsigned char *row, uint32_t sh, int whole, int V, const int *queue, int queued, uint64_t *list,
                                   int count, int keep, uint64_t *tmp, unsigned long long *s_bound) {
