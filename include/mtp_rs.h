@@ -373,9 +373,10 @@ int mtp_tv_loss_topk(const void *target_values, const int32_t *target_idx, const
  * 4096 times), Hq <= 2^16, B <= 2^20, 1 <= D <= 256, 0 < scale <= 1e30, at least
  * one page and one column of the table, max_pages * page_size <= 2^31 - 2^16
  * (else MTP_ERR_INVALID_ARG); pointers aligned to their elements (else
- * MTP_ERR_MISALIGNED).  Scores, softmax statistics and outputs are accumulated in float32; with bfloat16 storage the softmax
- * weights are rounded to bfloat16 for their product with the values (the
- * weights' sum is not).
+ * MTP_ERR_MISALIGNED); scores of at most 2^29 in magnitude (rows with larger
+ * ones may be NaN).  Scores, softmax statistics and outputs are accumulated in
+ * float32; with bfloat16 storage the softmax weights are rounded to bfloat16 for
+ * their product with the values (the weights' sum is not).
  */
 typedef struct mtp_tree_attention_args {
     const void *q, *k_new, *v_new, *k_cache, *v_cache;

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mtp_speculative_decoding_row_gb300 as mtp
+from tests import tree_ref
 from tests.test_gpu_tree_ops import attn_case, check_attention, check_commit, commit_case, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -302,3 +303,33 @@ def test_float32_keeps_its_bits(B, T, Hq, Hkv, D, L):
         far += (r.out[b].double() - o).square().sum().item()
         size += o.square().sum().item()
     assert math.sqrt(far / size) < 1e-6
+
+
+@pytest.mark.parametrize("dtype, T, D", [("bf16", 1, 64), ("bf16", 9, 128), ("bf16", 40, 64), ("bf16", 3, 256), ("f32", 1, 64), ("f32", 9, 96)])
+def test_scores_up_to_2_to_the_29(dtype, T, D):
+    """Queries and keys of whole numbers, a scale of 2^21 and scores of up to
+    2^21 D: every row is the mean of the values whose keys have its largest score.
+    The products with log2(e) round by up to 16 there, in all weights of a row
+    alike; what is left is the sum of the weights' and the output's rounding."""
+    x = attn_case(D + T, dtype, 2, T, 8, 2, D, 16, [700, 33], "random")
+    g = torch.Generator().manual_seed(D)
+    for k in ("q", "k_new", "k_cache"):
+        x[k] = torch.randint(-1, 2, x[k].shape, generator=g).to(x[k].dtype)
+    r = mtp.mtp_tree_attention(**on_gpu(x), scale=2.0 ** 21, with_lse=True)
+    torch.cuda.synchronize()
+    half = torch.finfo(x["q"].dtype).eps / 2
+    for b in range(2):
+        n = int(x["cache_len"][b])
+        at = torch.arange(n)
+        page, row = x["page_table"][b].long()[at // 16], at % 16
+        see = torch.cat([torch.ones(T, n, dtype=torch.bool), tree_ref.ancestors(x["parents"][b].tolist(), T)], 1)
+        for hq in range(8):
+            K = torch.cat([x["k_cache"][page, row, hq // 4], x["k_new"][b, :, hq // 4]]).double()
+            V = torch.cat([x["v_cache"][page, row, hq // 4], x["v_new"][b, :, hq // 4]]).double()
+            s = (x["q"][b, :, hq].double() @ K.T).masked_fill(~see, -math.inf)
+            top = s.amax(1, keepdim=True)
+            w = (s == top).double()
+            w = w / w.sum(1, keepdim=True)
+            want, mass = w @ V, w @ V.abs()
+            assert ((r.out[b, :, hq].double().cpu() - want).abs() <= 2.1 * half * mass + 2.0 ** -20 * mass).all()
+            assert ((r.lse[b, :, hq].double().cpu() - top[:, 0] * 2.0 ** 21).abs() <= 2.0 ** -22 * (top[:, 0] * 2.0 ** 21).abs() + 10).all()
