@@ -498,6 +498,144 @@ typedef struct mtp_tree_commit_args {
 int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t stream);
 
 /*
+ * Around a verification step.  The calls below prepare what tree attention and
+ * verification take: rotated queries and keys, a filled cache, adjusted logits.
+ * An output may be its input itself (the same address and strides); otherwise
+ * the memory from its first to its last byte must not meet that of an input
+ * (MTP_ERR_INVALID_ARG where two such ranges are found to meet).
+ */
+#define MTP_MAX_BIAS 1024   /* biases of a sequence in mtp_adjust_logits */
+
+/*
+ * mtp_rope -- rotary positions of queries and keys, or their gradients.
+ *
+ * With t = positions[b, t'] inv_freq[i], pair i < pairs of every head becomes
+ *   (a, c) -> factor (a cos t - c sin t, c cos t + a sin t),
+ * (a, c) = (x[i], x[pairs + i]), or with `interleaved` (x[2i], x[2i + 1]); with
+ * `inverse` t is negated: the transpose, so the gradient of the call without
+ * it.  Elements from 2 pairs on are copied.  Angles are exact products (taken
+ * modulo a turn in whole numbers, to 2^-32 turns for frequencies of up to 1 and
+ * any position), so that far positions lose nothing.
+ *
+ *   q [B, T, Hq, D], k [B, T, Hkv, D] and their outputs: elements of `dtype`,
+ *   D contiguous, the other strides in elements (Hq = 0 or Hkv = 0: none, NULL)
+ *   positions [B, T] int32, strides in elements; inv_freq [pairs] float32 (a
+ *   frequency that is not finite makes its pairs NaN).
+ * Requirements: 1 <= D <= 256, 2 pairs <= D, at most 65536 heads, a finite
+ * factor (else MTP_ERR_INVALID_ARG); pointers aligned to their elements.
+ */
+typedef struct mtp_rope_args {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3]; /* b, t, head */
+    int64_t pos_stride[2];                                              /* b, t */
+    int dtype; /* mtp_dtype */
+    int B, T, Hq, Hkv, D, pairs;
+    int interleaved, inverse;
+    float factor;
+} mtp_rope_args;
+
+int mtp_rope(const mtp_rope_args *args, mtp_stream_t stream);
+
+/*
+ * mtp_cache_append -- keys and values of new tokens written behind the cached
+ * ones, the keys rotated on the way.
+ *
+ * Token t < n_new[b] (NULL: T) of sequence b goes to token cache_len[b] + t of
+ * its pages; its key is rotated as by mtp_rope at positions[b, t], or without
+ * positions (NULL) at cache_len[b] + t.  The queries q (Hq > 0) are rotated the
+ * same way into q_out, and the rotated keys also go to k_out where it is given.
+ * new_len = cache_len + n_new.  Rows of tokens >= n_new are left as they were,
+ * in q_out, k_out and the cache.  pairs = 0 appends without a rotation.
+ *
+ * A length or count out of range, or no room in the page table for the new
+ * tokens, flags the sequence MTP_ROW_BAD_ID: new_len = cache_len, and none of
+ * its rows is written.  So does a page outside [0, num_pages) for any of the
+ * new tokens: new_len = cache_len, tokens of that page are not written, and
+ * what the others wrote lies behind cache_len.
+ *
+ *   q, k, v [B, T, heads, D], k_cache, v_cache [num_pages, page_size, Hkv, D]
+ *   as in mtp_tree_attention, q_out and k_out [B, T, heads, D] with strides.
+ * The pages that are written must belong to one sequence only.  new_len and
+ * row_flags must not overlap cache_len, n_new or page_table
+ * (MTP_ERR_INVALID_ARG).  Limits as for mtp_rope, and of the pages as for
+ * mtp_tree_attention; any T.
+ */
+typedef struct mtp_cache_append_args {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *k_cache, *v_cache;
+    const int32_t *positions;  /* [B, T] or NULL */
+    const int32_t *page_table; /* [B, max_pages] */
+    const int32_t *cache_len;  /* [B] */
+    const int32_t *n_new;      /* [B] or NULL */
+    const float *inv_freq;     /* [pairs] */
+    int32_t *new_len, *row_flags; /* [B]; [B] or NULL */
+    int64_t q_stride[3], k_stride[3], v_stride[3], q_out_stride[3], k_out_stride[3]; /* b, t, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];                                   /* page, token, head */
+    int64_t pos_stride[2];                                                          /* b, t */
+    int dtype;
+    int B, T, Hq, Hkv, D, pairs, interleaved;
+    int num_pages, page_size, max_pages;
+    float factor;
+} mtp_cache_append_args;
+
+int mtp_cache_append(const mtp_cache_append_args *args, mtp_stream_t stream);
+
+/*
+ * mtp_adjust_logits -- penalties for repeated tokens, biases and masks on the
+ * logits of a drafted chain or tree (S = gamma + 1 rows of a verification, the
+ * T nodes of a tree, or one row of a plain step).
+ *
+ * For sequence b and row s < n_nodes[b] (NULL: S), with
+ *   c(v) the occurrences of token v in history[b, prompt_len[b] ..
+ *        history_len[b]) and among tokens[b, i] of node s and its ancestors,
+ *   seen: c(v) > 0, or v occurs in history[b, .. prompt_len[b]),
+ *   x = seen ? (z > 0 ? z / repetition[b] : z repetition[b]) : z
+ *   x = x - frequency[b] c(v) - presence[b] [c(v) > 0]
+ *   x = x + the sum of bias[b, j] over bias_ids[b, j] = v
+ *   out[b, s, v] = -inf where bit v % 32 of mask[b, s, v / 32] is 0, else x,
+ * in float32, rounded once to the logits' type.  Row s holds the logits after
+ * node s: node 0 is the last token of the text (which `history` may leave out
+ * or tokens hold as -1), parents as for mtp_tree_attention (NULL: a chain).
+ * Token ids below 0 are empty places, in history, tokens and bias_ids alike.
+ * NULL means: no history (L = 0), no prompt (0), no tokens, repetition 1,
+ * frequency and presence 0, no mask (everything allowed).  A row whose mask
+ * allows nothing is -inf throughout (and flagged by what reads it).
+ *
+ * Rows of nodes >= n_nodes are left as they were.  An id >= V, a length, count
+ * or parent out of range flags the sequence MTP_ROW_BAD_ID, a penalty that is
+ * not finite or a repetition <= 0 MTP_ROW_NONFINITE: all its rows become NaN
+ * (with a count out of range all S rows).  Ids are looked at within
+ * history_len and n_nodes only.
+ *
+ *   logits, out [B, S, V] dtype, contiguous, 16-byte aligned (else
+ *   MTP_ERR_MISALIGNED), the same or apart; history [B, L] int32, tokens and
+ *   parents [B, S] int32, bias_ids int32 and bias float32 [B, n_bias], mask
+ *   rows of ceil(V / 32) words with strides in words (0: shared)
+ *   row_flags [B] or NULL.
+ * Requirements: S <= MTP_MAX_NODES, V <= 2^24, L <= 2^28, B <= 65535, n_bias <=
+ * MTP_MAX_BIAS (else MTP_ERR_INVALID_ARG).
+ */
+typedef struct mtp_adjust_args {
+    const void *logits;
+    void *out;
+    const int32_t *history, *history_len, *prompt_len;
+    const int32_t *tokens, *parents, *n_nodes;
+    const float *repetition, *frequency, *presence; /* [B] or NULL */
+    const int32_t *bias_ids;
+    const float *bias;
+    const int32_t *mask;
+    int32_t *row_flags;
+    int64_t mask_stride[2]; /* b, s */
+    int dtype;
+    int B, S, V, L, n_bias;
+} mtp_adjust_args;
+
+int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t stream);
+
+/*
  * mtp_query_plan -- the launch plan a call would use on the current device
  * (diagnostics; launches nothing).  op: 0 = mtp_rs_verify, 1 = mtp_rs_verify
  * with statistics, 2 = mtp_row_stats, 3 = mtp_tv_loss_fwd_bwd, 4 =

@@ -1,5 +1,5 @@
-// binding.cpp -- native argument marshalling of the tree-draft operators: the
-// checks of the tensors and the call of the C ABI.
+// binding.cpp -- native argument marshalling of the tree-draft operators and of
+// those around a verification step: the checks of the tensors and the call of the C ABI.
 //
 // These calls sit between the small launches of a decoding loop.  With up to
 // 15 tensors each, looking at type, shape, strides, device and address from
@@ -28,6 +28,9 @@ struct Functions {
     decltype(&mtp_beam_select_workspace) select_ws = nullptr;
     decltype(&mtp_beam_reorder) reorder = nullptr;
     decltype(&mtp_tree_commit) commit = nullptr;
+    decltype(&mtp_rope) rope = nullptr;
+    decltype(&mtp_cache_append) append = nullptr;
+    decltype(&mtp_adjust_logits) adjust = nullptr;
 } fn;
 
 constexpr int NOT_BOUND = -1;  // what a call returns before bind()
@@ -132,7 +135,7 @@ PyObject *guarded(F f) {
         if (PyErr_Occurred()) return nullptr;
         return PyLong_FromLong(rc);
     } catch (const Refusal &r) {
-        PyErr_SetString(r.type, r.text.c_str());
+        if (r.type) PyErr_SetString(r.type, r.text.c_str());  // (else Python's own error is set)
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
@@ -355,11 +358,212 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the six functions, in the order of Functions)
+// What mtp_rope and mtp_cache_append have in common: the frequencies and what
+// their number has to fit.
+int pairs_of(PyObject *o, const float **inv_freq, int64_t D, int index) {
+    const at::Tensor &f = tensor(o, "inv_freq");
+    dims(f, "inv_freq", 1);
+    const int64_t n = f.size(0);
+    if (2 * n > D) value_error("inv_freq has " + std::to_string(n) + " angles: more than pairs in a head of " + std::to_string(D));
+    *inv_freq = static_cast<float *>(whole(o, "inv_freq", at::kFloat, {n}, index));
+    return static_cast<int>(n);
+}
+const int32_t *positions_of(PyObject *o, int64_t B, int64_t T, int index, int64_t *strides) {
+    const at::Tensor &p = tensor(o, "positions");
+    check(p, "positions", at::kInt, {B, T}, index);
+    strides[0] = p.stride(0);
+    strides[1] = p.stride(1);
+    return static_cast<int32_t *>(p.data_ptr());
+}
+float finite(PyObject *o, const char *name) {
+    const double x = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+    const float f = static_cast<float>(x);
+    if (!(f - f == 0.f)) value_error(std::string(name) + " must be finite, got " + std::to_string(x));
+    return f;
+}
+void small(std::initializer_list<int64_t> sizes) {
+    for (int64_t x : sizes)
+        if (x > 0x7fffffff) value_error("a dimension is too large");
+}
+void head_size(int64_t D) {
+    if (D < 1 || D > 256) value_error("heads have 1 to 256 elements, got " + std::to_string(D));
+}
+
+// rope(q, k, positions, inv_freq, interleaved, factor, inverse, q_out, k_out, stream)
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count(n, 10)) return nullptr;
+    return guarded([&]() -> long {
+        const at::Tensor &q = tensor(a[0], "q");
+        dims(q, "q", 4);
+        mtp_rope_args s = {};
+        const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3);
+        const at::ScalarType dt = q.scalar_type();
+        s.dtype = dtype_code(q);
+        head_size(D);
+        const int index = index_of(q);
+        int64_t Hkv = 0;
+        s.q_out = strided(tensor(a[7], "out.q"), "out.q", dt, {B, T, Hq, D}, index, s.q_out_stride);
+        if (a[1] != Py_None) {
+            const at::Tensor &k = tensor(a[1], "k");
+            dims(k, "k", 4);
+            Hkv = k.size(2);
+            s.k = strided(k, "k", dt, {B, T, Hkv, D}, index, s.k_stride);
+            s.k_out = strided(tensor(a[8], "out.k"), "out.k", dt, {B, T, Hkv, D}, index, s.k_out_stride);
+        } else if (a[8] != Py_None) {
+            value_error("out.k is of no use without k");
+        }
+        s.q = strided(q, "q", dt, {B, T, Hq, D}, index, s.q_stride);
+        s.positions = positions_of(a[2], B, T, index, s.pos_stride);
+        s.pairs = pairs_of(a[3], &s.inv_freq, D, index);
+        s.factor = finite(a[5], "factor");
+        on_gpu(index, "q");
+        small({B, T, Hq, Hkv});
+        s.B = static_cast<int>(B);
+        s.T = static_cast<int>(T);
+        s.Hq = static_cast<int>(Hq);
+        s.Hkv = static_cast<int>(Hkv);
+        s.D = static_cast<int>(D);
+        s.interleaved = a[4] == Py_True;
+        s.inverse = a[6] == Py_True;
+        if (!fn.rope) return NOT_BOUND;
+        const mtp_stream_t stream = stream_of(a[9]);
+        const auto f = fn.rope;
+        return call([&] { return f(&s, stream); });
+    });
+}
+
+// cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_new, q,
+//   inv_freq, positions, interleaved, factor, new_len, q_out, k_out, row_flags, stream)
+PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count(n, 17)) return nullptr;
+    return guarded([&]() -> long {
+        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache"),
+                         &table = tensor(a[4], "page_table");
+        dims(k, "k", 4);
+        dims(kc, "k_cache", 4);
+        dims(table, "page_table", 2);
+        mtp_cache_append_args s = {};
+        const int64_t B = k.size(0), T = k.size(1), Hkv = k.size(2), D = k.size(3), pages = kc.size(0), page = kc.size(1), most = table.size(1);
+        const at::ScalarType dt = k.scalar_type();
+        s.dtype = dtype_code(k);
+        head_size(D);
+        const int index = index_of(k);
+        s.new_len = static_cast<int32_t *>(whole(a[12], "out.cache_len", at::kInt, {B}, index));
+        s.row_flags = static_cast<int32_t *>(whole_or_null(a[15], "out.row_flags", at::kInt, {B}, index));
+        s.k = strided(k, "k", dt, {B, T, Hkv, D}, index, s.k_stride);
+        s.v = strided(v, "v", dt, {B, T, Hkv, D}, index, s.v_stride);
+        s.k_cache = strided(kc, "k_cache", dt, {pages, page, Hkv, D}, index, s.k_cache_stride);
+        s.v_cache = strided(vc, "v_cache", dt, {pages, page, Hkv, D}, index, s.v_cache_stride);
+        s.page_table = static_cast<int32_t *>(whole(a[4], "page_table", at::kInt, {B, most}, index));
+        s.cache_len = static_cast<int32_t *>(whole(a[5], "cache_len", at::kInt, {B}, index));
+        s.n_new = static_cast<int32_t *>(whole_or_null(a[6], "n_new", at::kInt, {B}, index));
+        int64_t Hq = 0;
+        if (a[7] != Py_None) {
+            const at::Tensor &q = tensor(a[7], "q");
+            dims(q, "q", 4);
+            Hq = q.size(2);
+            if (a[8] == Py_None) value_error("q is of no use without inv_freq");
+            s.q = strided(q, "q", dt, {B, T, Hq, D}, index, s.q_stride);
+            s.q_out = strided(tensor(a[13], "out.q"), "out.q", dt, {B, T, Hq, D}, index, s.q_out_stride);
+        } else if (a[13] != Py_None) {
+            value_error("out.q is of no use without q");
+        }
+        if (a[14] != Py_None) s.k_out = strided(tensor(a[14], "out.k"), "out.k", dt, {B, T, Hkv, D}, index, s.k_out_stride);
+        if (a[8] != Py_None) s.pairs = pairs_of(a[8], &s.inv_freq, D, index);
+        if (a[9] != Py_None) {
+            if (a[8] == Py_None) value_error("positions are of no use without inv_freq");
+            s.positions = positions_of(a[9], B, T, index, s.pos_stride);
+        }
+        s.factor = finite(a[11], "factor");
+        on_gpu(index, "k");
+        small({B, T, Hq, Hkv, pages, page, most});
+        s.B = static_cast<int>(B);
+        s.T = static_cast<int>(T);
+        s.Hq = static_cast<int>(Hq);
+        s.Hkv = static_cast<int>(Hkv);
+        s.D = static_cast<int>(D);
+        s.interleaved = a[10] == Py_True;
+        s.num_pages = static_cast<int>(pages);
+        s.page_size = static_cast<int>(page);
+        s.max_pages = static_cast<int>(most);
+        if (!fn.append) return NOT_BOUND;
+        const mtp_stream_t stream = stream_of(a[16]);
+        const auto f = fn.append;
+        return call([&] { return f(&s, stream); });
+    });
+}
+
+// adjust_logits(logits, history, history_len, prompt_len, tokens, parents,
+//   n_nodes, repetition, frequency, presence, bias_ids, bias, mask, out, row_flags, stream)
+PyObject *adjust_logits(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count(n, 16)) return nullptr;
+    return guarded([&]() -> long {
+        const at::Tensor &z = tensor(a[0], "logits");
+        dims(z, "logits", 3);
+        mtp_adjust_args s = {};
+        const int64_t B = z.size(0), S = z.size(1), V = z.size(2);
+        s.dtype = dtype_code(z);
+        if (S < 1 || S > MTP_MAX_NODES)
+            value_error("1 to " + std::to_string(MTP_MAX_NODES) + " rows of a sequence, got " + std::to_string(S));
+        const int index = index_of(z);
+        s.out = whole(a[13], "out.logits", z.scalar_type(), {B, S, V}, index);
+        s.row_flags = static_cast<int32_t *>(whole_or_null(a[14], "out.row_flags", at::kInt, {B}, index));
+        s.logits = whole(a[0], "logits", z.scalar_type(), {B, S, V}, index);
+        int64_t L = 0;
+        if (a[1] != Py_None) {
+            const at::Tensor &h = tensor(a[1], "history");
+            dims(h, "history", 2);
+            L = h.size(1);
+            s.history = static_cast<int32_t *>(whole(a[1], "history", at::kInt, {B, L}, index));
+            s.history_len = static_cast<int32_t *>(whole(a[2], "history_len", at::kInt, {B}, index));
+            s.prompt_len = static_cast<int32_t *>(whole_or_null(a[3], "prompt_len", at::kInt, {B}, index));
+        } else if (a[2] != Py_None || a[3] != Py_None) {
+            value_error("history_len and prompt_len are of no use without history");
+        }
+        s.tokens = static_cast<int32_t *>(whole_or_null(a[4], "tokens", at::kInt, {B, S}, index));
+        s.parents = static_cast<int32_t *>(whole_or_null(a[5], "parents", at::kInt, {B, S}, index));
+        if (s.parents && !s.tokens) value_error("parents are of no use without tokens");
+        s.n_nodes = static_cast<int32_t *>(whole_or_null(a[6], "n_nodes", at::kInt, {B}, index));
+        s.repetition = static_cast<float *>(whole_or_null(a[7], "repetition", at::kFloat, {B}, index));
+        s.frequency = static_cast<float *>(whole_or_null(a[8], "frequency", at::kFloat, {B}, index));
+        s.presence = static_cast<float *>(whole_or_null(a[9], "presence", at::kFloat, {B}, index));
+        if ((a[10] == Py_None) != (a[11] == Py_None)) value_error("bias_ids and bias are of no use without each other");
+        int64_t biases = 0;
+        if (a[10] != Py_None) {
+            const at::Tensor &ids = tensor(a[10], "bias_ids");
+            dims(ids, "bias_ids", 2);
+            biases = ids.size(1);
+            if (biases > MTP_MAX_BIAS) value_error("at most " + std::to_string(MTP_MAX_BIAS) + " biases, got " + std::to_string(biases));
+            s.bias_ids = static_cast<int32_t *>(whole(a[10], "bias_ids", at::kInt, {B, biases}, index));
+            s.bias = static_cast<float *>(whole(a[11], "bias", at::kFloat, {B, biases}, index));
+        }
+        if (a[12] != Py_None) {
+            const at::Tensor &m = tensor(a[12], "mask");
+            s.mask = static_cast<int32_t *>(strided(m, "mask", at::kInt, {B, S, (V + 31) / 32}, index, s.mask_stride));
+        }
+        on_gpu(index, "logits");
+        if (B > 65535) value_error("at most 65535 sequences, got " + std::to_string(B));
+        if (V < 1 || V > (1 << 24)) value_error("a vocabulary has 1 to 2^24 entries, got " + std::to_string(V));
+        if (L > (1 << 28)) value_error("a history has at most 2^28 tokens, got " + std::to_string(L));
+        s.B = static_cast<int>(B);
+        s.S = static_cast<int>(S);
+        s.V = static_cast<int>(V);
+        s.L = static_cast<int>(L);
+        s.n_bias = static_cast<int>(biases);
+        if (!fn.adjust) return NOT_BOUND;
+        const mtp_stream_t stream = stream_of(a[15]);
+        const auto f = fn.adjust;
+        return call([&] { return f(&s, stream); });
+    });
+}
+
+// bind(addresses of the functions, in the order of Functions)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!count(n, 6)) return nullptr;
-    void *p[6];
-    for (int i = 0; i < 6; ++i) {
+    constexpr int N = 9;
+    if (!count(n, N)) return nullptr;
+    void *p[N];
+    for (int i = 0; i < N; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -369,6 +573,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     fn.select_ws = reinterpret_cast<decltype(fn.select_ws)>(p[3]);
     fn.reorder = reinterpret_cast<decltype(fn.reorder)>(p[4]);
     fn.commit = reinterpret_cast<decltype(fn.commit)>(p[5]);
+    fn.rope = reinterpret_cast<decltype(fn.rope)>(p[6]);
+    fn.append = reinterpret_cast<decltype(fn.append)>(p[7]);
+    fn.adjust = reinterpret_cast<decltype(fn.adjust)>(p[8]);
     Py_RETURN_NONE;
 }
 
@@ -377,6 +584,9 @@ PyMethodDef methods[] = {
     {"beam_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_select)), METH_FASTCALL, nullptr},
     {"beam_reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_reorder)), METH_FASTCALL, nullptr},
     {"tree_commit", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_commit)), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
+    {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
+    {"adjust_logits", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adjust_logits)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

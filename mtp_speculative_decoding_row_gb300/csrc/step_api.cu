@@ -1,0 +1,260 @@
+// step_api.cu -- the C ABI of the rotary positions, the cache append and the
+// adjustment of logits (include/mtp_rs.h): argument validation and launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "launch.h"
+#include "mtp_rs.h"
+#include "step.h"
+
+namespace {
+
+using namespace mtp;
+
+// A tensor [n0, n1, n2, row] of `row` contiguous bytes: its byte strides (of a
+// dimension of one: 0, it says nothing) and the memory between its first and
+// last byte.
+struct Span {
+    uintptr_t lo = 0, hi = 0;
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+};
+struct Rows {
+    Span span;
+    bool gaps = true;  // no stride of 0: no two indices are one place
+    uintptr_t low = 0; // the bits of the address and the strides
+    // False for a stride or a tensor that no memory has (|stride| < 2^40 elements
+    // times the dimension within 2^62 bytes).
+    bool set(const void *p, const int64_t *stride, const int (&n)[3], long long row, int es, long long *out) {
+        span.lo = reinterpret_cast<uintptr_t>(p);
+        unsigned long long reach = 0;
+        low = span.lo;
+        for (int i = 0; i < 3; ++i) {
+            out[i] = 0;
+            if (n[i] <= 1) continue;
+            if (stride[i] < 0 || stride[i] >= (1ll << 40)) return false;
+            out[i] = stride[i] * es;
+            if (out[i] == 0) gaps = false;
+            low |= static_cast<uintptr_t>(out[i]);
+            const unsigned long long far = static_cast<unsigned long long>(out[i]) * (n[i] - 1);
+            if (out[i] > 0 && far / out[i] != static_cast<unsigned long long>(n[i] - 1)) return false;
+            reach += far;
+            if (far >= (1ull << 61) || reach >= (1ull << 61)) return false;
+        }
+        span.hi = span.lo + reach + row;
+        return true;
+    }
+};
+
+bool same(const long long (&a)[3], const long long (&b)[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
+
+// `out` of a tensor `in`, of the same shape: in place, or apart from it and
+// from `other` (the call's second input, which may lie between the rows of an
+// output that is in place).
+bool out_of(const Rows &out, const long long (&os)[3], const Rows &in, const long long (&is)[3], const Rows *other) {
+    if (!out.gaps) return false;
+    if (out.span.lo == in.span.lo && same(os, is)) return true;
+    return !out.span.meets(in.span) && !(other && out.span.meets(other->span));
+}
+
+Span ints(const int32_t *p, long long n) {
+    Span s;
+    s.lo = reinterpret_cast<uintptr_t>(p);
+    s.hi = p ? s.lo + static_cast<uintptr_t>(n) * 4 : s.lo;
+    return s;
+}
+
+constexpr int kMostHeads = 65536;
+
+int rot_launch(RotArgs &A, int dtype, uintptr_t low, bool interleaved, bool append, mtp_stream_t stream) {
+    int dev, sms;
+    if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
+    const int es = dtype == MTP_DTYPE_F32 ? 4 : 2, width = 16 / es;
+    const bool vec = low % 16 == 0 && A.n % width == 0 && A.D % width == 0;
+    const int piece = vec ? width : 1;
+    A.rot_units = A.n / piece;
+    A.units = A.rot_units + (A.D - 2 * A.n) / piece;
+    // Tokens of a block: one while the blocks fit the GPU at once, more where
+    // there are many, so that a block's angles and its start are shared.
+    const long long all = static_cast<long long>(A.B) * A.T, fit = static_cast<long long>(sms) * 8;
+    A.tokens = all <= fit ? 1 : all <= 4 * fit ? 2 : 4;
+    if (A.tokens > A.T) A.tokens = A.T;
+    A.chunks = (A.T + A.tokens - 1) / A.tokens;
+    const long long blocks = static_cast<long long>(A.B) * A.chunks;
+    if (blocks > 0x7fffffffll) return MTP_ERR_INVALID_ARG;
+    return launch(rot_func(dtype, vec, interleaved, append), dim3(static_cast<unsigned>(blocks)), ROT_THREADS, rot_smem(A), &A, stream);
+}
+
+bool aligned(const Rows &r, int es) { return r.span.lo % es == 0; }
+
+}  // namespace
+
+extern "C" int mtp_rope(const mtp_rope_args *args, mtp_stream_t stream) {
+    if (!args) return MTP_ERR_INVALID_ARG;
+    const mtp_rope_args &a = *args;
+    if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
+    if (a.B < 0 || a.T < 0 || a.Hq < 0 || a.Hkv < 0 || a.Hq > kMostHeads || a.Hkv > kMostHeads || a.D < 1 || a.D > 256 || a.pairs < 0 ||
+        2 * static_cast<long long>(a.pairs) > a.D || !(a.factor - a.factor == 0.f))
+        return MTP_ERR_INVALID_ARG;
+    if (a.B == 0 || a.T == 0 || (a.Hq == 0 && a.Hkv == 0)) return MTP_OK;
+    if ((a.Hq > 0 && (!a.q || !a.q_out)) || (a.Hkv > 0 && (!a.k || !a.k_out)) || !a.positions || (a.pairs > 0 && !a.inv_freq))
+        return MTP_ERR_INVALID_ARG;
+    const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
+    const long long row = static_cast<long long>(a.D) * es;
+    RotArgs A = {};
+    const int nq[3] = {a.B, a.T, a.Hq}, nk[3] = {a.B, a.T, a.Hkv};
+    Rows q, k, qo, ko;
+    uintptr_t low = 0;
+    if (a.Hq > 0) {
+        if (!q.set(a.q, a.q_stride, nq, row, es, A.qs) || !qo.set(a.q_out, a.q_out_stride, nq, row, es, A.qos)) return MTP_ERR_INVALID_ARG;
+        low |= q.low | qo.low;
+    }
+    if (a.Hkv > 0) {
+        if (!k.set(a.k, a.k_stride, nk, row, es, A.ks) || !ko.set(a.k_out, a.k_out_stride, nk, row, es, A.kos)) return MTP_ERR_INVALID_ARG;
+        low |= k.low | ko.low;
+    }
+    if ((a.Hq > 0 && !out_of(qo, A.qos, q, A.qs, a.Hkv > 0 ? &k : nullptr)) || (a.Hkv > 0 && !out_of(ko, A.kos, k, A.ks, a.Hq > 0 ? &q : nullptr)))
+        return MTP_ERR_INVALID_ARG;
+    if (low % es != 0) return MTP_ERR_MISALIGNED;
+    A.q = static_cast<const unsigned char *>(a.q);
+    A.k = static_cast<const unsigned char *>(a.k);
+    A.q_out = static_cast<unsigned char *>(a.q_out);
+    A.k_out = static_cast<unsigned char *>(a.k_out);
+    A.pos = a.positions;
+    A.ps[0] = a.B > 1 ? a.pos_stride[0] : 0;
+    A.ps[1] = a.T > 1 ? a.pos_stride[1] : 0;
+    A.inv_freq = a.inv_freq;
+    A.B = a.B;
+    A.T = a.T;
+    A.D = a.D;
+    A.n = a.pairs;
+    A.hq = a.Hq;
+    A.hk = a.Hkv;
+    A.factor = a.factor;
+    A.sign = a.inverse ? -1.f : 1.f;
+    return rot_launch(A, a.dtype, low, a.interleaved != 0, false, stream);
+}
+
+extern "C" int mtp_cache_append(const mtp_cache_append_args *args, mtp_stream_t stream) {
+    if (!args) return MTP_ERR_INVALID_ARG;
+    const mtp_cache_append_args &a = *args;
+    if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
+    if (a.B < 0 || a.T < 1 || a.Hq < 0 || a.Hkv < 1 || a.Hq > kMostHeads || a.Hkv > kMostHeads || a.D < 1 || a.D > 256 || a.pairs < 0 ||
+        2 * static_cast<long long>(a.pairs) > a.D || !(a.factor - a.factor == 0.f) || a.num_pages < 1 || a.page_size < 1 || a.max_pages < 1 ||
+        static_cast<long long>(a.max_pages) * a.page_size > 0x7fff0000ll)
+        return MTP_ERR_INVALID_ARG;
+    if (a.B == 0) return MTP_OK;
+    if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.page_table || !a.cache_len || !a.new_len || (a.Hq > 0 && (!a.q || !a.q_out)) ||
+        (a.pairs > 0 && !a.inv_freq))
+        return MTP_ERR_INVALID_ARG;
+    const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
+    const long long row = static_cast<long long>(a.D) * es;
+    RotArgs A = {};
+    const int nq[3] = {a.B, a.T, a.Hq}, nk[3] = {a.B, a.T, a.Hkv}, nc[3] = {a.num_pages, a.page_size, a.Hkv};
+    Rows q, k, v, qo, ko, kc, vc;
+    if (!k.set(a.k, a.k_stride, nk, row, es, A.ks) || !v.set(a.v, a.v_stride, nk, row, es, A.vs) ||
+        !kc.set(a.k_cache, a.k_cache_stride, nc, row, es, A.kcs) || !vc.set(a.v_cache, a.v_cache_stride, nc, row, es, A.vcs))
+        return MTP_ERR_INVALID_ARG;
+    uintptr_t low = k.low | v.low | kc.low | vc.low;
+    if (!kc.gaps || !vc.gaps || kc.span.meets(k.span) || kc.span.meets(v.span) || vc.span.meets(k.span) || vc.span.meets(v.span))
+        return MTP_ERR_INVALID_ARG;
+    if (a.Hq > 0) {
+        if (!q.set(a.q, a.q_stride, nq, row, es, A.qs) || !qo.set(a.q_out, a.q_out_stride, nq, row, es, A.qos)) return MTP_ERR_INVALID_ARG;
+        low |= q.low | qo.low;
+        if (!out_of(qo, A.qos, q, A.qs, &k) || kc.span.meets(q.span) || vc.span.meets(q.span) || kc.span.meets(qo.span) || vc.span.meets(qo.span))
+            return MTP_ERR_INVALID_ARG;
+        if (qo.span.lo != q.span.lo && qo.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
+    }
+    if (a.k_out) {
+        if (!ko.set(a.k_out, a.k_out_stride, nk, row, es, A.kos)) return MTP_ERR_INVALID_ARG;
+        low |= ko.low;
+        if (!out_of(ko, A.kos, k, A.ks, a.Hq > 0 ? &q : nullptr) || kc.span.meets(ko.span) || vc.span.meets(ko.span)) return MTP_ERR_INVALID_ARG;
+        if (ko.span.lo != k.span.lo && ko.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
+    }
+    if (low % es != 0) return MTP_ERR_MISALIGNED;
+    // every block of a sequence reads its lengths and pages, one writes the outputs
+    const Span in[] = {ints(a.cache_len, a.B), ints(a.n_new, a.B), ints(a.page_table, static_cast<long long>(a.B) * a.max_pages)};
+    for (const Span &o : {ints(a.new_len, a.B), ints(a.row_flags, a.B)})
+        for (const Span &i : in)
+            if (o.meets(i)) return MTP_ERR_INVALID_ARG;
+    A.q = static_cast<const unsigned char *>(a.q);
+    A.k = static_cast<const unsigned char *>(a.k);
+    A.v = static_cast<const unsigned char *>(a.v);
+    A.q_out = static_cast<unsigned char *>(a.q_out);
+    A.k_out = static_cast<unsigned char *>(a.k_out);
+    A.k_cache = static_cast<unsigned char *>(a.k_cache);
+    A.v_cache = static_cast<unsigned char *>(a.v_cache);
+    A.pos = a.positions;
+    A.ps[0] = a.B > 1 ? a.pos_stride[0] : 0;
+    A.ps[1] = a.T > 1 ? a.pos_stride[1] : 0;
+    A.inv_freq = a.inv_freq;
+    A.table = a.page_table;
+    A.len = a.cache_len;
+    A.count = a.n_new;
+    A.new_len = a.new_len;
+    A.flags = a.row_flags;
+    A.B = a.B;
+    A.T = a.T;
+    A.D = a.D;
+    A.n = a.pairs;
+    A.hq = a.Hq;
+    A.hk = a.Hkv;
+    A.hv = a.Hkv;
+    A.num_pages = a.num_pages;
+    A.page_size = a.page_size;
+    A.max_pages = a.max_pages;
+    A.factor = a.factor;
+    A.sign = 1.f;
+    return rot_launch(A, a.dtype, low, a.interleaved != 0, true, stream);
+}
+
+extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t stream) {
+    if (!args) return MTP_ERR_INVALID_ARG;
+    const mtp_adjust_args &a = *args;
+    if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
+    if (a.B < 0 || a.B > 65535 || a.S < 1 || a.S > MTP_MAX_NODES || a.V < 1 || a.V > (1 << 24) || a.L < 0 || a.L > (1 << 28) || a.n_bias < 0 ||
+        a.n_bias > MTP_MAX_BIAS)
+        return MTP_ERR_INVALID_ARG;
+    if (a.B == 0) return MTP_OK;
+    if (!a.logits || !a.out || (a.L > 0 && (!a.history || !a.history_len)) || (a.prompt_len && !a.history_len) || (a.parents && !a.tokens) ||
+        (a.n_bias > 0 && (!a.bias_ids || !a.bias)))
+        return MTP_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.out)) % 16 != 0) return MTP_ERR_MISALIGNED;
+    const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
+    const uintptr_t z = reinterpret_cast<uintptr_t>(a.logits), o = reinterpret_cast<uintptr_t>(a.out);
+    const uintptr_t bytes = static_cast<uintptr_t>(a.B) * a.S * a.V * es;
+    if (z != o && z < o + bytes && o < z + bytes) return MTP_ERR_INVALID_ARG;
+    if (a.mask && (a.mask_stride[0] < 0 || a.mask_stride[1] < 0)) return MTP_ERR_INVALID_ARG;
+    int dev, sms;
+    if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
+    AdjArgs A = {};
+    A.z = static_cast<const unsigned char *>(a.logits);
+    A.out = static_cast<unsigned char *>(a.out);
+    A.L = a.history ? a.L : 0;
+    A.history = a.history;
+    A.len = a.history_len;
+    A.prompt = a.prompt_len;
+    A.tokens = a.tokens;
+    A.parents = a.parents;
+    A.nodes = a.n_nodes;
+    A.rho = a.repetition;
+    A.freq = a.frequency;
+    A.pres = a.presence;
+    A.bias_ids = a.bias_ids;
+    A.bias = a.bias;
+    A.n_bias = a.n_bias;
+    A.mask = reinterpret_cast<const uint32_t *>(a.mask);
+    A.mask_s[0] = a.B > 1 ? a.mask_stride[0] : 0;
+    A.mask_s[1] = a.S > 1 ? a.mask_stride[1] : 0;
+    A.flags = a.row_flags;
+    A.B = a.B;
+    A.S = a.S;
+    A.V = a.V;
+    A.vec_history = reinterpret_cast<uintptr_t>(a.history) % 16 == 0 && a.L % 4 == 0;
+    // Slices as large as leaves two blocks for every SM: each reads the text.
+    A.slice = 8192;
+    while (A.slice > 1024 && static_cast<long long>(a.B) * ((a.V + A.slice - 1) / A.slice) < 2 * sms) A.slice /= 2;
+    A.rows = a.S;
+    const dim3 grid((a.V + A.slice - 1) / A.slice, a.B, (a.S + A.rows - 1) / A.rows);
+    return launch(adj_func(a.dtype), grid, ADJ_THREADS, adj_smem(A.slice, A.n_bias), &A, stream);
+}

@@ -69,14 +69,14 @@ def _bind(lib) -> None:
     import ctypes
 
     names = ("mtp_tree_attention", "mtp_tree_attention_workspace", "mtp_beam_select", "mtp_beam_select_workspace",
-             "mtp_beam_reorder", "mtp_tree_commit")
+             "mtp_beam_reorder", "mtp_tree_commit", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits")
     _binding().bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
 
 
 def unbind() -> None:
     """Another library was loaded: the next call looks its functions up."""
     if _native is not None:
-        _native.bind(0, 0, 0, 0, 0, 0)
+        _native.bind(*[0] * 9)
 
 
 def _call(name, args):
