@@ -597,8 +597,8 @@ int mtp_cache_append(const mtp_cache_append_args *args, mtp_stream_t stream);
  *   x = x + the sum of bias[b, j] over bias_ids[b, j] = v
  *   out[b, s, v] = -inf where bit v % 32 of mask[b, s, v / 32] is 0, else x,
  * in float32, rounded once to the logits' type.  Row s holds the logits after
- * node s: node 0 is the last token of the text (which `history` may leave out
- * or tokens hold as -1), parents as for mtp_tree_attention (NULL: a chain).
+ * node s: node 0 is the last token of the text (in `history`, tokens then hold -1
+ * for it, or in tokens alone: in both it counts twice), parents as for mtp_tree_attention (NULL: a chain).
  * Token ids below 0 are empty places, in history, tokens and bias_ids alike.
  * NULL means: no history (L = 0), no prompt (0), no tokens, repetition 1,
  * frequency and presence 0, no mask (everything allowed).  A row whose mask
@@ -615,7 +615,7 @@ int mtp_cache_append(const mtp_cache_append_args *args, mtp_stream_t stream);
  *   parents [B, S] int32, bias_ids int32 and bias float32 [B, n_bias], mask
  *   rows of ceil(V / 32) words with strides in words (0: shared)
  *   row_flags [B] or NULL.
- * Requirements: S <= MTP_MAX_NODES, V <= 2^24, L <= 2^28, B <= 65535, n_bias <=
+ * Requirements: S <= MTP_MAX_NODES, V <= 2^24, L <= 2^28, B <= 2^20, n_bias <=
  * MTP_MAX_BIAS (else MTP_ERR_INVALID_ARG).
  */
 typedef struct mtp_adjust_args {

@@ -8,13 +8,16 @@
 //   x = x - freq c - pres [c > 0] + sum of v's biases
 //   x = -inf                      where the mask has no bit.
 //
-// One pass: memory bounds it, every logit is read and written once.  A block has
-// a slice of the vocabulary and some rows of one sequence.  It counts the
-// slice's tokens of the text in shared memory (integers: the order of the atomic
-// additions changes nothing), with one bit for each entry that needs more than
-// its mask, and then streams the rows: a vector whose bits are clear is copied.
-// Rows differ in their paths only; the few tokens of the drafts are looked up
-// in the path's list where they occur, so that the counts serve all rows.
+// Memory bounds it: every logit is read and written once.  A block has a slice
+// of the vocabulary and some rows of one sequence.  It streams the rows through
+// their masks, counts the slice's tokens of the text in shared memory (integers:
+// the order of the atomic additions changes nothing), lists the entries that
+// anything but the mask changes, and writes those once more, a thread to an
+// entry.  A text's words crowd in few places: dealt out from a list they keep
+// all threads busy, where looking for them beside the streamed vectors left one
+// block with nearly all the work (64 x 4 rows, 8192 tokens: 118 us).  Rows
+// differ in their paths only; the few drafted tokens are looked up in the path
+// where they occur, so that one count serves all rows.
 #include "common.cuh"
 #include "step.h"
 
@@ -60,35 +63,36 @@ struct Shared {
     uint64_t path[ADJ_MAX_ROWS];  // nodes on the way to a node, itself included
     int above[ADJ_MAX_ROWS];
     int biases;                   // of this slice
+    int listed;
     int flag;
 };
 
-// Bits v .. v + 31 of a row of words that are zero from word `n` on.
-__device__ __forceinline__ uint32_t bits_at(const uint32_t *w, int v, int n) {
-    const int i = v >> 5, r = v & 31;
-    const uint32_t lo = w[i];
-    if (r == 0) return lo;
-    return __funnelshift_r(lo, i + 1 < n ? w[i + 1] : 0u, r);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArgs A) {
-    constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES, AHEAD = 4;
+    constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES, AHEAD = 4, EARLY = 2, ROWS = 4;
+    constexpr uint32_t ALL = (1u << VEC) - 1u;
     extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t *table = smem;                   // [slice]
-    uint32_t *touched = table + A.slice;      // [slice / 32] bits: look at the entry
-    int *bias_id = reinterpret_cast<int *>(touched + A.slice / 32);     // [n_bias] of this slice, in their order
-    float *bias_sum = reinterpret_cast<float *>(bias_id + A.n_bias);    // [n_bias] sum of all biases of the id
+    uint32_t *table = smem;                                             // [slice]
+    uint16_t *list = reinterpret_cast<uint16_t *>(table + A.slice);     // [slice] entries that are not 0
+    int *bias_id = reinterpret_cast<int *>(list + A.slice);             // [n_bias] of this slice, in their order
+    float *bias_of = reinterpret_cast<float *>(bias_id + A.n_bias);     // [n_bias]
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.y, s0 = blockIdx.z * A.rows;
-    const int lo = blockIdx.x * A.slice, hi = min(A.V, lo + A.slice);  // this block's tokens
-    if (tid == 0) sh.flag = 0;
-    for (int i = tid; i < (A.slice + A.slice / 32) / 4; i += NT) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int b = blockIdx.x, s0 = blockIdx.z * A.rows;
+    const int lo = blockIdx.y * A.slice, hi = min(A.V, lo + A.slice);  // this block's tokens
+    if (tid == 0) sh.flag = sh.listed = 0;
+    for (int i = tid; i < A.slice / 4; i += NT) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- what the sequence has; every block finds the same flag ----
+    const int32_t *text = A.history + static_cast<size_t>(b) * A.L;
+    int4 early[EARLY];  // the text's first tokens are on their way while the rows go by
+#pragma unroll
+    for (int e = 0; e < EARLY; ++e) {
+        const int i = tid + e * NT;
+        early[e] = A.vec_history && 4 * i < A.L ? __ldg(reinterpret_cast<const int4 *>(text) + i) : make_int4(-1, -1, -1, -1);
+    }
     int flag = 0;
     int n = A.nodes ? __ldg(A.nodes + b) : A.S, len = A.len ? __ldg(A.len + b) : 0, prompt = A.prompt ? __ldg(A.prompt + b) : 0;
     if (n < 0 || n > A.S) {
@@ -102,6 +106,64 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
     if (prompt < 0 || prompt > len) flag |= F_BAD_ID;
     const float rho = A.rho ? __ldg(A.rho + b) : 1.f, freq = A.freq ? __ldg(A.freq + b) : 0.f, pres = A.pres ? __ldg(A.pres + b) : 0.f;
     if (!(rho > 0.f && rho < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) flag |= F_NONFINITE;
+    const int s1 = min(n, s0 + A.rows);
+
+    // ---- the rows through their masks ----
+    const int words = (A.V + 31) / 32;
+    const bool in_place = A.out == A.z;
+    auto mask_of = [&](int s) { return A.mask ? A.mask + b * A.mask_s[0] + s * A.mask_s[1] : nullptr; };
+    auto allowed = [&](const uint32_t *mask, int v) {  // bits of entries v, v + 1, .. v + VEC - 1
+        if (!mask) return ~0u;
+        const int i = v >> 5, r = v & 31;
+        const uint32_t w = __ldg(mask + i);
+        return r + VEC <= 32 ? w >> r : __funnelshift_r(w, i + 1 < words ? __ldg(mask + i + 1) : 0u, r);
+    };
+    auto row_of = [&](int s) { return (static_cast<size_t>(b) * A.S + s) * A.V; };
+    if (!in_place || A.mask) {
+        for (int s = s0; s < s1; ++s) {
+            const size_t row = row_of(s);
+            const unsigned char *z = A.z + row * ES;
+            unsigned char *out = A.out + row * ES;
+            const uint32_t *mask = mask_of(s);
+            // vectors of the row that lie in the slice, wherever the row starts
+            const int first = min(hi, lo + static_cast<int>((VEC - (row + lo) % VEC) % VEC)), vecs = (hi - first) / VEC;
+            for (int i0 = tid; i0 < vecs; i0 += NT * AHEAD) {
+                uint4 x[AHEAD];
+                uint32_t may[AHEAD];
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int i = i0 + a * NT;
+                    if (i >= vecs) break;
+                    x[a] = *reinterpret_cast<const uint4 *>(z + static_cast<size_t>(first + i * VEC) * ES);
+                    may[a] = allowed(mask, first + i * VEC) & ALL;
+                }
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int i = i0 + a * NT;
+                    if (i >= vecs) break;
+                    if (may[a] != ALL) {
+                        float y[VEC];
+                        Store<T>::unpack(x[a], y);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (!((may[a] >> e) & 1u)) y[e] = -INFINITY;
+                        x[a] = pack<T>(y);
+                    } else if (in_place) {
+                        continue;
+                    }
+                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(first + i * VEC) * ES) = x[a];
+                }
+            }
+            // the entries before the first vector and behind the last
+            const int head = first - lo, tail = hi - first - vecs * VEC;
+            if (tid < head + tail) {
+                const int v = tid < head ? lo + tid : hi - tail + (tid - head);
+                store1<T>(out + static_cast<size_t>(v) * ES, allowed(mask, v) & 1u ? load1<T>(z + static_cast<size_t>(v) * ES) : -INFINITY);
+            }
+        }
+    }
+
+    // ---- the tree ----
     if (A.tokens && tid < 32) {
         for (int i = lane; i < A.S; i += 32) {
             const int t = i < n ? __ldg(A.tokens + static_cast<size_t>(b) * A.S + i) : -1;
@@ -141,166 +203,109 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
             __syncwarp();
         }
     }
-    __syncthreads();  // the table is clear
+    __syncthreads();  // the table is clear, the tokens are there
 
-    auto touch = [&](int i, uint32_t add) {
-        atomicAdd(table + i, add);
-        atomicOr(touched + (i >> 5), 1u << (i & 31));
-    };
-    // ---- the text ----
+    // ---- the text, drafted tokens, biases ----
     {
-        const int32_t *text = A.history + static_cast<size_t>(b) * A.L;
         auto see = [&](int id, int at) {
+            if (at >= len) return;
             if (id >= A.V) flag |= F_BAD_ID;
-            if (id >= lo && id < hi) {
-                if (at < prompt) {
-                    atomicOr(table + (id - lo), PROMPT);
-                    atomicOr(touched + ((id - lo) >> 5), 1u << ((id - lo) & 31));
-                } else {
-                    touch(id - lo, ONE);
-                }
-            }
+            if (id < lo || id >= hi) return;
+            if (at < prompt)
+                atomicOr(table + (id - lo), PROMPT);
+            else
+                atomicAdd(table + (id - lo), ONE);
         };
-        int done = 0;
+        auto four = [&](const int4 &x, int at) {
+            see(x.x, at);
+            see(x.y, at + 1);
+            see(x.z, at + 2);
+            see(x.w, at + 3);
+        };
         if (A.vec_history) {
-            const int vecs = len / 4;
+#pragma unroll
+            for (int e = 0; e < EARLY; ++e) four(early[e], 4 * (tid + e * NT));
 #pragma unroll 4
-            for (int i = tid; i < vecs; i += NT) {
-                const int4 x = __ldg(reinterpret_cast<const int4 *>(text) + i);
-                see(x.x, 4 * i);
-                see(x.y, 4 * i + 1);
-                see(x.z, 4 * i + 2);
-                see(x.w, 4 * i + 3);
-            }
-            done = 4 * vecs;
+            for (int i = tid + EARLY * NT; 4 * i < len; i += NT) four(__ldg(reinterpret_cast<const int4 *>(text) + i), 4 * i);
+        } else {
+#pragma unroll 4
+            for (int i = tid; i < len; i += NT) see(__ldg(text + i), i);
         }
-#pragma unroll 4
-        for (int i = done + tid; i < len; i += NT) see(__ldg(text + i), i);
     }
-    // ---- drafted tokens, biases ----
     if (A.tokens && tid < n) {
         const int id = sh.token[tid];
-        if (id >= lo && id < hi) {
-            atomicOr(table + (id - lo), DRAFT);
-            atomicOr(touched + ((id - lo) >> 5), 1u << ((id - lo) & 31));
-        }
+        if (id >= lo && id < hi) atomicOr(table + (id - lo), DRAFT);
     }
-    if (A.n_bias > 0) {
+    if (A.n_bias > 0 && tid < 32) {  // in their order, so that a sum of several has one value
         const int32_t *ids = A.bias_ids + static_cast<size_t>(b) * A.n_bias;
         const float *bias = A.bias + static_cast<size_t>(b) * A.n_bias;
-        if (tid < 32) {  // in their order, so that a sum of several has one value
-            int found = 0;
-            for (int i0 = 0; i0 < A.n_bias; i0 += 32) {
-                const int id = i0 + lane < A.n_bias ? __ldg(ids + i0 + lane) : -1;
-                if (id >= A.V) flag |= F_BAD_ID;
-                const bool in = id >= lo && id < hi;
-                const uint32_t who = __ballot_sync(FULL, in);
-                if (in) {
-                    const int at = found + __popc(who & ((1u << lane) - 1u));
-                    bias_id[at] = id;
-                    bias_sum[at] = __ldg(bias + i0 + lane);
-                    atomicOr(table + (id - lo), BIAS);
-                    atomicOr(touched + ((id - lo) >> 5), 1u << ((id - lo) & 31));
-                }
-                found += __popc(who);
+        int found = 0;
+        for (int i0 = 0; i0 < A.n_bias; i0 += 32) {
+            const int id = i0 + lane < A.n_bias ? __ldg(ids + i0 + lane) : -1;
+            if (id >= A.V) flag |= F_BAD_ID;
+            const bool in = id >= lo && id < hi;
+            const uint32_t who = __ballot_sync(FULL, in);
+            if (in) {
+                const int at = found + __popc(who & ((1u << lane) - 1u));
+                bias_id[at] = id;
+                bias_of[at] = __ldg(bias + i0 + lane);
+                atomicOr(table + (id - lo), BIAS);
             }
-            if (lane == 0) sh.biases = found;
+            found += __popc(who);
         }
-        __syncthreads();
-        float sum[ADJ_MAX_BIAS / NT];
-#pragma unroll
-        for (int e = 0; e < ADJ_MAX_BIAS / NT; ++e) {
-            const int j = tid + e * NT;
-            sum[e] = 0.f;
-            if (j < sh.biases)
-                for (int i = 0; i < sh.biases; ++i)
-                    if (bias_id[i] == bias_id[j]) sum[e] += bias_sum[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < ADJ_MAX_BIAS / NT; ++e)
-            if (tid + e * NT < sh.biases) bias_sum[tid + e * NT] = sum[e];
+        if (lane == 0) sh.biases = found;
     }
     if (flag) atomicOr(&sh.flag, flag);
     __syncthreads();
     flag = sh.flag;
-    if (A.flags && tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) A.flags[b] = flag;
+    if (A.flags && tid == 0 && blockIdx.y == 0 && blockIdx.z == 0) A.flags[b] = flag;
+    if (flag) {
+        for (int s = s0; s < s1; ++s)
+            for (int v = lo + tid; v < hi; v += NT) store1<T>(A.out + (row_of(s) + v) * ES, NAN);
+        return;
+    }
 
-    // ---- the rows ----
-    auto adjust = [&](float x, int v, int s) {
-        const uint32_t e = table[v - lo];
-        uint32_t count = e / ONE;
-        if (e & DRAFT)
-            for (int i = 0; i <= s; ++i) count += ((sh.path[s] >> i) & 1ull) && sh.token[i] == v ? 1u : 0u;
-        if (count > 0 || (e & PROMPT)) x = x > 0.f ? __fdiv_rn(x, rho) : x * rho;
-        if (count > 0) x = fmaf(-freq, static_cast<float>(count), x) - pres;
+    // ---- the entries that change ----
+    for (int i0 = tid - lane; i0 < hi - lo; i0 += NT) {
+        const bool on = i0 + lane < hi - lo && table[i0 + lane] != 0u;
+        const uint32_t who = __ballot_sync(FULL, on);
+        int at = 0;
+        if (lane == 0 && who) at = atomicAdd(&sh.listed, __popc(who));
+        at = __shfl_sync(FULL, at, 0);
+        if (on) list[at + __popc(who & ((1u << lane) - 1u))] = static_cast<uint16_t>(i0 + lane);
+    }
+    __syncthreads();
+    const int listed = sh.listed, turns = (s1 - s0 + ROWS - 1) / ROWS;
+    for (int j = tid; j < listed * turns; j += NT) {
+        const int turn = j / listed, at = list[j - turn * listed], v = lo + at, r0 = s0 + turn * ROWS;
+        const uint32_t e = table[at];
+        float x[ROWS];
+        uint32_t may[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (r0 + r >= s1) break;
+            x[r] = load1<T>(A.z + (row_of(r0 + r) + v) * ES);
+            const uint32_t *mask = mask_of(r0 + r);
+            may[r] = mask ? (__ldg(mask + (v >> 5)) >> (v & 31)) & 1u : 1u;
+        }
+        float bias = 0.f;
         if (e & BIAS)
             for (int i = 0; i < sh.biases; ++i)
-                if (bias_id[i] == v) {
-                    x += bias_sum[i];
-                    break;
-                }
-        return x;
-    };
-    const int words = (A.V + 31) / 32;
-    const bool in_place = A.out == A.z;
-    for (int s = s0; s < min(n, s0 + A.rows); ++s) {
-        const size_t row = (static_cast<size_t>(b) * A.S + s) * A.V;
-        const unsigned char *z = A.z + row * ES;
-        unsigned char *out = A.out + row * ES;
-        const uint32_t *mask = A.mask ? A.mask + b * A.mask_s[0] + s * A.mask_s[1] : nullptr;
-        auto allowed = [&](int v) {  // bits of entries v, v + 1, ..
-            if (!mask) return ~0u;
-            const int i = v >> 5, r = v & 31;
-            const uint32_t w = __ldg(mask + i);
-            return r + VEC <= 32 ? w >> r : __funnelshift_r(w, i + 1 < words ? __ldg(mask + i + 1) : 0u, r);
-        };
-        // vectors of the row that lie in the slice, wherever the row starts
-        const int first = min(hi, lo + static_cast<int>((VEC - (row + lo) % VEC) % VEC)), vecs = (hi - first) / VEC;
-        constexpr uint32_t ALL = (1u << VEC) - 1u;
-        for (int i0 = tid; i0 < vecs; i0 += NT * AHEAD) {
-            uint4 x[AHEAD];
-            uint32_t may[AHEAD];
+                if (bias_id[i] == v) bias += bias_of[i];
 #pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int i = i0 + a * NT;
-                if (i >= vecs) break;
-                x[a] = *reinterpret_cast<const uint4 *>(z + static_cast<size_t>(first + i * VEC) * ES);
-                may[a] = allowed(first + i * VEC) & ALL;
+        for (int r = 0; r < ROWS; ++r) {
+            const int s = r0 + r;
+            if (s >= s1) break;
+            uint32_t count = e / ONE;
+            if (e & DRAFT) {
+                const uint64_t path = sh.path[s];
+                for (int i = 0; i <= s; ++i) count += ((path >> i) & 1ull) && sh.token[i] == v ? 1u : 0u;
             }
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int i = i0 + a * NT, v = first + i * VEC;
-                if (i >= vecs) break;
-                const uint32_t look = bits_at(touched, v - lo, A.slice / 32) & ALL;
-                if (flag) {
-                    float y[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) y[e] = NAN;
-                    x[a] = pack<T>(y);
-                } else if (look || may[a] != ALL) {
-                    float y[VEC];
-                    Store<T>::unpack(x[a], y);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        if ((look >> e) & 1u) y[e] = adjust(y[e], v + e, s);
-                        if (!((may[a] >> e) & 1u)) y[e] = -INFINITY;
-                    }
-                    x[a] = pack<T>(y);
-                } else if (in_place) {
-                    continue;
-                }
-                *reinterpret_cast<uint4 *>(out + static_cast<size_t>(v) * ES) = x[a];
-            }
-        }
-        // the entries before the first vector and behind the last
-        const int head = first - lo, tail = hi - first - vecs * VEC;
-        if (tid < head + tail) {
-            const int v = tid < head ? lo + tid : hi - tail + (tid - head);
-            float y = load1<T>(z + static_cast<size_t>(v) * ES);
-            if ((touched[(v - lo) >> 5] >> (v & 31)) & 1u) y = adjust(y, v, s);
-            if (!(allowed(v) & 1u)) y = -INFINITY;
-            store1<T>(out + static_cast<size_t>(v) * ES, flag ? NAN : y);
+            float y = x[r];
+            if (count > 0 || (e & PROMPT)) y = y > 0.f ? __fdiv_rn(y, rho) : y * rho;
+            if (count > 0) y = fmaf(-freq, static_cast<float>(count), y) - pres;
+            if (e & BIAS) y += bias;
+            if (may[r]) store1<T>(A.out + (row_of(s) + v) * ES, y);
         }
     }
 }
@@ -311,6 +316,6 @@ const void *adj_func(int dtype) {
     return dtype == 0 ? reinterpret_cast<const void *>(adjust_impl<float>) : reinterpret_cast<const void *>(adjust_impl<bf16_t>);
 }
 
-uint32_t adj_smem(int slice, int n_bias) { return static_cast<uint32_t>(slice) * 4 + slice / 8 + n_bias * 8; }
+uint32_t adj_smem(int slice, int n_bias) { return static_cast<uint32_t>(slice) * 6 + n_bias * 8; }
 
 }  // namespace mtp

@@ -543,7 +543,7 @@ PyObject *adjust_logits(PyObject *, PyObject *const *a, Py_ssize_t n) {
             s.mask = static_cast<int32_t *>(strided(m, "mask", at::kInt, {B, S, (V + 31) / 32}, index, s.mask_stride));
         }
         on_gpu(index, "logits");
-        if (B > 65535) value_error("at most 65535 sequences, got " + std::to_string(B));
+        if (B > (1 << 20)) value_error("at most 2^20 sequences, got " + std::to_string(B));
         if (V < 1 || V > (1 << 24)) value_error("a vocabulary has 1 to 2^24 entries, got " + std::to_string(V));
         if (L > (1 << 28)) value_error("a history has at most 2^28 tokens, got " + std::to_string(L));
         s.B = static_cast<int>(B);

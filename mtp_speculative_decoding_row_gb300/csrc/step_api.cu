@@ -212,7 +212,7 @@ extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t strea
     if (!args) return MTP_ERR_INVALID_ARG;
     const mtp_adjust_args &a = *args;
     if (!good_dtype(a.dtype)) return MTP_ERR_UNSUPPORTED_DTYPE;
-    if (a.B < 0 || a.B > 65535 || a.S < 1 || a.S > MTP_MAX_NODES || a.V < 1 || a.V > (1 << 24) || a.L < 0 || a.L > (1 << 28) || a.n_bias < 0 ||
+    if (a.B < 0 || a.B > (1 << 20) || a.S < 1 || a.S > MTP_MAX_NODES || a.V < 1 || a.V > (1 << 24) || a.L < 0 || a.L > (1 << 28) || a.n_bias < 0 ||
         a.n_bias > MTP_MAX_BIAS)
         return MTP_ERR_INVALID_ARG;
     if (a.B == 0) return MTP_OK;
@@ -255,6 +255,10 @@ extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t strea
     A.slice = 8192;
     while (A.slice > 1024 && static_cast<long long>(a.B) * ((a.V + A.slice - 1) / A.slice) < 2 * sms) A.slice /= 2;
     A.rows = a.S;
-    const dim3 grid((a.V + A.slice - 1) / A.slice, a.B, (a.S + A.rows - 1) / A.rows);
+    // (the sequences next to one another: the first slices, of the most frequent
+    // words, start first)
+    const dim3 grid(a.B, (a.V + A.slice - 1) / A.slice, (a.S + A.rows - 1) / A.rows);
+    // the shared memory of a block is at most 56 KB: the limit has to be raised
+    if (resident(dev, adj_func(a.dtype), adj_smem(8192, MTP_MAX_BIAS), ADJ_THREADS) < 1) return MTP_ERR_NO_DEVICE;
     return launch(adj_func(a.dtype), grid, ADJ_THREADS, adj_smem(A.slice, A.n_bias), &A, stream);
 }
