@@ -404,6 +404,37 @@ int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream)
 int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
 
 /*
+ * mtp_prefix_attention -- mtp_tree_attention for sequences that share long
+ * prefixes (the samples of one prompt), each prefix's keys and values read once
+ * for all of its sequences.
+ *
+ * Sequences group_start[p] .. group_start[p + 1] - 1 continue prefix p: its
+ * prefix_len[p] tokens lie in the pages prefix_table[p, ..] of the same cache,
+ * page_table and cache_len are those of the sequence's own tokens behind it,
+ * from the start of a page of its own on.  Every row attends over the prefix,
+ * its sequence's own cached tokens and its own path; prefixes of no tokens and
+ * of no sequences are allowed.  The rest is as in mtp_tree_attention.
+ *
+ * A sequence is flagged as there, for a bad length or page of its prefix too;
+ * all rows of a flagged sequence are NaN.  A group_start that does not rise
+ * from 0 to B flags every sequence MTP_ROW_BAD_ID.
+ * Requirements: those of mtp_tree_attention (own.workspace is this call's, of
+ * mtp_prefix_attention_workspace bytes), 1 <= prefixes <= 2^20, at least one
+ * column of the prefix table, max_prefix_pages * page_size <= 2^31 - 2^16, B T Hq
+ * < 2^31 (else MTP_ERR_INVALID_ARG).
+ */
+typedef struct mtp_prefix_attention_args {
+    mtp_tree_attention_args own;
+    const int32_t *prefix_table; /* [prefixes, max_prefix_pages] */
+    const int32_t *prefix_len;   /* [prefixes] */
+    const int32_t *group_start;  /* [prefixes + 1] */
+    int prefixes, max_prefix_pages;
+} mtp_prefix_attention_args;
+
+int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_stream_t stream);
+int64_t mtp_prefix_attention_workspace(const mtp_prefix_attention_args *args);
+
+/*
  * mtp_beam_select -- the K best continuations of a sequence's W beams (one
  * level of a draft tree, or one step of beam search): over w < W, v < V
  *   score(w, v) = scores[b,w] + ln softmax(logits[b,w] / T_b)(v),

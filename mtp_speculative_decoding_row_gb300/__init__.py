@@ -23,7 +23,7 @@ __all__ = [
     "mtp_rs_verify", "mtp_to_verify", "mtp_gumbel_verify", "mtp_draft_sample", "mtp_row_stats",
     "mtp_rs_diagnostics", "mtp_tv_loss_fwd_bwd", "mtp_tv_loss_ex", "mtp_tv_loss_topk",
     "mtp_tree_attention", "mtp_beam_select", "mtp_beam_reorder", "mtp_tree_commit",
-    "mtp_rope", "mtp_cache_append", "mtp_adjust_logits", "rope_frequencies",
+    "mtp_prefix_attention", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits", "rope_frequencies",
     "mtp_query_plan", "mtp_status_string", "mtp_set_tuning", "mtp_get_tuning", "tuning", "check_row_flags",
     "MTPError", "load_library", "MTP_ERR_TIMEOUT", "KERNEL_AUTO", "KERNEL_STREAM", "KERNEL_RESIDENT", "KERNEL_TMEM",
     "VerifyResult", "TOVerifyResult", "StatsResult", "DiagResult", "TVLossResult", "SampleResult",
@@ -39,7 +39,8 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 EXPORTED_SYMBOLS = ("mtp_rs_verify", "mtp_to_verify", "mtp_gumbel_verify", "mtp_draft_sample", "mtp_row_stats",
                     "mtp_rs_diagnostics", "mtp_tv_loss_fwd_bwd", "mtp_tv_loss_ex", "mtp_tv_loss_topk",
                     "mtp_tree_attention", "mtp_tree_attention_workspace", "mtp_beam_select", "mtp_beam_select_workspace",
-                    "mtp_beam_reorder", "mtp_tree_commit", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits",
+                    "mtp_beam_reorder", "mtp_tree_commit", "mtp_prefix_attention", "mtp_prefix_attention_workspace",
+                    "mtp_rope", "mtp_cache_append", "mtp_adjust_logits",
                     "mtp_query_plan", "mtp_set_tuning", "mtp_get_tuning", "mtp_status_string")
 MTP_OK, MTP_ERR_INVALID_ARG, MTP_ERR_UNSUPPORTED_DTYPE, MTP_ERR_MISALIGNED, MTP_ERR_CUDA, MTP_ERR_TIMEOUT, \
     MTP_ERR_NO_DEVICE = range(7)
@@ -112,7 +113,9 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False):
     lib.mtp_beam_select_workspace.restype = L
     lib.mtp_beam_reorder.argtypes = [P, P, I, I, I, I, L, P, P, P]
     lib.mtp_beam_reorder.restype = I
-    for name in ("mtp_tree_commit", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits"):
+    lib.mtp_prefix_attention_workspace.argtypes = [S]
+    lib.mtp_prefix_attention_workspace.restype = L
+    for name in ("mtp_tree_commit", "mtp_prefix_attention", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits"):
         getattr(lib, name).argtypes = [S, P]
         getattr(lib, name).restype = I
     lib.mtp_query_plan.argtypes = [I, I, I, I, I, P, P, P, P]
@@ -573,6 +576,6 @@ def mtp_tv_loss_fwd_bwd(target_logits, draft_logits, temperature: float = 1.0, g
 
 from .tree import (  # noqa: E402
     MAX_BEAMS, MAX_NODES, MAX_SELECT, BeamResult, CommitResult, ReorderResult, TreeAttentionResult, mtp_beam_reorder,
-    mtp_beam_select, mtp_tree_attention, mtp_tree_commit)
+    mtp_beam_select, mtp_prefix_attention, mtp_tree_attention, mtp_tree_commit)
 from .step import (  # noqa: E402
     MAX_BIAS, AdjustResult, AppendResult, RopeResult, mtp_adjust_logits, mtp_cache_append, mtp_rope, rope_frequencies)

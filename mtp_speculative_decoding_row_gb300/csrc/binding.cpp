@@ -28,6 +28,8 @@ struct Functions {
     decltype(&mtp_beam_select_workspace) select_ws = nullptr;
     decltype(&mtp_beam_reorder) reorder = nullptr;
     decltype(&mtp_tree_commit) commit = nullptr;
+    decltype(&mtp_prefix_attention) prefix = nullptr;
+    decltype(&mtp_prefix_attention_workspace) prefix_ws = nullptr;
     decltype(&mtp_rope) rope = nullptr;
     decltype(&mtp_cache_append) append = nullptr;
     decltype(&mtp_adjust_logits) adjust = nullptr;
@@ -148,63 +150,102 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
     return false;
 }
 
+// The arguments that tree_attention and prefix_attention share: q, k_new, v_new,
+// k_cache, v_cache at a; page_table, cache_len, parents, n_nodes, scale, out,
+// lse, row_flags at r.
+int attention_args(PyObject *const *a, PyObject *const *r, mtp_tree_attention_args &s) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"),
+                     &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache"), &table = tensor(r[0], "page_table");
+    dims(q, "q", 4);
+    dims(k, "k_new", 4);
+    dims(kc, "k_cache", 4);
+    dims(table, "page_table", 2);
+    const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3), Hkv = k.size(2), pages = kc.size(0),
+                  page = kc.size(1), most = table.size(1);
+    const at::ScalarType dt = q.scalar_type();
+    s.dtype = dtype_code(q);
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 4096)
+        value_error("q has " + std::to_string(Hq) + " heads: not a multiple (up to 4096) of the " + std::to_string(Hkv) + " of k_new");
+    if (T < 1 || T > MTP_MAX_NODES)
+        value_error("trees have 1 to " + std::to_string(MTP_MAX_NODES) + " nodes, got " + std::to_string(T));
+    if (D < 1 || D > 256) value_error("heads have 1 to 256 elements, got " + std::to_string(D));
+    const double scale = PyFloat_AsDouble(r[4]);
+    if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+    if (!(scale > 0.0 && scale < 1e30)) value_error("scale must be positive, got " + std::to_string(scale));
+    const int index = index_of(q);
+    s.out = whole(r[5], "out.out", dt, {B, T, Hq, D}, index);
+    s.lse = static_cast<float *>(whole_or_null(r[6], "out.lse", at::kFloat, {B, T, Hq}, index));
+    s.row_flags = static_cast<int32_t *>(whole_or_null(r[7], "out.row_flags", at::kInt, {B}, index));
+    s.q = strided(q, "q", dt, {B, T, Hq, D}, index, s.q_stride);
+    s.k_new = strided(k, "k_new", dt, {B, T, Hkv, D}, index, s.k_new_stride);
+    s.v_new = strided(v, "v_new", dt, {B, T, Hkv, D}, index, s.v_new_stride);
+    s.k_cache = strided(kc, "k_cache", dt, {pages, page, Hkv, D}, index, s.k_cache_stride);
+    s.v_cache = strided(vc, "v_cache", dt, {pages, page, Hkv, D}, index, s.v_cache_stride);
+    s.page_table = static_cast<int32_t *>(whole(r[0], "page_table", at::kInt, {B, most}, index));
+    s.cache_len = static_cast<int32_t *>(whole(r[1], "cache_len", at::kInt, {B}, index));
+    s.parents = static_cast<int32_t *>(whole_or_null(r[2], "parents", at::kInt, {B, T}, index));
+    s.n_nodes = static_cast<int32_t *>(whole_or_null(r[3], "n_nodes", at::kInt, {B}, index));
+    on_gpu(index, "q");
+    for (int64_t x : {B, Hq, Hkv, pages, page, most})
+        if (x > 0x7fffffff) value_error("a dimension is too large");
+    s.B = static_cast<int>(B);
+    s.T = static_cast<int>(T);
+    s.Hq = static_cast<int>(Hq);
+    s.Hkv = static_cast<int>(Hkv);
+    s.D = static_cast<int>(D);
+    s.num_pages = static_cast<int>(pages);
+    s.page_size = static_cast<int>(page);
+    s.max_pages = static_cast<int>(most);
+    s.scale = static_cast<float>(scale);
+    return index;
+}
+
 // tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
 //   parents, n_nodes, scale, out, lse, row_flags, stream)
 PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count(n, 14)) return nullptr;
     return guarded([&]() -> long {
-        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"),
-                         &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache"), &table = tensor(a[5], "page_table");
-        dims(q, "q", 4);
-        dims(k, "k_new", 4);
-        dims(kc, "k_cache", 4);
-        dims(table, "page_table", 2);
         mtp_tree_attention_args s = {};
-        const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3), Hkv = k.size(2), pages = kc.size(0),
-                      page = kc.size(1), most = table.size(1);
-        const at::ScalarType dt = q.scalar_type();
-        s.dtype = dtype_code(q);
-        if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 4096)
-            value_error("q has " + std::to_string(Hq) + " heads: not a multiple (up to 4096) of the " + std::to_string(Hkv) + " of k_new");
-        if (T < 1 || T > MTP_MAX_NODES)
-            value_error("trees have 1 to " + std::to_string(MTP_MAX_NODES) + " nodes, got " + std::to_string(T));
-        if (D < 1 || D > 256) value_error("heads have 1 to 256 elements, got " + std::to_string(D));
-        const double scale = PyFloat_AsDouble(a[9]);
-        if (PyErr_Occurred()) return 0;
-        if (!(scale > 0.0 && scale < 1e30)) value_error("scale must be positive, got " + std::to_string(scale));
-        const int index = index_of(q);
-        s.out = whole(a[10], "out.out", dt, {B, T, Hq, D}, index);
-        s.lse = static_cast<float *>(whole_or_null(a[11], "out.lse", at::kFloat, {B, T, Hq}, index));
-        s.row_flags = static_cast<int32_t *>(whole_or_null(a[12], "out.row_flags", at::kInt, {B}, index));
-        s.q = strided(q, "q", dt, {B, T, Hq, D}, index, s.q_stride);
-        s.k_new = strided(k, "k_new", dt, {B, T, Hkv, D}, index, s.k_new_stride);
-        s.v_new = strided(v, "v_new", dt, {B, T, Hkv, D}, index, s.v_new_stride);
-        s.k_cache = strided(kc, "k_cache", dt, {pages, page, Hkv, D}, index, s.k_cache_stride);
-        s.v_cache = strided(vc, "v_cache", dt, {pages, page, Hkv, D}, index, s.v_cache_stride);
-        s.page_table = static_cast<int32_t *>(whole(a[5], "page_table", at::kInt, {B, most}, index));
-        s.cache_len = static_cast<int32_t *>(whole(a[6], "cache_len", at::kInt, {B}, index));
-        s.parents = static_cast<int32_t *>(whole_or_null(a[7], "parents", at::kInt, {B, T}, index));
-        s.n_nodes = static_cast<int32_t *>(whole_or_null(a[8], "n_nodes", at::kInt, {B}, index));
-        on_gpu(index, "q");
-        for (int64_t x : {B, Hq, Hkv, pages, page, most})
-            if (x > 0x7fffffff) value_error("a dimension is too large");
-        s.B = static_cast<int>(B);
-        s.T = static_cast<int>(T);
-        s.Hq = static_cast<int>(Hq);
-        s.Hkv = static_cast<int>(Hkv);
-        s.D = static_cast<int>(D);
-        s.num_pages = static_cast<int>(pages);
-        s.page_size = static_cast<int>(page);
-        s.max_pages = static_cast<int>(most);
-        s.scale = static_cast<float>(scale);
+        attention_args(a, a + 5, s);
         if (!fn.attention) return NOT_BOUND;
         const int64_t bytes = fn.attention_ws(&s);
         if (bytes < 0) return MTP_ERR_INVALID_ARG;
-        const at::Tensor hold = workspace(bytes, q);
+        const at::Tensor hold = workspace(bytes, THPVariable_Unpack(a[0]));
         s.workspace = hold.data_ptr();
         s.workspace_bytes = bytes;
         const mtp_stream_t stream = stream_of(a[13]);
         const auto f = fn.attention;  // (another thread may bind meanwhile)
+        return call([&] { return f(&s, stream); });
+    });
+}
+
+// prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix_len,
+//   group_start, page_table, cache_len, parents, n_nodes, scale, out, lse, row_flags, stream)
+PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count(n, 17)) return nullptr;
+    return guarded([&]() -> long {
+        mtp_prefix_attention_args s = {};
+        const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[5], "prefix_table");
+        dims(table, "prefix_table", 2);
+        const int index = index_of(q);
+        const int64_t P = table.size(0), most = table.size(1);
+        if (P < 1 || most < 1) value_error("at least one prefix and one page of it are needed, got " + show(table.sizes()));
+        s.prefix_table = static_cast<int32_t *>(whole(a[5], "prefix_table", at::kInt, {P, most}, index));
+        s.prefix_len = static_cast<int32_t *>(whole(a[6], "prefix_len", at::kInt, {P}, index));
+        s.group_start = static_cast<int32_t *>(whole(a[7], "group_start", at::kInt, {P + 1}, index));
+        attention_args(a, a + 8, s.own);
+        for (int64_t x : {P, most})
+            if (x > 0x7fffffff) value_error("a dimension is too large");
+        s.prefixes = static_cast<int>(P);
+        s.max_prefix_pages = static_cast<int>(most);
+        if (!fn.prefix) return NOT_BOUND;
+        const int64_t bytes = fn.prefix_ws(&s);
+        if (bytes < 0) return MTP_ERR_INVALID_ARG;
+        const at::Tensor hold = workspace(bytes, q);
+        s.own.workspace = hold.data_ptr();
+        s.own.workspace_bytes = bytes;
+        const mtp_stream_t stream = stream_of(a[16]);
+        const auto f = fn.prefix;
         return call([&] { return f(&s, stream); });
     });
 }
@@ -560,7 +601,7 @@ PyObject *adjust_logits(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // bind(addresses of the functions, in the order of Functions)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    constexpr int N = 9;
+    constexpr int N = 11;
     if (!count(n, N)) return nullptr;
     void *p[N];
     for (int i = 0; i < N; ++i) {
@@ -573,9 +614,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     fn.select_ws = reinterpret_cast<decltype(fn.select_ws)>(p[3]);
     fn.reorder = reinterpret_cast<decltype(fn.reorder)>(p[4]);
     fn.commit = reinterpret_cast<decltype(fn.commit)>(p[5]);
-    fn.rope = reinterpret_cast<decltype(fn.rope)>(p[6]);
-    fn.append = reinterpret_cast<decltype(fn.append)>(p[7]);
-    fn.adjust = reinterpret_cast<decltype(fn.adjust)>(p[8]);
+    fn.prefix = reinterpret_cast<decltype(fn.prefix)>(p[6]);
+    fn.prefix_ws = reinterpret_cast<decltype(fn.prefix_ws)>(p[7]);
+    fn.rope = reinterpret_cast<decltype(fn.rope)>(p[8]);
+    fn.append = reinterpret_cast<decltype(fn.append)>(p[9]);
+    fn.adjust = reinterpret_cast<decltype(fn.adjust)>(p[10]);
     Py_RETURN_NONE;
 }
 
@@ -584,6 +627,7 @@ PyMethodDef methods[] = {
     {"beam_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_select)), METH_FASTCALL, nullptr},
     {"beam_reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_reorder)), METH_FASTCALL, nullptr},
     {"tree_commit", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_commit)), METH_FASTCALL, nullptr},
+    {"prefix_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attention)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"adjust_logits", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adjust_logits)), METH_FASTCALL, nullptr},

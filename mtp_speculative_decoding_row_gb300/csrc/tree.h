@@ -42,6 +42,18 @@ struct TreeAttnArgs {
     unsigned long long number;  // the call's
     uint32_t wait_us;           // limit of every wait
     int fault_cta;              // 1 + a CTA whose loader leaves out a signal (tests), else 0
+    // Attention with shared prefixes (mtp_prefix_attention): partial results of
+    // all units go to a join of the two kernels' parts (null and 0 otherwise).
+    float *row_m, *row_l, *row_o;  // of whole units, by the row of the output: [B T Hq], [B T Hq], [B T Hq, D]
+    int2 *units;                   // of each unit: parts (0: whole), first part's slot (see attn_write_units)
+    int32_t *flags_out;            // [B] or null: the sequences' flags, its own and its prefix's
+    int overlap;                   // launched behind the kernel of the prefixes, beside which it may run
+    // The kernel of the prefixes: B, table, len, max_pages, flags and late are those of
+    // the prefixes; q, T and the rows of the output those of the sequences.
+    const int32_t *starts;  // [B + 1] first sequence of each prefix
+    int32_t *bad_starts;    // whether they are none
+    int sequences;
+    int tile_rows;          // query rows of one tile
 };
 
 constexpr int ATTN_DESC = 4;
@@ -52,19 +64,22 @@ __host__ __device__ inline size_t attn_slot_floats(int bm, int d) { return stati
 
 // SIMT kernel (csrc/tree_attention_simt.cu).
 constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256;
-const void *attn_simt_func(int dtype, int D);
+const void *attn_simt_func(int dtype, int D, bool prefix);
 uint32_t attn_simt_smem(int D);
 // Tensor-core kernel (csrc/tree_attention_umma.cu): bfloat16, D 64, 128, 256.
 constexpr uint32_t UMMA_SMEM = 232448;  // 227 KB per CTA
 constexpr int UMMA_EXTRA = 3;
 struct UmmaPlan {
     const void *func;
-    int threads, bm, qrows, qbufs, slots;
+    int threads, bm, tile_rows, qrows, qbufs, slots;
     uint32_t smem;
 };
 UmmaPlan attn_umma_plan(int D, int rows);
+// The kernel of the prefixes: `rows` query rows to a prefix on average, `most` in all.
+UmmaPlan prefix_umma_plan(int D, int rows, long long most);
 int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype, int D);
+const void *prefix_join_func(int dtype, int D);
 constexpr int JOIN_ROWS = 4, JOIN_THREADS = 128;  // rows of a block, a warp each
 
 // ------------------------------------------------------- beam selection --

@@ -22,7 +22,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct AttnPlan {
     const void *func = nullptr;
     uint32_t smem = 0;
-    int threads = 0, bm = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
+    int threads = 0, bm = 0, tile_rows = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0, late_bytes = 0;
     bool whole = false;       // units are not split
@@ -47,10 +47,25 @@ bool umma_sizes(const mtp_tree_attention_args &a) {
            (a.page_size % 8 == 0 || a.page_size >= attn_umma_bn(a.D));
 }
 
+// Keys of a tile for these pages, and the tiles of a page table.
+void umma_tiles(const mtp_tree_attention_args &a, AttnPlan &p) {
+    const int bn = attn_umma_bn(a.D);
+    p.per_page = a.page_size > bn && a.page_size % bn != 0 ? (a.page_size + bn - 1) / bn : 0;
+    p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
+}
+long long most_tiles(const AttnPlan &p, int max_pages, int page_size) {
+    return p.per_page ? static_cast<long long>(max_pages) * p.per_page
+                      : (static_cast<long long>(max_pages) * page_size + p.ktile - 1) / p.ktile;
+}
+
+// Slots for the parts of split units, two to a CTA.
+size_t slot_bytes(const AttnPlan &p, int D) {
+    return (attn_slot_floats(p.bm, D) * 4 * 2 * p.groups * p.mtiles + 15) / 16 * 16;
+}
+
 int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     int dev, sms;
     if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
-    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
     p.rows = a.T * (a.Hq / a.Hkv);
     if (umma) {
         const UmmaPlan u = attn_umma_plan(a.D, p.rows);
@@ -61,11 +76,9 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
         p.qrows = u.qrows;
         p.qbufs = u.qbufs;
         p.slots = u.slots;
-        const int bn = attn_umma_bn(a.D);
-        p.per_page = a.page_size > bn && a.page_size % bn != 0 ? (a.page_size + bn - 1) / bn : 0;
-        p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
+        umma_tiles(a, p);
     } else {
-        p.func = attn_simt_func(a.dtype, a.D);
+        p.func = attn_simt_func(a.dtype, a.D, false);
         p.smem = attn_simt_smem(a.D);
         p.threads = SIMT_THREADS;
         p.bm = SIMT_BM;
@@ -74,7 +87,7 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     const int per_sm = resident(dev, p.func, p.smem, p.threads);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
     p.mtiles = (p.rows + p.bm - 1) / p.bm;
-    p.max_tiles = 1 + (p.per_page ? static_cast<long long>(a.max_pages) * p.per_page : (cap + p.ktile - 1) / p.ktile);
+    p.max_tiles = 1 + most_tiles(p, a.max_pages, a.page_size);
     if (p.max_tiles * a.Hkv > 0x7fffffffll) return MTP_ERR_INVALID_ARG;  // tiles of a sequence are counted in 32 bits
     long long groups = static_cast<long long>(sms) * per_sm / p.mtiles;
     // Units are not split where that costs less.  Whole, the CTAs take them in
@@ -93,8 +106,7 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
     const long long all = p.whole ? units : p.max_tiles * units;
     if (groups > all) groups = all;
     p.groups = static_cast<int>(groups < 1 ? 1 : groups);
-    p.part_bytes = attn_slot_floats(p.bm, a.D) * 4 * 2 * p.groups * p.mtiles;
-    p.part_bytes = (p.part_bytes + 15) / 16 * 16;
+    p.part_bytes = slot_bytes(p, a.D);
     p.desc_bytes = static_cast<size_t>(p.groups) * ATTN_DESC * sizeof(int32_t);
     p.late_bytes = umma ? (static_cast<size_t>(a.B) * 8 + 15) / 16 * 16 : 0;
     return MTP_OK;
@@ -170,12 +182,11 @@ extern "C" int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *a
     return static_cast<int64_t>(bytes);
 }
 
-extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream) {
-    if (!args) return MTP_ERR_INVALID_ARG;
-    const mtp_tree_attention_args &a = *args;
-    const int rc = attn_sizes(a);
-    if (rc != MTP_OK) return rc;
-    if (a.B == 0) return MTP_OK;
+namespace {
+
+// The kernel's arguments but for the plan and the workspace, and whether the
+// tensor-core kernel takes them (then the caches' maps).
+int attn_args(const mtp_tree_attention_args &a, TreeAttnArgs &A, bool &umma, CUtensorMap &kmap, CUtensorMap &vmap) {
     if (!a.q || !a.k_new || !a.v_new || !a.k_cache || !a.v_cache || !a.page_table || !a.cache_len || !a.out || !a.workspace)
         return MTP_ERR_INVALID_ARG;
     const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
@@ -183,7 +194,6 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
                           reinterpret_cast<uintptr_t>(a.v_new) | reinterpret_cast<uintptr_t>(a.k_cache) |
                           reinterpret_cast<uintptr_t>(a.v_cache) | reinterpret_cast<uintptr_t>(a.out);
     if (low % es != 0 || reinterpret_cast<uintptr_t>(a.workspace) % 16 != 0) return MTP_ERR_MISALIGNED;
-    TreeAttnArgs A = {};
     A.q = a.q;
     A.k_new = a.k_new;
     A.v_new = a.v_new;
@@ -221,17 +231,13 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     // the tensor cores wherever sizes and alignment allow: at one query row
     // of 128 they still keep up with the memory (a tile's products take 0.7
     // us, its bytes 1.5 us)
-    CUtensorMap kmap, vmap;
     const int bn = attn_umma_bn(a.D), boxrows = a.page_size < bn ? a.page_size : bn;
-    const bool umma = umma_sizes(a) && A.vec && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
-                      cache_map(&kmap, a, a.k_cache, A.kcs, boxrows) && cache_map(&vmap, a, a.v_cache, A.vcs, boxrows);
-    AttnPlan p;
-    const int pc = attn_plan(a, umma, p);
-    if (pc != MTP_OK) return pc;
-    if (a.workspace_bytes < static_cast<int64_t>(p.bytes())) return MTP_ERR_INVALID_ARG;
-    A.desc = static_cast<int32_t *>(a.workspace);
-    A.late = reinterpret_cast<unsigned long long *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
-    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes + p.late_bytes);
+    umma = umma_sizes(a) && A.vec && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+           cache_map(&kmap, a, a.k_cache, A.kcs, boxrows) && cache_map(&vmap, a, a.v_cache, A.vcs, boxrows);
+    return MTP_OK;
+}
+
+void attn_set_plan(TreeAttnArgs &A, const AttnPlan &p, bool umma) {
     if (umma) {
         mtp_tuning tuning;
         (void)mtp_get_tuning(&tuning);
@@ -243,6 +249,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.mtiles = p.mtiles;
     A.groups = p.groups;
     A.bm = p.bm;
+    A.tile_rows = p.tile_rows;
     A.whole = p.whole;
     A.ktile = p.ktile;
     A.extra = umma ? UMMA_EXTRA : 0;
@@ -250,9 +257,175 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.qbufs = p.qbufs;
     A.slots = p.slots;
     A.per_page = p.per_page;
+}
+
+}  // namespace
+
+extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_stream_t stream) {
+    if (!args) return MTP_ERR_INVALID_ARG;
+    const mtp_tree_attention_args &a = *args;
+    const int rc = attn_sizes(a);
+    if (rc != MTP_OK) return rc;
+    if (a.B == 0) return MTP_OK;
+    TreeAttnArgs A = {};
+    CUtensorMap kmap, vmap;
+    bool umma;
+    const int ac = attn_args(a, A, umma, kmap, vmap);
+    if (ac != MTP_OK) return ac;
+    AttnPlan p;
+    const int pc = attn_plan(a, umma, p);
+    if (pc != MTP_OK) return pc;
+    if (a.workspace_bytes < static_cast<int64_t>(p.bytes())) return MTP_ERR_INVALID_ARG;
+    A.desc = static_cast<int32_t *>(a.workspace);
+    A.late = reinterpret_cast<unsigned long long *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
+    A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes + p.late_bytes);
+    attn_set_plan(A, p, umma);
     const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, &kmap, &vmap);
     if (e != MTP_OK || !p.joins()) return e;
     return launch(attn_join_func(a.dtype, a.D), dim3(p.groups * p.mtiles, ((p.rows < p.bm ? p.rows : p.bm) + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A, stream);
+}
+
+// ----------------------------------------------------- shared prefixes ----
+
+namespace {
+
+int prefix_sizes(const mtp_prefix_attention_args &x) {
+    const mtp_tree_attention_args &a = x.own;
+    const int rc = attn_sizes(a);
+    if (rc != MTP_OK) return rc;
+    if (x.prefixes < 1 || x.prefixes > (1 << 20) || x.max_prefix_pages < 1 || static_cast<long long>(x.max_prefix_pages) * a.page_size > 0x7fff0000ll ||
+        static_cast<long long>(a.B) * a.T * a.Hq > 0x7fffffffll)
+        return MTP_ERR_INVALID_ARG;
+    return MTP_OK;
+}
+
+// The plan of the prefixes' kernel.  What their rows and lengths are only the
+// device knows: row tiles are as large as the average number of rows fills, and
+// there are no more CTAs than tiles that a full page table could have.
+int prefix_plan(const mtp_prefix_attention_args &x, bool umma, AttnPlan &p) {
+    const mtp_tree_attention_args &a = x.own;
+    int dev, sms;
+    if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
+    p.rows = a.T * (a.Hq / a.Hkv);
+    const long long all = static_cast<long long>(a.B) * p.rows;
+    if (umma) {
+        const long long mean = (all + x.prefixes - 1) / x.prefixes;
+        const UmmaPlan u = prefix_umma_plan(a.D, static_cast<int>(mean < 1024 ? mean : 1024), all);
+        p.func = u.func;
+        p.smem = u.smem;
+        p.threads = u.threads;
+        p.bm = u.bm;
+        p.tile_rows = u.tile_rows;
+        p.qrows = u.qrows;
+        p.qbufs = u.qbufs;
+        p.slots = u.slots;
+        umma_tiles(a, p);
+    } else {
+        p.func = attn_simt_func(a.dtype, a.D, true);
+        p.smem = attn_simt_smem(a.D);
+        p.threads = SIMT_THREADS;
+        p.bm = p.tile_rows = SIMT_BM;
+        p.ktile = SIMT_BN;
+    }
+    const int per_sm = resident(dev, p.func, p.smem, p.threads);
+    if (per_sm < 1) return MTP_ERR_NO_DEVICE;
+    p.mtiles = 1;
+    const long long mtiles = all / p.tile_rows + x.prefixes;  // of all prefixes, at most
+    p.max_tiles = most_tiles(p, x.max_prefix_pages, a.page_size);
+    long long groups = static_cast<long long>(sms) * per_sm;
+    const long long units = mtiles * a.Hkv;
+    if (units < groups && units * p.max_tiles < groups) groups = units * p.max_tiles;
+    p.groups = static_cast<int>(groups < 1 ? 1 : groups);
+    p.part_bytes = slot_bytes(p, a.D);
+    p.late_bytes = umma ? (static_cast<size_t>(x.prefixes) * 8 + 15) / 16 * 16 : 0;
+    return MTP_OK;
+}
+
+// The workspace: for each of the two kernels slots, whole units' results by
+// rows, the units' parts, flags and late reports.
+struct PrefixSpace {
+    size_t bytes = 0;
+    unsigned char *base = nullptr;
+    template <typename T>
+    T *take(size_t n) {
+        T *p = reinterpret_cast<T *>(base + bytes);
+        bytes += (n * sizeof(T) + 255) / 256 * 256;
+        return p;
+    }
+};
+
+size_t prefix_layout(const mtp_prefix_attention_args &x, const AttnPlan &own, const AttnPlan &pre, void *base, TreeAttnArgs &A, TreeAttnArgs &S) {
+    const mtp_tree_attention_args &a = x.own;
+    PrefixSpace w;
+    w.base = static_cast<unsigned char *>(base);
+    const size_t rows = static_cast<size_t>(a.B) * a.T * a.Hq;
+    for (int k = 0; k < 2; ++k) {
+        TreeAttnArgs &X = k ? S : A;
+        const AttnPlan &p = k ? pre : own;
+        X.row_m = w.take<float>(rows);
+        X.row_l = w.take<float>(rows);
+        X.row_o = w.take<float>(rows * a.D);
+        X.part = w.take<float>(p.whole ? 0 : p.part_bytes / 4);
+        X.late = w.take<unsigned long long>(p.late_bytes / 8);
+        X.flags = w.take<int32_t>(k ? x.prefixes : a.B);
+        X.units = w.take<int2>(static_cast<size_t>(a.Hkv) * (k ? static_cast<size_t>(a.B) * p.rows / p.tile_rows + x.prefixes : a.B));
+    }
+    S.bad_starts = w.take<int32_t>(1);
+    return w.bytes;
+}
+
+}  // namespace
+
+extern "C" int64_t mtp_prefix_attention_workspace(const mtp_prefix_attention_args *args) {
+    if (!args || prefix_sizes(*args) != MTP_OK) return -1;
+    size_t most = 0;
+    for (int umma = 0; umma < (umma_sizes(args->own) ? 2 : 1); ++umma) {
+        AttnPlan own, pre;
+        TreeAttnArgs A = {}, S = {};
+        if (attn_plan(args->own, umma != 0, own) != MTP_OK || prefix_plan(*args, umma != 0, pre) != MTP_OK) return -1;
+        const size_t bytes = prefix_layout(*args, own, pre, nullptr, A, S);
+        if (bytes > most) most = bytes;
+    }
+    return static_cast<int64_t>(most);
+}
+
+extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_stream_t stream) {
+    if (!args) return MTP_ERR_INVALID_ARG;
+    const mtp_prefix_attention_args &x = *args;
+    const mtp_tree_attention_args &a = x.own;
+    const int rc = prefix_sizes(x);
+    if (rc != MTP_OK) return rc;
+    if (a.B == 0) return MTP_OK;
+    if (!x.prefix_table || !x.prefix_len || !x.group_start) return MTP_ERR_INVALID_ARG;
+    TreeAttnArgs A = {};
+    CUtensorMap kmap, vmap;
+    bool umma;
+    const int ac = attn_args(a, A, umma, kmap, vmap);
+    if (ac != MTP_OK) return ac;
+    AttnPlan own, pre;
+    const int pc = attn_plan(a, umma, own);
+    if (pc != MTP_OK) return pc;
+    const int qc = prefix_plan(x, umma, pre);
+    if (qc != MTP_OK) return qc;
+    TreeAttnArgs S = A;
+    if (a.workspace_bytes < static_cast<int64_t>(prefix_layout(x, own, pre, a.workspace, A, S))) return MTP_ERR_INVALID_ARG;
+    attn_set_plan(A, own, umma);
+    attn_set_plan(S, pre, umma);
+    A.flags_out = a.row_flags;
+    A.overlap = 1;
+    S.table = x.prefix_table;
+    S.len = x.prefix_len;
+    S.max_pages = x.max_prefix_pages;
+    S.starts = x.group_start;
+    S.sequences = a.B;
+    S.B = x.prefixes;
+    S.parents = S.nodes = nullptr;
+    const int e = launch(pre.func, dim3(pre.groups), pre.threads, pre.smem, &S, stream, &kmap, &vmap);
+    if (e != MTP_OK) return e;
+    const int f = launch(own.func, dim3(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &kmap, &vmap);
+    if (f != MTP_OK) return f;
+    const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
+    return launch(prefix_join_func(a.dtype, a.D), dim3(static_cast<unsigned>((rows + JOIN_ROWS - 1) / JOIN_ROWS)), JOIN_THREADS, 0, &A, stream, &S);
 }
 
 // ------------------------------------------------------- beam selection --

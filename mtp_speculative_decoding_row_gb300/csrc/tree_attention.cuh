@@ -77,7 +77,22 @@ __device__ __forceinline__ void attn_tile(const TreeAttnArgs &A, int len, int t,
 struct AttnPiece {
     int b, h, len, prefix, t0, t1;
     bool first;  // the first piece of the group's range
+    __device__ __forceinline__ int tiles() const { return prefix + 1; }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == prefix + 1; }
+};
+
+// The same of a shared prefix b: tiles [t0, t1) of its keys (prefix of them in
+// all) for one tile of the rows that read it, rows row0 .. of the rows of its
+// sequences, token after token, the query heads of key head h each.
+struct PrefixPiece {
+    int b, h, len, prefix, t0, t1;
+    bool first;
+    int mt;          // the row tile
+    int start;       // the prefix's first sequence
+    int rows;        // rows of this tile
+    int token, rest; // its first row: token of the prefix's sequences, head
+    __device__ __forceinline__ int tiles() const { return prefix; }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == prefix; }
 };
 
 // Groups that have tiles: none of their ranges is empty.
@@ -91,10 +106,27 @@ __device__ __forceinline__ long long attn_lo(long long W, int g, int groups) {
     return x >> 32 ? static_cast<long long>(x / groups) : static_cast<uint32_t>(x) / static_cast<uint32_t>(groups);
 }
 
+// The sequences of prefix p, in bounds whatever `starts` holds: the first and
+// how many.
+__device__ __forceinline__ int prefix_group(const TreeAttnArgs &A, int p, int &count) {
+    const int a = min(max(__ldg(A.starts + p), 0), A.sequences), z = min(max(__ldg(A.starts + p + 1), a), A.sequences);
+    count = z - a;
+    return a;
+}
+
+// Unit (row tile mt of prefix p, key head h) in the list of units.  `first` is
+// the prefix's first row.  (Tiles of one prefix are tile_rows rows apart, and
+// ceil(c) - 1 + floor(a) <= floor(a + c): no two have one number, and none is
+// beyond floor(rows / tile_rows) + prefixes.)
+__device__ __forceinline__ size_t prefix_unit(const TreeAttnArgs &A, int p, long long first, int mt, int h) {
+    return (static_cast<size_t>(first / A.tile_rows) + mt + p) * A.Hkv + h;
+}
+
 // The walk over a group's pieces.  start() finds the first one, in every warp
 // by itself (a lane takes a stretch of the sequences): a barrier would cost
 // more than the second reading of a few lengths.
 struct AttnWalk {
+    using Piece = AttnPiece;
     long long hi = 0, at = 0;    // the end of this group's range, the next tile
     int b = 0, h = 0, tile = 0;  // where `at` is
     int len = 0, prefix = 0;
@@ -225,6 +257,121 @@ struct AttnWalk {
     }
 };
 
+// The same over the tiles of the shared prefixes: units (prefix, key head, row
+// tile), the row tiles of one head next to one another, so that the CTAs that
+// read the same keys do so at about the same time.  Prefixes without tokens or
+// sequences have no units.
+struct PrefixWalk {
+    using Piece = PrefixPiece;
+    long long hi = 0, at = 0;
+    int b = 0, h = 0, mt = 0, tile = 0;
+    int len = 0, prefix = 0, start_ = 0, count = 0, mts = 0;
+    int extra = 0;
+    bool begins = true;
+
+    // Prefix p and its units (0 for an empty one).
+    __device__ __forceinline__ long long read(const TreeAttnArgs &A, int p) {
+        bool bad;
+        len = attn_len(A, p, bad);
+        prefix = attn_prefix_tiles(A, len);
+        start_ = prefix_group(A, p, count);
+        mts = static_cast<int>((static_cast<long long>(count) * A.rows + A.tile_rows - 1) / A.tile_rows);
+        return prefix > 0 ? static_cast<long long>(mts) * A.Hkv : 0;
+    }
+
+    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
+        const int lane = threadIdx.x & 31;
+        const int per = (A.B + 31) / 32;
+        const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
+        long long sum = 0, units = 0;
+        for (int i = b0; i < b1; ++i) {
+            const long long n = read(A, i);
+            units += n;
+            sum += n * prefix;
+        }
+        long long inc = sum, uinc = units;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(FULL, inc, d), u = __shfl_up_sync(FULL, uinc, d);
+            if (lane >= d) {
+                inc += o;
+                uinc += u;
+            }
+        }
+        const long long real = __shfl_sync(FULL, inc, 31);
+        if (real >= 4ll * A.groups) extra = A.extra;
+        const long long W = real + __shfl_sync(FULL, uinc, 31) * extra;
+        inc += uinc * extra;
+        sum += units * extra;
+        const int groups = attn_groups(A, W);
+        const long long lo = attn_lo(W, min(g, groups), groups);
+        hi = attn_lo(W, min(g + 1, groups), groups);
+        at = lo;
+        const long long from = inc - sum;
+        const uint32_t own = __ballot_sync(FULL, lo < hi && lo >= from && lo < inc);
+        if (own == 0) return W;
+        long long x = lo - from;
+        int i = b0;
+        if ((own >> lane) & 1u) {
+            for (;; ++i) {
+                const long long n = read(A, i) * (prefix + extra);
+                if (x < n) break;  // (x lies in this lane's stretch)
+                x -= n;
+            }
+        }
+        const int src = __ffs(own) - 1;
+        b = __shfl_sync(FULL, i, src);
+        x = __shfl_sync(FULL, x, src);
+        read(A, b);
+        const long long unit = x / (prefix + extra);
+        tile = static_cast<int>(x - unit * (prefix + extra));
+        h = static_cast<int>(unit / mts);
+        mt = static_cast<int>(unit - static_cast<long long>(h) * mts);
+        if (tile >= prefix) {  // the range begins behind a unit's tiles
+            at += prefix + extra - tile;
+            step(A);
+        }
+        return W;
+    }
+
+    __device__ __forceinline__ void step(const TreeAttnArgs &A) {
+        if (at >= hi) return;
+        tile = 0;
+        if (++mt < mts) return;
+        mt = 0;
+        if (++h < A.Hkv) return;
+        h = 0;
+        while (++b < A.B && read(A, b) == 0) {
+        }
+    }
+
+    __device__ __forceinline__ bool next(const TreeAttnArgs &A, PrefixPiece &p) {
+        if (at >= hi || b >= A.B) return false;
+        p.b = b;
+        p.h = h;
+        p.mt = mt;
+        p.len = len;
+        p.prefix = prefix;
+        p.start = start_;
+        p.first = begins;
+        begins = false;
+        const long long row0 = static_cast<long long>(mt) * A.tile_rows, left_rows = static_cast<long long>(count) * A.rows - row0;
+        p.rows = static_cast<int>(left_rows < A.tile_rows ? left_rows : A.tile_rows);
+        p.token = static_cast<int>(row0 / A.G);
+        p.rest = static_cast<int>(row0 - static_cast<long long>(p.token) * A.G);
+        p.t0 = tile;
+        const long long left = hi - at;
+        p.t1 = static_cast<int>(tile + left < prefix ? tile + left : prefix);
+        at += p.t1 - p.t0;
+        tile = p.t1;
+        if (tile == prefix) {
+            at += extra;
+            step(A);
+        }
+        return true;
+    }
+};
+
 // Slot of a piece that is not a whole unit: a piece that begins its group's
 // range takes slot 0, a piece that ends it slot 1.
 __device__ __forceinline__ size_t attn_slot(const TreeAttnArgs &A, int group, int mtile, bool first) {
@@ -237,6 +384,17 @@ __device__ __forceinline__ size_t attn_slot(const TreeAttnArgs &A, int group, in
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The groups that a unit lies in that begins in group g with its last piece
+// `p` and goes on in the next ones.
+template <class Piece>
+__device__ __forceinline__ int attn_parts(const TreeAttnArgs &A, int g, long long W, long long hi, const Piece &p) {
+    const long long end = hi + (p.tiles() - p.t1);  // one past the unit's last tile (the range ended inside of the unit)
+    const int groups = attn_groups(A, W);
+    int n = 1;
+    while (g + n < groups && attn_lo(W, g + n, groups) < end) ++n;
+    return n;
+}
+
 // Tell the join about the unit that begins in this group and goes on in the
 // next ones (at most one does): {b, h, parts, slot of the first part}.
 __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, long long W, long long hi,
@@ -247,14 +405,56 @@ __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, lo
         d[2] = 0;
         return;
     }
-    const long long end = hi + (last.prefix + 1 - last.t1);  // one past the unit's last tile (the range ended inside of the unit)
-    const int groups = attn_groups(A, W);
-    int n = 1;
-    while (g + n < groups && attn_lo(W, g + n, groups) < end) ++n;
+    const int n = attn_parts(A, g, W, hi, last);
     d[0] = last.b;
     d[1] = last.h;
     d[3] = last.first ? 0 : 1;
     d[2] = n;
+}
+
+// Tell the join of the two kernels about every unit that begins in this group:
+// {parts, slot of the first}; 0 parts: a whole unit, whose results lie by rows.
+__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, long long W, long long hi, const AttnPiece &p) {
+    if (p.t0 != 0) return;
+    const int n = p.whole() ? 0 : attn_parts(A, g, W, hi, p);
+    A.units[static_cast<size_t>(p.b) * A.Hkv + p.h] = make_int2(n, 2 * g + (p.first ? 0 : 1));
+}
+__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, long long W, long long hi, const PrefixPiece &p) {
+    if (p.t0 != 0) return;
+    const int n = p.whole() ? 0 : attn_parts(A, g, W, hi, p);
+    A.units[prefix_unit(A, p.b, static_cast<long long>(p.start) * A.rows, p.mt, p.h)] = make_int2(n, 2 * g + (p.first ? 0 : 1));
+}
+
+// What one thread of a group tells the join when its pieces are done.
+__device__ __forceinline__ void attn_report(const TreeAttnArgs &A, int g, long long W, AttnWalk w) {
+    AttnPiece p, last = {};
+    while (w.next(A, p)) {
+        last = p;
+        if (A.units) attn_write_unit(A, g, W, w.hi, p);
+    }
+    if (!A.units) attn_write_desc(A, g, W, w.hi, last);
+}
+__device__ __forceinline__ void attn_report(const TreeAttnArgs &A, int g, long long W, PrefixWalk w) {
+    PrefixPiece p;
+    while (w.next(A, p)) attn_write_unit(A, g, W, w.hi, p);
+}
+
+// The row of the output that row r of a piece's tile has.
+__device__ __forceinline__ size_t prefix_row(const TreeAttnArgs &A, const PrefixPiece &p, int r) {
+    const int d = node_of(A, p.rest + r);  // (rest < G, r < 256: (rest + r) G < 2^32)
+    return (static_cast<size_t>(p.start) * A.T + p.token + d) * A.Hq + p.h * A.G + (p.rest + r - d * A.G);
+}
+
+// By one warp: whether the starts rise from 0 to the number of sequences.
+__device__ __forceinline__ void prefix_check_starts(const TreeAttnArgs &A) {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    for (int i = lane; i < A.B; i += 32) {
+        const int a = __ldg(A.starts + i), z = __ldg(A.starts + i + 1);
+        bad |= a < 0 || z < a || z > A.sequences || (i == 0 && a != 0) || (i == A.B - 1 && z != A.sequences);
+    }
+    bad = __any_sync(FULL, bad);
+    if (lane == 0) *A.bad_starts = bad ? 1 : 0;
 }
 
 // Ancestor masks of a tree's n nodes (a node's own bit included) into `mask`,

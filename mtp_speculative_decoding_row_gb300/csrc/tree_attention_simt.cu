@@ -19,6 +19,8 @@
 // the shorter sums; 128 without the four rows to a warp and the values four at a time).  What bounds
 // it: half of the issue slots, and as many empty while warps wait for shared
 // memory and for each other (28 rows); memory runs at 14 % of its rate.
+#include <type_traits>
+
 #include "tree_attention.cuh"
 
 namespace mtp {
@@ -79,8 +81,11 @@ __device__ __forceinline__ void put(bf16_t *p, float x) {
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(p->bits) : "f"(x));
 }
 
-template <typename T, int DC>
+// PREFIX: the keys of shared prefixes, as in the tensor-core kernel.
+template <typename T, int DC, bool PREFIX>
 __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ TreeAttnArgs A) {
+    using Walk = typename std::conditional<PREFIX, PrefixWalk, AttnWalk>::type;
+    using Piece = typename Walk::Piece;
     constexpr int DP = DC * 64, KS = DP + 4;  // key row stride: rows of a float4 column in different banks
     extern __shared__ __align__(16) unsigned char smem[];
     float *sq = reinterpret_cast<float *>(smem);  // [BM][KS]
@@ -92,25 +97,33 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     float *sf = sl + BM;                          // [BM] factor of the old rows
     uint64_t *smask = reinterpret_cast<uint64_t *>(sf + BM);  // [MAX_NODES]
     __shared__ int s_flag, s_above[MAX_NODES];
+    __shared__ __align__(16) unsigned char s_begin[sizeof(Walk)];
 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int group = blockIdx.x / A.mtiles, mtile = blockIdx.x - group * A.mtiles;
-    const int row0 = mtile * BM, rows = min(BM, A.rows - row0);
+    const int row0 = PREFIX ? 0 : mtile * BM;
     const bool vec = A.vec != 0;
-    const bool works = 4 * (tid >> 5) < rows;  // a warp has rows 4 w .. 4 w + 3 from the scores to the output
 
-    pdl_wait();
+    if (PREFIX || !A.overlap) pdl_wait();
     pdl_next();
-    AttnWalk walk;
+    Walk walk;
     const long long W = walk.start(A, group);
-    AttnPiece pc, last = {};
+    if (tid == 0) *reinterpret_cast<Walk *>(s_begin) = walk;  // for the end
+    if (PREFIX && blockIdx.x == 0 && tid < 32) prefix_check_starts(A);
+    Piece pc;
     while (walk.next(A, pc)) {
-        last = pc;
         const int b = pc.b, h = pc.h;
-        bool bad_len, bad_nodes;
+        bool bad_len, bad_nodes = false;
         attn_len(A, b, bad_len);
-        const int n = attn_nodes(A, b, bad_nodes);
-        const int rows_n = bad_nodes ? A.rows : n * A.G;  // rows that are written
+        int n = 0, rows, rows_n;  // nodes; rows of the tile; rows that are written
+        if constexpr (PREFIX) {
+            rows = rows_n = pc.rows;
+        } else {
+            n = attn_nodes(A, b, bad_nodes);
+            rows = min(BM, A.rows - row0);
+            rows_n = bad_nodes ? A.rows : n * A.G;
+        }
+        const bool works = 4 * (tid >> 5) < rows;  // a warp has rows 4 w .. 4 w + 3 from the scores to the output
         if (tid == 0) s_flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
         __syncthreads();
         // This thread's part of the keys or of the values of tile t, one row for
@@ -121,11 +134,12 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         };
         auto fetch = [&](bool values, int t, int pid) {
             const int j = tid >> 2;
-            if (t < pc.t1 && j < (t == pc.prefix ? n : min(BN, pc.len - t * BN))) {
+            const bool fresh = !PREFIX && t == pc.prefix;
+            if (t < pc.t1 && j < (fresh ? n : min(BN, pc.len - t * BN))) {
                 const int off = (t * BN + j) % A.page_size;
                 const int64_t *cs = values ? A.vcs : A.kcs, *ns = values ? A.vs : A.ks;
-                const int64_t from = t == pc.prefix ? b * ns[0] + j * ns[1] + h * ns[2] : pid * cs[0] + off * cs[1] + h * cs[2];
-                const void *src = t == pc.prefix ? (values ? A.v_new : A.k_new) : (values ? A.v_cache : A.k_cache);
+                const int64_t from = fresh ? b * ns[0] + j * ns[1] + h * ns[2] : pid * cs[0] + off * cs[1] + h * cs[2];
+                const void *src = fresh ? (values ? A.v_new : A.k_new) : (values ? A.v_cache : A.k_cache);
                 row_async<T, DP>(values ? sv + j * DP : sk + j * KS, src, from, A.D, tid & 3, 4, vec);
             }
             cp_async_commit();
@@ -133,15 +147,26 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         int pid = page_of(pc.t0);
         fetch(false, pc.t0, pid);
         fetch(true, pc.t0, pid);
-        int bad = attn_check_pages(A, b, pc.len, tid, NT);
-        if (tid < 32) bad |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, smask, s_above);
+        int bad = 0;
+        if constexpr (PREFIX) {
+            if (h == 0 && pc.mt == 0 && pc.t0 == 0) bad = attn_check_pages(A, b, pc.len, tid, NT);
+        } else {
+            bad = attn_check_pages(A, b, pc.len, tid, NT);
+        }
+        if (!PREFIX && tid < 32) bad |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, smask, s_above);
         if (bad) atomicOr(&s_flag, bad);
         {
             const int r = tid >> 3;  // 8 threads a row
-            const int t = (row0 + r) / A.G, g = row0 + r - t * A.G;
+            int64_t from = 0;
+            if constexpr (PREFIX) {
+                const int d = node_of(A, pc.rest + r), tok = pc.token + d, s = tok / A.T;
+                from = (pc.start + s) * A.qs[0] + (tok - s * A.T) * A.qs[1] + (static_cast<int64_t>(h) * A.G + (pc.rest + r - d * A.G)) * A.qs[2];
+            } else {
+                const int t = (row0 + r) / A.G, g = row0 + r - t * A.G;
+                from = b * A.qs[0] + t * A.qs[1] + (static_cast<int64_t>(h) * A.G + g) * A.qs[2];
+            }
             if (r < rows)
-                row_to_smem<T, DP>(sq + r * KS, A.q, b * A.qs[0] + t * A.qs[1] + (static_cast<int64_t>(h) * A.G + g) * A.qs[2],
-                                   A.D, tid & 7, 8, vec);
+                row_to_smem<T, DP>(sq + r * KS, A.q, from, A.D, tid & 7, 8, vec);
             else
                 for (int c = tid & 7; c < DP; c += 8) sq[r * KS + c] = 0.f;
         }
@@ -156,7 +181,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
             for (int c = 0; c < DC * 4; ++c) acc[i][c] = 0.f;
 
         for (int t = pc.t0; t < pc.t1; ++t) {
-            const bool tree = t == pc.prefix;
+            const bool tree = !PREFIX && t == pc.prefix;
             const int valid = tree ? n : min(BN, pc.len - t * BN);
             pid = page_of(t + 1);
             cp_async_wait<1>();  // the keys
@@ -313,7 +338,11 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         }
 
         const int flag = s_flag;
-        if (A.flags && tid == 0 && h == 0 && mtile == 0) A.flags[b] = flag;
+        if constexpr (PREFIX) {
+            if (tid == 0 && h == 0 && pc.mt == 0 && pc.t0 == 0) A.flags[b] = flag;
+        } else {
+            if (A.flags && tid == 0 && h == 0 && mtile == 0) A.flags[b] = flag;
+        }
         const bool whole = pc.whole();
         float *slot = whole ? nullptr : A.part + attn_slot(A, group, mtile, pc.first) * attn_slot_floats(BM, A.D);
 #pragma unroll
@@ -321,9 +350,14 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
             const int r = 2 * ty + i;
             if (row0 + r >= rows_n || r >= rows) continue;
             const float l = flag ? NAN : sl[r];
-            if (whole) {
+            size_t at;
+            if constexpr (PREFIX) {
+                at = prefix_row(A, pc, r);
+            } else {
                 const int t = (row0 + r) / A.G, hq = h * A.G + row0 + r - t * A.G;
-                const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
+                at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
+            }
+            if (!PREFIX && whole && !A.row_o) {
                 const float inv = 1.f / l;
                 T *o = static_cast<T *>(A.out) + at * A.D;
 #pragma unroll
@@ -333,21 +367,22 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                 }
                 if (A.lse && tx == 0) A.lse[at] = (sm[r] * A.scale_log2 + log2f(l)) * LN2;
             } else {
-                float *o = slot + 2 * BM + static_cast<size_t>(r) * A.D;
+                float *o = whole ? A.row_o + at * A.D : slot + 2 * BM + static_cast<size_t>(r) * A.D;
 #pragma unroll
                 for (int c = 0; c < DC * 4; ++c) {
                     const int d = 64 * (c >> 2) + 4 * tx + (c & 3);
                     if (d < A.D) o[d] = acc[i][c];
                 }
                 if (tx == 0) {
-                    slot[r] = sm[r] * A.scale_log2;
-                    slot[BM + r] = l;
+                    *(whole ? A.row_m + at : slot + r) = sm[r] * A.scale_log2;
+                    *(whole ? A.row_l + at : slot + BM + r) = l;
                 }
             }
         }
         __syncthreads();
     }
-    if (mtile == 0 && tid == 0) attn_write_desc(A, group, W, walk.hi, last);
+    if (mtile == 0 && tid == 0) attn_report(A, group, W, *reinterpret_cast<const Walk *>(s_begin));
+    if (!PREFIX && A.overlap) pdl_wait();  // the join waits for this kernel, and so for the one before
 }
 
 // Join one unit that begins in group blockIdx.x / mtiles and goes on in the
@@ -439,6 +474,143 @@ __global__ void __launch_bounds__(JOIN_THREADS, Store<T>::ES == 4 ? 5 : 10) attn
     if (A.lse && lane == 0) A.lse[at] = (ref + log2f(l)) * LN2;
 }
 
+// Join of a sequence's own parts (A) with those of its prefix (S), both from
+// the kernels above: a warp takes one row of the output, finds the row's two
+// units and joins their parts as attn_join_impl does, the prefix's first.
+template <typename T, int NQ>
+__global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TreeAttnArgs S) {
+    constexpr int AHEAD = 4;
+    pdl_wait();
+    pdl_next();
+    const int lane = threadIdx.x & 31;
+    const long long at = static_cast<long long>(blockIdx.x) * JOIN_ROWS + (threadIdx.x >> 5), token = at / A.Hq;
+    if (token >= static_cast<long long>(A.B) * A.T) return;
+    const int hq = static_cast<int>(at - token * A.Hq), b = static_cast<int>(token / A.T), t = static_cast<int>(token - static_cast<long long>(b) * A.T);
+    const int h = hq / A.G, g = hq - h * A.G;
+    bool bad_nodes;
+    const int n = attn_nodes(A, b, bad_nodes);
+    const bool speaks = t == 0 && hq == 0;  // for the sequence
+    if (!speaks && t >= (bad_nodes ? A.T : n)) return;
+    const bool bad_starts = *S.bad_starts != 0;
+    int flag = __ldg(A.flags + b) | (bad_starts ? F_BAD_ID : 0);
+    // the sequence's prefix: the last that starts at or before it, 32 guesses at a time
+    int lo = 0, hi = S.B;
+    while (hi - lo > 1) {
+        const int stride = (hi - lo + 31) / 32, i = lo + lane * stride;
+        const uint32_t under = __ballot_sync(FULL, i < hi && __ldg(S.starts + i) <= b);
+        const int last = under ? 31 - __clz(under) : 0;
+        hi = min(hi, lo + (last + 1) * stride);
+        lo += last * stride;
+    }
+    const int p = lo;
+    bool bad_len;
+    const int plen = attn_len(S, p, bad_len);
+    if (bad_len) flag |= F_BAD_ID;
+    if (plen > 0 && !bad_starts) flag |= __ldg(S.flags + p);
+    if (speaks && A.flags_out && lane == 0) A.flags_out[b] = flag;
+    if (t >= (bad_nodes ? A.T : n)) return;
+
+    T *out = static_cast<T *>(A.out) + at * A.D;
+    if (flag) {
+        for (int c = lane; c < A.D; c += 32) put(out + c, NAN);
+        if (A.lse && lane == 0) A.lse[at] = NAN;
+        return;
+    }
+    // a row's parts: of a whole unit one, by rows; else one in a slot of each group
+    struct Parts {
+        const float *m, *o;          // the first part's maximum and row
+        long long l, m_next, o_next; // from the maximum to the sum; from the first part to the second, if there is one
+        long long step;              // from the second on
+        int n;
+    };
+    auto parts_of = [&](const TreeAttnArgs &X, int2 u, int mtile, int row) {
+        Parts q = {};
+        if (u.x == 0) {
+            q.m = X.row_m + at;
+            q.l = X.row_l - X.row_m;
+            q.o = X.row_o + at * X.D;
+            q.n = 1;
+            return q;
+        }
+        const long long slot = static_cast<long long>(attn_slot_floats(X.bm, X.D));
+        const int group = u.y >> 1;
+        const float *first = X.part + attn_slot(X, group, mtile, (u.y & 1) == 0) * slot;
+        q.m = first + row;
+        q.l = X.bm;
+        q.o = first + 2 * X.bm + static_cast<long long>(row) * X.D;
+        q.m_next = X.part + attn_slot(X, group + 1, mtile, true) * slot - first;
+        q.step = 2 * slot * X.mtiles;
+        q.n = u.x;
+        return q;
+    };
+    const int row = t * A.G + g;
+    Parts own = parts_of(A, __ldg(A.units + static_cast<size_t>(b) * A.Hkv + h), row / A.bm, row % A.bm), pre = {};
+    if (plen > 0) {
+        const int first = __ldg(S.starts + p);
+        const long long r = static_cast<long long>(b - first) * A.rows + row;
+        const int mt = static_cast<int>(r / S.tile_rows);
+        pre = parts_of(S, __ldg(S.units + prefix_unit(S, p, static_cast<long long>(first) * A.rows, mt, h)), 0, static_cast<int>(r - static_cast<long long>(mt) * S.tile_rows));
+    }
+    const int parts = pre.n + own.n;
+    auto far = [&](const Parts &q, int k) { return k == 0 ? 0ll : q.m_next + (k - 1) * q.step; };
+    auto m_of = [&](int k) { return k < pre.n ? pre.m + far(pre, k) : own.m + far(own, k - pre.n); };
+    auto o_of = [&](int k) { return k < pre.n ? pre.o + far(pre, k) : own.o + far(own, k - pre.n); };
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = max_nan(top, *m_of(k));
+#pragma unroll
+    for (int e = 1; e < 32; e <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, e));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f, o[NQ][4] = {};
+    const bool quads = A.D % 4 == 0;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float w = 0.f;
+        if (k0 + lane < parts) {
+            const float *m = m_of(k0 + lane);
+            w = exp2f(*m - ref);
+            l = fmaf(w, m[k0 + lane < pre.n ? pre.l : own.l], l);
+        }
+        const int here = min(32, parts - k0);
+        for (int i0 = 0; i0 < here; i0 += AHEAD) {
+            float4 x[AHEAD][NQ];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int c = 4 * lane + 128 * q;
+                    x[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i0 + i >= here || c >= A.D) continue;
+                    const float *s = o_of(k0 + i0 + i) + c;
+                    if (quads)
+                        x[i][q] = *reinterpret_cast<const float4 *>(s);
+                    else
+                        x[i][q] = make_float4(s[0], c + 1 < A.D ? s[1] : 0.f, c + 2 < A.D ? s[2] : 0.f, c + 3 < A.D ? s[3] : 0.f);
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float wi = __shfl_sync(FULL, w, (i0 + i) & 31);
+                if (i0 + i >= here) continue;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    o[q][0] = fmaf(wi, x[i][q].x, o[q][0]);
+                    o[q][1] = fmaf(wi, x[i][q].y, o[q][1]);
+                    o[q][2] = fmaf(wi, x[i][q].z, o[q][2]);
+                    o[q][3] = fmaf(wi, x[i][q].w, o[q][3]);
+                }
+            }
+        }
+    }
+    l = warp_allsum(l);
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = 4 * lane + 128 * q + e;
+            if (c < A.D) put(out + c, o[q][e] * inv);
+        }
+    if (A.lse && lane == 0) A.lse[at] = (ref + log2f(l)) * LN2;
+}
+
 }  // namespace
 
 uint32_t attn_simt_smem(int D) {
@@ -447,15 +619,26 @@ uint32_t attn_simt_smem(int D) {
     return static_cast<uint32_t>(f * 4 + MAX_NODES * 8);
 }
 
-const void *attn_simt_func(int dtype, int D) {
-    const int dc = D <= 64 ? 1 : D <= 128 ? 2 : 4;
-    if (dtype == 0)
-        return dc == 1   ? reinterpret_cast<const void *>(attn_simt_impl<float, 1>)
-               : dc == 2 ? reinterpret_cast<const void *>(attn_simt_impl<float, 2>)
-                         : reinterpret_cast<const void *>(attn_simt_impl<float, 4>);
-    return dc == 1   ? reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 1>)
-           : dc == 2 ? reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 2>)
-                     : reinterpret_cast<const void *>(attn_simt_impl<bf16_t, 4>);
+namespace {
+template <typename T, bool PREFIX>
+const void *pick(int D) {
+    return D <= 64    ? reinterpret_cast<const void *>(attn_simt_impl<T, 1, PREFIX>)
+           : D <= 128 ? reinterpret_cast<const void *>(attn_simt_impl<T, 2, PREFIX>)
+                      : reinterpret_cast<const void *>(attn_simt_impl<T, 4, PREFIX>);
+}
+}  // namespace
+
+const void *attn_simt_func(int dtype, int D, bool prefix) {
+    if (dtype == 0) return prefix ? pick<float, true>(D) : pick<float, false>(D);
+    return prefix ? pick<bf16_t, true>(D) : pick<bf16_t, false>(D);
+}
+
+const void *prefix_join_func(int dtype, int D) {
+    if (D <= 128)
+        return dtype == 0 ? reinterpret_cast<const void *>(prefix_join_impl<float, 1>)
+                          : reinterpret_cast<const void *>(prefix_join_impl<bf16_t, 1>);
+    return dtype == 0 ? reinterpret_cast<const void *>(prefix_join_impl<float, 2>)
+                      : reinterpret_cast<const void *>(prefix_join_impl<bf16_t, 2>);
 }
 
 const void *attn_join_func(int dtype, int D) {

@@ -69,14 +69,15 @@ def _bind(lib) -> None:
     import ctypes
 
     names = ("mtp_tree_attention", "mtp_tree_attention_workspace", "mtp_beam_select", "mtp_beam_select_workspace",
-             "mtp_beam_reorder", "mtp_tree_commit", "mtp_rope", "mtp_cache_append", "mtp_adjust_logits")
+             "mtp_beam_reorder", "mtp_tree_commit", "mtp_prefix_attention", "mtp_prefix_attention_workspace", "mtp_rope",
+             "mtp_cache_append", "mtp_adjust_logits")
     _binding().bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
 
 
 def unbind() -> None:
     """Another library was loaded: the next call looks its functions up."""
     if _native is not None:
-        _native.bind(*[0] * 9)
+        _native.bind(*[0] * 11)
 
 
 def _call(name, args):
@@ -154,6 +155,37 @@ def mtp_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_len,
                                              torch.empty(q.shape[:1], dtype=torch.int32, device=dev))
         _call("tree_attention",
               (q, k_new, v_new, k_cache, v_cache, page_table, cache_len, parents, n_nodes,
+               q.shape[-1] ** -0.5 if scale is None else scale, out.out, out.lse, out.row_flags, on.raw(torch, index, mine)))
+    return out
+
+
+def mtp_prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix_len, group_start, page_table, cache_len, parents=None,
+                         n_nodes=None, *, scale: Optional[float] = None, with_lse: bool = False,
+                         out: Optional[TreeAttentionResult] = None, stream=None) -> TreeAttentionResult:
+    """mtp_tree_attention for sequences that share prefixes, each prefix read
+    once for all of its sequences (see mtp_prefix_attention in
+    include/mtp_rs.h).
+
+    prefix_table [P, max_prefix_pages] and prefix_len [P] int32 are the pages
+    and tokens of the prefixes; sequences group_start[p] .. group_start[p + 1] - 1
+    (group_start [P + 1] int32, from 0 to B) continue prefix p with their own
+    cache_len tokens in the pages of page_table.  The rest is as in
+    mtp_tree_attention; all rows of a flagged sequence are NaN."""
+    torch = _m._torch()
+    index = q.get_device()
+    if out is not None and with_lse and out.lse is None:
+        raise ValueError("mtp_prefix_attention: with_lse needs out.lse")
+    with _on(torch, index, stream) as on:
+        mine = ()
+        if out is None:
+            if q.dim() != 4:
+                raise ValueError(f"q must have 4 dimensions, got {tuple(q.shape)}")
+            dev = q.device
+            out = mine = TreeAttentionResult(torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                             torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None,
+                                             torch.empty(q.shape[:1], dtype=torch.int32, device=dev))
+        _call("prefix_attention",
+              (q, k_new, v_new, k_cache, v_cache, prefix_table, prefix_len, group_start, page_table, cache_len, parents, n_nodes,
                q.shape[-1] ** -0.5 if scale is None else scale, out.out, out.lse, out.row_flags, on.raw(torch, index, mine)))
     return out
 
