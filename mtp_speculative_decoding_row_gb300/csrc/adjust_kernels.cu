@@ -8,14 +8,16 @@
 //   x = x - freq c - pres [c > 0] + sum of v's biases
 //   x = -inf                      where the mask has no bit.
 //
-// Memory bounds it: every logit is read and written once.  A block has a slice
-// of the vocabulary and some rows of one sequence.  It streams the rows through
-// their masks, counts the slice's tokens of the text in shared memory (integers:
-// the order of the atomic additions changes nothing), lists the entries that
-// anything but the mask changes, and writes those once more, a thread to an
-// entry.  A text's words crowd in few places: dealt out from a list they keep
-// all threads busy, where looking for them beside the streamed vectors left one
-// block with nearly all the work (64 x 4 rows, 8192 tokens: 118 us).  Rows
+// Memory bounds it: every logit is read and written once, by a kernel that
+// streams the rows through their masks.  A second one, a block to a slice of the
+// vocabulary of one sequence, counts the slice's tokens of the text in shared
+// memory (integers: the order of the atomic additions changes nothing) and lists
+// the entries that anything but the mask changes while the first still runs, then
+// rewrites those, a thread to an entry.  A text's words crowd in few places:
+// dealt out from a list they keep all threads busy (64 x 4 rows, 8192 tokens:
+// 118 us where they were looked for beside the streamed vectors, 63 us with the
+// list in one kernel, whose blocks spent their time in waits one after the other
+// -- counting, streaming, listing -- with room for four of them on an SM).  Rows
 // differ in their paths only; the few drafted tokens are looked up in the path
 // where they occur, so that one count serves all rows.
 #include "common.cuh"
@@ -24,7 +26,7 @@
 namespace mtp {
 namespace {
 
-constexpr int NT = ADJ_THREADS;
+constexpr int NT = ADJ_THREADS, CT = ADJ_COUNT_THREADS;
 // An entry of the table: in the text's first part; a drafted token; has a
 // bias; occurrences in the rest of the text.
 constexpr uint32_t PROMPT = 1u, DRAFT = 2u, BIAS = 4u, ONE = 8u;
@@ -35,12 +37,24 @@ __device__ __forceinline__ uint32_t bf16_of(float lo, float hi) {
     return r;
 }
 
+// -inf in place of the elements whose bit is clear, the others bit for bit.
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[Store<T>::VEC]) {
-    if constexpr (Store<T>::ES == 4)
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    else
-        return make_uint4(bf16_of(x[0], x[1]), bf16_of(x[2], x[3]), bf16_of(x[4], x[5]), bf16_of(x[6], x[7]));
+__device__ __forceinline__ void masked(uint4 &x, uint32_t may) {
+    if constexpr (Store<T>::ES == 4) {
+        if (!(may & 1u)) x.x = 0xff800000u;
+        if (!(may & 2u)) x.y = 0xff800000u;
+        if (!(may & 4u)) x.z = 0xff800000u;
+        if (!(may & 8u)) x.w = 0xff800000u;
+    } else {
+        auto two = [](uint32_t w, uint32_t bits) {
+            const uint32_t keep = (bits & 1u) * 0xffffu | (bits & 2u) * 0x7fff8000u;
+            return (w & keep) | (0xff80ff80u & ~keep);
+        };
+        x.x = two(x.x, may);
+        x.y = two(x.y, may >> 2);
+        x.z = two(x.z, may >> 4);
+        x.w = two(x.w, may >> 6);
+    }
 }
 
 template <typename T>
@@ -67,10 +81,79 @@ struct Shared {
     int flag;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArgs A) {
-    constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES, AHEAD = 4, EARLY = 2, ROWS = 4;
+// Nodes that sequence b has (all rows where the count is none: they become NaN).
+__device__ __forceinline__ int nodes_of(const AdjArgs &A, int b, int &flag) {
+    const int n = A.nodes ? __ldg(A.nodes + b) : A.S;
+    if (n >= 0 && n <= A.S) return n;
+    flag |= F_BAD_ID;
+    return A.S;
+}
+
+// Bits of entries v, v + 1, .. v + VEC - 1 of a row's mask.
+template <int VEC>
+__device__ __forceinline__ uint32_t allowed(const uint32_t *mask, int v, int words) {
+    if (!mask) return ~0u;
+    const int i = v >> 5, r = v & 31;
+    const uint32_t w = __ldg(mask + i);
+    return r + VEC <= 32 ? w >> r : __funnelshift_r(w, i + 1 < words ? __ldg(mask + i + 1) : 0u, r);
+}
+
+// Row blockIdx.x through its mask: a block takes NT * AHEAD vectors, wherever the
+// row starts, and the first one the entries before and behind them.
+template <typename T, int AHEAD>
+__global__ void __launch_bounds__(NT, 8) mask_impl(const __grid_constant__ AdjArgs A) {
+    constexpr int VEC = Store<T>::VEC, ES = Store<T>::ES;
     constexpr uint32_t ALL = (1u << VEC) - 1u;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, b = blockIdx.x / A.S, s = blockIdx.x - b * A.S, words = (A.V + 31) / 32;
+    const bool in_place = A.out == A.z;
+    const uint32_t *mask = A.mask ? A.mask + b * A.mask_s[0] + s * A.mask_s[1] : nullptr;
+    const size_t row = static_cast<size_t>(blockIdx.x) * A.V;
+    const unsigned char *z = A.z + row * ES;
+    unsigned char *out = A.out + row * ES;
+    const int first = min(A.V, static_cast<int>((VEC - row % VEC) % VEC)), vecs = (A.V - first) / VEC, i0 = blockIdx.y * (NT * AHEAD) + tid;
+    uint4 x[AHEAD];
+    uint32_t may[AHEAD];
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+        const int i = i0 + a * NT;
+        if (i >= vecs) break;
+        x[a] = *reinterpret_cast<const uint4 *>(z + static_cast<size_t>(first + i * VEC) * ES);
+        may[a] = allowed<VEC>(mask, first + i * VEC, words);
+    }
+    int flag = 0;
+    const int n = nodes_of(A, b, flag);  // (the loads are on their way)
+    if (A.alone) {  // no second kernel follows
+        if (A.flags && s == 0 && blockIdx.y == 0 && tid == 0) A.flags[b] = flag;
+        if (flag) {
+            for (int v = blockIdx.y * (NT * AHEAD) * VEC + tid; v < min(A.V, (static_cast<int>(blockIdx.y) + 1) * (NT * AHEAD) * VEC); v += NT)
+                store1<T>(out + static_cast<size_t>(v) * ES, NAN);
+            return;
+        }
+    }
+    if (s >= n) return;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+        const int i = i0 + a * NT;
+        if (i >= vecs) break;
+        if ((may[a] & ALL) != ALL)
+            masked<T>(x[a], may[a]);
+        else if (in_place)
+            continue;
+        *reinterpret_cast<uint4 *>(out + static_cast<size_t>(first + i * VEC) * ES) = x[a];
+    }
+    if (blockIdx.y != 0) return;
+    const int tail = A.V - first - vecs * VEC;
+    if (tid < first + tail) {
+        const int v = tid < first ? tid : A.V - tail + (tid - first);
+        store1<T>(out + static_cast<size_t>(v) * ES, allowed<1>(mask, v, words) & 1u ? load1<T>(z + static_cast<size_t>(v) * ES) : -INFINITY);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ AdjArgs A) {
+    constexpr int ES = Store<T>::ES, ROWS = 4;
     extern __shared__ __align__(16) uint32_t smem[];
     uint32_t *table = smem;                                             // [slice]
     uint16_t *list = reinterpret_cast<uint16_t *>(table + A.slice);     // [slice] entries that are not 0
@@ -78,27 +161,19 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
     float *bias_of = reinterpret_cast<float *>(bias_id + A.n_bias);     // [n_bias]
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.x, s0 = blockIdx.z * A.rows;
+    const int b = blockIdx.x;
     const int lo = blockIdx.y * A.slice, hi = min(A.V, lo + A.slice);  // this block's tokens
     if (tid == 0) sh.flag = sh.listed = 0;
-    for (int i = tid; i < A.slice / 4; i += NT) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < A.slice / 4; i += CT) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    // (the first kernel has waited for those before it and writes nothing that is
+    // read before it is done)
+    if (!A.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- what the sequence has; every block finds the same flag ----
-    const int32_t *text = A.history + static_cast<size_t>(b) * A.L;
-    int4 early[EARLY];  // the text's first tokens are on their way while the rows go by
-#pragma unroll
-    for (int e = 0; e < EARLY; ++e) {
-        const int i = tid + e * NT;
-        early[e] = A.vec_history && 4 * i < A.L ? __ldg(reinterpret_cast<const int4 *>(text) + i) : make_int4(-1, -1, -1, -1);
-    }
     int flag = 0;
-    int n = A.nodes ? __ldg(A.nodes + b) : A.S, len = A.len ? __ldg(A.len + b) : 0, prompt = A.prompt ? __ldg(A.prompt + b) : 0;
-    if (n < 0 || n > A.S) {
-        flag |= F_BAD_ID;
-        n = A.S;
-    }
+    const int n = nodes_of(A, b, flag);
+    int len = A.len ? __ldg(A.len + b) : 0, prompt = A.prompt ? __ldg(A.prompt + b) : 0;
     if (len < 0 || len > A.L) {
         flag |= F_BAD_ID;
         len = 0;
@@ -106,62 +181,7 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
     if (prompt < 0 || prompt > len) flag |= F_BAD_ID;
     const float rho = A.rho ? __ldg(A.rho + b) : 1.f, freq = A.freq ? __ldg(A.freq + b) : 0.f, pres = A.pres ? __ldg(A.pres + b) : 0.f;
     if (!(rho > 0.f && rho < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) flag |= F_NONFINITE;
-    const int s1 = min(n, s0 + A.rows);
-
-    // ---- the rows through their masks ----
-    const int words = (A.V + 31) / 32;
-    const bool in_place = A.out == A.z;
-    auto mask_of = [&](int s) { return A.mask ? A.mask + b * A.mask_s[0] + s * A.mask_s[1] : nullptr; };
-    auto allowed = [&](const uint32_t *mask, int v) {  // bits of entries v, v + 1, .. v + VEC - 1
-        if (!mask) return ~0u;
-        const int i = v >> 5, r = v & 31;
-        const uint32_t w = __ldg(mask + i);
-        return r + VEC <= 32 ? w >> r : __funnelshift_r(w, i + 1 < words ? __ldg(mask + i + 1) : 0u, r);
-    };
     auto row_of = [&](int s) { return (static_cast<size_t>(b) * A.S + s) * A.V; };
-    if (!in_place || A.mask) {
-        for (int s = s0; s < s1; ++s) {
-            const size_t row = row_of(s);
-            const unsigned char *z = A.z + row * ES;
-            unsigned char *out = A.out + row * ES;
-            const uint32_t *mask = mask_of(s);
-            // vectors of the row that lie in the slice, wherever the row starts
-            const int first = min(hi, lo + static_cast<int>((VEC - (row + lo) % VEC) % VEC)), vecs = (hi - first) / VEC;
-            for (int i0 = tid; i0 < vecs; i0 += NT * AHEAD) {
-                uint4 x[AHEAD];
-                uint32_t may[AHEAD];
-#pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    const int i = i0 + a * NT;
-                    if (i >= vecs) break;
-                    x[a] = *reinterpret_cast<const uint4 *>(z + static_cast<size_t>(first + i * VEC) * ES);
-                    may[a] = allowed(mask, first + i * VEC) & ALL;
-                }
-#pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    const int i = i0 + a * NT;
-                    if (i >= vecs) break;
-                    if (may[a] != ALL) {
-                        float y[VEC];
-                        Store<T>::unpack(x[a], y);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (!((may[a] >> e) & 1u)) y[e] = -INFINITY;
-                        x[a] = pack<T>(y);
-                    } else if (in_place) {
-                        continue;
-                    }
-                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(first + i * VEC) * ES) = x[a];
-                }
-            }
-            // the entries before the first vector and behind the last
-            const int head = first - lo, tail = hi - first - vecs * VEC;
-            if (tid < head + tail) {
-                const int v = tid < head ? lo + tid : hi - tail + (tid - head);
-                store1<T>(out + static_cast<size_t>(v) * ES, allowed(mask, v) & 1u ? load1<T>(z + static_cast<size_t>(v) * ES) : -INFINITY);
-            }
-        }
-    }
 
     // ---- the tree ----
     if (A.tokens && tid < 32) {
@@ -203,54 +223,57 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
             __syncwarp();
         }
     }
-    __syncthreads();  // the table is clear, the tokens are there
+    for (int i = tid; i < A.n_bias; i += CT) {
+        bias_id[i] = __ldg(A.bias_ids + static_cast<size_t>(b) * A.n_bias + i);
+        bias_of[i] = __ldg(A.bias + static_cast<size_t>(b) * A.n_bias + i);
+    }
+    __syncthreads();  // the table is clear, the tokens and biases are there
 
     // ---- the text, drafted tokens, biases ----
     {
+        int most = -1;
+        const int32_t *text = A.history + static_cast<size_t>(b) * A.L;
         auto see = [&](int id, int at) {
-            if (at >= len) return;
-            if (id >= A.V) flag |= F_BAD_ID;
-            if (id < lo || id >= hi) return;
+            most = max(most, id);
+            if (static_cast<uint32_t>(id - lo) >= static_cast<uint32_t>(hi - lo)) return;
             if (at < prompt)
                 atomicOr(table + (id - lo), PROMPT);
             else
                 atomicAdd(table + (id - lo), ONE);
         };
-        auto four = [&](const int4 &x, int at) {
-            see(x.x, at);
-            see(x.y, at + 1);
-            see(x.z, at + 2);
-            see(x.w, at + 3);
-        };
-        if (A.vec_history) {
-#pragma unroll
-            for (int e = 0; e < EARLY; ++e) four(early[e], 4 * (tid + e * NT));
+        const int vecs = A.vec_history ? len / 4 : 0;
 #pragma unroll 4
-            for (int i = tid + EARLY * NT; 4 * i < len; i += NT) four(__ldg(reinterpret_cast<const int4 *>(text) + i), 4 * i);
-        } else {
-#pragma unroll 4
-            for (int i = tid; i < len; i += NT) see(__ldg(text + i), i);
+        for (int i = tid; i < vecs; i += CT) {
+            const int4 x = __ldg(reinterpret_cast<const int4 *>(text) + i);
+            see(x.x, 4 * i);
+            see(x.y, 4 * i + 1);
+            see(x.z, 4 * i + 2);
+            see(x.w, 4 * i + 3);
         }
+#pragma unroll 4
+        for (int i = 4 * vecs + tid; i < len; i += CT) see(__ldg(text + i), i);
+        if (most >= A.V) flag |= F_BAD_ID;
     }
     if (A.tokens && tid < n) {
         const int id = sh.token[tid];
         if (id >= lo && id < hi) atomicOr(table + (id - lo), DRAFT);
     }
-    if (A.n_bias > 0 && tid < 32) {  // in their order, so that a sum of several has one value
-        const int32_t *ids = A.bias_ids + static_cast<size_t>(b) * A.n_bias;
-        const float *bias = A.bias + static_cast<size_t>(b) * A.n_bias;
+    if (A.n_bias > 0 && tid < 32) {  // this slice's, in their order, so that a sum of several has one value
         int found = 0;
         for (int i0 = 0; i0 < A.n_bias; i0 += 32) {
-            const int id = i0 + lane < A.n_bias ? __ldg(ids + i0 + lane) : -1;
+            const bool there = i0 + lane < A.n_bias;
+            const int id = there ? bias_id[i0 + lane] : -1;
+            const float value = there ? bias_of[i0 + lane] : 0.f;
             if (id >= A.V) flag |= F_BAD_ID;
             const bool in = id >= lo && id < hi;
             const uint32_t who = __ballot_sync(FULL, in);
             if (in) {
                 const int at = found + __popc(who & ((1u << lane) - 1u));
                 bias_id[at] = id;
-                bias_of[at] = __ldg(bias + i0 + lane);
+                bias_of[at] = value;
                 atomicOr(table + (id - lo), BIAS);
             }
+            __syncwarp();
             found += __popc(who);
         }
         if (lane == 0) sh.biases = found;
@@ -258,36 +281,43 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
     if (flag) atomicOr(&sh.flag, flag);
     __syncthreads();
     flag = sh.flag;
-    if (A.flags && tid == 0 && blockIdx.y == 0 && blockIdx.z == 0) A.flags[b] = flag;
+    if (A.flags && tid == 0 && blockIdx.y == 0) A.flags[b] = flag;
     if (flag) {
-        for (int s = s0; s < s1; ++s)
-            for (int v = lo + tid; v < hi; v += NT) store1<T>(A.out + (row_of(s) + v) * ES, NAN);
+        if (A.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int s = 0; s < n; ++s)
+            for (int v = lo + tid; v < hi; v += CT) store1<T>(A.out + (row_of(s) + v) * ES, NAN);
         return;
     }
 
     // ---- the entries that change ----
-    for (int i0 = tid - lane; i0 < hi - lo; i0 += NT) {
-        const bool on = i0 + lane < hi - lo && table[i0 + lane] != 0u;
-        const uint32_t who = __ballot_sync(FULL, on);
+    for (int i = tid; i < A.slice / 4; i += CT) {  // (a slice is a multiple of four times the threads of a warp)
+        const uint4 e = reinterpret_cast<const uint4 *>(table)[i];
+        const int mine = (e.x != 0u) + (e.y != 0u) + (e.z != 0u) + (e.w != 0u);
+        if (!__any_sync(FULL, mine)) continue;
+        int before = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(FULL, before, d);
+            if (lane >= d) before += o;
+        }
         int at = 0;
-        if (lane == 0 && who) at = atomicAdd(&sh.listed, __popc(who));
-        at = __shfl_sync(FULL, at, 0);
-        if (on) list[at + __popc(who & ((1u << lane) - 1u))] = static_cast<uint16_t>(i0 + lane);
+        if (lane == 31) at = atomicAdd(&sh.listed, before);
+        at = __shfl_sync(FULL, at, 31) + before - mine;
+        if (e.x) list[at++] = static_cast<uint16_t>(4 * i);
+        if (e.y) list[at++] = static_cast<uint16_t>(4 * i + 1);
+        if (e.z) list[at++] = static_cast<uint16_t>(4 * i + 2);
+        if (e.w) list[at++] = static_cast<uint16_t>(4 * i + 3);
     }
     __syncthreads();
-    const int listed = sh.listed, turns = (s1 - s0 + ROWS - 1) / ROWS;
-    for (int j = tid; j < listed * turns; j += NT) {
-        const int turn = j / listed, at = list[j - turn * listed], v = lo + at, r0 = s0 + turn * ROWS;
+    if (A.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int listed = sh.listed, turns = (n + ROWS - 1) / ROWS;
+    for (int j = tid; j < listed * turns; j += CT) {
+        const int turn = j / listed, at = list[j - turn * listed], v = lo + at, r0 = turn * ROWS;
         const uint32_t e = table[at];
-        float x[ROWS];
-        uint32_t may[ROWS];
+        float x[ROWS];  // as they are behind their masks
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (r0 + r >= s1) break;
-            x[r] = load1<T>(A.z + (row_of(r0 + r) + v) * ES);
-            const uint32_t *mask = mask_of(r0 + r);
-            may[r] = mask ? (__ldg(mask + (v >> 5)) >> (v & 31)) & 1u : 1u;
-        }
+        for (int r = 0; r < ROWS; ++r)
+            if (r0 + r < n) x[r] = load1<T>(A.out + (row_of(r0 + r) + v) * ES);
         float bias = 0.f;
         if (e & BIAS)
             for (int i = 0; i < sh.biases; ++i)
@@ -295,17 +325,21 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int s = r0 + r;
-            if (s >= s1) break;
+            if (s >= n) break;
             uint32_t count = e / ONE;
             if (e & DRAFT) {
                 const uint64_t path = sh.path[s];
                 for (int i = 0; i <= s; ++i) count += ((path >> i) & 1ull) && sh.token[i] == v ? 1u : 0u;
             }
             float y = x[r];
+            if (y == -INFINITY) {  // masked, or what no finite change would change
+                const uint32_t *mask = A.mask ? A.mask + b * A.mask_s[0] + s * A.mask_s[1] : nullptr;
+                if (bias < INFINITY || !(allowed<1>(mask, v, 0) & 1u)) continue;
+            }
             if (count > 0 || (e & PROMPT)) y = y > 0.f ? __fdiv_rn(y, rho) : y * rho;
             if (count > 0) y = fmaf(-freq, static_cast<float>(count), y) - pres;
             if (e & BIAS) y += bias;
-            if (may[r]) store1<T>(A.out + (row_of(s) + v) * ES, y);
+            store1<T>(A.out + (row_of(s) + v) * ES, y);
         }
     }
 }
@@ -314,6 +348,11 @@ __global__ void __launch_bounds__(NT) adjust_impl(const __grid_constant__ AdjArg
 
 const void *adj_func(int dtype) {
     return dtype == 0 ? reinterpret_cast<const void *>(adjust_impl<float>) : reinterpret_cast<const void *>(adjust_impl<bf16_t>);
+}
+
+const void *mask_func(int dtype, bool few) {
+    if (dtype == 0) return few ? reinterpret_cast<const void *>(mask_impl<float, 1>) : reinterpret_cast<const void *>(mask_impl<float, 4>);
+    return few ? reinterpret_cast<const void *>(mask_impl<bf16_t, 1>) : reinterpret_cast<const void *>(mask_impl<bf16_t, 4>);
 }
 
 uint32_t adj_smem(int slice, int n_bias) { return static_cast<uint32_t>(slice) * 6 + n_bias * 8; }

@@ -34,7 +34,7 @@ uint32_t rot_smem(const RotArgs &A);
 
 // ----------------------------------------------------- adjust logits ----
 
-constexpr int ADJ_THREADS = 256, ADJ_MAX_ROWS = 64, ADJ_MAX_BIAS = 1024;
+constexpr int ADJ_THREADS = 256, ADJ_COUNT_THREADS = 512, ADJ_MAX_ROWS = 64, ADJ_MAX_BIAS = 1024;
 
 struct AdjArgs {
     const unsigned char *z;  // [B, S, V]
@@ -50,10 +50,12 @@ struct AdjArgs {
     int32_t *flags;
     int B, S, V, L, n_bias;
     int slice;               // vocabulary entries of a block (a multiple of 32)
-    int rows;                // rows of a block
+    int alone;               // nothing but masks: the first kernel is the only one
+    int overlap;             // launched behind the kernel of the masks, beside which it may run
     int vec_history;         // 16-byte loads of the history are aligned
 };
 const void *adj_func(int dtype);
+const void *mask_func(int dtype, bool few);  // few: a block takes a quarter of the vectors
 uint32_t adj_smem(int slice, int n_bias);
 
 }  // namespace mtp

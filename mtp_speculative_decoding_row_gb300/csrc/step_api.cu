@@ -251,14 +251,23 @@ extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t strea
     A.S = a.S;
     A.V = a.V;
     A.vec_history = reinterpret_cast<uintptr_t>(a.history) % 16 == 0 && a.L % 4 == 0;
+    const void *adjust = adj_func(a.dtype);
+    // the shared memory of a block is at most 56 KB: the limit has to be raised
+    if (resident(dev, adjust, adj_smem(8192, MTP_MAX_BIAS), ADJ_COUNT_THREADS) < 1) return MTP_ERR_NO_DEVICE;
+    if (z != o || a.mask) {  // (in place and without a mask nothing is streamed)
+        const long long rows = static_cast<long long>(a.B) * a.S, vecs = (static_cast<long long>(a.V) * es + 15) / 16;
+        const bool few = rows * ((vecs + 4 * ADJ_THREADS - 1) / (4 * ADJ_THREADS)) < 4 * sms;
+        A.alone = !a.history && !a.tokens && a.n_bias == 0 && !a.repetition && !a.frequency && !a.presence;
+        const long long each = ADJ_THREADS * (few ? 1 : 4);
+        const int rc = launch(mask_func(a.dtype, few), dim3(static_cast<unsigned>(rows), static_cast<unsigned>((vecs + each - 1) / each)),
+                              ADJ_THREADS, 0, &A, stream);
+        if (rc != MTP_OK || A.alone) return rc;
+        A.overlap = 1;
+    }
     // Slices as large as leaves two blocks for every SM: each reads the text.
     A.slice = 8192;
     while (A.slice > 1024 && static_cast<long long>(a.B) * ((a.V + A.slice - 1) / A.slice) < 2 * sms) A.slice /= 2;
-    A.rows = a.S;
     // (the sequences next to one another: the first slices, of the most frequent
     // words, start first)
-    const dim3 grid(a.B, (a.V + A.slice - 1) / A.slice, (a.S + A.rows - 1) / A.rows);
-    // the shared memory of a block is at most 56 KB: the limit has to be raised
-    if (resident(dev, adj_func(a.dtype), adj_smem(8192, MTP_MAX_BIAS), ADJ_THREADS) < 1) return MTP_ERR_NO_DEVICE;
-    return launch(adj_func(a.dtype), grid, ADJ_THREADS, adj_smem(A.slice, A.n_bias), &A, stream);
+    return launch(adjust, dim3(a.B, (a.V + A.slice - 1) / A.slice), ADJ_COUNT_THREADS, adj_smem(A.slice, A.n_bias), &A, stream);
 }
