@@ -71,12 +71,15 @@ constexpr uint32_t UMMA_SMEM = 232448;  // 227 KB per CTA
 constexpr int UMMA_EXTRA = 3;
 struct UmmaPlan {
     const void *func;
-    int threads, bm, tile_rows, qrows, qbufs, slots;
+    int threads, bm, tile_rows, qrows, qbufs, slots, bn;
     uint32_t smem;
 };
 UmmaPlan attn_umma_plan(int D, int rows);
 // The kernel of the prefixes: `rows` query rows to a prefix on average, `most` in all.
 UmmaPlan prefix_umma_plan(int D, int rows, long long most);
+// Both of mtp_prefix_attention's kernels with few rows (csrc/few_attention_umma.cu):
+// heads of 128 (up to 32 rows) or 256 (up to 16), tiles of 128 keys.
+UmmaPlan few_umma_plan(int D, int rows, bool prefix);
 int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype, int D);
 const void *prefix_join_func(int dtype, int D);

@@ -22,7 +22,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct AttnPlan {
     const void *func = nullptr;
     uint32_t smem = 0;
-    int threads = 0, bm = 0, tile_rows = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
+    int threads = 0, bm = 0, tile_rows = 0, bn = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0, late_bytes = 0;
     bool whole = false;       // units are not split
@@ -49,7 +49,7 @@ bool umma_sizes(const mtp_tree_attention_args &a) {
 
 // Keys of a tile for these pages, and the tiles of a page table.
 void umma_tiles(const mtp_tree_attention_args &a, AttnPlan &p) {
-    const int bn = attn_umma_bn(a.D);
+    const int bn = p.bn;
     p.per_page = a.page_size > bn && a.page_size % bn != 0 ? (a.page_size + bn - 1) / bn : 0;
     p.ktile = a.page_size >= bn ? bn : bn / a.page_size * a.page_size;
 }
@@ -63,19 +63,30 @@ size_t slot_bytes(const AttnPlan &p, int D) {
     return (attn_slot_floats(p.bm, D) * 4 * 2 * p.groups * p.mtiles + 15) / 16 * 16;
 }
 
-int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p) {
+void set_umma(AttnPlan &p, const UmmaPlan &u) {
+    p.func = u.func;
+    p.smem = u.smem;
+    p.threads = u.threads;
+    p.bm = u.bm;
+    p.tile_rows = u.tile_rows;
+    p.qrows = u.qrows;
+    p.qbufs = u.qbufs;
+    p.slots = u.slots;
+    p.bn = u.bn;
+}
+
+// `few`: by the kernel for few rows (of mtp_prefix_attention), where it takes the
+// sizes.
+bool few_sizes(const mtp_tree_attention_args &a, long long rows) {
+    return ((a.D == 128 && rows <= 32) || (a.D == 256 && rows <= 16)) && (a.page_size % 8 == 0 || a.page_size >= 128);
+}
+
+int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p, bool few = false) {
     int dev, sms;
     if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
     p.rows = a.T * (a.Hq / a.Hkv);
     if (umma) {
-        const UmmaPlan u = attn_umma_plan(a.D, p.rows);
-        p.func = u.func;
-        p.smem = u.smem;
-        p.threads = u.threads;
-        p.bm = u.bm;
-        p.qrows = u.qrows;
-        p.qbufs = u.qbufs;
-        p.slots = u.slots;
+        set_umma(p, few && few_sizes(a, p.rows) ? few_umma_plan(a.D, p.rows, false) : attn_umma_plan(a.D, p.rows));
         umma_tiles(a, p);
     } else {
         p.func = attn_simt_func(a.dtype, a.D, false);
@@ -184,9 +195,18 @@ extern "C" int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *a
 
 namespace {
 
+// The caches' maps for tiles of bn keys.
+struct Maps {
+    CUtensorMap k, v;
+};
+bool cache_maps(const mtp_tree_attention_args &a, const TreeAttnArgs &A, int bn, Maps &m) {
+    const int boxrows = a.page_size < bn ? a.page_size : bn;
+    return cache_map(&m.k, a, a.k_cache, A.kcs, boxrows) && cache_map(&m.v, a, a.v_cache, A.vcs, boxrows);
+}
+
 // The kernel's arguments but for the plan and the workspace, and whether the
-// tensor-core kernel takes them (then the caches' maps).
-int attn_args(const mtp_tree_attention_args &a, TreeAttnArgs &A, bool &umma, CUtensorMap &kmap, CUtensorMap &vmap) {
+// tensor-core kernels may take them (if the caches can be mapped).
+int attn_args(const mtp_tree_attention_args &a, TreeAttnArgs &A, bool &umma) {
     if (!a.q || !a.k_new || !a.v_new || !a.k_cache || !a.v_cache || !a.page_table || !a.cache_len || !a.out || !a.workspace)
         return MTP_ERR_INVALID_ARG;
     const int es = a.dtype == MTP_DTYPE_F32 ? 4 : 2;
@@ -231,9 +251,7 @@ int attn_args(const mtp_tree_attention_args &a, TreeAttnArgs &A, bool &umma, CUt
     // the tensor cores wherever sizes and alignment allow: at one query row
     // of 128 they still keep up with the memory (a tile's products take 0.7
     // us, its bytes 1.5 us)
-    const int bn = attn_umma_bn(a.D), boxrows = a.page_size < bn ? a.page_size : bn;
-    umma = umma_sizes(a) && A.vec && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
-           cache_map(&kmap, a, a.k_cache, A.kcs, boxrows) && cache_map(&vmap, a, a.v_cache, A.vcs, boxrows);
+    umma = umma_sizes(a) && A.vec && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
     return MTP_OK;
 }
 
@@ -268,10 +286,11 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     if (rc != MTP_OK) return rc;
     if (a.B == 0) return MTP_OK;
     TreeAttnArgs A = {};
-    CUtensorMap kmap, vmap;
+    Maps maps;
     bool umma;
-    const int ac = attn_args(a, A, umma, kmap, vmap);
+    const int ac = attn_args(a, A, umma);
     if (ac != MTP_OK) return ac;
+    umma = umma && cache_maps(a, A, attn_umma_bn(a.D), maps);
     AttnPlan p;
     const int pc = attn_plan(a, umma, p);
     if (pc != MTP_OK) return pc;
@@ -280,7 +299,7 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
     A.late = reinterpret_cast<unsigned long long *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes);
     A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + p.desc_bytes + p.late_bytes);
     attn_set_plan(A, p, umma);
-    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, &kmap, &vmap);
+    const int e = launch(p.func, dim3(p.groups * p.mtiles), p.threads, p.smem, &A, stream, &maps.k, &maps.v);
     if (e != MTP_OK || !p.joins()) return e;
     return launch(attn_join_func(a.dtype, a.D), dim3(p.groups * p.mtiles, ((p.rows < p.bm ? p.rows : p.bm) + JOIN_ROWS - 1) / JOIN_ROWS), JOIN_THREADS, 0, &A, stream);
 }
@@ -310,15 +329,8 @@ int prefix_plan(const mtp_prefix_attention_args &x, bool umma, AttnPlan &p) {
     const long long all = static_cast<long long>(a.B) * p.rows;
     if (umma) {
         const long long mean = (all + x.prefixes - 1) / x.prefixes;
-        const UmmaPlan u = prefix_umma_plan(a.D, static_cast<int>(mean < 1024 ? mean : 1024), all);
-        p.func = u.func;
-        p.smem = u.smem;
-        p.threads = u.threads;
-        p.bm = u.bm;
-        p.tile_rows = u.tile_rows;
-        p.qrows = u.qrows;
-        p.qbufs = u.qbufs;
-        p.slots = u.slots;
+        const int rows = static_cast<int>(mean < 1024 ? mean : 1024);
+        set_umma(p, few_sizes(a, mean) ? few_umma_plan(a.D, rows, true) : prefix_umma_plan(a.D, rows, all));
         umma_tiles(a, p);
     } else {
         p.func = attn_simt_func(a.dtype, a.D, true);
@@ -382,7 +394,7 @@ extern "C" int64_t mtp_prefix_attention_workspace(const mtp_prefix_attention_arg
     for (int umma = 0; umma < (umma_sizes(args->own) ? 2 : 1); ++umma) {
         AttnPlan own, pre;
         TreeAttnArgs A = {}, S = {};
-        if (attn_plan(args->own, umma != 0, own) != MTP_OK || prefix_plan(*args, umma != 0, pre) != MTP_OK) return -1;
+        if (attn_plan(args->own, umma != 0, own, true) != MTP_OK || prefix_plan(*args, umma != 0, pre) != MTP_OK) return -1;
         const size_t bytes = prefix_layout(*args, own, pre, nullptr, A, S);
         if (bytes > most) most = bytes;
     }
@@ -398,15 +410,20 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     if (a.B == 0) return MTP_OK;
     if (!x.prefix_table || !x.prefix_len || !x.group_start) return MTP_ERR_INVALID_ARG;
     TreeAttnArgs A = {};
-    CUtensorMap kmap, vmap;
     bool umma;
-    const int ac = attn_args(a, A, umma, kmap, vmap);
+    const int ac = attn_args(a, A, umma);
     if (ac != MTP_OK) return ac;
     AttnPlan own, pre;
-    const int pc = attn_plan(a, umma, own);
-    if (pc != MTP_OK) return pc;
-    const int qc = prefix_plan(x, umma, pre);
-    if (qc != MTP_OK) return qc;
+    Maps own_maps, pre_maps;
+    for (;;) {
+        own = pre = AttnPlan();
+        const int pc = attn_plan(a, umma, own, true);
+        if (pc != MTP_OK) return pc;
+        const int qc = prefix_plan(x, umma, pre);
+        if (qc != MTP_OK) return qc;
+        if (!umma || (cache_maps(a, A, own.bn, own_maps) && cache_maps(a, A, pre.bn, pre_maps))) break;
+        umma = false;  // a cache that tiled copies cannot address
+    }
     TreeAttnArgs S = A;
     if (a.workspace_bytes < static_cast<int64_t>(prefix_layout(x, own, pre, a.workspace, A, S))) return MTP_ERR_INVALID_ARG;
     attn_set_plan(A, own, umma);
@@ -420,9 +437,9 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     S.sequences = a.B;
     S.B = x.prefixes;
     S.parents = S.nodes = nullptr;
-    const int e = launch(pre.func, dim3(pre.groups), pre.threads, pre.smem, &S, stream, &kmap, &vmap);
+    const int e = launch(pre.func, dim3(pre.groups), pre.threads, pre.smem, &S, stream, &pre_maps.k, &pre_maps.v);
     if (e != MTP_OK) return e;
-    const int f = launch(own.func, dim3(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &kmap, &vmap);
+    const int f = launch(own.func, dim3(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &own_maps.k, &own_maps.v);
     if (f != MTP_OK) return f;
     const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
     return launch(prefix_join_func(a.dtype, a.D), dim3(static_cast<unsigned>((rows + JOIN_ROWS - 1) / JOIN_ROWS)), JOIN_THREADS, 0, &A, stream, &S);

@@ -361,6 +361,46 @@ __device__ __noinline__ void add_far_values(float *part, bf16_t *out, const bf16
     }
 }
 
+// The new keys or values of n nodes into a slot, by one warp.  Of the keys no
+// more than the sequence's nodes is looked at; the values behind them are zero,
+// and so is one that is not finite (its rows get it later): those nodes' bits are
+// returned.
+template <int D, int BN>
+__device__ __forceinline__ uint64_t load_new(const TreeAttnArgs &A, unsigned char *dst, bool kv, int b, int h, int n) {
+    const int lane = threadIdx.x & 31;
+    uint64_t poison = 0;
+    const bf16_t *src = static_cast<const bf16_t *>(kv ? A.v_new : A.k_new);
+    const int64_t *st = kv ? A.vs : A.ks;
+    src += b * st[0] + h * st[2];
+    const int fill = (kv ? round16(n > 0 ? n : 1) : n) * (D / 8);
+#pragma unroll 1
+    for (int i0 = lane; i0 < fill; i0 += 32 * 4) {
+        uint4 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
+            y[e] = j < n ? __ldg(reinterpret_cast<const uint4 *>(src + j * st[1]) + u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
+            if (i0 + 32 * e >= fill) break;
+            if (kv) {
+                uint32_t w[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bool lo = (w[q] & 0x7f80u) == 0x7f80u, hi = (w[q] & 0x7f800000u) == 0x7f800000u;
+                    if (lo || hi) poison |= 1ull << j;
+                    w[q] = (lo ? 0u : w[q] & 0xffffu) | (hi ? 0u : w[q] & 0xffff0000u);
+                }
+                y[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4 *>(dst + (u >> 3) * (BN * 128) + sw128(j, u & 7)) = y[e];
+        }
+    }
+    return poison;
+}
+
 // Start copies of `rows` query rows from row `row` on, by `threads` threads, this
 // being number i.
 template <int D>
@@ -437,15 +477,15 @@ __device__ __noinline__ void give_up(const TreeAttnArgs &A, const Walk &begin, i
                     const int node = node_of(A, row0 + r), hq = p.h * A.G + row0 + r - node * A.G;
                     at = (static_cast<size_t>(p.b) * A.T + node) * A.Hq + hq;
                 }
-                if (PREFIX || A.row_o) {
+                if (A.row_o) {  // (of a prefix always)
                     if (tid == 0) {
                         A.row_m[at] = -INFINITY;
                         A.row_l[at] = NAN;
                     }
-                    continue;
+                } else {
+                    for (int c = tid; c < A.D; c += nt) static_cast<uint16_t *>(A.out)[at * A.D + c] = 0x7fffu;
+                    if (A.lse && tid == 0) A.lse[at] = NAN;
                 }
-                for (int c = tid; c < A.D; c += nt) static_cast<uint16_t *>(A.out)[at * A.D + c] = 0x7fffu;
-                if (A.lse && tid == 0) A.lse[at] = NAN;
             }
         } else {
             float *slot = A.part + attn_slot(A, group, mtile, p.first) * attn_slot_floats(A.bm, A.D);
@@ -773,41 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                 if (!ok) break;
                 ++grants;
                 for (int kv = 0; kv < 2; ++kv) {
-                    unsigned char *dst = ring + r.slot * C::SLOT;
-                    const bf16_t *src = static_cast<const bf16_t *>(kv ? A.v_new : A.k_new);
-                    const int64_t *st = kv ? A.vs : A.ks;
-                    src += b * st[0] + h * st[2];
-                    // Of the keys no more than the sequence's nodes is looked
-                    // at; the values behind them are zero, and so is one that
-                    // is not finite (its rows get it later).
-                    const int fill = (kv ? round16(n > 0 ? n : 1) : n) * (D / 8);
-                    {
-#pragma unroll 1
-                        for (int i0 = lane; i0 < fill; i0 += 32 * 4) {
-                            uint4 y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
-                                y[e] = j < n ? __ldg(reinterpret_cast<const uint4 *>(src + j * st[1]) + u) : make_uint4(0u, 0u, 0u, 0u);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = (i0 + 32 * e) / (D / 8), u = (i0 + 32 * e) % (D / 8);
-                                if (i0 + 32 * e >= fill) break;
-                                if (kv) {
-                                    uint32_t w[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        const bool lo = (w[q] & 0x7f80u) == 0x7f80u, hi = (w[q] & 0x7f800000u) == 0x7f800000u;
-                                        if (lo || hi) poison |= 1ull << j;
-                                        w[q] = (lo ? 0u : w[q] & 0xffffu) | (hi ? 0u : w[q] & 0xffff0000u);
-                                    }
-                                    y[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                                *reinterpret_cast<uint4 *>(dst + (u >> 3) * (C::BN * 128) + sw128(j, u & 7)) = y[e];
-                            }
-                        }
-                    }
+                    poison |= load_new<D, C::BN>(A, ring + r.slot * C::SLOT, kv != 0, b, h, n);
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ctl.full[r.full()]));
@@ -1126,6 +1132,7 @@ UmmaPlan umma_plan(int D, int rows, long long most) {
     }
     // the product reads 128 rows of every block of queries
     p.smem = p_bytes + q + p.slots * slot + static_cast<uint32_t>(sizeof(Ctl));
+    p.bn = attn_umma_bn(D);
     p.func = pick<PREFIX>(D, mode, [](auto, auto f) { return reinterpret_cast<const void *>(f); });
     p.threads = pick<PREFIX>(D, mode, [](auto c, auto) { return decltype(c)::NT; });
     return p;

@@ -122,6 +122,11 @@ CASES = [
     ("bf16", [3], [137], 2, 4, 2, 64, 13, [13, 26, 0], "random", None),
     ("bf16", [2], [40], 64, 8, 1, 64, 16, [12, 100], "random", [64, 33]),
     ("bf16", [1, 60], [90, 400], 1, 4, 1, 64, 16, [5] * 61, "chain", None),                    # one prefix has nearly all sequences
+    ("bf16", [3, 4], [300, 77], 4, 16, 2, 128, 64, [0, 1, 130, 128, 400, 5, 60], "random", [4, 0, 2, 4, 1, 3, 4]),  # 32 rows of a key head
+    ("bf16", [1, 2, 1], [700, 300, 15], 2, 8, 2, 256, 32, [3, 0, 129, 1000], "random", None),
+    ("bf16", [1, 1], [5000, 129], 3, 10, 2, 128, 16, [2000, 33], "chain", None),
+    ("bf16", [2], [5000], 5, 3, 1, 256, 128, [900, 127], "random", [5, 4]),
+    ("bf16", [1] * 70, [40] * 70, 1, 4, 1, 128, 8, [3] * 70, "chain", None),
     ("f32", [4], [100], 1, 8, 2, 64, 16, [0, 1, 16, 50], "chain", None),
     ("f32", [2, 0, 5, 1], [130, 50, 0, 257], 3, 8, 2, 128, 32, [3, 70, 0, 0, 1, 33, 64, 200], "random", [3, 3, 1, 0, 2, 3, 3, 2]),
     ("f32", [13], [999], 3, 9, 3, 50, 7, [8] * 13, "random", None),
@@ -222,12 +227,12 @@ def test_prefix_attention_bad_groups(dtype, starts):
     assert r.row_flags.tolist() == [mtp.ROW_BAD_ID] * 6 and r.out.isnan().all() and r.lse.isnan().all()
 
 
-@pytest.mark.parametrize("dtype, D", [("bf16", 128), ("bf16", 256), ("f32", 64)])
-def test_prefix_attention_repeatable_back_to_back(dtype, D):
+@pytest.mark.parametrize("dtype, D, Hq", [("bf16", 128, 8), ("bf16", 128, 20), ("bf16", 256, 8), ("f32", 64, 8)])
+def test_prefix_attention_repeatable_back_to_back(dtype, D, Hq):
     """The same bits every time, many launches behind one another."""
     rng = random.Random(D)
     sizes = [rng.randint(0, 12) for _ in range(7)] + [1]
-    x = prefix_case(25, dtype, sizes, [rng.choice([0, 1, 130, 700, 1500]) for _ in sizes], 3, 8, 2, D, 32,
+    x = prefix_case(25, dtype, sizes, [rng.choice([0, 1, 130, 700, 1500]) for _ in sizes], 3, Hq, 2, D, 32,
                     [rng.choice([0, 1, 60, 200]) for _ in range(sum(sizes))])
     a = run(x)
     g = on_gpu(x)
@@ -239,11 +244,32 @@ def test_prefix_attention_repeatable_back_to_back(dtype, D):
     assert wrong.item() == 0
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_prefix_attention_extreme_scores(dtype):
+@pytest.mark.parametrize("D, T, Hq", [(128, 2, 4), (128, 3, 20), (256, 2, 8), (64, 2, 8), (128, 20, 8)])
+def test_prefix_attention_values_out_of_sight(D, T, Hq):
+    """Infinite and NaN values of a node reach the rows that see it and no others."""
+    x = prefix_case(27, "bf16", [1, 1], [150, 30], T, Hq, 2, D, 16, [30, 150])
+    x["parents"] = torch.tensor([[-1] + [max(0, i - 2) for i in range(1, T)]] * 2, dtype=i32)
+    x["v_new"][0, 1, 0, 5], x["v_new"][0, 1, 1, D - 1], x["v_new"][1, 0, 1, 9] = math.inf, -math.inf, math.nan
+    r = mtp.mtp_prefix_attention(**on_gpu(x)).out.cpu()
+    y = dict(x, v_new=torch.where(x["v_new"].isfinite(), x["v_new"], torch.zeros_like(x["v_new"])))
+    want = mtp.mtp_prefix_attention(**on_gpu(y)).out.cpu()
+    assert want.isfinite().all()
+    for b, node, h, d, value in ((0, 1, 0, 5, math.inf), (0, 1, 1, D - 1, -math.inf), (1, 0, 1, 9, math.nan)):
+        for i in range(T):
+            j = i
+            while j > node:
+                j = int(x["parents"][b, j])
+            if j == node:
+                want[b, i, h * (Hq // 2):(h + 1) * (Hq // 2), d] = value
+    assert torch.equal(r.isnan(), want.isnan())
+    assert torch.equal(torch.nan_to_num(r, nan=0.0), torch.nan_to_num(want, nan=0.0))
+
+
+@pytest.mark.parametrize("dtype, D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_prefix_attention_extreme_scores(dtype, D):
     """The largest scores in the prefix for some rows, in the sequence's own
     tokens for others, far apart: weights of either side underflow."""
-    x = prefix_case(26, dtype, [4], [300], 2, 4, 2, 64, 16, [100, 100, 0, 33])
+    x = prefix_case(26, dtype, [4], [300], 2, 4, 2, D, 16, [100, 100, 0, 33])
     pos = torch.arange(300)
     x["k_cache"][x["prefix_table"][0].long()[pos // 16], pos % 16] += (pos / 20.0)[:, None, None].to(x["q"].dtype) * x["q"][0, 0, ::2][None]
     at = torch.arange(100)
@@ -296,7 +322,8 @@ def test_prefix_attention_no_sequences():
     assert mtp.mtp_prefix_attention(**x).out.shape == (0, 2, 4, 64)
 
 
-@pytest.mark.parametrize("sizes, T, Hq, D", [([40], 2, 8, 128), ([8, 8], 2, 8, 128), ([1, 2], 2, 4, 64), ([6, 3], 3, 8, 256)])
+@pytest.mark.parametrize("sizes, T, Hq, D", [([40], 2, 8, 128), ([8, 8], 2, 8, 128), ([1, 2], 2, 4, 64), ([6, 3], 3, 8, 256), ([1, 1], 2, 4, 128),
+                                                 ([1, 1], 2, 8, 256)])
 def test_prefix_attention_a_wait_that_runs_out_is_reported(sizes, T, Hq, D):
     """In every mode: a CTA of either kernel whose loader leaves out a signal gives
     up after its time.  Each row is NaN or right, exactly the sequences with NaN
