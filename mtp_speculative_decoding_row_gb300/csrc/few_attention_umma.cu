@@ -11,16 +11,16 @@
 // against all R rows in registers, and the products cost an eighth.  Nothing of a
 // tile is then summed over lanes: a thread keeps the sums of its own keys'
 // weights until a piece ends, and of the maxima the threads only vote whether
-// any row's reference has to rise (by more than 2^8, as in the other kernel);
-// where it has, and in a piece's first tile, the maxima are found by halving
-// exchanges.  Weights lie in shared memory as bfloat16 (in TMEM a product's
+// a score lies far above its row's reference; where one does the maxima are found
+// by halving exchanges.  Weights lie in shared memory as bfloat16 (in TMEM a product's
 // second operand cannot lie).
 //   warp 0      copies key and value tiles, as in the other kernel
 //   warp 1      issues the products; those with the keys of tile j + 1 before
 //               those with the values of tile j, so that the tensor cores' and
 //               the softmax's latencies overlap
-//   warp 3      new keys and values, masks, page tables
-//   warps 4..7  softmax, queries, results
+//   warp 2      masks, new values, page tables
+//   warp 3      queries, new keys
+//   warps 4..7  softmax, results
 // Two score buffers, two of weights and two accumulators: the next piece begins
 // while the last one's results are written.
 //
@@ -30,6 +30,11 @@
 
 namespace mtp {
 namespace {
+
+// A row's reference rises when a score lies 2^30 above it: the weights are then
+// at most 2^30, their sums far below float32's largest, and what float32 cannot
+// hold below a reference that low is nothing beside the largest weight.
+constexpr float RISE = 30.f;
 
 template <int D, int R>
 struct Few {
@@ -44,15 +49,15 @@ template <class Walk>
 struct FewControl {
     uint64_t full[2 * MAX_SLOTS], empty[MAX_SLOTS], s_full[2], s_empty[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty[2];
     uint64_t grant[8], masks[4], ready[4], done[4];  // as in the other kernel
-    uint64_t vote, tops, sums;                       // the softmax warps' exchanges
+    uint64_t vote, tops, sums, begun;                // the softmax warps' exchanges
     uint64_t mask[4][MAX_NODES];
     uint64_t poison[4];
-    int flag[4];
     int above[MAX_NODES];
     long long W;
     Walk begin;
     alignas(16) int votes[2][4];
     alignas(16) float top[2][32][4], sum[2][32][4];  // row, warp
+    alignas(16) float first[2][32];                  // scores of a piece's first key
     uint32_t tmem;
     int dead;
 };
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
             mbar_init(smem_addr(&ctl.p_full[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.o_free[i]), 4);
-            mbar_init(smem_addr(&ctl.q_full[i]), 128);
+            mbar_init(smem_addr(&ctl.q_full[i]), 32);
             mbar_init(smem_addr(&ctl.q_empty[i]), 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&ctl.grant[i]), 1);
@@ -145,6 +150,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
         mbar_init(smem_addr(&ctl.vote), 4);
         mbar_init(smem_addr(&ctl.tops), 4);
         mbar_init(smem_addr(&ctl.sums), 4);
+        mbar_init(smem_addr(&ctl.begun), 4);
         ctl.dead = 0;
         fence_mbar_init();
         tma_prefetch_map(&kmap);
@@ -288,68 +294,85 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
             }
             if (elect_one()) umma_commit(smem_addr(&ctl.q_empty[qi]));
             __syncwarp();
+            if (ok && have) pv();  // (the piece's results wait for it)
         }
-        if (ok && have) pv();
-    } else if (PREFIX && warp == 3) {
-        // --------------------------------------------- page tables ----
-        if (blockIdx.x == 0) prefix_check_starts(A);
-        for (int np = 0; ok && walk.next(A, pc); ++np) {
-            if (np >= 4) {
-                ok = wait_for(A, smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
-                ok = __all_sync(FULL, ok);
-                if (!ok) break;
-            }
-            if (np > 0 || A.fault_cta != static_cast<int>(blockIdx.x) + 1) mbar_arrive(smem_addr(&ctl.ready[np & 3]));
-            if (flags_owner(pc, 0)) {
-                const int flag = __reduce_or_sync(FULL, attn_check_pages(A, pc.b, pc.len, lane, LOADERS));
-                if (lane == 0) put_flag(A, pc.b, flag);
-            }
-        }
-    } else if (!PREFIX && warp == 3) {
-        // --------------------------------------- new keys and values ----
+    } else if (warp == 2 || warp == 3) {
+        // ---- warp 2: masks, new values, pages; warp 3: queries, new keys ----
+        // (One piece of a sequence or prefix looks at its pages and speaks for all:
+        // the join makes the rows of what is flagged NaN.)
         Ring r(A.slots);
         int grants = 0;
-        for (int np = 0; ok && walk.next(A, pc); ++np) {
-            const int b = pc.b, h = pc.h;
-            bool bad_len, bad_nodes;
-            attn_len(A, b, bad_len);
-            const int n = attn_nodes(A, b, bad_nodes);
-            if (np >= 4) {
+        // Queries of piece `np`, into the buffer that the piece before the last had.
+        auto copy_q = [&](const Piece &p, int np) {
+            const int qi = np & 1;
+            if (np >= 2) ok = wait_for(A, smem_addr(&ctl.q_empty[qi]), ((np >> 1) - 1) & 1) && ok;
+            ok = __all_sync(FULL, ok);
+            if (!ok) return;
+            if constexpr (PREFIX)
+                copy_prefix_queries<D>(A, p, 0, p.rows, sq + qi * C::CH * QBLOCK, lane, 32);
+            else
+                copy_queries<D>(static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2], A, 0, A.rows,
+                                sq + qi * C::CH * QBLOCK, lane, 32);
+            cp_async_wait_all();
+            fence_proxy_async();
+            mbar_arrive(smem_addr(&ctl.q_full[qi]));
+        };
+        if (PREFIX && warp == 2 && blockIdx.x == 0) prefix_check_starts(A);
+        Piece next;
+        bool more = walk.next(A, next);
+        if (warp == 3 && more) copy_q(next, 0);
+        for (int np = 0; ok && more; ++np) {
+            pc = next;
+            more = walk.next(A, next);
+            if (warp == 3 && more) copy_q(next, np + 1);
+            if (!ok) break;
+            if (warp == 2 && np >= 4) {
                 ok = wait_for(A, smem_addr(&ctl.done[np & 3]), ((np >> 2) - 1) & 1) && ok;
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
             }
-            int flag = (bad_len || bad_nodes) ? F_BAD_ID : 0;
-            flag |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, ctl.mask[np & 3], ctl.above);
-            mbar_arrive(smem_addr(&ctl.masks[np & 3]));
-            for (int t = pc.t0; t < min(pc.t1, pc.prefix); ++t) {
-                r.step();
-                r.step();
-            }
-            uint64_t poison = 0;
-            if (pc.t1 > pc.prefix) {
-                ok = wait_for(A, smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
-                ok = __all_sync(FULL, ok);
-                if (!ok) break;
-                ++grants;
-                for (int kv = 0; kv < 2; ++kv) {
-                    poison |= load_new<D, C::BN>(A, ring + r.slot * C::SLOT, kv != 0, b, h, n);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ctl.full[r.full()]));
+            int flag = 0;
+            if constexpr (!PREFIX) {
+                const int b = pc.b, h = pc.h;
+                bool bad_len, bad_nodes;
+                attn_len(A, b, bad_len);
+                const int n = attn_nodes(A, b, bad_nodes);
+                if (bad_len || bad_nodes) flag = F_BAD_ID;
+                if (warp == 2) {
+                    flag |= attn_masks(A.parents ? A.parents + static_cast<size_t>(b) * A.T : nullptr, n, ctl.mask[np & 3], ctl.above);
+                    mbar_arrive(smem_addr(&ctl.masks[np & 3]));
+                }
+                for (int t = pc.t0; t < min(pc.t1, pc.prefix); ++t) {
+                    r.step();
                     r.step();
                 }
+                uint64_t poison = 0;
+                if (pc.t1 > pc.prefix) {
+                    ok = wait_for(A, smem_addr(&ctl.grant[grants & 7]), (grants >> 3) & 1) && ok;
+                    ok = __all_sync(FULL, ok);
+                    if (!ok) break;
+                    ++grants;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (kv == (warp == 2)) {
+                            poison = load_new<D, C::BN>(A, ring + r.slot * C::SLOT, kv != 0, b, h, n);
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_addr(&ctl.full[r.full()]));
+                        }
+                        r.step();
+                    }
+                }
+                const uint32_t plo = __reduce_or_sync(FULL, static_cast<uint32_t>(poison));
+                const uint32_t phi = __reduce_or_sync(FULL, static_cast<uint32_t>(poison >> 32));
+                if (warp == 2 && lane == 0) ctl.poison[np & 3] = (static_cast<uint64_t>(phi) << 32) | plo;
             }
-            flag |= attn_check_pages(A, b, pc.len, lane, LOADERS);
-            flag = __reduce_or_sync(FULL, flag);
-            const uint32_t plo = __reduce_or_sync(FULL, static_cast<uint32_t>(poison));
-            const uint32_t phi = __reduce_or_sync(FULL, static_cast<uint32_t>(poison >> 32));
-            if (lane == 0) {
-                ctl.flag[np & 3] = flag;
-                ctl.poison[np & 3] = (static_cast<uint64_t>(phi) << 32) | plo;
-            }
+            if (warp == 3) continue;
             if (np > 0 || A.fault_cta != static_cast<int>(blockIdx.x) + 1) mbar_arrive(smem_addr(&ctl.ready[np & 3]));
-            if (A.flags && lane == 0 && flags_owner(pc, 0)) put_flag(A, b, flag);
+            if (flags_owner(pc, 0)) {
+                flag |= attn_check_pages(A, pc.b, pc.len, lane, LOADERS);
+                flag = __reduce_or_sync(FULL, flag);
+                if (lane == 0) put_flag(A, pc.b, flag);
+            }
         }
     } else if (warp >= 4) {
         // --------------------------------------------------- softmax ----
@@ -357,25 +380,8 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         Ring r(A.slots);
         int count = 0;                           // tiles so far
-        uint32_t votes = 0, exchanges = 0;
-        auto copy_q = [&](const Piece &p, int np) {
-            const int qi = (np & 1);
-            if (np >= 2) ok = wait_for(A, smem_addr(&ctl.q_empty[qi]), ((np >> 1) - 1) & 1) && ok;
-            ok = __all_sync(FULL, ok);
-            if (!ok) return;
-            if constexpr (PREFIX)
-                copy_prefix_queries<D>(A, p, 0, p.rows, sq + qi * C::CH * QBLOCK, wt, 128);
-            else
-                copy_queries<D>(static_cast<const bf16_t *>(A.q) + p.b * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2], A, 0, A.rows,
-                                sq + qi * C::CH * QBLOCK, wt, 128);
-        };
-        // (the turn before the first piece only loads its queries)
-        Piece next = {};
-        bool more = true;
-        for (int np = -1; ok && more; ++np) {
-            pc = next;
-            more = walk.next(A, next);
-            if (more) copy_q(next, np + 1);  // during this piece
+        uint32_t votes = 0, exchanges = 0, begun = 0;
+        for (int np = 0; ok && walk.next(A, pc); ++np) {
             bool bad = false;
             const int n = PREFIX ? 0 : attn_nodes(A, pc.b, bad);
             int live;  // rows of the piece
@@ -419,15 +425,33 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.s_empty[buf]));
+#pragma unroll
+                for (int i = 0; i < R; ++i) s[i] = (see >> i) & 1u ? __float_as_uint(__uint_as_float(s[i]) * A.scale_log2) : 0xff800000u;
+                if (first && !tree) {
+                    // any key's score serves as a reference until one lies far above it:
+                    // those of the first key, which all rows see
+                    if (wt == 0)
+#pragma unroll
+                        for (int i = 0; i < R; i += 4)
+                            *reinterpret_cast<uint4 *>(&ctl.first[np & 1][i]) = make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl.begun));
+                    ok = wait_for(A, smem_addr(&ctl.begun), begun & 1) && ok;
+                    ++begun;
+#pragma unroll
+                    for (int i = 0; i < R; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&ctl.first[np & 1][i]);
+                        m[i] = x.x;
+                        m[i + 1] = x.y;
+                        m[i + 2] = x.z;
+                        m[i + 3] = x.w;
+                    }
+                }
                 float over = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float x = (see >> i) & 1u ? __uint_as_float(s[i]) * A.scale_log2 : -INFINITY;
-                    s[i] = __float_as_uint(x);
-                    over = fmaxf(over, x - m[i]);  // (a NaN is passed over, as a maximum does)
-                }
+                for (int i = 0; i < R; ++i) over = fmaxf(over, __uint_as_float(s[i]) - m[i]);  // (a NaN is passed over, as a maximum does)
                 // does any row's reference have to rise?
-                const bool up = __any_sync(FULL, first || over > RESCALE);
+                const bool up = __any_sync(FULL, over > RISE);
                 if (lane == 0) {
                     ctl.votes[votes & 1][w] = up;
                     mbar_arrive(smem_addr(&ctl.vote));
@@ -451,7 +475,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
                         const float4 x = *reinterpret_cast<const float4 *>(ctl.top[exchanges & 1][i]);
                         const float y = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
                         f[i] = 1.f;
-                        if (y > m[i] + RESCALE || (m[i] == -INFINITY && y > m[i])) {
+                        if (y > m[i] + RISE || (m[i] == -INFINITY && y > m[i])) {
                             f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - y);
                             m[i] = y;
                         }
@@ -508,19 +532,12 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
                 ok = __all_sync(FULL, ok);
             }
             if (!ok) break;
-            if (more) {
-                cp_async_wait_all();
-                fence_proxy_async();
-                mbar_arrive(smem_addr(&ctl.q_full[(np + 1) & 1]));
-                if (!ok) break;
-            }
-            if (np < 0) continue;
             // ------------------------------------------------ results ----
             const float mine = join_rows<R, true>(l);
             if (R == 32 || (lane & 1) == 0) ctl.sum[np & 1][R == 32 ? lane : lane >> 1][w] = mine;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&ctl.sums));
-            ok = wait_for(A, smem_addr(&ctl.sums), np & 1) && ok;
+            if (w == 0) ok = wait_for(A, smem_addr(&ctl.sums), np & 1) && ok;
             ok = wait_for(A, smem_addr(&ctl.ready[np & 3]), (np >> 2) & 1) && ok;
             ok = wait_for(A, smem_addr(&ctl.o_done[(count - 1) & 1]), ((count - 1) >> 1) & 1) && ok;
             ok = __all_sync(FULL, ok);
@@ -528,14 +545,9 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
             tmem_fence_after_sync();
             const bool whole = pc.whole();
             float *slot = A.part + attn_slot(A, group, 0, pc.first) * attn_slot_floats(R, D);
-            auto row_at = [&](int i) {
-                if constexpr (PREFIX) {
-                    return prefix_row(A, pc, i);
-                } else {
-                    const int node = node_of(A, i);
-                    return (static_cast<size_t>(pc.b) * A.T + node) * A.Hq + pc.h * A.G + i - node * A.G;
-                }
-            };
+            const size_t place = unit_row(A, pc);
+            float *part_m = whole ? A.row_m + place : slot, *part_l = whole ? A.row_l + place : slot + R;
+            float *part_o = whole ? A.row_o + place * D : slot + 2 * R;
             uint64_t poison = 0;
             if constexpr (!PREFIX)
                 if (pc.t1 == pc.prefix + 1) poison = ctl.poison[np & 3];
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < R; ++i)
-                    if (i < live) (whole ? A.row_o + row_at(i) * D : slot + 2 * R + static_cast<size_t>(i) * D)[d] = __uint_as_float(o[i]);
+                    if (i < live) part_o[i * D + d] = __uint_as_float(o[i]);
             }
             if (w == 0) {
                 float top = 0.f;
@@ -565,11 +577,8 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
                     if (lane == i) top = m[i];
                 if (lane < live && lane < R) {
                     const float4 x = *reinterpret_cast<const float4 *>(ctl.sum[np & 1][lane]);
-                    float sum = (x.x + x.y) + (x.z + x.w);
-                    if (!PREFIX && ctl.flag[np & 3]) sum = NAN;
-                    const size_t at = row_at(lane);
-                    *(whole ? A.row_m + at : slot + lane) = top;
-                    *(whole ? A.row_l + at : slot + R + lane) = sum;
+                    part_m[lane] = top;
+                    part_l[lane] = (x.x + x.y) + (x.z + x.w);
                 }
             }
             tmem_fence_before_sync();

@@ -44,9 +44,10 @@ struct TreeAttnArgs {
     int fault_cta;              // 1 + a CTA whose loader leaves out a signal (tests), else 0
     // Attention with shared prefixes (mtp_prefix_attention): partial results of
     // all units go to a join of the two kernels' parts (null and 0 otherwise).
-    float *row_m, *row_l, *row_o;  // of whole units, by the row of the output: [B T Hq], [B T Hq], [B T Hq, D]
+    float *row_m, *row_l, *row_o;  // of whole units: maxima, sums and unnormalised rows, unit after unit (see unit_row)
     int2 *units;                   // of each unit: parts (0: whole), first part's slot (see attn_write_units)
     int32_t *flags_out;            // [B] or null: the sequences' flags, its own and its prefix's
+    int wide_out;                  // the output's rows may be stored four elements at a time
     int overlap;                   // launched behind the kernel of the prefixes, beside which it may run
     // The kernel of the prefixes: B, table, len, max_pages, flags and late are those of
     // the prefixes; q, T and the rows of the output those of the sequences.
@@ -84,6 +85,7 @@ int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype, int D);
 const void *prefix_join_func(int dtype, int D);
 constexpr int JOIN_ROWS = 4, JOIN_THREADS = 128;  // rows of a block, a warp each
+constexpr int PREFIX_JOIN_ROWS = JOIN_THREADS / 8;  // of prefix_join_func
 
 // ------------------------------------------------------- beam selection --
 

@@ -353,8 +353,8 @@ int prefix_plan(const mtp_prefix_attention_args &x, bool umma, AttnPlan &p) {
     return MTP_OK;
 }
 
-// The workspace: for each of the two kernels slots, whole units' results by
-// rows, the units' parts, flags and late reports.
+// The workspace: for each of the two kernels slots, whole units' results, the
+// units' parts, flags and late reports.
 struct PrefixSpace {
     size_t bytes = 0;
     unsigned char *base = nullptr;
@@ -370,17 +370,18 @@ size_t prefix_layout(const mtp_prefix_attention_args &x, const AttnPlan &own, co
     const mtp_tree_attention_args &a = x.own;
     PrefixSpace w;
     w.base = static_cast<unsigned char *>(base);
-    const size_t rows = static_cast<size_t>(a.B) * a.T * a.Hq;
     for (int k = 0; k < 2; ++k) {
         TreeAttnArgs &X = k ? S : A;
         const AttnPlan &p = k ? pre : own;
+        const size_t units = static_cast<size_t>(a.Hkv) * (k ? static_cast<size_t>(a.B) * p.rows / p.tile_rows + x.prefixes : a.B);
+        const size_t rows = units * (k ? p.tile_rows : p.rows);
         X.row_m = w.take<float>(rows);
         X.row_l = w.take<float>(rows);
         X.row_o = w.take<float>(rows * a.D);
         X.part = w.take<float>(p.whole ? 0 : p.part_bytes / 4);
         X.late = w.take<unsigned long long>(p.late_bytes / 8);
         X.flags = w.take<int32_t>(k ? x.prefixes : a.B);
-        X.units = w.take<int2>(static_cast<size_t>(a.Hkv) * (k ? static_cast<size_t>(a.B) * p.rows / p.tile_rows + x.prefixes : a.B));
+        X.units = w.take<int2>(units);
     }
     S.bad_starts = w.take<int32_t>(1);
     return w.bytes;
@@ -429,6 +430,7 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     attn_set_plan(A, own, umma);
     attn_set_plan(S, pre, umma);
     A.flags_out = a.row_flags;
+    A.wide_out = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.dtype == MTP_DTYPE_F32 ? 16 : 8) == 0;
     A.overlap = 1;
     S.table = x.prefix_table;
     S.len = x.prefix_len;
@@ -442,7 +444,7 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     const int f = launch(own.func, dim3(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &own_maps.k, &own_maps.v);
     if (f != MTP_OK) return f;
     const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
-    return launch(prefix_join_func(a.dtype, a.D), dim3(static_cast<unsigned>((rows + JOIN_ROWS - 1) / JOIN_ROWS)), JOIN_THREADS, 0, &A, stream, &S);
+    return launch(prefix_join_func(a.dtype, a.D), dim3(static_cast<unsigned>((rows + PREFIX_JOIN_ROWS - 1) / PREFIX_JOIN_ROWS)), JOIN_THREADS, 0, &A, stream, &S);
 }
 
 // ------------------------------------------------------- beam selection --

@@ -439,10 +439,12 @@ __device__ __forceinline__ void attn_report(const TreeAttnArgs &A, int g, long l
     while (w.next(A, p)) attn_write_unit(A, g, W, w.hi, p);
 }
 
-// The row of the output that row r of a piece's tile has.
-__device__ __forceinline__ size_t prefix_row(const TreeAttnArgs &A, const PrefixPiece &p, int r) {
-    const int d = node_of(A, p.rest + r);  // (rest < G, r < 256: (rest + r) G < 2^32)
-    return (static_cast<size_t>(p.start) * A.T + p.token + d) * A.Hq + p.h * A.G + (p.rest + r - d * A.G);
+// Where a whole unit's results lie, by rows: its first row's place.
+__device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const AttnPiece &p) {
+    return (static_cast<size_t>(p.b) * A.Hkv + p.h) * A.rows;
+}
+__device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const PrefixPiece &p) {
+    return prefix_unit(A, p.b, static_cast<long long>(p.start) * A.rows, p.mt, p.h) * A.tile_rows;
 }
 
 // By one warp: whether the starts rise from 0 to the number of sequences.

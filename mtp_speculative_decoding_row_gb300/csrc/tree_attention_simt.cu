@@ -350,14 +350,9 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
             const int r = 2 * ty + i;
             if (row0 + r >= rows_n || r >= rows) continue;
             const float l = flag ? NAN : sl[r];
-            size_t at;
-            if constexpr (PREFIX) {
-                at = prefix_row(A, pc, r);
-            } else {
-                const int t = (row0 + r) / A.G, hq = h * A.G + row0 + r - t * A.G;
-                at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
-            }
             if (!PREFIX && whole && !A.row_o) {
+                const int t = (row0 + r) / A.G, hq = h * A.G + row0 + r - t * A.G;
+                const size_t at = (static_cast<size_t>(b) * A.T + t) * A.Hq + hq;
                 const float inv = 1.f / l;
                 T *o = static_cast<T *>(A.out) + at * A.D;
 #pragma unroll
@@ -367,15 +362,16 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
                 }
                 if (A.lse && tx == 0) A.lse[at] = (sm[r] * A.scale_log2 + log2f(l)) * LN2;
             } else {
-                float *o = whole ? A.row_o + at * A.D : slot + 2 * BM + static_cast<size_t>(r) * A.D;
+                const size_t place = unit_row(A, pc) + row0 + r;
+                float *o = whole ? A.row_o + place * A.D : slot + 2 * BM + static_cast<size_t>(r) * A.D;
 #pragma unroll
                 for (int c = 0; c < DC * 4; ++c) {
                     const int d = 64 * (c >> 2) + 4 * tx + (c & 3);
                     if (d < A.D) o[d] = acc[i][c];
                 }
                 if (tx == 0) {
-                    *(whole ? A.row_m + at : slot + r) = sm[r] * A.scale_log2;
-                    *(whole ? A.row_l + at : slot + BM + r) = l;
+                    *(whole ? A.row_m + place : slot + r) = sm[r] * A.scale_log2;
+                    *(whole ? A.row_l + place : slot + BM + r) = l;
                 }
             }
         }
@@ -475,120 +471,134 @@ __global__ void __launch_bounds__(JOIN_THREADS, Store<T>::ES == 4 ? 5 : 10) attn
 }
 
 // Join of a sequence's own parts (A) with those of its prefix (S), both from
-// the kernels above: a warp takes one row of the output, finds the row's two
-// units and joins their parts as attn_join_impl does, the prefix's first.
+// the kernels above: eight lanes take one row of the output, find the row's two
+// units and join their parts as attn_join_impl does, the prefix's first.  What
+// bounds it is a chain of loads (flags and starts, lengths and units, maxima,
+// rows): with a warp to a row 8192 rows were two and a half rounds of it, now
+// they are one.
 template <typename T, int NQ>
 __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TreeAttnArgs S) {
-    constexpr int AHEAD = 4;
+    constexpr int LANES = 8, AHEAD = NQ <= 4 ? 2 : 1;
     pdl_wait();
     pdl_next();
-    const int lane = threadIdx.x & 31;
-    const long long at = static_cast<long long>(blockIdx.x) * JOIN_ROWS + (threadIdx.x >> 5), token = at / A.Hq;
-    if (token >= static_cast<long long>(A.B) * A.T) return;
+    const int lane = threadIdx.x & (LANES - 1), shift = threadIdx.x & 24;  // in the row's lanes; theirs in the warp
+    const long long rows = static_cast<long long>(A.B) * A.T * A.Hq, row_of_grid = (static_cast<long long>(blockIdx.x) * JOIN_THREADS + threadIdx.x) / LANES;
+    const bool there = row_of_grid < rows;
+    const long long at = there ? row_of_grid : rows - 1, token = at / A.Hq;
     const int hq = static_cast<int>(at - token * A.Hq), b = static_cast<int>(token / A.T), t = static_cast<int>(token - static_cast<long long>(b) * A.T);
     const int h = hq / A.G, g = hq - h * A.G;
-    bool bad_nodes;
-    const int n = attn_nodes(A, b, bad_nodes);
-    const bool speaks = t == 0 && hq == 0;  // for the sequence
-    if (!speaks && t >= (bad_nodes ? A.T : n)) return;
+    const size_t own_at = static_cast<size_t>(b) * A.Hkv + h;
+    const int2 own_unit = __ldg(A.units + own_at);
     const bool bad_starts = *S.bad_starts != 0;
     int flag = __ldg(A.flags + b) | (bad_starts ? F_BAD_ID : 0);
-    // the sequence's prefix: the last that starts at or before it, 32 guesses at a time
+    bool bad_nodes;
+    const int n = attn_nodes(A, b, bad_nodes);
+    // the sequence's prefix: the last that starts at or before it, 8 guesses at a time
     int lo = 0, hi = S.B;
-    while (hi - lo > 1) {
-        const int stride = (hi - lo + 31) / 32, i = lo + lane * stride;
-        const uint32_t under = __ballot_sync(FULL, i < hi && __ldg(S.starts + i) <= b);
+    while (__any_sync(FULL, hi - lo > 1)) {
+        const int stride = (hi - lo + LANES - 1) / LANES, i = lo + lane * stride;
+        const uint32_t under = (__ballot_sync(FULL, i < hi && __ldg(S.starts + i) <= b) >> shift) & 255u;
         const int last = under ? 31 - __clz(under) : 0;
         hi = min(hi, lo + (last + 1) * stride);
         lo += last * stride;
     }
-    const int p = lo;
+    const int p = lo, first = __ldg(S.starts + p);
     bool bad_len;
     const int plen = attn_len(S, p, bad_len);
     if (bad_len) flag |= F_BAD_ID;
-    if (plen > 0 && !bad_starts) flag |= __ldg(S.flags + p);
-    if (speaks && A.flags_out && lane == 0) A.flags_out[b] = flag;
-    if (t >= (bad_nodes ? A.T : n)) return;
-
+    const bool shared = plen > 0 && !bad_starts;
+    const int row = t * A.G + g;
+    int mt = 0, prow = 0;
+    int2 pre_unit = make_int2(0, 0);
+    size_t pre_at = 0;
+    if (shared) {
+        const long long r = static_cast<long long>(b - first) * A.rows + row;
+        mt = static_cast<int>(r / S.tile_rows);
+        prow = static_cast<int>(r - static_cast<long long>(mt) * S.tile_rows);
+        pre_at = prefix_unit(S, p, static_cast<long long>(first) * A.rows, mt, h);
+        pre_unit = __ldg(S.units + pre_at);
+        flag |= __ldg(S.flags + p);
+    }
+    if (there && t == 0 && hq == 0 && A.flags_out && lane == 0) A.flags_out[b] = flag;
+    const bool live = there && t < (bad_nodes ? A.T : n);
     T *out = static_cast<T *>(A.out) + at * A.D;
-    if (flag) {
-        for (int c = lane; c < A.D; c += 32) put(out + c, NAN);
+    if (live && flag) {
+        for (int c = lane; c < A.D; c += LANES) put(out + c, NAN);
         if (A.lse && lane == 0) A.lse[at] = NAN;
-        return;
     }
     // a row's parts: of a whole unit one, by rows; else one in a slot of each group
     struct Parts {
-        const float *m, *o;          // the first part's maximum and row
-        long long l, m_next, o_next; // from the maximum to the sum; from the first part to the second, if there is one
-        long long step;              // from the second on
+        const float *m, *o;    // the first part's maximum and row
+        long long l;           // from the maximum to the sum
+        long long next, step;  // from the first part to the second, if there is one; from each to the next
         int n;
     };
-    auto parts_of = [&](const TreeAttnArgs &X, int2 u, int mtile, int row) {
+    auto parts_of = [&](const TreeAttnArgs &X, int2 u, size_t place, int mtile, int r) {
         Parts q = {};
         if (u.x == 0) {
-            q.m = X.row_m + at;
+            q.m = X.row_m + place;
             q.l = X.row_l - X.row_m;
-            q.o = X.row_o + at * X.D;
+            q.o = X.row_o + place * X.D;
             q.n = 1;
             return q;
         }
         const long long slot = static_cast<long long>(attn_slot_floats(X.bm, X.D));
         const int group = u.y >> 1;
-        const float *first = X.part + attn_slot(X, group, mtile, (u.y & 1) == 0) * slot;
-        q.m = first + row;
+        const float *start = X.part + attn_slot(X, group, mtile, (u.y & 1) == 0) * slot;
+        q.m = start + r;
         q.l = X.bm;
-        q.o = first + 2 * X.bm + static_cast<long long>(row) * X.D;
-        q.m_next = X.part + attn_slot(X, group + 1, mtile, true) * slot - first;
+        q.o = start + 2 * X.bm + static_cast<long long>(r) * X.D;
+        q.next = X.part + attn_slot(X, group + 1, mtile, true) * slot - start;
         q.step = 2 * slot * X.mtiles;
         q.n = u.x;
         return q;
     };
-    const int row = t * A.G + g;
-    Parts own = parts_of(A, __ldg(A.units + static_cast<size_t>(b) * A.Hkv + h), row / A.bm, row % A.bm), pre = {};
-    if (plen > 0) {
-        const int first = __ldg(S.starts + p);
-        const long long r = static_cast<long long>(b - first) * A.rows + row;
-        const int mt = static_cast<int>(r / S.tile_rows);
-        pre = parts_of(S, __ldg(S.units + prefix_unit(S, p, static_cast<long long>(first) * A.rows, mt, h)), 0, static_cast<int>(r - static_cast<long long>(mt) * S.tile_rows));
+    Parts own = {}, pre = {};
+    if (live && !flag) {
+        own = parts_of(A, own_unit, own_at * A.rows + row, row / A.bm, row % A.bm);
+        if (shared) pre = parts_of(S, pre_unit, pre_at * S.tile_rows + prow, 0, prow);
     }
     const int parts = pre.n + own.n;
-    auto far = [&](const Parts &q, int k) { return k == 0 ? 0ll : q.m_next + (k - 1) * q.step; };
+    auto far = [&](const Parts &q, int k) { return k == 0 ? 0ll : q.next + (k - 1) * q.step; };
     auto m_of = [&](int k) { return k < pre.n ? pre.m + far(pre, k) : own.m + far(own, k - pre.n); };
     auto o_of = [&](int k) { return k < pre.n ? pre.o + far(pre, k) : own.o + far(own, k - pre.n); };
     float top = -INFINITY;
-    for (int k = lane; k < parts; k += 32) top = max_nan(top, *m_of(k));
+    for (int k = lane; k < parts; k += LANES) top = max_nan(top, *m_of(k));
 #pragma unroll
-    for (int e = 1; e < 32; e <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, e));
+    for (int e = 1; e < LANES; e <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, e));
     const float ref = top == -INFINITY ? 0.f : top;
     float l = 0.f, o[NQ][4] = {};
     const bool quads = A.D % 4 == 0;
-    for (int k0 = 0; k0 < parts; k0 += 32) {
+    for (int k0 = 0; __any_sync(FULL, k0 < parts); k0 += LANES) {
         float w = 0.f;
         if (k0 + lane < parts) {
             const float *m = m_of(k0 + lane);
             w = exp2f(*m - ref);
             l = fmaf(w, m[k0 + lane < pre.n ? pre.l : own.l], l);
         }
-        const int here = min(32, parts - k0);
-        for (int i0 = 0; i0 < here; i0 += AHEAD) {
+#pragma unroll
+        for (int i0 = 0; i0 < LANES; i0 += AHEAD) {
+            if (!__any_sync(FULL, k0 + i0 < parts)) break;
             float4 x[AHEAD][NQ];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
+            for (int i = 0; i < AHEAD; ++i) {
+                const float *from = k0 + i0 + i < parts ? o_of(k0 + i0 + i) : nullptr;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    const int c = 4 * lane + 128 * q;
+                    const int c = 4 * lane + 4 * LANES * q;
                     x[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i0 + i >= here || c >= A.D) continue;
-                    const float *s = o_of(k0 + i0 + i) + c;
+                    if (!from || c >= A.D) continue;
+                    const float *s = from + c;
                     if (quads)
                         x[i][q] = *reinterpret_cast<const float4 *>(s);
                     else
                         x[i][q] = make_float4(s[0], c + 1 < A.D ? s[1] : 0.f, c + 2 < A.D ? s[2] : 0.f, c + 3 < A.D ? s[3] : 0.f);
                 }
+            }
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                const float wi = __shfl_sync(FULL, w, (i0 + i) & 31);
-                if (i0 + i >= here) continue;
+                const float wi = __shfl_sync(FULL, w, i0 + i, LANES);
+                if (k0 + i0 + i >= parts) continue;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     o[q][0] = fmaf(wi, x[i][q].x, o[q][0]);
@@ -599,15 +609,29 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
             }
         }
     }
-    l = warp_allsum(l);
+#pragma unroll
+    for (int e = 1; e < LANES; e <<= 1) l += __shfl_xor_sync(FULL, l, e);
+    if (!live || flag) return;
     const float inv = 1.f / l;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
+    for (int q = 0; q < NQ; ++q) {
+        const int c = 4 * lane + 4 * LANES * q;
+        if (c >= A.D) break;
+        if (A.wide_out) {
+            if constexpr (Store<T>::ES == 4)
+                *reinterpret_cast<float4 *>(out + c) = make_float4(o[q][0] * inv, o[q][1] * inv, o[q][2] * inv, o[q][3] * inv);
+            else {
+                uint2 y;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(o[q][1] * inv), "f"(o[q][0] * inv));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(o[q][3] * inv), "f"(o[q][2] * inv));
+                *reinterpret_cast<uint2 *>(out + c) = y;
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = 4 * lane + 128 * q + e;
-            if (c < A.D) put(out + c, o[q][e] * inv);
+            for (int e = 0; e < 4; ++e)
+                if (c + e < A.D) put(out + c + e, o[q][e] * inv);
         }
+    }
     if (A.lse && lane == 0) A.lse[at] = (ref + log2f(l)) * LN2;
 }
 
@@ -633,13 +657,16 @@ const void *attn_simt_func(int dtype, int D, bool prefix) {
     return prefix ? pick<bf16_t, true>(D) : pick<bf16_t, false>(D);
 }
 
-const void *prefix_join_func(int dtype, int D) {
-    if (D <= 128)
-        return dtype == 0 ? reinterpret_cast<const void *>(prefix_join_impl<float, 1>)
-                          : reinterpret_cast<const void *>(prefix_join_impl<bf16_t, 1>);
-    return dtype == 0 ? reinterpret_cast<const void *>(prefix_join_impl<float, 2>)
-                      : reinterpret_cast<const void *>(prefix_join_impl<bf16_t, 2>);
+namespace {
+template <typename T>
+const void *pick_join(int D) {
+    return D <= 64    ? reinterpret_cast<const void *>(prefix_join_impl<T, 2>)
+           : D <= 128 ? reinterpret_cast<const void *>(prefix_join_impl<T, 4>)
+                      : reinterpret_cast<const void *>(prefix_join_impl<T, 8>);
 }
+}  // namespace
+
+const void *prefix_join_func(int dtype, int D) { return dtype == 0 ? pick_join<float>(D) : pick_join<bf16_t>(D); }
 
 const void *attn_join_func(int dtype, int D) {
     if (D <= 128)

@@ -470,19 +470,14 @@ __device__ __noinline__ void give_up(const TreeAttnArgs &A, const Walk &begin, i
         }
         if (p.whole()) {
             for (int r = 0; r < live; ++r) {
-                size_t at;
-                if constexpr (PREFIX) {
-                    at = prefix_row(A, p, r);
-                } else {
-                    const int node = node_of(A, row0 + r), hq = p.h * A.G + row0 + r - node * A.G;
-                    at = (static_cast<size_t>(p.b) * A.T + node) * A.Hq + hq;
-                }
                 if (A.row_o) {  // (of a prefix always)
                     if (tid == 0) {
-                        A.row_m[at] = -INFINITY;
-                        A.row_l[at] = NAN;
+                        A.row_m[unit_row(A, p) + row0 + r] = -INFINITY;
+                        A.row_l[unit_row(A, p) + row0 + r] = NAN;
                     }
                 } else {
+                    const int node = node_of(A, row0 + r), hq = p.h * A.G + row0 + r - node * A.G;
+                    const size_t at = (static_cast<size_t>(p.b) * A.T + node) * A.Hq + hq;
                     for (int c = tid; c < A.D; c += nt) static_cast<uint16_t *>(A.out)[at * A.D + c] = 0x7fffu;
                     if (A.lse && tid == 0) A.lse[at] = NAN;
                 }
@@ -1000,9 +995,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             }
             uint64_t seen = 0;
             size_t at = 0;
-            if constexpr (PREFIX) {
-                if (live) at = prefix_row(A, pc, lrow);
-            } else {
+            if constexpr (!PREFIX) {
                 const int flag = ctl.flag[np & 3];
                 if (pc.t1 == pc.prefix + 1 && live && node < n) seen = ctl.mask[np & 3][node] & ctl.poison[np & 3];
                 if (flag) l = NAN;
@@ -1012,7 +1005,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
             // the finished row, or a part of it: of a whole unit by rows, else in a slot
             const bool whole = pc.whole(), done = !PREFIX && whole && !A.row_o;
             float *slot = A.part + attn_slot(A, group, mtile, pc.first) * attn_slot_floats(BM, D);
-            float *part_o = whole ? A.row_o + at * D : slot + 2 * BM + static_cast<size_t>(lrow) * D;
+            const size_t place = unit_row(A, pc) + row0 + lrow;
+            float *part_o = whole ? A.row_o + place * D : slot + 2 * BM + static_cast<size_t>(lrow) * D;
             const float inv = 1.f / l;
             // columns of this group (a piece of one tile: the first group had it, and has all)
             const int c0 = two ? wg * (D / 2) : 0, c1 = two ? c0 + D / 2 : C::TURNS && wg == 1 ? 0 : D;
@@ -1055,8 +1049,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
                                    A.vs[1], seen, c0, c1);
                 if (mine && c0 == 0 && c1 > 0) {
                     if (!done) {
-                        *(whole ? A.row_m + at : slot + lrow) = m;
-                        *(whole ? A.row_l + at : slot + BM + lrow) = l;
+                        *(whole ? A.row_m + place : slot + lrow) = m;
+                        *(whole ? A.row_l + place : slot + BM + lrow) = l;
                     } else if (A.lse) {
                         A.lse[at] = (m + log2f(l)) * LN2;
                     }
