@@ -242,6 +242,7 @@ int attn_args(const mtp_tree_attention_args &a, TreeAttnArgs &A, bool &umma) {
     A.D = a.D;
     A.G = a.Hq / a.Hkv;
     A.g_inverse = A.G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + A.G - 1) / A.G);
+    A.t_inverse = A.T == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + A.T - 1) / A.T);
     A.num_pages = a.num_pages;
     A.page_size = a.page_size;
     A.max_pages = a.max_pages;

@@ -118,8 +118,8 @@ __device__ __forceinline__ int prefix_group(const TreeAttnArgs &A, int p, int &c
 // the prefix's first row.  (Tiles of one prefix are tile_rows rows apart, and
 // ceil(c) - 1 + floor(a) <= floor(a + c): no two have one number, and none is
 // beyond floor(rows / tile_rows) + prefixes.)
-__device__ __forceinline__ size_t prefix_unit(const TreeAttnArgs &A, int p, long long first, int mt, int h) {
-    return (static_cast<size_t>(first / A.tile_rows) + mt + p) * A.Hkv + h;
+__device__ __forceinline__ size_t prefix_unit(const TreeAttnArgs &A, int p, uint32_t first, int mt, int h) {
+    return (static_cast<size_t>(first / static_cast<uint32_t>(A.tile_rows)) + mt + p) * A.Hkv + h;
 }
 
 // The walk over a group's pieces.  start() finds the first one, in every warp
@@ -269,14 +269,15 @@ struct PrefixWalk {
     int extra = 0;
     bool begins = true;
 
-    // Prefix p and its units (0 for an empty one).
-    __device__ __forceinline__ long long read(const TreeAttnArgs &A, int p) {
+    // Prefix p and its units (0 for an empty one).  (Rows of a call are counted
+    // in 31 bits.)
+    __device__ __forceinline__ uint32_t read(const TreeAttnArgs &A, int p) {
         bool bad;
+        start_ = prefix_group(A, p, count);
         len = attn_len(A, p, bad);
         prefix = attn_prefix_tiles(A, len);
-        start_ = prefix_group(A, p, count);
-        mts = static_cast<int>((static_cast<long long>(count) * A.rows + A.tile_rows - 1) / A.tile_rows);
-        return prefix > 0 ? static_cast<long long>(mts) * A.Hkv : 0;
+        mts = static_cast<int>((static_cast<uint32_t>(count) * A.rows + A.tile_rows - 1) / static_cast<uint32_t>(A.tile_rows));
+        return prefix > 0 ? static_cast<uint32_t>(mts) * A.Hkv : 0u;
     }
 
     __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
@@ -284,10 +285,11 @@ struct PrefixWalk {
         const int per = (A.B + 31) / 32;
         const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
         long long sum = 0, units = 0;
+        uint32_t n = 0;
         for (int i = b0; i < b1; ++i) {
-            const long long n = read(A, i);
+            n = read(A, i);
             units += n;
-            sum += n * prefix;
+            sum += static_cast<long long>(n) * prefix;
         }
         long long inc = sum, uinc = units;
 #pragma unroll
@@ -310,23 +312,28 @@ struct PrefixWalk {
         const long long from = inc - sum;
         const uint32_t own = __ballot_sync(FULL, lo < hi && lo >= from && lo < inc);
         if (own == 0) return W;
-        long long x = lo - from;
+        unsigned long long x = lo - from;
         int i = b0;
         if ((own >> lane) & 1u) {
             for (;; ++i) {
-                const long long n = read(A, i) * (prefix + extra);
-                if (x < n) break;  // (x lies in this lane's stretch)
-                x -= n;
+                if (per > 1) n = read(A, i);  // (one prefix to a lane: it is here)
+                const unsigned long long all = static_cast<unsigned long long>(n) * (prefix + extra);
+                if (x < all) break;  // (x lies in this lane's stretch)
+                x -= all;
             }
         }
         const int src = __ffs(own) - 1;
         b = __shfl_sync(FULL, i, src);
         x = __shfl_sync(FULL, x, src);
-        read(A, b);
-        const long long unit = x / (prefix + extra);
-        tile = static_cast<int>(x - unit * (prefix + extra));
-        h = static_cast<int>(unit / mts);
-        mt = static_cast<int>(unit - static_cast<long long>(h) * mts);
+        len = __shfl_sync(FULL, len, src);
+        prefix = __shfl_sync(FULL, prefix, src);
+        start_ = __shfl_sync(FULL, start_, src);
+        count = __shfl_sync(FULL, count, src);
+        mts = __shfl_sync(FULL, mts, src);
+        const uint32_t each = prefix + extra, unit = x >> 32 ? static_cast<uint32_t>(x / each) : static_cast<uint32_t>(x) / each;
+        tile = static_cast<int>(x - static_cast<unsigned long long>(unit) * each);
+        h = static_cast<int>(unit / static_cast<uint32_t>(mts));
+        mt = static_cast<int>(unit - static_cast<uint32_t>(h) * mts);
         if (tile >= prefix) {  // the range begins behind a unit's tiles
             at += prefix + extra - tile;
             step(A);
@@ -355,10 +362,10 @@ struct PrefixWalk {
         p.start = start_;
         p.first = begins;
         begins = false;
-        const long long row0 = static_cast<long long>(mt) * A.tile_rows, left_rows = static_cast<long long>(count) * A.rows - row0;
-        p.rows = static_cast<int>(left_rows < A.tile_rows ? left_rows : A.tile_rows);
-        p.token = static_cast<int>(row0 / A.G);
-        p.rest = static_cast<int>(row0 - static_cast<long long>(p.token) * A.G);
+        const uint32_t row0 = static_cast<uint32_t>(mt) * A.tile_rows, all = static_cast<uint32_t>(count) * A.rows;
+        p.rows = static_cast<int>(min(all - row0, static_cast<uint32_t>(A.tile_rows)));
+        p.token = static_cast<int>(A.G == 1 ? row0 : row0 / static_cast<uint32_t>(A.G));
+        p.rest = static_cast<int>(row0 - static_cast<uint32_t>(p.token) * A.G);
         p.t0 = tile;
         const long long left = hi - at;
         p.t1 = static_cast<int>(tile + left < prefix ? tile + left : prefix);
@@ -422,7 +429,7 @@ __device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, lo
 __device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, long long W, long long hi, const PrefixPiece &p) {
     if (p.t0 != 0) return;
     const int n = p.whole() ? 0 : attn_parts(A, g, W, hi, p);
-    A.units[prefix_unit(A, p.b, static_cast<long long>(p.start) * A.rows, p.mt, p.h)] = make_int2(n, 2 * g + (p.first ? 0 : 1));
+    A.units[prefix_unit(A, p.b, static_cast<uint32_t>(p.start) * A.rows, p.mt, p.h)] = make_int2(n, 2 * g + (p.first ? 0 : 1));
 }
 
 // What one thread of a group tells the join when its pieces are done.
@@ -444,7 +451,7 @@ __device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const AttnPiec
     return (static_cast<size_t>(p.b) * A.Hkv + p.h) * A.rows;
 }
 __device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const PrefixPiece &p) {
-    return prefix_unit(A, p.b, static_cast<long long>(p.start) * A.rows, p.mt, p.h) * A.tile_rows;
+    return prefix_unit(A, p.b, static_cast<uint32_t>(p.start) * A.rows, p.mt, p.h) * A.tile_rows;
 }
 
 // By one warp: whether the starts rise from 0 to the number of sequences.

@@ -482,10 +482,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
     pdl_wait();
     pdl_next();
     const int lane = threadIdx.x & (LANES - 1), shift = threadIdx.x & 24;  // in the row's lanes; theirs in the warp
-    const long long rows = static_cast<long long>(A.B) * A.T * A.Hq, row_of_grid = (static_cast<long long>(blockIdx.x) * JOIN_THREADS + threadIdx.x) / LANES;
-    const bool there = row_of_grid < rows;
-    const long long at = there ? row_of_grid : rows - 1, token = at / A.Hq;
-    const int hq = static_cast<int>(at - token * A.Hq), b = static_cast<int>(token / A.T), t = static_cast<int>(token - static_cast<long long>(b) * A.T);
+    // (the call's rows are counted in 31 bits)
+    const uint32_t rows = static_cast<uint32_t>(A.B) * A.T * A.Hq, mine = (blockIdx.x * JOIN_THREADS + threadIdx.x) / LANES;
+    const bool there = mine < rows;
+    const uint32_t row_out = there ? mine : rows - 1, token = row_out / A.Hq;
+    const size_t at = row_out;
+    const int hq = static_cast<int>(row_out - token * A.Hq), b = static_cast<int>(token / A.T), t = static_cast<int>(token - static_cast<uint32_t>(b) * A.T);
     const int h = hq / A.G, g = hq - h * A.G;
     const size_t own_at = static_cast<size_t>(b) * A.Hkv + h;
     const int2 own_unit = __ldg(A.units + own_at);
@@ -512,10 +514,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
     int2 pre_unit = make_int2(0, 0);
     size_t pre_at = 0;
     if (shared) {
-        const long long r = static_cast<long long>(b - first) * A.rows + row;
-        mt = static_cast<int>(r / S.tile_rows);
-        prow = static_cast<int>(r - static_cast<long long>(mt) * S.tile_rows);
-        pre_at = prefix_unit(S, p, static_cast<long long>(first) * A.rows, mt, h);
+        const uint32_t r = static_cast<uint32_t>(b - first) * A.rows + row;
+        mt = static_cast<int>(r / static_cast<uint32_t>(S.tile_rows));
+        prow = static_cast<int>(r - static_cast<uint32_t>(mt) * S.tile_rows);
+        pre_at = prefix_unit(S, p, static_cast<uint32_t>(first) * A.rows, mt, h);
         pre_unit = __ldg(S.units + pre_at);
         flag |= __ldg(S.flags + p);
     }

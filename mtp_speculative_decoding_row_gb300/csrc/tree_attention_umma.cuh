@@ -418,13 +418,14 @@ __device__ __noinline__ void copy_queries(const bf16_t *q, const TreeAttnArgs &A
 template <int D>
 __device__ __noinline__ void copy_prefix_queries(const TreeAttnArgs &A, const PrefixPiece &p, int row, int rows, uint32_t dst, int i, int threads) {
     constexpr int VECS = D / 8;
-    const int seq0 = p.token / A.T, t0 = p.token - seq0 * A.T;
-    const bf16_t *q = static_cast<const bf16_t *>(A.q) + (p.start + seq0) * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2];
-#pragma unroll 1
-    for (; i < rows * VECS; i += threads) {
-        const int r = i / VECS, u = i % VECS, d = node_of(A, p.rest + row + r), t = t0 + d, s = t / A.T;
-        cp_async16(dst + (u >> 3) * A.qrows * 128 + sw128(r, u & 7),
-                   q + s * A.qs[0] + (t - s * A.T) * A.qs[1] + (p.rest + row + r - d * A.G) * A.qs[2] + 8 * u);
+    const int seq0 = A.T == 1 ? p.token : p.token / A.T, t0 = p.token - seq0 * A.T, u = i % VECS;  // (threads is a multiple of VECS)
+    const bf16_t *q = static_cast<const bf16_t *>(A.q) + (p.start + seq0) * A.qs[0] + static_cast<int64_t>(p.h) * A.G * A.qs[2] + 8 * u;
+    dst += (u >> 3) * A.qrows * 128;
+#pragma unroll 4
+    for (int r = i / VECS; r < rows; r += threads / VECS) {
+        const int d = node_of(A, p.rest + row + r), t = t0 + d;
+        const int s = A.T == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), A.t_inverse));  // (t < T + 257, T <= 64: exact)
+        cp_async16(dst + sw128(r, u & 7), q + s * A.qs[0] + (t - s * A.T) * A.qs[1] + (p.rest + row + r - d * A.G) * A.qs[2]);
     }
 }
 
