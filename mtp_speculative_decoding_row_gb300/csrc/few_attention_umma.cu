@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
     pdl_next();
     Walk walk;
     {
-        const long long W = walk.start(A, group);
+        const long long W = walk.start(A, group, attn_limit<PREFIX>(A));
         if (tid == 0) {
             ctl.W = W;
             ctl.begin = walk;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(Few<D, R>::NT, 1)
         give_up(A, ctl.begin, group, 0, 0, PREFIX ? 0 : A.rows, tid, NT);
     }
     if (tid == 0) attn_report(A, group, ctl.W, ctl.begin);
-    if (!PREFIX && A.overlap) pdl_wait();
+    if (!PREFIX && A.overlap && blockIdx.x == 0) pdl_wait();
     tmem_fence_after_sync();
     __syncthreads();
     if (warp == 1) {
@@ -620,6 +620,7 @@ UmmaPlan plan_of() {
     p.qbufs = 2;
     p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     p.bn = C::BN;
+    p.cost = D == 256 ? 250 : 100;
     p.smem = fixed + p.slots * C::SLOT;
     return p;
 }

@@ -73,17 +73,20 @@ int resident(int dev, const void *func, uint32_t smem, int threads) {
 // (griddepcontrol.wait) before it touches memory, and lets the next one's CTAs
 // be set up early, so all are launched programmatically.
 int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream,
-           const void *map1, const void *map2) {
+           const void *map1, const void *map2, int cluster) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     void *kargs[] = {const_cast<void *>(args), const_cast<void *>(map1), const_cast<void *>(map2)};
     return cudaLaunchKernelExC(&cfg, func, kargs) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }

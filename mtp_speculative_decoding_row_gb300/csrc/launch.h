@@ -17,7 +17,8 @@ bool device_sms(int &dev, int &sms);
 // where it does not fit.
 int resident(int dev, const void *func, uint32_t smem, int threads);
 // Launch programmatically; args, map1 and map2 are the kernel's parameters.
+// cluster: thread blocks of a cluster (the grid is a multiple of it).
 int launch(const void *func, dim3 grid, int threads, uint32_t smem, const void *args, mtp_stream_t stream,
-           const void *map1 = nullptr, const void *map2 = nullptr);
+           const void *map1 = nullptr, const void *map2 = nullptr, int cluster = 1);
 
 }  // namespace mtp

@@ -55,6 +55,16 @@ struct TreeAttnArgs {
     int32_t *bad_starts;    // whether they are none
     int sequences;
     int tile_rows;          // query rows of one tile
+    // Both kernels: what their shares of the GPU follow from (see prefix_share).
+    struct Side {
+        const int32_t *len;
+        int n, cap;          // sequences or prefixes, and the tokens that one can have
+        int ktile;           // keys of a tile
+        int cost, start;     // of a tile and of a unit, in 10 ns
+    } own, pre;
+    int own_tiles;          // row tiles of a sequence
+    int tile_rows_pre;      // query rows of a prefix's tile
+    int share_slots;        // CTAs that the GPU holds at a time
 };
 
 constexpr int ATTN_DESC = 4;
@@ -64,7 +74,7 @@ constexpr int ATTN_DESC = 4;
 __host__ __device__ inline size_t attn_slot_floats(int bm, int d) { return static_cast<size_t>(bm) * (d + 2); }
 
 // SIMT kernel (csrc/tree_attention_simt.cu).
-constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256;
+constexpr int SIMT_BM = 32, SIMT_BN = 64, SIMT_THREADS = 256, SIMT_COST = 200;
 const void *attn_simt_func(int dtype, int D, bool prefix);
 uint32_t attn_simt_smem(int D);
 // Tensor-core kernel (csrc/tree_attention_umma.cu): bfloat16, D 64, 128, 256.
@@ -73,6 +83,7 @@ constexpr int UMMA_EXTRA = 3;
 struct UmmaPlan {
     const void *func;
     int threads, bm, tile_rows, qrows, qbufs, slots, bn;
+    int cost;  // of a tile, in 10 ns (measured; see prefix_share)
     uint32_t smem;
 };
 UmmaPlan attn_umma_plan(int D, int rows);

@@ -22,7 +22,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct AttnPlan {
     const void *func = nullptr;
     uint32_t smem = 0;
-    int threads = 0, bm = 0, tile_rows = 0, bn = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
+    int threads = 0, bm = 0, tile_rows = 0, bn = 0, cost = 0, resident_ctas = 0, ktile = 0, per_page = 0, rows = 0, mtiles = 0, groups = 0, qrows = 0, qbufs = 1, slots = 0;
     long long max_tiles = 0;  // of one unit, the new keys' tile included
     size_t part_bytes = 0, desc_bytes = 0, late_bytes = 0;
     bool whole = false;       // units are not split
@@ -73,6 +73,7 @@ void set_umma(AttnPlan &p, const UmmaPlan &u) {
     p.qbufs = u.qbufs;
     p.slots = u.slots;
     p.bn = u.bn;
+    p.cost = u.cost;
 }
 
 // `few`: by the kernel for few rows (of mtp_prefix_attention), where it takes the
@@ -94,9 +95,11 @@ int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p, bool few
         p.threads = SIMT_THREADS;
         p.bm = SIMT_BM;
         p.ktile = SIMT_BN;
+        p.cost = SIMT_COST;
     }
     const int per_sm = resident(dev, p.func, p.smem, p.threads);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
+    p.resident_ctas = sms * per_sm;
     p.mtiles = (p.rows + p.bm - 1) / p.bm;
     p.max_tiles = 1 + most_tiles(p, a.max_pages, a.page_size);
     if (p.max_tiles * a.Hkv > 0x7fffffffll) return MTP_ERR_INVALID_ARG;  // tiles of a sequence are counted in 32 bits
@@ -309,6 +312,8 @@ extern "C" int mtp_tree_attention(const mtp_tree_attention_args *args, mtp_strea
 
 namespace {
 
+constexpr int PIECE_COST = 350;  // of a unit beside its tiles, in 10 ns (see prefix_share)
+
 int prefix_sizes(const mtp_prefix_attention_args &x) {
     const mtp_tree_attention_args &a = x.own;
     const int rc = attn_sizes(a);
@@ -339,9 +344,11 @@ int prefix_plan(const mtp_prefix_attention_args &x, bool umma, AttnPlan &p) {
         p.threads = SIMT_THREADS;
         p.bm = p.tile_rows = SIMT_BM;
         p.ktile = SIMT_BN;
+        p.cost = SIMT_COST;
     }
     const int per_sm = resident(dev, p.func, p.smem, p.threads);
     if (per_sm < 1) return MTP_ERR_NO_DEVICE;
+    p.resident_ctas = sms * per_sm;
     p.mtiles = 1;
     const long long mtiles = all / p.tile_rows + x.prefixes;  // of all prefixes, at most
     p.max_tiles = most_tiles(p, x.max_prefix_pages, a.page_size);
@@ -436,13 +443,22 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     S.table = x.prefix_table;
     S.len = x.prefix_len;
     S.max_pages = x.max_prefix_pages;
-    S.starts = x.group_start;
-    S.sequences = a.B;
     S.B = x.prefixes;
     S.parents = S.nodes = nullptr;
-    const int e = launch(pre.func, dim3(pre.groups), pre.threads, pre.smem, &S, stream, &pre_maps.k, &pre_maps.v);
+    for (TreeAttnArgs *X : {&A, &S}) {
+        X->starts = x.group_start;
+        X->sequences = a.B;
+        X->own = {a.cache_len, a.B, static_cast<int>(static_cast<long long>(a.max_pages) * a.page_size), own.ktile, own.cost, PIECE_COST};
+        X->pre = {x.prefix_len, x.prefixes, static_cast<int>(static_cast<long long>(x.max_prefix_pages) * a.page_size), pre.ktile, pre.cost, PIECE_COST};
+        X->own_tiles = own.mtiles;
+        X->tile_rows_pre = pre.tile_rows;
+        X->share_slots = own.resident_ctas < pre.resident_ctas ? own.resident_ctas : pre.resident_ctas;
+    }
+    const int pair = umma ? 2 : 1;
+    const auto even = [&](int n) { return dim3(static_cast<unsigned>((n + pair - 1) / pair * pair)); };  // (a CTA too many has no work)
+    const int e = launch(pre.func, even(pre.groups), pre.threads, pre.smem, &S, stream, &pre_maps.k, &pre_maps.v, pair);
     if (e != MTP_OK) return e;
-    const int f = launch(own.func, dim3(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &own_maps.k, &own_maps.v);
+    const int f = launch(own.func, even(own.groups * own.mtiles), own.threads, own.smem, &A, stream, &own_maps.k, &own_maps.v, pair);
     if (f != MTP_OK) return f;
     const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
     return launch(prefix_join_func(a.dtype, a.D), dim3(static_cast<unsigned>((rows + PREFIX_JOIN_ROWS - 1) / PREFIX_JOIN_ROWS)), JOIN_THREADS, 0, &A, stream, &S);

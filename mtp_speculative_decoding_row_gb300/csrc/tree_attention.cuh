@@ -95,10 +95,9 @@ struct PrefixPiece {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == prefix; }
 };
 
-// Groups that have tiles: none of their ranges is empty.
-__device__ __forceinline__ int attn_groups(const TreeAttnArgs &A, long long W) {
-    return W < A.groups ? static_cast<int>(W) : A.groups;
-}
+// Groups that have tiles, of the `limit` that take part: none of their ranges is
+// empty.
+__device__ __forceinline__ int attn_groups(int limit, long long W) { return W < limit ? static_cast<int>(W) : limit; }
 // The first tile of group g's range (a 64-bit division only where it is needed).
 __device__ __forceinline__ long long attn_lo(long long W, int g, int groups) {
     if (W == groups) return g;
@@ -132,14 +131,16 @@ struct AttnWalk {
     int len = 0, prefix = 0;
     int extra = 0;               // a unit ends with so many tiles that are none (see start)
     bool begins = true;          // no piece was taken yet
+    int limit = 0;               // groups that take part
 
     // Returns the number of all tiles (of all units where they are not split;
     // hi and at count units then).
-    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
+    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g, int most) {
+        limit = most;
         if (A.whole) {
             const long long units = static_cast<long long>(A.B) * A.Hkv;
-            at = attn_lo(units, min(g, A.groups), A.groups);
-            hi = attn_lo(units, min(g + 1, A.groups), A.groups);
+            at = attn_lo(units, min(g, limit), limit);
+            hi = attn_lo(units, min(g + 1, limit), limit);
             b = static_cast<int>(at / A.Hkv);
             h = static_cast<int>(at - static_cast<long long>(b) * A.Hkv);
             if (at < hi) read(A);
@@ -171,11 +172,11 @@ struct AttnWalk {
         // beside its tiles: 1000 tokens of 32 sequences took 152 us without
         // and 177 us with three tiles.)
         const long long real = __shfl_sync(FULL, inc, 31);
-        if (real >= 4ll * A.groups) extra = A.extra;
+        if (real >= 4ll * limit) extra = A.extra;
         const long long W = real + static_cast<long long>(A.B) * A.Hkv * extra;
         inc += static_cast<long long>(b1) * A.Hkv * extra;
         sum += static_cast<long long>(b1 - b0) * A.Hkv * extra;
-        const int groups = attn_groups(A, W);
+        const int groups = attn_groups(limit, W);
         const long long lo = attn_lo(W, min(g, groups), groups);
         hi = attn_lo(W, min(g + 1, groups), groups);
         at = lo;
@@ -268,6 +269,7 @@ struct PrefixWalk {
     int len = 0, prefix = 0, start_ = 0, count = 0, mts = 0;
     int extra = 0;
     bool begins = true;
+    int limit = 0;
 
     // Prefix p and its units (0 for an empty one).  (Rows of a call are counted
     // in 31 bits.)
@@ -280,7 +282,8 @@ struct PrefixWalk {
         return prefix > 0 ? static_cast<uint32_t>(mts) * A.Hkv : 0u;
     }
 
-    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g) {
+    __device__ __forceinline__ long long start(const TreeAttnArgs &A, int g, int most) {
+        limit = most;
         const int lane = threadIdx.x & 31;
         const int per = (A.B + 31) / 32;
         const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
@@ -301,11 +304,11 @@ struct PrefixWalk {
             }
         }
         const long long real = __shfl_sync(FULL, inc, 31);
-        if (real >= 4ll * A.groups) extra = A.extra;
+        if (real >= 4ll * limit) extra = A.extra;
         const long long W = real + __shfl_sync(FULL, uinc, 31) * extra;
         inc += uinc * extra;
         sum += units * extra;
-        const int groups = attn_groups(A, W);
+        const int groups = attn_groups(limit, W);
         const long long lo = attn_lo(W, min(g, groups), groups);
         hi = attn_lo(W, min(g + 1, groups), groups);
         at = lo;
@@ -394,9 +397,9 @@ __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch
 // The groups that a unit lies in that begins in group g with its last piece
 // `p` and goes on in the next ones.
 template <class Piece>
-__device__ __forceinline__ int attn_parts(const TreeAttnArgs &A, int g, long long W, long long hi, const Piece &p) {
+__device__ __forceinline__ int attn_parts(int limit, int g, long long W, long long hi, const Piece &p) {
     const long long end = hi + (p.tiles() - p.t1);  // one past the unit's last tile (the range ended inside of the unit)
-    const int groups = attn_groups(A, W);
+    const int groups = attn_groups(limit, W);
     int n = 1;
     while (g + n < groups && attn_lo(W, g + n, groups) < end) ++n;
     return n;
@@ -404,7 +407,7 @@ __device__ __forceinline__ int attn_parts(const TreeAttnArgs &A, int g, long lon
 
 // Tell the join about the unit that begins in this group and goes on in the
 // next ones (at most one does): {b, h, parts, slot of the first part}.
-__device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, long long W, long long hi,
+__device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int limit, int g, long long W, long long hi,
                                                 const AttnPiece &last) {
     if (A.whole) return;
     int *d = A.desc + static_cast<size_t>(g) * ATTN_DESC;
@@ -412,7 +415,7 @@ __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, lo
         d[2] = 0;
         return;
     }
-    const int n = attn_parts(A, g, W, hi, last);
+    const int n = attn_parts(limit, g, W, hi, last);
     d[0] = last.b;
     d[1] = last.h;
     d[3] = last.first ? 0 : 1;
@@ -421,14 +424,14 @@ __device__ __forceinline__ void attn_write_desc(const TreeAttnArgs &A, int g, lo
 
 // Tell the join of the two kernels about every unit that begins in this group:
 // {parts, slot of the first}; 0 parts: a whole unit, whose results lie by rows.
-__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, long long W, long long hi, const AttnPiece &p) {
+__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int limit, int g, long long W, long long hi, const AttnPiece &p) {
     if (p.t0 != 0) return;
-    const int n = p.whole() ? 0 : attn_parts(A, g, W, hi, p);
+    const int n = p.whole() ? 0 : attn_parts(limit, g, W, hi, p);
     A.units[static_cast<size_t>(p.b) * A.Hkv + p.h] = make_int2(n, 2 * g + (p.first ? 0 : 1));
 }
-__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int g, long long W, long long hi, const PrefixPiece &p) {
+__device__ __forceinline__ void attn_write_unit(const TreeAttnArgs &A, int limit, int g, long long W, long long hi, const PrefixPiece &p) {
     if (p.t0 != 0) return;
-    const int n = p.whole() ? 0 : attn_parts(A, g, W, hi, p);
+    const int n = p.whole() ? 0 : attn_parts(limit, g, W, hi, p);
     A.units[prefix_unit(A, p.b, static_cast<uint32_t>(p.start) * A.rows, p.mt, p.h)] = make_int2(n, 2 * g + (p.first ? 0 : 1));
 }
 
@@ -437,13 +440,13 @@ __device__ __forceinline__ void attn_report(const TreeAttnArgs &A, int g, long l
     AttnPiece p, last = {};
     while (w.next(A, p)) {
         last = p;
-        if (A.units) attn_write_unit(A, g, W, w.hi, p);
+        if (A.units) attn_write_unit(A, w.limit, g, W, w.hi, p);
     }
-    if (!A.units) attn_write_desc(A, g, W, w.hi, last);
+    if (!A.units) attn_write_desc(A, w.limit, g, W, w.hi, last);
 }
 __device__ __forceinline__ void attn_report(const TreeAttnArgs &A, int g, long long W, PrefixWalk w) {
     PrefixPiece p;
-    while (w.next(A, p)) attn_write_unit(A, g, W, w.hi, p);
+    while (w.next(A, p)) attn_write_unit(A, w.limit, g, W, w.hi, p);
 }
 
 // Where a whole unit's results lie, by rows: its first row's place.
@@ -452,6 +455,52 @@ __device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const AttnPiec
 }
 __device__ __forceinline__ size_t unit_row(const TreeAttnArgs &A, const PrefixPiece &p) {
     return prefix_unit(A, p.b, static_cast<uint32_t>(p.start) * A.rows, p.mt, p.h) * A.tile_rows;
+}
+
+// The kernel of the prefixes and that of the sequences' own tokens run side by
+// side, each on a part of the GPU: of the slots (CTAs that it holds at a time)
+// the first has as many as its share of the work.  Both launches have a CTA for
+// every slot; both find the same number here, and the CTAs beyond it leave, so
+// that all that stay run at one time.  (One after the other each begins with some
+// 10 us of empty pipes and cold code, and the first, which the tensor cores or
+// its softmax bound, leaves the memory idle that the second waits for: 64
+// samples of a prompt of 16384 tokens 147 us in turn.)  The costs of a tile are measured: they
+// decide how well the two end together, nothing else.  The shares are even and
+// the tensor-core kernels launched in clusters of two, which lie on one pair of
+// SMs: where the two SMs of a pair ran different kernels, whose code the pair's
+// instruction cache does not hold, each took up to twice as long (190 us).
+__device__ __forceinline__ int prefix_share(const TreeAttnArgs &A) {
+    const int lane = threadIdx.x & 31;
+    auto tiles = [](const TreeAttnArgs::Side &s, int i) {
+        const int n = __ldg(s.len + i);
+        return n <= 0 || n > s.cap ? 0 : (n + s.ktile - 1) / s.ktile;
+    };
+    unsigned long long own = 0, pre = 0;
+#pragma unroll 4
+    for (int i = lane; i < A.own.n; i += 32) own += static_cast<unsigned long long>(tiles(A.own, i) + 1) * A.own.cost + A.own.start;
+    for (int i = lane; i < A.pre.n; i += 32) {
+        int count;
+        (void)prefix_group(A, i, count);
+        const int n = tiles(A.pre, i);
+        const uint32_t mts = (static_cast<uint32_t>(count) * A.rows + A.tile_rows_pre - 1) / static_cast<uint32_t>(A.tile_rows_pre);
+        if (n > 0) pre += (static_cast<unsigned long long>(n) * A.pre.cost + A.pre.start) * mts;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        own += __shfl_xor_sync(FULL, own, d);
+        pre += __shfl_xor_sync(FULL, pre, d);
+    }
+    own *= A.own_tiles;
+    // (as floats: what is rounded here is rounded alike in both kernels)
+    const int n = __float2int_rn(A.share_slots / 2 * (__ull2float_rn(pre) / __ull2float_rn(own + pre)));
+    return 2 * min(max(n, 1), A.share_slots / 2 - 1);
+}
+
+// Groups of this kernel that take part.
+template <bool PREFIX>
+__device__ __forceinline__ int attn_limit(const TreeAttnArgs &A) {
+    if (PREFIX) return min(A.groups, prefix_share(A));
+    return A.overlap ? min(A.groups, max(1, (A.share_slots - prefix_share(A)) / A.mtiles)) : A.groups;
 }
 
 // By one warp: whether the starts rise from 0 to the number of sequences.

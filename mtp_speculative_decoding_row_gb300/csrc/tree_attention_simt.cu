@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
     if (PREFIX || !A.overlap) pdl_wait();
     pdl_next();
     Walk walk;
-    const long long W = walk.start(A, group);
+    const long long W = walk.start(A, group, attn_limit<PREFIX>(A));
     if (tid == 0) *reinterpret_cast<Walk *>(s_begin) = walk;  // for the end
     if (PREFIX && blockIdx.x == 0 && tid < 32) prefix_check_starts(A);
     Piece pc;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(NT) attn_simt_impl(const __grid_constant__ Tre
         __syncthreads();
     }
     if (mtile == 0 && tid == 0) attn_report(A, group, W, *reinterpret_cast<const Walk *>(s_begin));
-    if (!PREFIX && A.overlap) pdl_wait();  // the join waits for this kernel, and so for the one before
+    if (!PREFIX && A.overlap && blockIdx.x == 0) pdl_wait();  // the join waits for this kernel, and so for the one before
 }
 
 // Join one unit that begins in group blockIdx.x / mtiles and goes on in the
@@ -472,14 +472,12 @@ __global__ void __launch_bounds__(JOIN_THREADS, Store<T>::ES == 4 ? 5 : 10) attn
 
 // Join of a sequence's own parts (A) with those of its prefix (S), both from
 // the kernels above: eight lanes take one row of the output, find the row's two
-// units and join their parts as attn_join_impl does, the prefix's first.  What
-// bounds it is a chain of loads (flags and starts, lengths and units, maxima,
-// rows): with a warp to a row 8192 rows were two and a half rounds of it, now
-// they are one.
+// units and join their parts in their order, the prefix's first.  What bounds it
+// is a chain of loads (units and flags, then references, sums and rows): with a
+// warp to a row 8192 rows were two and a half rounds of it, now they are one.
 template <typename T, int NQ>
 __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TreeAttnArgs S) {
     constexpr int LANES = 8, AHEAD = NQ <= 4 ? 2 : 1;
-    pdl_wait();
     pdl_next();
     const int lane = threadIdx.x & (LANES - 1), shift = threadIdx.x & 24;  // in the row's lanes; theirs in the warp
     // (the call's rows are counted in 31 bits)
@@ -489,10 +487,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
     const size_t at = row_out;
     const int hq = static_cast<int>(row_out - token * A.Hq), b = static_cast<int>(token / A.T), t = static_cast<int>(token - static_cast<uint32_t>(b) * A.T);
     const int h = hq / A.G, g = hq - h * A.G;
-    const size_t own_at = static_cast<size_t>(b) * A.Hkv + h;
-    const int2 own_unit = __ldg(A.units + own_at);
-    const bool bad_starts = *S.bad_starts != 0;
-    int flag = __ldg(A.flags + b) | (bad_starts ? F_BAD_ID : 0);
+    // The call's inputs were there before its first kernel: they are read before
+    // the second is done.
     bool bad_nodes;
     const int n = attn_nodes(A, b, bad_nodes);
     // the sequence's prefix: the last that starts at or before it, 8 guesses at a time
@@ -504,23 +500,26 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
         hi = min(hi, lo + (last + 1) * stride);
         lo += last * stride;
     }
-    const int p = lo, first = __ldg(S.starts + p);
+    // (in bounds whatever the starts hold)
+    int group;
+    const int p = lo, first = prefix_group(S, p, group);
     bool bad_len;
     const int plen = attn_len(S, p, bad_len);
-    if (bad_len) flag |= F_BAD_ID;
-    const bool shared = plen > 0 && !bad_starts;
+    const bool inside = b >= first && b < first + group, shared = plen > 0 && inside;
     const int row = t * A.G + g;
+    const size_t own_at = static_cast<size_t>(b) * A.Hkv + h;
     int mt = 0, prow = 0;
-    int2 pre_unit = make_int2(0, 0);
     size_t pre_at = 0;
     if (shared) {
         const uint32_t r = static_cast<uint32_t>(b - first) * A.rows + row;
         mt = static_cast<int>(r / static_cast<uint32_t>(S.tile_rows));
         prow = static_cast<int>(r - static_cast<uint32_t>(mt) * S.tile_rows);
         pre_at = prefix_unit(S, p, static_cast<uint32_t>(first) * A.rows, mt, h);
-        pre_unit = __ldg(S.units + pre_at);
-        flag |= __ldg(S.flags + p);
     }
+    pdl_wait();
+    const int2 own_unit = A.units[own_at], pre_unit = shared ? S.units[pre_at] : make_int2(0, 0);
+    int flag = A.flags[b] | (*S.bad_starts || bad_len || !inside ? F_BAD_ID : 0);
+    if (shared) flag |= S.flags[p];
     if (there && t == 0 && hq == 0 && A.flags_out && lane == 0) A.flags_out[b] = flag;
     const bool live = there && t < (bad_nodes ? A.T : n);
     T *out = static_cast<T *>(A.out) + at * A.D;
@@ -564,24 +563,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
     auto far = [&](const Parts &q, int k) { return k == 0 ? 0ll : q.next + (k - 1) * q.step; };
     auto m_of = [&](int k) { return k < pre.n ? pre.m + far(pre, k) : own.m + far(own, k - pre.n); };
     auto o_of = [&](int k) { return k < pre.n ? pre.o + far(pre, k) : own.o + far(own, k - pre.n); };
-    float top = -INFINITY;
-    for (int k = lane; k < parts; k += LANES) top = max_nan(top, *m_of(k));
-#pragma unroll
-    for (int e = 1; e < LANES; e <<= 1) top = max_nan(top, __shfl_xor_sync(FULL, top, e));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o[NQ][4] = {};
+    // Weights of eight parts at a time, relative to the largest reference so far;
+    // the rows of the first parts are on their way while those are found.
+    float top = -INFINITY, l = 0.f, o[NQ][4] = {};
     const bool quads = A.D % 4 == 0;
     for (int k0 = 0; __any_sync(FULL, k0 < parts); k0 += LANES) {
-        float w = 0.f;
-        if (k0 + lane < parts) {
-            const float *m = m_of(k0 + lane);
-            w = exp2f(*m - ref);
-            l = fmaf(w, m[k0 + lane < pre.n ? pre.l : own.l], l);
-        }
-#pragma unroll
-        for (int i0 = 0; i0 < LANES; i0 += AHEAD) {
-            if (!__any_sync(FULL, k0 + i0 < parts)) break;
-            float4 x[AHEAD][NQ];
+        float4 x[AHEAD][NQ];
+        auto load = [&](int i0) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const float *from = k0 + i0 + i < parts ? o_of(k0 + i0 + i) : nullptr;
@@ -597,6 +585,30 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
                         x[i][q] = make_float4(s[0], c + 1 < A.D ? s[1] : 0.f, c + 2 < A.D ? s[2] : 0.f, c + 3 < A.D ? s[3] : 0.f);
                 }
             }
+        };
+        float m = -INFINITY, sum = 0.f;
+        if (k0 + lane < parts) {
+            const float *at_m = m_of(k0 + lane);
+            m = at_m[0];
+            sum = at_m[k0 + lane < pre.n ? pre.l : own.l];
+        }
+        load(0);
+        float here = m;
+#pragma unroll
+        for (int e = 1; e < LANES; e <<= 1) here = max_nan(here, __shfl_xor_sync(FULL, here, e));
+        here = max_nan(here, top);
+        const float ref = here == -INFINITY ? 0.f : here, old = top == -INFINITY ? 0.f : exp2f(top - ref);
+        top = here;
+        const float w = k0 + lane < parts ? exp2f(m - ref) : 0.f;
+        l = fmaf(w, sum, l * old);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[q][e] *= old;
+#pragma unroll
+        for (int i0 = 0; i0 < LANES; i0 += AHEAD) {
+            if (!__any_sync(FULL, k0 + i0 < parts)) break;
+            if (i0 > 0) load(i0);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const float wi = __shfl_sync(FULL, w, i0 + i, LANES);
@@ -611,6 +623,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_impl(const __grid_co
             }
         }
     }
+    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int e = 1; e < LANES; e <<= 1) l += __shfl_xor_sync(FULL, l, e);
     if (!live || flag) return;

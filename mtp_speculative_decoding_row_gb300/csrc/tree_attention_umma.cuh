@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
     pdl_next();
     Walk walk;
     {
-        const long long W = walk.start(A, group);
+        const long long W = walk.start(A, group, attn_limit<PREFIX>(A));
         if (tid == 0) {  // for the end
             ctl.W = W;
             ctl.begin = walk;
@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::NT, 1)
         give_up(A, ctl.begin, group, mtile, row0, rows, tid, NT);
     }
     if (mtile == 0 && tid == 0) attn_report(A, group, ctl.W, ctl.begin);
-    if (!PREFIX && A.overlap) pdl_wait();  // the join waits for this kernel, and so for the one before
+    if (!PREFIX && A.overlap && blockIdx.x == 0) pdl_wait();  // the join waits for this kernel, and so for the one before
     tmem_fence_after_sync();
     __syncthreads();
     if (warp == 1) {
@@ -1128,6 +1128,7 @@ UmmaPlan umma_plan(int D, int rows, long long most) {
     // the product reads 128 rows of every block of queries
     p.smem = p_bytes + q + p.slots * slot + static_cast<uint32_t>(sizeof(Ctl));
     p.bn = attn_umma_bn(D);
+    p.cost = mode == ROWS ? 230 : mode == ONE ? 130 : mode == KEYS ? 150 : 110;
     p.func = pick<PREFIX>(D, mode, [](auto, auto f) { return reinterpret_cast<const void *>(f); });
     p.threads = pick<PREFIX>(D, mode, [](auto c, auto) { return decltype(c)::NT; });
     return p;
