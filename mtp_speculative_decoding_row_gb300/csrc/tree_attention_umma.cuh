@@ -1128,7 +1128,7 @@ UmmaPlan umma_plan(int D, int rows, long long most) {
     // the product reads 128 rows of every block of queries
     p.smem = p_bytes + q + p.slots * slot + static_cast<uint32_t>(sizeof(Ctl));
     p.bn = attn_umma_bn(D);
-    p.cost = mode == ROWS ? 230 : mode == ONE ? 130 : mode == KEYS ? 150 : 110;
+    p.cost = mode == ROWS ? 230 : mode == ONE ? 170 : mode == KEYS ? 150 : 110;
     p.func = pick<PREFIX>(D, mode, [](auto, auto f) { return reinterpret_cast<const void *>(f); });
     p.threads = pick<PREFIX>(D, mode, [](auto c, auto) { return decltype(c)::NT; });
     return p;
