@@ -16,8 +16,8 @@
 // rewrites those, a thread to an entry.  A text's words crowd in few places:
 // dealt out from a list they keep all threads busy (64 x 4 rows, 8192 tokens:
 // 118 us where they were looked for beside the streamed vectors, 63 us with the
-// list in one kernel, whose blocks spent their time in waits one after the other
-// -- counting, streaming, listing -- with room for four of them on an SM).  Rows
+// list in one kernel, whose blocks spent their time in waits one after the other:
+// counting, streaming, listing).  Rows
 // differ in their paths only; the few drafted tokens are looked up in the path
 // where they occur, so that one count serves all rows.
 #include "common.cuh"
@@ -27,9 +27,29 @@ namespace mtp {
 namespace {
 
 constexpr int NT = ADJ_THREADS, CT = ADJ_COUNT_THREADS;
-// An entry of the table: in the text's first part; a drafted token; has a
-// bias; occurrences in the rest of the text.
-constexpr uint32_t PROMPT = 1u, DRAFT = 2u, BIAS = 4u, ONE = 8u;
+// An entry of the table: in the text's first part; drafted or biased (look at
+// the lists); occurrences in the rest of the text.  In 16 bits where the text is
+// short enough for 14 bits of those: half the shared memory, so that all blocks
+// of 64 sequences run at one time, beside the streaming kernel.
+constexpr uint32_t PROMPT = 1u, LOOK = 2u, ONE = 4u;
+
+template <bool SMALL>
+struct Table {
+    uint32_t *words;
+    __device__ __forceinline__ void add(int i, uint32_t x) const {
+        if (SMALL)
+            atomicAdd(words + (i >> 1), x << (16 * (i & 1)));
+        else
+            atomicAdd(words + i, x);
+    }
+    __device__ __forceinline__ void set(int i, uint32_t bits) const {
+        if (SMALL)
+            atomicOr(words + (i >> 1), bits << (16 * (i & 1)));
+        else
+            atomicOr(words + i, bits);
+    }
+    __device__ __forceinline__ uint32_t get(int i) const { return SMALL ? reinterpret_cast<const uint16_t *>(words)[i] : words[i]; }
+};
 
 __device__ __forceinline__ uint32_t bf16_of(float lo, float hi) {
     uint32_t r;
@@ -151,20 +171,21 @@ __global__ void __launch_bounds__(NT, 8) mask_impl(const __grid_constant__ AdjAr
     }
 }
 
-template <typename T>
+template <typename T, bool SMALL>
 __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ AdjArgs A) {
     constexpr int ES = Store<T>::ES, ROWS = 4;
     extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t *table = smem;                                             // [slice]
-    uint16_t *list = reinterpret_cast<uint16_t *>(table + A.slice);     // [slice] entries that are not 0
-    int *bias_id = reinterpret_cast<int *>(list + A.slice);             // [n_bias] of this slice, in their order
-    float *bias_of = reinterpret_cast<float *>(bias_id + A.n_bias);     // [n_bias]
+    constexpr int PER = SMALL ? 8 : 4;                                  // entries of 16 bytes
+    const Table<SMALL> table = {smem};                                  // [slice]
+    uint16_t *list = reinterpret_cast<uint16_t *>(smem + A.slice / PER * 4);  // [listed_most] entries that are not 0
+    int *bias_id = reinterpret_cast<int *>(list + A.listed_most);       // [bias_room] of this slice, in their order, then -1
+    float *bias_of = reinterpret_cast<float *>(bias_id + A.bias_room);  // [bias_room]
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.x;
     const int lo = blockIdx.y * A.slice, hi = min(A.V, lo + A.slice);  // this block's tokens
-    if (tid == 0) sh.flag = sh.listed = 0;
-    for (int i = tid; i < A.slice / 4; i += CT) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) sh.flag = sh.listed = sh.biases = 0;
+    for (int i = tid; i < A.slice / PER; i += CT) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     // (the first kernel has waited for those before it and writes nothing that is
     // read before it is done)
     if (!A.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -235,11 +256,11 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
         const int32_t *text = A.history + static_cast<size_t>(b) * A.L;
         auto see = [&](int id, int at) {
             most = max(most, id);
-            if (static_cast<uint32_t>(id - lo) >= static_cast<uint32_t>(hi - lo)) return;
+            if (static_cast<uint32_t>(id) - static_cast<uint32_t>(lo) >= static_cast<uint32_t>(hi - lo)) return;
             if (at < prompt)
-                atomicOr(table + (id - lo), PROMPT);
+                table.set(id - lo, PROMPT);
             else
-                atomicAdd(table + (id - lo), ONE);
+                table.add(id - lo, ONE);
         };
         const int vecs = A.vec_history ? len / 4 : 0;
 #pragma unroll 4
@@ -256,7 +277,7 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
     }
     if (A.tokens && tid < n) {
         const int id = sh.token[tid];
-        if (id >= lo && id < hi) atomicOr(table + (id - lo), DRAFT);
+        if (id >= lo && id < hi) table.set(id - lo, LOOK);
     }
     if (A.n_bias > 0 && tid < 32) {  // this slice's, in their order, so that a sum of several has one value
         int found = 0;
@@ -271,11 +292,12 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
                 const int at = found + __popc(who & ((1u << lane) - 1u));
                 bias_id[at] = id;
                 bias_of[at] = value;
-                atomicOr(table + (id - lo), BIAS);
+                table.set(id - lo, LOOK);
             }
             __syncwarp();
             found += __popc(who);
         }
+        if (lane < 4 && found + lane < A.bias_room) bias_id[found + lane] = -1;  // (read four at a time)
         if (lane == 0) sh.biases = found;
     }
     if (flag) atomicOr(&sh.flag, flag);
@@ -290,10 +312,13 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
     }
 
     // ---- the entries that change ----
-    for (int i = tid; i < A.slice / 4; i += CT) {  // (a slice is a multiple of four times the threads of a warp)
-        const uint4 e = reinterpret_cast<const uint4 *>(table)[i];
-        const int mine = (e.x != 0u) + (e.y != 0u) + (e.z != 0u) + (e.w != 0u);
-        if (!__any_sync(FULL, mine)) continue;
+    for (int i = tid; i < A.slice / PER; i += CT) {  // (a slice is a multiple of PER times the threads of a warp)
+        const uint4 e = reinterpret_cast<const uint4 *>(smem)[i];
+        if (!__any_sync(FULL, (e.x | e.y | e.z | e.w) != 0u)) continue;
+        const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mine += SMALL ? ((w[k] & 0xffffu) != 0u) + (w[k] >> 16 != 0u) : w[k] != 0u;
         int before = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -303,31 +328,44 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
         int at = 0;
         if (lane == 31) at = atomicAdd(&sh.listed, before);
         at = __shfl_sync(FULL, at, 31) + before - mine;
-        if (e.x) list[at++] = static_cast<uint16_t>(4 * i);
-        if (e.y) list[at++] = static_cast<uint16_t>(4 * i + 1);
-        if (e.z) list[at++] = static_cast<uint16_t>(4 * i + 2);
-        if (e.w) list[at++] = static_cast<uint16_t>(4 * i + 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (SMALL) {
+                if (w[k] & 0xffffu) list[at++] = static_cast<uint16_t>(PER * i + 2 * k);
+                if (w[k] >> 16) list[at++] = static_cast<uint16_t>(PER * i + 2 * k + 1);
+            } else if (w[k]) {
+                list[at++] = static_cast<uint16_t>(PER * i + k);
+            }
+        }
     }
     __syncthreads();
     if (A.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int listed = sh.listed, turns = (n + ROWS - 1) / ROWS;
     for (int j = tid; j < listed * turns; j += CT) {
         const int turn = j / listed, at = list[j - turn * listed], v = lo + at, r0 = turn * ROWS;
-        const uint32_t e = table[at];
+        const uint32_t e = table.get(at);
         float x[ROWS];  // as they are behind their masks
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
             if (r0 + r < n) x[r] = load1<T>(A.out + (row_of(r0 + r) + v) * ES);
         float bias = 0.f;
-        if (e & BIAS)
-            for (int i = 0; i < sh.biases; ++i)
-                if (bias_id[i] == v) bias += bias_of[i];
+        bool biased = false;
+        if (e & LOOK)
+            for (int i = 0; i < sh.biases; i += 4) {
+                const int4 id = *reinterpret_cast<const int4 *>(bias_id + i);
+                if (id.x != v && id.y != v && id.z != v && id.w != v) continue;
+                biased = true;
+                if (id.x == v) bias += bias_of[i];
+                if (id.y == v) bias += bias_of[i + 1];
+                if (id.z == v) bias += bias_of[i + 2];
+                if (id.w == v) bias += bias_of[i + 3];
+            }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int s = r0 + r;
             if (s >= n) break;
             uint32_t count = e / ONE;
-            if (e & DRAFT) {
+            if ((e & LOOK) && A.tokens) {
                 const uint64_t path = sh.path[s];
                 for (int i = 0; i <= s; ++i) count += ((path >> i) & 1ull) && sh.token[i] == v ? 1u : 0u;
             }
@@ -338,7 +376,7 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
             }
             if (count > 0 || (e & PROMPT)) y = y > 0.f ? __fdiv_rn(y, rho) : y * rho;
             if (count > 0) y = fmaf(-freq, static_cast<float>(count), y) - pres;
-            if (e & BIAS) y += bias;
+            if (biased) y += bias;
             store1<T>(A.out + (row_of(s) + v) * ES, y);
         }
     }
@@ -346,8 +384,9 @@ __global__ void __launch_bounds__(CT, 4) adjust_impl(const __grid_constant__ Adj
 
 }  // namespace
 
-const void *adj_func(int dtype) {
-    return dtype == 0 ? reinterpret_cast<const void *>(adjust_impl<float>) : reinterpret_cast<const void *>(adjust_impl<bf16_t>);
+const void *adj_func(int dtype, bool small) {
+    if (dtype == 0) return small ? reinterpret_cast<const void *>(adjust_impl<float, true>) : reinterpret_cast<const void *>(adjust_impl<float, false>);
+    return small ? reinterpret_cast<const void *>(adjust_impl<bf16_t, true>) : reinterpret_cast<const void *>(adjust_impl<bf16_t, false>);
 }
 
 const void *mask_func(int dtype, bool few) {
@@ -355,6 +394,8 @@ const void *mask_func(int dtype, bool few) {
     return few ? reinterpret_cast<const void *>(mask_impl<bf16_t, 1>) : reinterpret_cast<const void *>(mask_impl<bf16_t, 4>);
 }
 
-uint32_t adj_smem(int slice, int n_bias) { return static_cast<uint32_t>(slice) * 6 + n_bias * 8; }
+uint32_t adj_smem(int slice, int listed, int biases, bool small) {
+    return static_cast<uint32_t>(slice) * (small ? 2 : 4) + static_cast<uint32_t>(listed) * 2 + static_cast<uint32_t>(biases) * 8;
+}
 
 }  // namespace mtp

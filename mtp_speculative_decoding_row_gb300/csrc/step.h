@@ -49,13 +49,16 @@ struct AdjArgs {
     long long mask_s[2];
     int32_t *flags;
     int B, S, V, L, n_bias;
-    int slice;               // vocabulary entries of a block (a multiple of 32)
+    int slice;               // vocabulary entries of a block (a multiple of 256)
+    int listed_most;         // entries of a slice that can change (a multiple of 8)
+    int bias_room;           // n_bias and four more, a multiple of 4; 0 for none
     int alone;               // nothing but masks: the first kernel is the only one
     int overlap;             // launched behind the kernel of the masks, beside which it may run
     int vec_history;         // 16-byte loads of the history are aligned
 };
-const void *adj_func(int dtype);
+const void *adj_func(int dtype, bool small);  // small: tables of 16 bits, texts of up to ADJ_SMALL tokens
 const void *mask_func(int dtype, bool few);  // few: a block takes a quarter of the vectors
-uint32_t adj_smem(int slice, int n_bias);
+constexpr int ADJ_SMALL = 16383, ADJ_SLICE = 8192, ADJ_SMALL_SLICE = 20480;
+uint32_t adj_smem(int slice, int listed, int biases, bool small);
 
 }  // namespace mtp

@@ -251,9 +251,24 @@ extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t strea
     A.S = a.S;
     A.V = a.V;
     A.vec_history = reinterpret_cast<uintptr_t>(a.history) % 16 == 0 && a.L % 4 == 0;
-    const void *adjust = adj_func(a.dtype);
-    // the shared memory of a block is at most 56 KB: the limit has to be raised
-    if (resident(dev, adjust, adj_smem(8192, MTP_MAX_BIAS), ADJ_COUNT_THREADS) < 1) return MTP_ERR_NO_DEVICE;
+    // Slices as large as leaves a block for every place on the GPU: each reads the
+    // text, and those that wait for a place count nothing beside the first kernel.
+    // (64 sequences of 8192 tokens, 4 rows of 151936: SLICES)
+    const bool small = A.L <= ADJ_SMALL;
+    const void *adjust = adj_func(a.dtype, small);
+    const int most = small ? ADJ_SMALL_SLICE : ADJ_SLICE;
+    A.bias_room = a.n_bias > 0 ? (a.n_bias + 7) / 4 * 4 : 0;
+    // (raises the kernel's limit of shared memory, too)
+    const int per_sm = resident(dev, adjust, adj_smem(most, most, MTP_MAX_BIAS + 4, small), ADJ_COUNT_THREADS);
+    if (per_sm < 1) return MTP_ERR_NO_DEVICE;
+    const long long places = static_cast<long long>(sms) * (2048 / ADJ_COUNT_THREADS);
+    long long parts = places / a.B;
+    parts = parts < 1 ? 1 : parts;
+    const long long each = (a.V + parts - 1) / parts;
+    A.slice = static_cast<int>(each < 1024 ? 1024 : each > most ? most : (each + 255) / 256 * 256);
+    if (A.slice > most) A.slice = most;
+    const long long events = (static_cast<long long>(A.L) + (a.tokens ? a.S : 0) + a.n_bias + 7) / 8 * 8;
+    A.listed_most = static_cast<int>(events < A.slice ? events : A.slice);
     if (z != o || a.mask) {  // (in place and without a mask nothing is streamed)
         const long long rows = static_cast<long long>(a.B) * a.S, vecs = (static_cast<long long>(a.V) * es + 15) / 16;
         const bool few = rows * ((vecs + 4 * ADJ_THREADS - 1) / (4 * ADJ_THREADS)) < 4 * sms;
@@ -264,10 +279,7 @@ extern "C" int mtp_adjust_logits(const mtp_adjust_args *args, mtp_stream_t strea
         if (rc != MTP_OK || A.alone) return rc;
         A.overlap = 1;
     }
-    // Slices as large as leaves two blocks for every SM: each reads the text.
-    A.slice = 8192;
-    while (A.slice > 1024 && static_cast<long long>(a.B) * ((a.V + A.slice - 1) / A.slice) < 2 * sms) A.slice /= 2;
     // (the sequences next to one another: the first slices, of the most frequent
     // words, start first)
-    return launch(adjust, dim3(a.B, (a.V + A.slice - 1) / A.slice), ADJ_COUNT_THREADS, adj_smem(A.slice, A.n_bias), &A, stream);
+    return launch(adjust, dim3(a.B, (a.V + A.slice - 1) / A.slice), ADJ_COUNT_THREADS, adj_smem(A.slice, A.listed_most, A.bias_room, small), &A, stream);
 }
