@@ -1,8 +1,9 @@
 /*
  * mtp_rs.h -- C ABI of the GB300 (sm_103a) library for multi-token-prediction
  * rejection-sampling verification, per-position row statistics, the fused
- * forward+backward of the end-to-end TV loss, and the operators of
- * tree-shaped drafts (attention, beam selection, commit).
+ * forward+backward of the end-to-end TV loss, the operators of tree-shaped
+ * drafts (attention, also over shared prefixes, beam selection, commit) and those
+ * around a verification step (rotary positions, cache append, logit adjustment).
  *
  * Method references (page title, section):
  *   [BB] "Breaking Entropy Bounds: Accelerating RL Training via MTP with
@@ -727,13 +728,14 @@ typedef struct mtp_tuning {
     int pair_l2_mb;          /* streaming row-pair kernel: the same cap for sequences; 0 = no cap */
     int row_streams;         /* cluster-resident row kernel: sequences in flight per CTA, 1 or 2; 0 = planner */
     /* Fault injection for tests of the bounded waits (both 0 in normal use).
-     * They act on the TMEM-resident TV kernel and on the tensor-core kernel of
-     * mtp_tree_attention only. */
+     * They act on the TMEM-resident TV kernel and on the tensor-core kernels of
+     * mtp_tree_attention and mtp_prefix_attention only. */
     int fault_wait_us;       /* limit of every on-chip wait in microseconds; 0 = 2 s */
     int fault_skip_position; /* 1 + the position whose first exchange push the cluster's first warp
                                 skips: every wait on it gives up, and that position and the later ones
                                 of its cluster come back flagged MTP_ROW_TIMEOUT; tree attention: 1 +
-                                the CTA whose loader leaves out the first of its signals; 0 = none */
+                                the CTA whose loader leaves out the first of its signals (prefix
+                                attention: of both kernels); 0 = none */
 } mtp_tuning;
 
 /* Set (t != NULL) or clear (t == NULL) the overrides; affects calls made

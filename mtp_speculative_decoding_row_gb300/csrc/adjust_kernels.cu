@@ -8,18 +8,20 @@
 //   x = x - freq c - pres [c > 0] + sum of v's biases
 //   x = -inf                      where the mask has no bit.
 //
-// Memory bounds it: every logit is read and written once, by a kernel that
-// streams the rows through their masks.  A second one, a block to a slice of the
-// vocabulary of one sequence, counts the slice's tokens of the text in shared
-// memory (integers: the order of the atomic additions changes nothing) and lists
-// the entries that anything but the mask changes while the first still runs, then
-// rewrites those, a thread to an entry.  A text's words crowd in few places:
-// dealt out from a list they keep all threads busy (64 x 4 rows, 8192 tokens:
-// 118 us where they were looked for beside the streamed vectors, 63 us with the
-// list in one kernel, whose blocks spent their time in waits one after the other:
-// counting, streaming, listing).  Rows
-// differ in their paths only; the few drafted tokens are looked up in the path
-// where they occur, so that one count serves all rows.
+// Memory bounds the rows: every logit is read and written once, by a kernel that
+// streams them through their masks (64 x 4 rows of 151936: 25 us, 28 with masks;
+// floor 23).  A second one, a block to a slice of the vocabulary of one sequence,
+// counts the slice's tokens of the text in shared memory (integers: the order of
+// the atomic additions changes nothing) and lists the entries that anything but
+// the mask changes, then, when the first is done, rewrites those, a thread to an
+// entry.  A text's words crowd in few places: dealt out from a list they keep all
+// threads busy (texts of 8192 tokens: 118 us where each streamed vector looked for
+// its own, 54 so).  What bounds the second: its blocks' instructions -- each goes
+// through the whole text of its sequence -- and the blocks of the first slices,
+// where most words are.  Both in one kernel, with the rows in shared memory, took
+// 71 us: a text was then counted four times as often.  Rows differ in their paths
+// only; the few drafted tokens are looked up in the path where they occur, so that
+// one count serves all rows.
 #include "common.cuh"
 #include "step.h"
 
