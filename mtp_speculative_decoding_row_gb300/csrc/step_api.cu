@@ -74,10 +74,13 @@ int rot_launch(RotArgs &A, int dtype, uintptr_t low, bool interleaved, bool appe
     const int piece = vec ? width : 1;
     A.rot_units = A.n / piece;
     A.units = A.rot_units + (A.D - 2 * A.n) / piece;
-    // Tokens of a block: one while the blocks fit the GPU at once, more where
-    // there are many, so that a block's angles and its start are shared.
-    const long long all = static_cast<long long>(A.B) * A.T, fit = static_cast<long long>(sms) * 8;
-    A.tokens = all <= fit ? 1 : all <= 4 * fit ? 2 : 4;
+    // Tokens of a block, which share its start: one where few tokens leave SMs idle
+    // (256 tokens: one 4.0 us, four 4.2; appended 4.7 and 5.4), else four (16384 of
+    // 40 heads: one 70 us, two 58, four 54, eight 55), or eight where there are many
+    // and their heads few (16384 of 9 heads: four 20.0 us, eight 17.7; but 3063 of
+    // 10 heads 6.3 and 7.9).
+    const long long all = static_cast<long long>(A.B) * A.T, units = 4ll * (A.hq + A.hk + A.hv) * A.units;
+    A.tokens = all <= 2ll * sms ? 1 : units < 4 * ROT_THREADS && all > 32ll * sms ? 8 : 4;
     if (A.tokens > A.T) A.tokens = A.T;
     A.chunks = (A.T + A.tokens - 1) / A.tokens;
     const long long blocks = static_cast<long long>(A.B) * A.chunks;
