@@ -16,8 +16,8 @@
 //
 // Memory bounds it: 16384 tokens of 32 and 8 heads of 128 (bfloat16) 54 us, 6.2
 // TB/s, 0.92 of a copy's rate; appended with their values and rotated queries 86
-// us for 20,480 tokens, 0.86.  256 tokens take 4 us: the launch and three loads
-// that wait for one another (length, page, row).
+// us for 20,481 tokens, 0.86.  256 tokens take 3 us: the launch, and where they are
+// appended three loads that wait for one another (length, page, row).
 #include "common.cuh"
 #include "step.h"
 

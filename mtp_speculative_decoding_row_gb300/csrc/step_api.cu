@@ -74,13 +74,15 @@ int rot_launch(RotArgs &A, int dtype, uintptr_t low, bool interleaved, bool appe
     const int piece = vec ? width : 1;
     A.rot_units = A.n / piece;
     A.units = A.rot_units + (A.D - 2 * A.n) / piece;
-    // Tokens of a block, which share its start: one where few tokens leave SMs idle
-    // (256 tokens: one 4.0 us, four 4.2; appended 4.7 and 5.4), else four (16384 of
-    // 40 heads: one 70 us, two 58, four 54, eight 55), or eight where there are many
-    // and their heads few (16384 of 9 heads: four 20.0 us, eight 17.7; but 3063 of
-    // 10 heads 6.3 and 7.9).
+    // Tokens of a block, which share its start (heads of 128, bfloat16, captured
+    // calls in turn).  Few tokens, few to a block, so that no SM is idle: of 40 heads
+    // 256 tokens take 2.9, 3.1 and 4.0 us with one, two and four (160 appended ones
+    // 3.8, 4.2 and 5.2), 512 tokens 4.0, 3.5 and 4.1.  Then four (1024: 5.7, 5.7
+    // and 4.9; 16384: 71, 58 and 54, eight 55), though 2048 in two waves take 9.0
+    // and with two 7.4.  Eight where there are many and their heads few (16384 of 9
+    // heads: four 19.8, eight 17.5; but 4096 6.4 and 7.3).
     const long long all = static_cast<long long>(A.B) * A.T, units = 4ll * (A.hq + A.hk + A.hv) * A.units;
-    A.tokens = all <= 2ll * sms ? 1 : units < 4 * ROT_THREADS && all > 32ll * sms ? 8 : 4;
+    A.tokens = all <= 2ll * sms ? 1 : all <= 4ll * sms ? 2 : units < 4 * ROT_THREADS && all > 32ll * sms ? 8 : 4;
     if (A.tokens > A.T) A.tokens = A.T;
     A.chunks = (A.T + A.tokens - 1) / A.tokens;
     const long long blocks = static_cast<long long>(A.B) * A.chunks;
