@@ -84,7 +84,7 @@ int rot_launch(RotArgs &A, int dtype, uintptr_t low, bool interleaved, bool appe
     const long long all = static_cast<long long>(A.B) * A.T, units = 4ll * (A.hq + A.hk + A.hv) * A.units;
     A.tokens = all <= 2ll * sms ? 1 : all <= 4ll * sms ? 2 : units < 4 * ROT_THREADS && all > 32ll * sms ? 8 : 4;
     if (A.tokens > A.T) A.tokens = A.T;
-    A.chunks = (A.T + A.tokens - 1) / A.tokens;
+    A.chunks = static_cast<int>((static_cast<long long>(A.T) + A.tokens - 1) / A.tokens);
     const long long blocks = static_cast<long long>(A.B) * A.chunks;
     if (blocks > 0x7fffffffll) return MTP_ERR_INVALID_ARG;
     return launch(rot_func(dtype, vec, interleaved, append), dim3(static_cast<unsigned>(blocks)), ROT_THREADS, rot_smem(A), &A, stream);

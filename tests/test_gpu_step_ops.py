@@ -479,3 +479,11 @@ def test_step_operators_in_graphs_and_on_streams():
         assert torch.equal(z.logits, z2.logits)
         for b, m in enumerate(x["n_new"].tolist()):
             assert torch.equal(a.q[b, :m], a2.q[b, :m]) and torch.equal(a.k[b, :m], a2.k[b, :m])
+
+
+def test_rope_of_the_longest_sequence():
+    """The blocks of a sequence whose tokens end at the last 32-bit number."""
+    T = (1 << 31) - 1
+    q = torch.empty(1, T, 1, 1, dtype=bf16, device="cuda").uniform_()
+    r = mtp.mtp_rope(q, None, torch.zeros(1, 1, dtype=i32, device="cuda").expand(1, T), torch.empty(0, device="cuda"))
+    assert torch.equal(r.q.view(torch.int16), q.view(torch.int16))
