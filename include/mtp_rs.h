@@ -534,7 +534,9 @@ int mtp_tree_commit(const mtp_tree_commit_args *args, mtp_stream_t stream);
  * verification take: rotated queries and keys, a filled cache, adjusted logits.
  * An output may be its input itself (the same address and strides); otherwise
  * the memory from its first to its last byte must not meet that of an input
- * (MTP_ERR_INVALID_ARG where two such ranges are found to meet).
+ * (MTP_ERR_INVALID_ARG where two such ranges are found to meet).  Outputs that
+ * are their inputs, and outputs of one call, may be parts of one tensor (a fused
+ * projection, a cache of both), of the same strides and without a common element.
  */
 #define MTP_MAX_BIAS 1024   /* biases of a sequence in mtp_adjust_logits */
 

@@ -34,7 +34,7 @@ uint32_t rot_smem(const RotArgs &A);
 
 // ----------------------------------------------------- adjust logits ----
 
-constexpr int ADJ_THREADS = 256, ADJ_COUNT_THREADS = 512, ADJ_MAX_ROWS = 64, ADJ_MAX_BIAS = 1024;
+constexpr int ADJ_THREADS = 256, ADJ_COUNT_THREADS = 512, ADJ_MAX_ROWS = 64;
 
 struct AdjArgs {
     const unsigned char *z;  // [B, S, V]

@@ -23,21 +23,28 @@ struct Rows {
     Span span;
     bool gaps = true;  // no stride of 0: no two indices are one place
     uintptr_t low = 0; // the bits of the address and the strides
+    int n[3] = {};     // sizes; 1 where the stride is 0
+    long long s[3] = {}, row = 0;
     // False for a stride or a tensor that no memory has (|stride| < 2^40 elements
     // times the dimension within 2^62 bytes).
-    bool set(const void *p, const int64_t *stride, const int (&n)[3], long long row, int es, long long *out) {
+    bool set(const void *p, const int64_t *stride, const int (&size)[3], long long bytes, int es, long long *out) {
         span.lo = reinterpret_cast<uintptr_t>(p);
         unsigned long long reach = 0;
         low = span.lo;
+        row = bytes;
         for (int i = 0; i < 3; ++i) {
             out[i] = 0;
-            if (n[i] <= 1) continue;
+            n[i] = 1;
+            if (size[i] <= 1) continue;
             if (stride[i] < 0 || stride[i] >= (1ll << 40)) return false;
-            out[i] = stride[i] * es;
-            if (out[i] == 0) gaps = false;
+            out[i] = s[i] = stride[i] * es;
+            if (out[i] == 0)
+                gaps = false;
+            else
+                n[i] = size[i];
             low |= static_cast<uintptr_t>(out[i]);
-            const unsigned long long far = static_cast<unsigned long long>(out[i]) * (n[i] - 1);
-            if (out[i] > 0 && far / out[i] != static_cast<unsigned long long>(n[i] - 1)) return false;
+            const unsigned long long far = static_cast<unsigned long long>(out[i]) * (size[i] - 1);
+            if (out[i] > 0 && far / out[i] != static_cast<unsigned long long>(size[i] - 1)) return false;
             reach += far;
             if (far >= (1ull << 61) || reach >= (1ull << 61)) return false;
         }
@@ -48,12 +55,60 @@ struct Rows {
 
 bool same(const long long (&a)[3], const long long (&b)[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
 
-// `out` of a tensor `in`, of the same shape: in place, or apart from it and
-// from `other` (the call's second input, which may lie between the rows of an
-// output that is in place).
+// Whether a row at `off` bytes meets one at a sum of d_i s[i], -back[i] <= d_i <=
+// ahead[i], strides falling: of each d_i only those matter that leave what the
+// other strides reach.
+bool reaches(long long off, const long long *s, const long long *back, const long long *ahead, int i, long long row) {
+    if (i == 3) return -row < off && off < row;
+    long long left = row, right = row;  // off lies in (-left, right) of the rest
+    for (int j = i + 1; j < 3; ++j) {
+        left += back[j] * s[j];
+        right += ahead[j] * s[j];
+    }
+    if (s[i] == 0) return reaches(off, s, back, ahead, i + 1, row);
+    long long lo = -back[i], hi = ahead[i];
+    while (lo <= hi && off - lo * s[i] >= right) {  // too far ahead: d has to be larger
+        const long long step = (off - lo * s[i] - right) / s[i] + 1;
+        lo += step;
+    }
+    while (lo <= hi && off - hi * s[i] <= -left) {
+        const long long step = (-left - (off - hi * s[i])) / s[i] + 1;
+        hi -= step;
+    }
+    if (hi - lo > 3) return true;  // strides that do not nest: taken for a meeting
+    for (long long d = lo; d <= hi; ++d)
+        if (reaches(off - d * s[i], s, back, ahead, i + 1, row)) return true;
+    return false;
+}
+
+// Whether two tensors have a byte in common.  Parts of one tensor, of the same
+// strides, may lie between one another's rows; of other strides they are taken to
+// meet where their ranges do.
+bool meet(const Rows &a, const Rows &b) {
+    if (!a.span.meets(b.span)) return false;
+    long long s[3], back[3], ahead[3];
+    for (int i = 0; i < 3; ++i) {
+        if (a.n[i] > 1 && b.n[i] > 1 && a.s[i] != b.s[i]) return true;
+        s[i] = a.n[i] > 1 ? a.s[i] : b.n[i] > 1 ? b.s[i] : 0;
+        back[i] = b.n[i] - 1;  // the place of a less that of b: (index of a - index of b) strides
+        ahead[i] = a.n[i] - 1;
+    }
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (s[j] < s[j + 1]) {
+                const long long t[3] = {s[j], back[j], ahead[j]};
+                s[j] = s[j + 1], back[j] = back[j + 1], ahead[j] = ahead[j + 1];
+                s[j + 1] = t[0], back[j + 1] = t[1], ahead[j + 1] = t[2];
+            }
+    return reaches(static_cast<long long>(b.span.lo - a.span.lo), s, back, ahead, 0, a.row);
+}
+
+// `out` of a tensor `in`, of the same shape: in place, or apart from it; and
+// apart from `other`, another input of the call (which may lie between the rows of
+// an output that is in place, but is read by other threads than write it).
 bool out_of(const Rows &out, const long long (&os)[3], const Rows &in, const long long (&is)[3], const Rows *other) {
     if (!out.gaps) return false;
-    if (out.span.lo == in.span.lo && same(os, is)) return true;
+    if (out.span.lo == in.span.lo && same(os, is)) return !(other && meet(out, *other));
     return !out.span.meets(in.span) && !(other && out.span.meets(other->span));
 }
 
@@ -120,6 +175,7 @@ extern "C" int mtp_rope(const mtp_rope_args *args, mtp_stream_t stream) {
     }
     if ((a.Hq > 0 && !out_of(qo, A.qos, q, A.qs, a.Hkv > 0 ? &k : nullptr)) || (a.Hkv > 0 && !out_of(ko, A.kos, k, A.ks, a.Hq > 0 ? &q : nullptr)))
         return MTP_ERR_INVALID_ARG;
+    if (a.Hq > 0 && a.Hkv > 0 && meet(qo, ko)) return MTP_ERR_INVALID_ARG;
     if (low % es != 0) return MTP_ERR_MISALIGNED;
     A.q = static_cast<const unsigned char *>(a.q);
     A.k = static_cast<const unsigned char *>(a.k);
@@ -161,20 +217,21 @@ extern "C" int mtp_cache_append(const mtp_cache_append_args *args, mtp_stream_t 
         !kc.set(a.k_cache, a.k_cache_stride, nc, row, es, A.kcs) || !vc.set(a.v_cache, a.v_cache_stride, nc, row, es, A.vcs))
         return MTP_ERR_INVALID_ARG;
     uintptr_t low = k.low | v.low | kc.low | vc.low;
-    if (!kc.gaps || !vc.gaps || kc.span.meets(k.span) || kc.span.meets(v.span) || vc.span.meets(k.span) || vc.span.meets(v.span))
+    if (!kc.gaps || !vc.gaps || meet(kc, vc) || kc.span.meets(k.span) || kc.span.meets(v.span) || vc.span.meets(k.span) || vc.span.meets(v.span))
         return MTP_ERR_INVALID_ARG;
     if (a.Hq > 0) {
         if (!q.set(a.q, a.q_stride, nq, row, es, A.qs) || !qo.set(a.q_out, a.q_out_stride, nq, row, es, A.qos)) return MTP_ERR_INVALID_ARG;
         low |= q.low | qo.low;
         if (!out_of(qo, A.qos, q, A.qs, &k) || kc.span.meets(q.span) || vc.span.meets(q.span) || kc.span.meets(qo.span) || vc.span.meets(qo.span))
             return MTP_ERR_INVALID_ARG;
-        if (qo.span.lo != q.span.lo && qo.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
+        if (qo.span.lo == q.span.lo ? meet(qo, v) : qo.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
     }
     if (a.k_out) {
         if (!ko.set(a.k_out, a.k_out_stride, nk, row, es, A.kos)) return MTP_ERR_INVALID_ARG;
         low |= ko.low;
         if (!out_of(ko, A.kos, k, A.ks, a.Hq > 0 ? &q : nullptr) || kc.span.meets(ko.span) || vc.span.meets(ko.span)) return MTP_ERR_INVALID_ARG;
-        if (ko.span.lo != k.span.lo && ko.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
+        if (ko.span.lo == k.span.lo ? meet(ko, v) : ko.span.meets(v.span)) return MTP_ERR_INVALID_ARG;
+        if (a.Hq > 0 && meet(qo, ko)) return MTP_ERR_INVALID_ARG;
     }
     if (low % es != 0) return MTP_ERR_MISALIGNED;
     // every block of a sequence reads its lengths and pages, one writes the outputs

@@ -336,3 +336,57 @@ def test_reference_angles_are_exact():
     want = pos.double()[..., None] * f.double()
     got = step_ref.angles(pos, f)
     assert torch.allclose(got.cos(), want.cos(), atol=1e-9) and torch.allclose(got.sin(), want.sin(), atol=1e-9)
+
+
+# ------------------------------------------- outputs that are another tensor --
+
+FUSED = dict(q_stride=(1536, 512, 64), k_stride=(1536, 512, 64), q_out_stride=(1536, 512, 64), k_out_stride=(1536, 512, 64))  # 4 + 2 + 2 heads
+Q0, K0, KO = 1 << 30, (1 << 30) + 4 * 64 * 4, 4 << 30
+
+
+@pytest.mark.parametrize("new", [
+    dict(FUSED, k=Q0, q_out=Q0),                            # q in place, and the same memory is k
+    dict(FUSED, k=K0 - 256, q_out=Q0),                      # k begins in q's last head
+    dict(FUSED, q_out=3 << 30, k=Q0, k_out=Q0),             # k in place, and the same memory is q
+    dict(FUSED, q_out=KO, k_out=KO),                        # both outputs in one place
+    dict(FUSED, q_out=KO, k_out=KO + 512 * 4),              # one token on
+    dict(FUSED, q_out=Q0, k=K0, k_stride=(1536, 500, 64)),  # ranges that meet, strides that differ
+])
+def test_rope_refuses_outputs_on_other_tensors(lib, new):
+    assert answer(lib.mtp_rope, rope_abi(**new)) == 1
+
+
+@pytest.mark.parametrize("new", [
+    dict(FUSED, k=K0, q_out=Q0, k_out=K0),                  # both in place, of one tensor
+    dict(FUSED, q_out=KO, k_out=KO + 4 * 64 * 4),           # outputs of one tensor
+    dict(FUSED, k=K0, q_out=Q0, k_out=K0, Hkv=1, k_stride=(1536, 512, 7), k_out_stride=(1536, 512, 7)),
+    dict(FUSED, k=Q0 + 256, q_out=Q0, k_out=Q0 + 256, Hq=2, Hkv=2, q_stride=(1536, 512, 192), k_stride=(1536, 512, 192),
+         q_out_stride=(1536, 512, 192), k_out_stride=(1536, 512, 192)),  # heads of (q, k, v)
+])
+def test_rope_takes_parts_of_one_tensor(lib, new):
+    assert answer(lib.mtp_rope, rope_abi(**new)) != 1
+
+
+S3 = (384, 128, 64)
+
+
+@pytest.mark.parametrize("new", [
+    dict(v=2 << 30, k_out=2 << 30),                                   # v is k, which is rotated in place
+    dict(k=1 << 30, k_stride=(768, 256, 64), q_out=1 << 30, k_out=None),  # q in place, k its first heads
+    dict(v=1 << 30, v_stride=(768, 256, 64), q_out=1 << 30),          # q in place, v its first heads
+    dict(v_cache=6 << 30),                                            # one cache for both
+    dict(v_cache=(6 << 30) + 64 * 4),                                 # a head on
+    dict(q_out=4 << 30, k_out=(4 << 30) + 256, k_out_stride=(768, 256, 64)),
+])
+def test_cache_append_refuses_outputs_on_other_tensors(lib, new):
+    assert answer(lib.mtp_cache_append, append_abi(**new)) == 1
+
+
+@pytest.mark.parametrize("new", [
+    dict(k_cache_stride=(4096, 128, 64), v_cache_stride=(4096, 128, 64), v_cache=(6 << 30) + 2048 * 4),  # pages of keys, then values
+    dict(k_cache_stride=(4096, 256, 64), v_cache_stride=(4096, 256, 64), v_cache=(6 << 30) + 128 * 4),   # of tokens
+    dict(k=K0, v=K0 + 512, q_out=Q0, k_out=K0, q_stride=(1536, 512, 64), q_out_stride=(1536, 512, 64), k_stride=(1536, 512, 64),
+         k_out_stride=(1536, 512, 64), v_stride=(1536, 512, 64)),
+])
+def test_cache_append_takes_parts_of_one_tensor(lib, new):
+    assert answer(lib.mtp_cache_append, append_abi(**new)) != 1
