@@ -416,6 +416,9 @@ int64_t mtp_tree_attention_workspace(const mtp_tree_attention_args *args);
  * its sequence's own cached tokens and its own path; prefixes of no tokens and
  * of no sequences are allowed.  The rest is as in mtp_tree_attention.
  *
+ * With bfloat16 storage the weights are rounded to bfloat16 for their product as
+ * there, or (where the prefixes have few rows, by a choice of kernels) to 16 bits.
+ *
  * A sequence is flagged as there, for a bad length or page of its prefix too;
  * all rows of a flagged sequence are NaN.  A group_start that does not rise
  * from 0 to B flags every sequence MTP_ROW_BAD_ID.

@@ -91,7 +91,7 @@ UmmaPlan attn_umma_plan(int D, int rows);
 UmmaPlan prefix_umma_plan(int D, int rows, long long most);
 // Both of mtp_prefix_attention's kernels with few rows (csrc/few_attention_umma.cu):
 // heads of 128 (up to 32 rows) or 256 (up to 16), tiles of 128 keys.
-UmmaPlan few_umma_plan(int D, int rows, bool prefix);
+UmmaPlan few_umma_plan(int D, int rows, bool prefix, bool precise);
 int attn_umma_bn(int D);  // keys of a tile
 const void *attn_join_func(int dtype, int D);
 const void *prefix_join_func(int dtype, int D);

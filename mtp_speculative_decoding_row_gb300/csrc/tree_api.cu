@@ -82,12 +82,12 @@ bool few_sizes(const mtp_tree_attention_args &a, long long rows) {
     return ((a.D == 128 && rows <= 32) || (a.D == 256 && rows <= 16)) && (a.page_size % 8 == 0 || a.page_size >= 128);
 }
 
-int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p, bool few = false) {
+int attn_plan(const mtp_tree_attention_args &a, bool umma, AttnPlan &p, bool few = false, bool precise = false) {
     int dev, sms;
     if (!device_sms(dev, sms)) return MTP_ERR_CUDA;
     p.rows = a.T * (a.Hq / a.Hkv);
     if (umma) {
-        set_umma(p, few && few_sizes(a, p.rows) ? few_umma_plan(a.D, p.rows, false) : attn_umma_plan(a.D, p.rows));
+        set_umma(p, few && few_sizes(a, p.rows) ? few_umma_plan(a.D, p.rows, false, precise) : attn_umma_plan(a.D, p.rows));
         umma_tiles(a, p);
     } else {
         p.func = attn_simt_func(a.dtype, a.D, false);
@@ -324,6 +324,12 @@ int prefix_sizes(const mtp_prefix_attention_args &x) {
     return MTP_OK;
 }
 
+// Query rows of a key head that a prefix has on average.
+long long mean_rows(const mtp_prefix_attention_args &x) {
+    const long long all = static_cast<long long>(x.own.B) * x.own.T * (x.own.Hq / x.own.Hkv);
+    return (all + x.prefixes - 1) / x.prefixes;
+}
+
 // The plan of the prefixes' kernel.  What their rows and lengths are only the
 // device knows: row tiles are as large as the average number of rows fills, and
 // there are no more CTAs than tiles that a full page table could have.
@@ -334,9 +340,9 @@ int prefix_plan(const mtp_prefix_attention_args &x, bool umma, AttnPlan &p) {
     p.rows = a.T * (a.Hq / a.Hkv);
     const long long all = static_cast<long long>(a.B) * p.rows;
     if (umma) {
-        const long long mean = (all + x.prefixes - 1) / x.prefixes;
+        const long long mean = mean_rows(x);
         const int rows = static_cast<int>(mean < 1024 ? mean : 1024);
-        set_umma(p, few_sizes(a, mean) ? few_umma_plan(a.D, rows, true) : prefix_umma_plan(a.D, rows, all));
+        set_umma(p, few_sizes(a, mean) ? few_umma_plan(a.D, rows, true, true) : prefix_umma_plan(a.D, rows, all));
         umma_tiles(a, p);
     } else {
         p.func = attn_simt_func(a.dtype, a.D, true);
@@ -403,7 +409,7 @@ extern "C" int64_t mtp_prefix_attention_workspace(const mtp_prefix_attention_arg
     for (int umma = 0; umma < (umma_sizes(args->own) ? 2 : 1); ++umma) {
         AttnPlan own, pre;
         TreeAttnArgs A = {}, S = {};
-        if (attn_plan(args->own, umma != 0, own, true) != MTP_OK || prefix_plan(*args, umma != 0, pre) != MTP_OK) return -1;
+        if (attn_plan(args->own, umma != 0, own, true, few_sizes(args->own, mean_rows(*args))) != MTP_OK || prefix_plan(*args, umma != 0, pre) != MTP_OK) return -1;
         const size_t bytes = prefix_layout(*args, own, pre, nullptr, A, S);
         if (bytes > most) most = bytes;
     }
@@ -426,7 +432,7 @@ extern "C" int mtp_prefix_attention(const mtp_prefix_attention_args *args, mtp_s
     Maps own_maps, pre_maps;
     for (;;) {
         own = pre = AttnPlan();
-        const int pc = attn_plan(a, umma, own, true);
+        const int pc = attn_plan(a, umma, own, true, few_sizes(a, mean_rows(x)));
         if (pc != MTP_OK) return pc;
         const int qc = prefix_plan(x, umma, pre);
         if (qc != MTP_OK) return qc;

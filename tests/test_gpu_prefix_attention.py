@@ -342,3 +342,37 @@ def test_prefix_attention_a_wait_that_runs_out_is_reported(sizes, T, Hq, D):
         if cta == 0:
             assert lost.any()
         assert torch.equal(mtp.mtp_prefix_attention(**g).out, good.out)
+
+
+def few_keys(x):
+    """out, its bound and what weights rounded once to bfloat16 would give, in 64
+    bits, of sequences whose every node sees its whole text (T = 1).
+
+    A weight is off by 2^-16 (two roundings of 2^-8) and by its score's error,
+    which a product of D terms in float32 keeps below D 2^-23 of the terms' sum; the
+    weights' sum likewise.  The output is rounded once, by 2^-8 of itself."""
+    q, k, v, kc, vc, table, lens, _, _ = one_text(x)
+    B, _, Hq, D = q.shape
+    G = Hq // k.shape[2]
+    ref, tol, once = (torch.zeros(B, 1, Hq, D, dtype=torch.float64) for _ in range(3))
+    for b in range(B):
+        rows = table[b, :int(lens[b])].long()
+        keys, values = (torch.cat([c[rows, 0], n[b]]).double().repeat_interleave(G, 1) for c, n in ((kc, k), (vc, v)))
+        terms = q[b, 0].double()[None] * keys * D ** -0.5
+        s = terms.sum(-1)
+        e = D * 2.0 ** -23 * terms.abs().sum(-1).max()
+        p = (s - s[0]).exp()
+        w = p / p.sum(0)
+        ref[b, 0] = (w[..., None] * values).sum(0)
+        tol[b, 0] = 2.0 ** -8 * ref[b, 0].abs() + (2.0 ** -16 + 2 * e + 2.0 ** -20) * (w[..., None] * values.abs()).sum(0) + 2.0 ** -130
+        once[b, 0] = (p.to(bf16).double()[..., None] * values).sum(0) / p.sum(0)[:, None]
+    return ref, tol, once
+
+
+@pytest.mark.parametrize("D, Hq", [(128, 4), (128, 20), (256, 8)])
+def test_prefix_attention_weights_of_two_parts(D, Hq):
+    x = prefix_case(5, "bf16", [1, 1], [5, 9], 1, Hq, 1, D, 16, [3, 0], "chain")
+    ref, tol, once = few_keys(x)
+    assert bool(((once - ref).abs() > tol).any())  # the bound tells one rounding of the weights
+    out = run(x).out.double().cpu()
+    assert bool(((out - ref).abs() <= tol).all()), float(((out - ref).abs() / tol).max())
